@@ -31,7 +31,21 @@ EXPORTS = ["mega_moe_create", "mega_moe_forward", "mega_moe_forward_mxfp4", "meg
            "mega_moe_last_error", "mega_moe_workspace_bytes", "mega_moe_token_alignment",
            "mega_moe_plan", "mega_moe_tile_order", "mega_moe_get_views", "mega_moe_set_recv_stats",
            "mega_moe_transform_w1", "mega_moe_profile_begin",
-           "mega_moe_profile_end", "mega_moe_check_xcd_layout", "mega_moe_forward_noalloc"]
+           "mega_moe_profile_end", "mega_moe_check_xcd_layout", "mega_moe_forward_noalloc",
+           "mega_moe_norm", "mega_moe_norm_backward", "mega_moe_norm_workspace_bytes",
+           "mega_moe_router_logits", "mega_moe_router_logits_backward",
+           "mega_moe_router_logits_workspace_bytes", "mega_moe_router_topk",
+           "mega_moe_balance_loss", "mega_moe_balance_loss_workspace_bytes",
+           "mega_moe_router_backward"]
+
+MEGA_MOE_BF16 = 0
+MEGA_MOE_F32 = 1
+MEGA_MOE_GATE_NONE = 0
+MEGA_MOE_GATE_TOKEN = 1
+MEGA_MOE_GATE_CHANNEL = 2
+MEGA_MOE_GATE_FULL = 3
+MEGA_MOE_SCORE_SOFTMAX = 0
+MEGA_MOE_SCORE_SIGMOID = 1
 
 
 class mega_moe_config(ctypes.Structure):
@@ -57,6 +71,85 @@ class mega_moe_views(ctypes.Structure):
                 ("l1_topk_weights", ctypes.c_void_p), ("l2_acts", ctypes.c_void_p),
                 ("l2_acts_sf", ctypes.c_void_p), ("combine_buf", ctypes.c_void_p),
                 ("pool_rows_capacity", ctypes.c_int64), ("last_num_tokens", ctypes.c_int32)]
+
+
+# ---- argument blocks of the operators around the layer -----------------------
+
+_TYPES = {"i32": ctypes.c_int32, "i64": ctypes.c_int64, "f32": ctypes.c_float,
+          "ptr": ctypes.c_void_p}
+
+
+def _fields(*runs):
+    return [(name, _TYPES[kind]) for kind, names in runs for name in names.split()]
+
+
+class _Args(ctypes.Structure):
+    """Filled by make_args and set_args, which keep the tensors given alive."""
+
+
+class mega_moe_norm_args(_Args):
+    _fields_ = _fields(("i32", "num_tokens hidden stream_type weight_type gate_kind gate_type"),
+                       ("f32", "post_eps pre_eps residual_scale"),
+                       ("i32", "reserved"),
+                       ("ptr", "h y gate post_weight pre_weight r n q q_sf"),
+                       ("i64", "h_stride y_stride gate_stride r_stride n_stride"))
+
+class mega_moe_norm_backward_args(_Args):
+    _fields_ = _fields(("i32", "num_tokens hidden stream_type weight_type gate_kind gate_type"),
+                       ("f32", "post_eps pre_eps residual_scale"),
+                       ("i32", "reserved"),
+                       ("ptr", "r y gate post_weight pre_weight dr dn dh dy dgate dpost_weight "
+                               "dpre_weight workspace"),
+                       ("i64", "workspace_bytes r_stride y_stride gate_stride dr_stride dn_stride "
+                               "dh_stride dy_stride dgate_stride"))
+
+class mega_moe_router_logits_args(_Args):
+    _fields_ = _fields(("i32", "num_tokens hidden num_experts weight_type"),
+                       ("ptr", "x w logits dlogits dx_add dx dw workspace"),
+                       ("i64", "workspace_bytes x_stride dx_add_stride dx_stride logits_stride "
+                               "dlogits_stride"))
+
+class mega_moe_router_topk_args(_Args):
+    _fields_ = _fields(("i32", "num_tokens num_experts num_topk logits_type score renormalize "
+                               "num_groups topk_groups group_top"),
+                       ("f32", "weight_scale"),
+                       ("ptr", "logits bias token_mask topk_idx topk_weights"),
+                       ("i64", "logits_stride"))
+
+class mega_moe_balance_loss_args(_Args):
+    _fields_ = _fields(("i32", "num_tokens num_experts num_topk logits_type score num_sequences"),
+                       ("f32", "balance_coeff z_coeff"),
+                       ("ptr", "logits topk_idx token_mask cu_seqlens loss counts tokens probs "
+                               "workspace"),
+                       ("i64", "workspace_bytes logits_stride"))
+
+class mega_moe_router_backward_args(_Args):
+    _fields_ = _fields(("i32", "num_tokens num_experts num_topk logits_type score renormalize "
+                               "num_sequences"),
+                       ("f32", "weight_scale balance_coeff z_coeff"),
+                       ("ptr", "logits topk_idx token_mask dweights dloss cu_seqlens counts tokens "
+                               "dlogits"),
+                       ("i64", "logits_stride dlogits_stride"))
+
+
+def make_args(cls, **fields):
+    """An argument block with these fields, the others 0.  A pointer field
+    takes a tensor (anything with data_ptr()), an address or None."""
+    return set_args(cls(), **fields)
+
+
+def set_args(args, **fields):
+    """Sets fields of an argument block and returns it."""
+    kept = args.__dict__.setdefault("tensors", {})
+    for name, value in fields.items():
+        if not any(name == f[0] for f in args._fields_):
+            raise AttributeError(f"{type(args).__name__} has no field {name}")
+        kept.pop(name, None)
+        if hasattr(value, "data_ptr"):
+            kept[name] = value
+            value = value.data_ptr()
+        setattr(args, name, value)
+    return args
 
 
 _lib = None
@@ -109,6 +202,20 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.mega_moe_check_xcd_layout.restype = ctypes.c_int
     lib.mega_moe_forward_noalloc.argtypes = [ctypes.POINTER(mega_moe_config), i32] + [vp] * 10 + [vp]
     lib.mega_moe_forward_noalloc.restype = ctypes.c_int
+    for name, cls in (("norm", mega_moe_norm_args),
+                      ("norm_backward", mega_moe_norm_backward_args),
+                      ("router_logits", mega_moe_router_logits_args),
+                      ("router_logits_backward", mega_moe_router_logits_args),
+                      ("router_topk", mega_moe_router_topk_args),
+                      ("balance_loss", mega_moe_balance_loss_args),
+                      ("router_backward", mega_moe_router_backward_args)):
+        f = getattr(lib, "mega_moe_" + name)
+        f.argtypes, f.restype = [ctypes.POINTER(cls), vp], ctypes.c_int
+    for name, cls in (("norm", mega_moe_norm_backward_args),
+                      ("router_logits", mega_moe_router_logits_args),
+                      ("balance_loss", mega_moe_balance_loss_args)):
+        f = getattr(lib, f"mega_moe_{name}_workspace_bytes")
+        f.argtypes, f.restype = [ctypes.POINTER(cls)], i64
     _lib = lib
     return lib
 
@@ -242,6 +349,48 @@ def mega_moe_profile_end(handle, capacity: int):
     n = ctypes.c_int32()
     _check(load().mega_moe_profile_end(handle, buf, capacity, ctypes.byref(n)))
     return [(buf[3 * i], buf[3 * i + 1], buf[3 * i + 2]) for i in range(n.value)]
+
+
+# ---- operators around the layer: one argument block each (see make_args) ------
+
+def mega_moe_norm(args: mega_moe_norm_args, stream) -> int:
+    return _check(load().mega_moe_norm(args, stream))
+
+
+def mega_moe_norm_backward(args: mega_moe_norm_backward_args, stream) -> int:
+    return _check(load().mega_moe_norm_backward(args, stream))
+
+
+def mega_moe_norm_workspace_bytes(args: mega_moe_norm_backward_args) -> int:
+    return load().mega_moe_norm_workspace_bytes(args)
+
+
+def mega_moe_router_logits(args: mega_moe_router_logits_args, stream) -> int:
+    return _check(load().mega_moe_router_logits(args, stream))
+
+
+def mega_moe_router_logits_backward(args: mega_moe_router_logits_args, stream) -> int:
+    return _check(load().mega_moe_router_logits_backward(args, stream))
+
+
+def mega_moe_router_logits_workspace_bytes(args: mega_moe_router_logits_args) -> int:
+    return load().mega_moe_router_logits_workspace_bytes(args)
+
+
+def mega_moe_router_topk(args: mega_moe_router_topk_args, stream) -> int:
+    return _check(load().mega_moe_router_topk(args, stream))
+
+
+def mega_moe_balance_loss(args: mega_moe_balance_loss_args, stream) -> int:
+    return _check(load().mega_moe_balance_loss(args, stream))
+
+
+def mega_moe_balance_loss_workspace_bytes(args: mega_moe_balance_loss_args) -> int:
+    return load().mega_moe_balance_loss_workspace_bytes(args)
+
+
+def mega_moe_router_backward(args: mega_moe_router_backward_args, stream) -> int:
+    return _check(load().mega_moe_router_backward(args, stream))
 
 
 # ---- convenience wrapper (still marshalling only) ---------------------------

@@ -11,6 +11,7 @@
 #include <string>
 #include <vector>
 
+#include "host.h"
 #include "mega_moe.h"
 #include "moe_args.h"
 #include "schedule.h"
@@ -28,10 +29,11 @@ void launch_transform_w1(const uint8_t* w1, const float* sf, uint8_t* out, float
 using namespace mega_moe;
 
 namespace {
-
 thread_local std::string g_last_error;
+}
 
-int fail(int code, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+namespace mega_moe {
+
 int fail(int code, const char* fmt, ...) {
     char buf[512];
     va_list ap;
@@ -46,6 +48,10 @@ int ok() {
     g_last_error.clear();
     return MEGA_MOE_OK;
 }
+
+}  // namespace mega_moe
+
+namespace {
 
 int64_t align_up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 
@@ -181,8 +187,6 @@ void plan(const mega_moe_config& c, int32_t T, mega_moe_plan_info* p) {
     p->l1_n_blocks = 2 * c.intermediate / bn;
     p->l2_n_blocks = c.hidden / bn;
 }
-
-bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
 
 // The argument block's sizes and options for cfg and its workspace pointers
 // for layout L placed at w.

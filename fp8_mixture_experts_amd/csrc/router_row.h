@@ -1,0 +1,50 @@
+// One token's logits in a wave: lane l holds experts l, l + 64, ...
+#pragma once
+
+#include "block_util.h"
+
+namespace mega_moe {
+
+template <int NI>
+__device__ __forceinline__ void load_row(const void* logits, int type, size_t row, int E, float (&l)[NI]) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        const int e = i * 64 + lane;
+        l[i] = -INFINITY;
+        if (e < E)
+            l[i] = type == MEGA_MOE_F32 ? static_cast<const float*>(logits)[row + e]
+                                        : bf16_value(static_cast<const uint16_t*>(logits)[row + e]);
+    }
+}
+
+// The largest logit of the row, and the sum of exp(logit - largest).  A row of
+// -inf alone has sum 0.  An infinity or NaN among the logits makes the sum NaN.
+template <int NI>
+__device__ __forceinline__ void row_exp(const float (&l)[NI], float (&ex)[NI], float& top, float& sum) {
+    top = l[0];
+#pragma unroll
+    for (int i = 1; i < NI; ++i) top = fmaxf(top, l[i]);
+    top = wave_max(top);
+    const float at = top == -INFINITY ? 0.0f : top;
+    sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        ex[i] = expf(l[i] - at);
+        sum += ex[i];
+    }
+    sum = wave_sum(sum);
+}
+
+// log sum exp of the row; 0 for a row of -inf alone, so that a token without
+// any expert adds nothing to a loss.
+__device__ __forceinline__ float row_lse(float top, float sum) { return sum == 0.0f ? 0.0f : logf(sum) + top; }
+
+// The derivative comes from exp(-|x|): s (1 - s) would cancel where s is near 1.
+__device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
+__device__ __forceinline__ float sigmoid_slope(float x) {
+    const float e = expf(-fabsf(x)), d = 1.0f / (1.0f + e);
+    return e * d * d;
+}
+
+}  // namespace mega_moe

@@ -344,6 +344,248 @@ int mega_moe_set_recv_stats(mega_moe_handle* h, int32_t* stats);
 int mega_moe_profile_begin(mega_moe_handle* h, int32_t max_calls);
 int mega_moe_profile_end(mega_moe_handle* h, float* ms_out, int32_t capacity, int32_t* n_out);
 
+/*
+ * Operators around the layer: what a transformer block does before and after
+ * mega_moe_forward.  The norm gives x and x_sf, the router topk_idx and
+ * topk_weights; the norm of the next block takes y back into the residual
+ * stream; and each has its gradient.  (The pages take x, topk_idx and
+ * topk_weights as given, SM90 design 16.1.)
+ *
+ * Conventions, besides those at the top:
+ *   - Each call takes one argument block, which the call reads and does not
+ *     keep.  Clear it first: a field that is 0 or NULL is off or the default.
+ *   - The current HIP device must be the one of the stream and the tensors; a
+ *     call whose stream or first tensor belongs to another device is refused.
+ *   - Calls are asynchronous on `stream`, allocate nothing, issue no memory
+ *     sets and keep nothing between calls, so they may run on several streams
+ *     at once and be captured in a HIP graph.  A call that needs a workspace
+ *     takes one from the caller (16-byte aligned, of at least the bytes that
+ *     its _workspace_bytes function says, contents of no matter); calls that
+ *     may overlap in time need one each.
+ *   - num_tokens is at most 2^21 (2097152).
+ *   - Row strides are in elements; 0 means dense rows.  Outputs must not
+ *     overlap inputs or each other, except where it is said.
+ *   - Sums are in float32, in an order that depends only on the argument
+ *     block: the same call gives the same bits.  Each output is rounded once.
+ */
+#define MEGA_MOE_BF16 0
+#define MEGA_MOE_F32 1
+
+#define MEGA_MOE_GATE_NONE 0     /* the gate is 1                               */
+#define MEGA_MOE_GATE_TOKEN 1    /* gate [T]: one factor per token              */
+#define MEGA_MOE_GATE_CHANNEL 2  /* gate [H]: one factor per column             */
+#define MEGA_MOE_GATE_FULL 3     /* gate [T, H]                                 */
+
+/*
+ * The norms before and after a block, fused with its gate, the residual
+ * stream and the layer's E4M3 input.  Per token, in float32:
+ *   z = y                                           without post_weight
+ *   z = y * rsqrt(mean(y^2) + post_eps) * post_weight
+ *   r = residual_scale * h + gate * z               (r = h without y)
+ *   n = r * rsqrt(mean(r^2) + pre_eps) * pre_weight
+ *   q_sf = max |n| over 128 columns / 448, q = e4m3(n / q_sf)
+ * n is taken of r before r is rounded to its type, and q of n before n is
+ * rounded.  Where a block's maximum is 0, q_sf and q are 0 (as in the layer's
+ * own re-quantisation); a block with a NaN has q_sf and q NaN.
+ */
+typedef struct mega_moe_norm_args {
+    int32_t num_tokens;       /* T; 0 is a no-op                                 */
+    int32_t hidden;           /* H, a multiple of 8 up to 16384 (128 with q)     */
+    int32_t stream_type;      /* type of h and r: MEGA_MOE_BF16 or MEGA_MOE_F32  */
+    int32_t weight_type;      /* type of post_weight and pre_weight              */
+    int32_t gate_kind;        /* MEGA_MOE_GATE_*                                 */
+    int32_t gate_type;        /* type of gate                                    */
+    float post_eps, pre_eps;  /* >= 0                                            */
+    float residual_scale;     /* finite; without y it must be 1                  */
+    int32_t reserved;         /* 0                                               */
+    const void* h;            /* [T, H] residual stream                          */
+    const uint16_t* y;        /* [T, H] BF16 output of the block, or NULL        */
+    const void* gate;         /* by gate_kind (NONE: NULL; needs y)              */
+    const void* post_weight;  /* [H], or NULL: y is not normed (needs y)         */
+    const void* pre_weight;   /* [H], or NULL: neither n nor q                   */
+    void* r;                  /* [T, H], or NULL: not written; may be h itself
+                                 (same stride): the stream is updated in place   */
+    uint16_t* n;              /* [T, H] BF16, or NULL                            */
+    uint8_t* q;               /* [T, H] E4M3, dense, or NULL (with q_sf)         */
+    float* q_sf;              /* [T, H/128]                                      */
+    int64_t h_stride, y_stride, gate_stride, r_stride, n_stride; /* >= H, of 8   */
+} mega_moe_norm_args;
+int mega_moe_norm(const mega_moe_norm_args* a, void* stream);
+
+/*
+ * The gradients of mega_moe_norm.  r is the stream as mega_moe_norm wrote it
+ * (without y: h), dr and dn the gradients of r and n; q has none of its own
+ * (what flows back through the experts' input is part of dn).  With
+ *   g  = dr + rsqrt(mean(r^2) + pre_eps) * (u - rh * mean(u * rh)),
+ *        rh = r * rsqrt(mean(r^2) + pre_eps), u = dn * pre_weight
+ * dh = residual_scale * g, dgate = z * g summed over what the gate is shared
+ * by, dy is gate * g taken back through the norm of y, and the weights' are
+ * summed over the tokens.  With num_tokens 0 those sums are set to 0.
+ */
+typedef struct mega_moe_norm_backward_args {
+    int32_t num_tokens, hidden, stream_type, weight_type, gate_kind, gate_type;
+    float post_eps, pre_eps, residual_scale;
+    int32_t reserved;         /* 0                                               */
+    const void* r;            /* [T, H] stream_type                              */
+    const uint16_t* y;        /* as in mega_moe_norm                             */
+    const void* gate;
+    const void* post_weight;
+    const void* pre_weight;
+    const void* dr;           /* [T, H] stream_type, or NULL: 0                  */
+    const uint16_t* dn;       /* [T, H] BF16, or NULL: 0 (needs pre_weight)      */
+    void* dh;                 /* [T, H] stream_type, or NULL; may be dr itself
+                                 (same stride)                                   */
+    uint16_t* dy;             /* [T, H] BF16, or NULL (needs y)                  */
+    void* dgate;              /* [T] or [H] float, FULL: [T, H] gate_type; or NULL */
+    float* dpost_weight;      /* [H] float, or NULL                              */
+    float* dpre_weight;       /* [H] float, or NULL                              */
+    void* workspace;          /* may be NULL where the bytes needed are 0        */
+    int64_t workspace_bytes;
+    int64_t r_stride, y_stride, gate_stride, dr_stride, dn_stride, dh_stride, dy_stride,
+        dgate_stride;         /* >= H, of 8                                      */
+} mega_moe_norm_backward_args;
+int mega_moe_norm_backward(const mega_moe_norm_backward_args* a, void* stream);
+
+/* Workspace bytes of a mega_moe_norm_backward call (-1 if invalid): from the
+ * sizes, the gate's kind and which of the gradients are not NULL.  Host-only. */
+int64_t mega_moe_norm_workspace_bytes(const mega_moe_norm_backward_args* a);
+
+/*
+ * The router's product and its gradients: logits = x . w^T, in float32, and
+ *   dx = dlogits . w (+ dx_add),   dw = dlogits^T . x.
+ * The products run on the BF16 matrix cores.  A float32 operand is split into
+ * BF16 terms: three where the result is float32 (the split is exact), two
+ * where it is rounded to BF16 (dx).  x, dlogits and w must be finite (an
+ * infinity may come out as NaN).
+ */
+typedef struct mega_moe_router_logits_args {
+    int32_t num_tokens;       /* T                                               */
+    int32_t hidden;           /* H, a multiple of 8 up to 16384                  */
+    int32_t num_experts;      /* E in [1, 1024]                                  */
+    int32_t weight_type;      /* type of w                                       */
+    const uint16_t* x;        /* [T, H] BF16                                     */
+    const void* w;            /* [E, H], dense                                   */
+    float* logits;            /* [T, E]               (mega_moe_router_logits)   */
+    const float* dlogits;     /* [T, E]               (.._backward)              */
+    const uint16_t* dx_add;   /* [T, H] BF16 added to dx, or NULL; may be dx
+                                 itself (same stride)                            */
+    uint16_t* dx;             /* [T, H] BF16, or NULL                            */
+    float* dw;                /* [E, H] float, dense, or NULL; 0 with T = 0      */
+    void* workspace;          /* may be NULL where the bytes needed are 0        */
+    int64_t workspace_bytes;
+    int64_t x_stride, dx_add_stride, dx_stride;      /* >= H, of 8               */
+    int64_t logits_stride, dlogits_stride;           /* >= E                     */
+} mega_moe_router_logits_args;
+int mega_moe_router_logits(const mega_moe_router_logits_args* a, void* stream);
+int mega_moe_router_logits_backward(const mega_moe_router_logits_args* a, void* stream);
+
+/* Workspace bytes that either call needs with these sizes (-1 if invalid).
+ * Host-only. */
+int64_t mega_moe_router_logits_workspace_bytes(const mega_moe_router_logits_args* a);
+
+#define MEGA_MOE_SCORE_SOFTMAX 0  /* s = softmax of the token's logits           */
+#define MEGA_MOE_SCORE_SIGMOID 1  /* s = 1 / (1 + exp(-logit))                   */
+
+/*
+ * The router's selection: topk_idx and topk_weights as mega_moe_forward takes
+ * them.  Experts are ordered by c = s + bias, computed in float64 (by the
+ * logits themselves where there is no bias and one group: the same order);
+ * equal ones by their index, the lowest first.  An expert whose logit or c is
+ * -inf or NaN is never taken.  With num_groups > 1 the experts, in num_groups equal
+ * runs, are first narrowed to the topk_groups groups with the largest sums of
+ * their group_top largest c (an expert never taken counts as -inf).  Slots are
+ * in falling order of c:
+ *   topk_weights = weight_scale * s / (renormalize ? sum of the token's taken s : 1)
+ * in float32.  Slots that find no expert, and all slots of a token whose
+ * token_mask is 0, get index -1 and weight 0.
+ */
+typedef struct mega_moe_router_topk_args {
+    int32_t num_tokens;       /* T                                               */
+    int32_t num_experts;      /* E in [1, 1024]                                  */
+    int32_t num_topk;         /* k in [1, E]                                     */
+    int32_t logits_type;      /* type of logits                                  */
+    int32_t score;            /* MEGA_MOE_SCORE_*                                */
+    int32_t renormalize;      /* 0 or 1                                          */
+    int32_t num_groups;       /* 0 or 1: none; else a divisor of E, up to 64     */
+    int32_t topk_groups;      /* with groups: [1, num_groups], of k experts or more */
+    int32_t group_top;        /* with groups: 1 or 2, up to E / num_groups       */
+    float weight_scale;       /* finite; 0: 1                                    */
+    const void* logits;       /* [T, E]                                          */
+    const float* bias;        /* [E], or NULL; only the selection sees it        */
+    const uint8_t* token_mask;/* [T], or NULL: every token counts                */
+    int32_t* topk_idx;        /* [T, k]                                          */
+    float* topk_weights;      /* [T, k]                                          */
+    int64_t logits_stride;    /* >= E                                            */
+} mega_moe_router_topk_args;
+int mega_moe_router_topk(const mega_moe_router_topk_args* a, void* stream);
+
+/*
+ * Per-expert route counts and the router's losses.  With p = softmax of the
+ * logits, or their sigmoids divided by the token's sum of them; for every
+ * sequence b of n_b > 0 tokens, over its tokens whose token_mask is not 0:
+ *   counts[b, e] = its routes to e,   probs[b, e] = sum of p[t, e] / n_b
+ *   loss[0] = balance_coeff * mean over those b of
+ *             sum over e of (E / (k * n_b)) * counts[b, e] * probs[b, e]
+ *   loss[1] = z_coeff * mean over all those tokens of (log sum exp(logits))^2
+ * The sequences are the token ranges [cu_seqlens[b], cu_seqlens[b + 1]);
+ * tokens outside of all count nowhere.  Routes with an index outside [0, E)
+ * are not counted.  A token whose logits are all -inf has p = 0 and log sum
+ * exp 0.  A sequence without tokens has zeros; without any token both losses
+ * are 0.  tokens[b] = n_b, tokens[B] = their sum and
+ * tokens[B + 1] = the number of sequences that have any.
+ */
+typedef struct mega_moe_balance_loss_args {
+    int32_t num_tokens;       /* T                                               */
+    int32_t num_experts;      /* E in [1, 1024]                                  */
+    int32_t num_topk;         /* k >= 1                                          */
+    int32_t logits_type;
+    int32_t score;
+    int32_t num_sequences;    /* B; 0 or 1 without cu_seqlens: all T tokens are one */
+    float balance_coeff, z_coeff;   /* finite                                    */
+    const void* logits;       /* [T, E]                                          */
+    const int32_t* topk_idx;  /* [T, k]                                          */
+    const uint8_t* token_mask;
+    const int32_t* cu_seqlens;/* [B + 1] not decreasing, in [0, T]; NULL         */
+    float* loss;              /* [2]                                             */
+    int32_t* counts;          /* [B, E] (B = 1 without cu_seqlens)               */
+    int32_t* tokens;          /* [B + 2]                                         */
+    float* probs;             /* [B, E], or NULL                                 */
+    void* workspace;
+    int64_t workspace_bytes;
+    int64_t logits_stride;    /* >= E                                            */
+} mega_moe_balance_loss_args;
+int mega_moe_balance_loss(const mega_moe_balance_loss_args* a, void* stream);
+
+/* Workspace bytes of a mega_moe_balance_loss call (-1 if invalid).  Host-only. */
+int64_t mega_moe_balance_loss_workspace_bytes(const mega_moe_balance_loss_args* a);
+
+/*
+ * The gradient of the logits: from that of the top-k weights (dweights), of
+ * the two losses (dloss), or of both.  topk_idx and its weights are those of
+ * mega_moe_router_topk with the same score, renormalize and weight_scale (the
+ * selection itself and the bias have no gradient); slots with an index outside
+ * [0, E) have none.  counts and tokens are those of mega_moe_balance_loss,
+ * held constant (they may be sums over several GPUs' batches).  Every row of
+ * dlogits is written; rows of tokens whose token_mask is 0 are 0.
+ */
+typedef struct mega_moe_router_backward_args {
+    int32_t num_tokens, num_experts, num_topk, logits_type, score;
+    int32_t renormalize;      /* as in mega_moe_router_topk (with dweights)      */
+    int32_t num_sequences;    /* as in mega_moe_balance_loss (with dloss)        */
+    float weight_scale, balance_coeff, z_coeff;
+    const void* logits;       /* [T, E]                                          */
+    const int32_t* topk_idx;  /* [T, k]; with dweights                           */
+    const uint8_t* token_mask;
+    const float* dweights;    /* [T, k], or NULL                                 */
+    const float* dloss;       /* [2], or NULL                                    */
+    const int32_t* cu_seqlens;
+    const int32_t* counts;    /* [B, E]; with dloss                              */
+    const int32_t* tokens;    /* [B + 2]; with dloss                             */
+    float* dlogits;           /* [T, E]                                          */
+    int64_t logits_stride, dlogits_stride;           /* >= E                     */
+} mega_moe_router_backward_args;
+int mega_moe_router_backward(const mega_moe_router_backward_args* a, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
