@@ -18,7 +18,7 @@ using namespace mega_moe;
 
 namespace {
 
-constexpr int32_t MAX_HIDDEN = 16384;
+constexpr int32_t MAX_HIDDEN = 8192;        // as the layer
 constexpr int32_t MAX_TOKENS = 1 << 21;     // one workgroup of up to 1024 threads per token
 constexpr int MAX_DEVICES = 64;
 
@@ -27,6 +27,12 @@ int bad(const char* what) { return fail(MEGA_MOE_ERR_INVALID_ARG, "%s", what); }
 int check_tokens(int32_t n) {
     if (n < 0 || n > MAX_TOKENS)
         return fail(MEGA_MOE_ERR_INVALID_ARG, "num_tokens must be in [0, %d], got %d", MAX_TOKENS, n);
+    return MEGA_MOE_OK;
+}
+
+int check_hidden(int32_t h) {
+    if (h < 8 || h % 8) return fail(MEGA_MOE_ERR_INVALID_ARG, "hidden must be a positive multiple of 8, got %d", h);
+    if (h > MAX_HIDDEN) return fail(MEGA_MOE_ERR_UNSUPPORTED, "built for hidden <= %d, got %d", MAX_HIDDEN, h);
     return MEGA_MOE_OK;
 }
 
@@ -147,8 +153,7 @@ int check_workspace(const void* ws, int64_t have, int64_t need) {
 template <typename Args>
 int check_norm(const Args& a, bool q) {
     if (const int rc = check_tokens(a.num_tokens)) return rc;
-    if (a.hidden < 8 || a.hidden > MAX_HIDDEN || a.hidden % 8)
-        return fail(MEGA_MOE_ERR_INVALID_ARG, "hidden must be a multiple of 8 up to %d, got %d", MAX_HIDDEN, a.hidden);
+    if (const int rc = check_hidden(a.hidden)) return rc;
     if (q && a.hidden % 128) return bad("q needs hidden to be a multiple of 128");
     if (!type_ok(a.stream_type) || !type_ok(a.weight_type) || !type_ok(a.gate_type))
         return bad("a type is neither MEGA_MOE_BF16 nor MEGA_MOE_F32");
@@ -193,14 +198,13 @@ int check_norm_backward(const mega_moe_norm_backward_args& a) {
 }
 
 int64_t norm_backward_bytes(const mega_moe_norm_backward_args& a) {
-    return (int64_t)norm_backward_blocks(a.num_tokens) * norm_sums(a) * a.hidden * 4;
+    return (int64_t)norm_backward_blocks(a.num_tokens, a.hidden) * norm_sums(a) * a.hidden * 4;
 }
 
 int check_logits_sizes(const mega_moe_router_logits_args* a) {
     if (!a) return bad("the argument block is NULL");
     if (const int rc = check_tokens(a->num_tokens)) return rc;
-    if (a->hidden < 8 || a->hidden > MAX_HIDDEN || a->hidden % 8)
-        return fail(MEGA_MOE_ERR_INVALID_ARG, "hidden must be a multiple of 8 up to %d, got %d", MAX_HIDDEN, a->hidden);
+    if (const int rc = check_hidden(a->hidden)) return rc;
     if (a->num_experts < 1 || a->num_experts > MAX_EXPERTS)
         return fail(MEGA_MOE_ERR_INVALID_ARG, "num_experts must be in [1, %d], got %d", MAX_EXPERTS, a->num_experts);
     if (!type_ok(a->weight_type)) return bad("weight_type is neither MEGA_MOE_BF16 nor MEGA_MOE_F32");

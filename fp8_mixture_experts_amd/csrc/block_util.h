@@ -28,6 +28,26 @@ __device__ __forceinline__ void unpack8(const u32x4_t& d, float (&v)[8]) {
     }
 }
 
+// Elements i .. i + 7 as they lie in memory: one 16-byte word or two.
+template <bool F32>
+__device__ __forceinline__ const u32x4_t* raw8(const void* p, size_t i) {
+    if constexpr (F32) return reinterpret_cast<const u32x4_t*>(static_cast<const float*>(p) + i);
+    else return reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(p) + i);
+}
+
+template <bool F32, int N>
+__device__ __forceinline__ void values8(const u32x4_t (&d)[N], float (&v)[8]) {
+    if constexpr (F32) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[j] = __uint_as_float(d[0][j]);
+            v[4 + j] = __uint_as_float(d[N - 1][j]);
+        }
+    } else {
+        unpack8(d[0], v);
+    }
+}
+
 // Elements i .. i+7 (i a multiple of 8, p 16-byte aligned).
 template <bool F32>
 __device__ __forceinline__ void load8(const void* p, size_t i, float (&v)[8]) {
@@ -113,6 +133,27 @@ __device__ __forceinline__ void block_sum(float (&v)[N], float (&part)[16][N]) {
     for (int w = 1; w < waves; ++w) {
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] += part[w][i];
+    }
+}
+
+// The same over groups of nt threads (whole waves), each for itself; every
+// group of the workgroup calls it.
+template <int N>
+__device__ __forceinline__ void group_sum(float (&v)[N], float (&part)[16][N], int group, int nt) {
+    const int wave = threadIdx.x >> 6, waves = nt >> 6;
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
+    if (waves == 1) return;
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) part[wave][i] = v[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = part[group * waves][i];
+    for (int w = 1; w < waves; ++w) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += part[group * waves + w][i];
     }
 }
 

@@ -14,7 +14,7 @@ __host__ __device__ inline int norm_sums(const mega_moe_norm_backward_args& a) {
 }
 
 // Workgroups of the backward kernel, each with sums of its own.
-int norm_backward_blocks(int tokens);
+int norm_backward_blocks(int tokens, int hidden);
 
 void launch_norm(const mega_moe_norm_args& a, hipStream_t stream);
 void launch_norm_backward(const mega_moe_norm_backward_args& a, hipStream_t stream);

@@ -125,181 +125,225 @@ moe_norm(mega_moe_norm_args a) {
     }
 }
 
-// Gradients.  A workgroup takes rows b, b + grid, ..., one at a time; its
-// threads keep their columns, and with them their part of the sums over
-// tokens, in registers; each workgroup's sums go to the workspace, [grid][3][H]
-// (those that are asked for), and moe_norm_reduce adds them up in order.
-template <bool SF32, int C>
+// Gradients.  A workgroup is G groups of nt threads, each group on a row of
+// its own; group i of workgroup b takes rows b * G + i, then every grid * G-th.
+// A thread keeps its eight columns from row to row, and with them its part of
+// the sums over tokens, in registers.  At the end the groups' sums meet in LDS
+// and the workgroup's go to the workspace, [grid][sums][H] (those that are
+// asked for), where moe_norm_reduce adds them up in order.
+//
+// Memory bound: the next row's loads stay in flight over the two row sums (the
+// barriers would leave the memory idle otherwise), and the weights lie in LDS.
+template <bool SF32, bool FULL>
 __global__ void __launch_bounds__(1024)
-moe_norm_backward(mega_moe_norm_backward_args a, float* ws) {
+moe_norm_backward(mega_moe_norm_backward_args a, float* ws, int nt) {
+    extern __shared__ float shared[];            // the weights, [3][H]; then a group's sums
     __shared__ float part1[16][3];
     __shared__ float part2[16][2];
-    const int nt = blockDim.x, tid = threadIdx.x;
-    const int H = a.hidden;
+    const int group = threadIdx.x / nt, tid = threadIdx.x - group * nt, G = blockDim.x / nt;
+    const int H = a.hidden, col = tid * 8;
+    const bool in = col < H;
     const float inv_h = 1.0f / (float)H;
     const bool normed = a.y && a.post_weight;
-    float s_pre[C][8], s_post[C][8], s_gate[C][8];
+    constexpr int SW = SF32 ? 2 : 1;
+    const u32x4_t none = {0u, 0u, 0u, 0u};
+    u32x4_t raw_r[SW], raw_dr[SW], raw_dn, raw_y, raw_g[2];
+    float raw_tg = 1.0f;
+
+    const auto fetch = [&](int64_t t) {
+        const bool live = in && t < a.num_tokens;
 #pragma unroll
-    for (int c = 0; c < C; ++c)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s_pre[c][i] = s_post[c][i] = s_gate[c][i] = 0.0f;
-    for (int64_t t = blockIdx.x; t < a.num_tokens; t += gridDim.x) {
-        float g[C][8], r[C][8], u[C][8], y[C][8];
-        float s1[3] = {0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const int col = (c * nt + tid) * 8;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) g[c][i] = r[c][i] = u[c][i] = y[c][i] = 0.0f;
-            if (col >= H) continue;
-            if (a.dr) load8<SF32>(a.dr, t * a.dr_stride + col, g[c]);
-            if (a.dn) {
-                load8<SF32>(a.r, t * a.r_stride + col, r[c]);
-                load8<false>(a.dn, t * a.dn_stride + col, u[c]);
-            }
-            if (a.y) load8<false>(a.y, t * a.y_stride + col, y[c]);
+        for (int i = 0; i < SW; ++i) {
+            raw_r[i] = raw_dr[i] = none;
+            if (live && a.dn) raw_r[i] = raw8<SF32>(a.r, t * a.r_stride + col)[i];
+            if (live && a.dr) raw_dr[i] = raw8<SF32>(a.dr, t * a.dr_stride + col)[i];
         }
+        raw_dn = raw_y = none;
+        if (live && a.dn) raw_dn = raw8<false>(a.dn, t * a.dn_stride + col)[0];
+        if (live && a.y) raw_y = raw8<false>(a.y, t * a.y_stride + col)[0];
+        if constexpr (FULL) {
+            raw_g[0] = raw_g[1] = none;
+            if (live && a.gate_type == MEGA_MOE_F32) {
+                raw_g[0] = raw8<true>(a.gate, t * a.gate_stride + col)[0];
+                raw_g[1] = raw8<true>(a.gate, t * a.gate_stride + col)[1];
+            } else if (live) {
+                raw_g[0] = raw8<false>(a.gate, t * a.gate_stride + col)[0];
+            }
+        } else if (a.gate_kind == MEGA_MOE_GATE_TOKEN && t < a.num_tokens) {
+            raw_tg = a.gate_type == MEGA_MOE_F32 ? static_cast<const float*>(a.gate)[t]
+                                                 : bf16_value(static_cast<const uint16_t*>(a.gate)[t]);
+        }
+    };
+    // the pre weight, the post weight and a gate by channel: 1 where there is none
+    const void* channel = a.gate_kind == MEGA_MOE_GATE_CHANNEL ? a.gate : nullptr;
+    for (int c = threadIdx.x * 8; c < H; c += blockDim.x * 8)
+        for (int which = 0; which < 3; ++which) {
+            const void* p = which == 0 ? a.pre_weight : which == 1 ? a.post_weight : channel;
+            float w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = 1.0f;
+            if (p) load8(p, which == 2 ? a.gate_type : a.weight_type, c, w);
+            store8<true>(shared, (size_t)which * H + c, w);
+        }
+    const auto weight = [&](int which, float (&w)[8]) {
+        if (in) load8<true>(shared, (size_t)which * H + col, w);
+    };
+
+    float s_pre[8], s_post[8], s_gate[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s_pre[i] = s_post[i] = s_gate[i] = 0.0f;
+
+    // every group makes the same number of rounds: the barriers are shared
+    const int64_t step = (int64_t)gridDim.x * G;
+    int64_t t = (int64_t)blockIdx.x * G + group;
+    const int64_t rounds = (a.num_tokens - (int64_t)blockIdx.x * G + step - 1) / step;
+    fetch(t);
+    __syncthreads();
+    for (int64_t round = 0; round < rounds; ++round, t += step) {
+        const bool live = in && t < a.num_tokens;
+        // this row stays packed until its values are needed
+        float g[8];
+        u32x4_t cur_r[SW], cur_g[2];
+        values8<SF32>(raw_dr, g);
+#pragma unroll
+        for (int i = 0; i < SW; ++i) cur_r[i] = raw_r[i];
+        const u32x4_t cur_dn = raw_dn, cur_y = raw_y;
+        if constexpr (FULL) {
+            cur_g[0] = raw_g[0];
+            cur_g[1] = raw_g[1];
+        }
+        const float tg = raw_tg;
+        if (round + 1 < rounds) fetch(t + step);
         // the sums that both norms need: of r^2 and u r, and of y^2
+        float s1[3] = {0.0f, 0.0f, 0.0f};
+        {
+            float w[8] = {}, r[8], u[8], y[8];
+            weight(0, w);
+            values8<SF32>(cur_r, r);
+            unpack8(cur_dn, u);
+            unpack8(cur_y, y);
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const int col = (c * nt + tid) * 8;
-            if (col >= H) continue;
-            if (a.dn) {
-                float w[8];
-                load8(a.pre_weight, a.weight_type, col, w);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    s1[0] += r[c][i] * r[c][i];
-                    s1[1] += u[c][i] * w[i] * r[c][i];
-                }
-            }
-            if (normed) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) s1[2] += y[c][i] * y[c][i];
+            for (int i = 0; i < 8; ++i) {
+                s1[0] += r[i] * r[i];
+                s1[1] += u[i] * w[i] * r[i];
+                s1[2] += y[i] * y[i];
             }
         }
-        block_sum(s1, part1);
+        group_sum(s1, part1, group, nt);
         if (a.dn) {
             const float rs = rsqrtf(s1[0] * inv_h + a.pre_eps);
             const float mean = s1[1] * rs * inv_h;       // mean of u * rh
+            float w[8] = {}, r[8], u[8];
+            weight(0, w);
+            values8<SF32>(cur_r, r);
+            unpack8(cur_dn, u);
 #pragma unroll
-            for (int c = 0; c < C; ++c) {
-                const int col = (c * nt + tid) * 8;
-                if (col >= H) continue;
-                float w[8];
-                load8(a.pre_weight, a.weight_type, col, w);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float rh = r[c][i] * rs;
-                    g[c][i] += rs * (u[c][i] * w[i] - rh * mean);
-                    s_pre[c][i] += u[c][i] * rh;
-                }
+            for (int i = 0; i < 8; ++i) {
+                const float rh = r[i] * rs;
+                g[i] += rs * (u[i] * w[i] - rh * mean);
+                // a group that is out of rows has u = 0, but rh may be infinite
+                if (live) s_pre[i] += u[i] * rh;
             }
         }
-        if (a.dh) {
+        if (a.dh && live) {
+            float o[8];
 #pragma unroll
-            for (int c = 0; c < C; ++c) {
-                const int col = (c * nt + tid) * 8;
-                float o[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = a.residual_scale * g[c][i];
-                if (col < H) store8<SF32>(a.dh, t * a.dh_stride + col, o);
-            }
+            for (int i = 0; i < 8; ++i) o[i] = a.residual_scale * g[i];
+            store8<SF32>(a.dh, t * a.dh_stride + col, o);
         }
         if (a.y) {
             const float ys = normed ? rsqrtf(s1[2] * inv_h + a.post_eps) : 1.0f;
-            float tg = 1.0f;
-            if (a.gate_kind == MEGA_MOE_GATE_TOKEN)
-                tg = a.gate_type == MEGA_MOE_F32 ? static_cast<const float*>(a.gate)[t]
-                                                 : bf16_value(static_cast<const uint16_t*>(a.gate)[t]);
             float s2[2] = {0.0f, 0.0f};
-            // g becomes v = gate * g * post_weight, y becomes yh
-#pragma unroll
-            for (int c = 0; c < C; ++c) {
-                const int col = (c * nt + tid) * 8;
-                if (col >= H) continue;
-                float w[8], ga[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) w[i] = 1.0f, ga[i] = tg;
-                if (normed) load8(a.post_weight, a.weight_type, col, w);
-                if (a.gate_kind >= MEGA_MOE_GATE_CHANNEL)
-                    load8(a.gate, a.gate_type,
-                          a.gate_kind == MEGA_MOE_GATE_FULL ? t * a.gate_stride + col : (size_t)col,
-                          ga);
-                float dg[8];
+            {
+                // g becomes v = gate * g * post_weight
+                float w[8] = {}, ga[8] = {}, dg[8], y[8];
+                weight(1, w);
+                if constexpr (FULL) {
+                    if (a.gate_type == MEGA_MOE_F32) values8<true>(cur_g, ga);
+                    else unpack8(cur_g[0], ga);
+                } else {
+                    weight(2, ga);
+                }
+                unpack8(cur_y, y);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    y[c][i] *= ys;
-                    dg[i] = y[c][i] * w[i] * g[c][i];
-                    const float dz = ga[i] * g[c][i];
-                    s_post[c][i] += dz * y[c][i];
-                    g[c][i] = dz * w[i];
-                    s2[0] += g[c][i] * y[c][i];
+                    y[i] *= ys;
+                    dg[i] = y[i] * w[i] * g[i];
+                    const float dz = (FULL ? ga[i] : ga[i] * tg) * g[i];
+                    if (live) {
+                        s_post[i] += dz * y[i];
+                        if (!FULL) s_gate[i] += dg[i];
+                    }
+                    g[i] = dz * w[i];
+                    s2[0] += g[i] * y[i];
                     s2[1] += dg[i];
-                    s_gate[c][i] += dg[i];
                 }
-                if (a.gate_kind == MEGA_MOE_GATE_FULL && a.dgate)
-                    store8(a.dgate, a.gate_type, t * a.dgate_stride + col, dg);
+                if (FULL && a.dgate && live) store8(a.dgate, a.gate_type, t * a.dgate_stride + col, dg);
             }
-            const bool token_grad = a.gate_kind == MEGA_MOE_GATE_TOKEN && a.dgate;
-            if (normed || token_grad) block_sum(s2, part2);
-            if (token_grad && tid == 0) static_cast<float*>(a.dgate)[t] = s2[1];
-            if (a.dy) {
+            const bool token_grad = !FULL && a.gate_kind == MEGA_MOE_GATE_TOKEN && a.dgate;
+            if (normed || token_grad) group_sum(s2, part2, group, nt);
+            if (token_grad && tid == 0 && t < a.num_tokens) static_cast<float*>(a.dgate)[t] = s2[1];
+            if (a.dy && live) {
                 const float mean = normed ? s2[0] * inv_h : 0.0f;
+                float o[8], y[8];
+                unpack8(cur_y, y);
 #pragma unroll
-                for (int c = 0; c < C; ++c) {
-                    const int col = (c * nt + tid) * 8;
-                    float o[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) o[i] = ys * (g[c][i] - y[c][i] * mean);
-                    if (col < H) store8<false>(a.dy, t * a.dy_stride + col, o);
-                }
+                for (int i = 0; i < 8; ++i) o[i] = ys * (g[i] - y[i] * ys * mean);
+                store8<false>(a.dy, t * a.dy_stride + col, o);
             }
         }
-        // part1 is written again by the next row: every wave has left it
+        // part1 is written again by the next round: every wave has left it
         __syncthreads();
     }
+    // nothing reads the weights any more (the last round ended in a barrier)
     int k = 0;
-    const auto put = [&](const float (&s)[C][8]) {
+    const auto put = [&](float (&s)[8]) {
+        // the groups in turn, onto the first one's sums
+        for (int q = 1; q < G; ++q) {
+            if (group == q && in) store8<true>(shared, (size_t)col, s);
+            __syncthreads();
+            if (group == 0 && in) {
+                float o[8];
+                load8<true>(shared, (size_t)col, o);
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const int col = (c * nt + tid) * 8;
-            if (col < H) store8<true>(ws, ((size_t)blockIdx.x * norm_sums(a) + k) * H + col, s[c]);
+                for (int i = 0; i < 8; ++i) s[i] += o[i];
+            }
+            __syncthreads();
         }
+        if (group == 0 && in) store8<true>(ws, ((size_t)blockIdx.x * norm_sums(a) + k) * H + col, s);
         ++k;
     };
     if (a.dpre_weight) put(s_pre);
     if (a.dpost_weight) put(s_post);
-    if (a.gate_kind == MEGA_MOE_GATE_CHANNEL && a.dgate) put(s_gate);
+    if (!FULL && a.gate_kind == MEGA_MOE_GATE_CHANNEL && a.dgate) put(s_gate);
 }
 
-// Adds the workgroups' sums: 64 columns per workgroup, four threads each, a
-// quarter of the rows apiece.
-__global__ void __launch_bounds__(256)
-moe_norm_reduce(mega_moe_norm_backward_args a, const float* ws, int rows) {
-    __shared__ float part[4][64];
+// Adds the workgroups' sums: 64 columns of one sum per workgroup; its eight
+// waves take every eighth row each, and meet in LDS.
+__global__ void __launch_bounds__(512)
+moe_norm_reduce(const float* ws, float* out0, float* out1, float* out2, int H, int rows) {
+    __shared__ float part[8][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int n = norm_sums(a);
-    const int col = blockIdx.x * 64 + lane;      // of the n * H sums
+    const int col = blockIdx.x * 64 + lane, sums = gridDim.y;
+    float* out = blockIdx.y == 0 ? out0 : blockIdx.y == 1 ? out1 : out2;
+    const float* p = ws + (size_t)blockIdx.y * H + col;
+    const size_t pitch = (size_t)sums * H;
     float s = 0.0f;
-    if (col < n * a.hidden)
-        for (int i = wave; i < rows; i += 4) s += ws[(size_t)i * n * a.hidden + col];
+    if (col < H) {
+#pragma unroll 8
+        for (int i = wave; i < rows; i += 8) s += p[i * pitch];
+    }
     part[wave][lane] = s;
     __syncthreads();
-    if (wave || col >= n * a.hidden) return;
-    s = (part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]);
-    float* outs[3];
-    int k = 0;
-    if (a.dpre_weight) outs[k++] = a.dpre_weight;
-    if (a.dpost_weight) outs[k++] = a.dpost_weight;
-    if (a.gate_kind == MEGA_MOE_GATE_CHANNEL && a.dgate) outs[k++] = static_cast<float*>(a.dgate);
-    const int which = col / a.hidden;
-    float* out = which == 0 ? outs[0] : which == 1 ? outs[1] : outs[2];
-    out[col - which * a.hidden] = s;
+    if (wave || col >= H) return;
+    s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) s += part[w][lane];
+    out[col] = s;
 }
 
 namespace {
-int chunks(int H) { return H <= 2048 ? 1 : H <= 8192 ? 2 : 4; }
+int chunks(int H) { return H <= 2048 ? 1 : 2; }
 unsigned threads(int H, int c) { return (unsigned)((H / 8 + c - 1) / c + 63) / 64 * 64; }
 }  // namespace
 
@@ -310,29 +354,47 @@ void launch_norm(const mega_moe_norm_args& a, hipStream_t stream) {
 #define NORM(CC)                                                                             \
     if (f) hipLaunchKernelGGL((moe_norm<true, CC>), grid, block, 0, stream, a);              \
     else hipLaunchKernelGGL((moe_norm<false, CC>), grid, block, 0, stream, a)
-    if (c == 1) { NORM(1); } else if (c == 2) { NORM(2); } else { NORM(4); }
+    if (c == 1) { NORM(1); } else { NORM(2); }
 #undef NORM
 }
 
-int norm_backward_blocks(int tokens) { return tokens < 512 ? tokens : 512; }
+// The backward kernel: a chunk per thread, and as many row groups as fit into
+// 1024 threads.
+namespace {
+int row_groups(int H) { return 1024 / (int)threads(H, 1); }
+}  // namespace
+
+int norm_backward_blocks(int tokens, int hidden) {
+    const int g = row_groups(hidden);
+    const int need = (tokens + g - 1) / g;
+    return need < 256 ? need : 256;
+}
 
 void launch_norm_backward(const mega_moe_norm_backward_args& a, hipStream_t stream) {
-    const int c = chunks(a.hidden);
-    const int rows = norm_backward_blocks(a.num_tokens);
-    const dim3 grid((unsigned)rows), block(threads(a.hidden, c));
-    const bool f = a.stream_type == MEGA_MOE_F32;
-    float* ws = static_cast<float*>(a.workspace);
-#define NORM(CC)                                                                                 \
-    if (f) hipLaunchKernelGGL((moe_norm_backward<true, CC>), grid, block, 0, stream, a, ws);     \
-    else hipLaunchKernelGGL((moe_norm_backward<false, CC>), grid, block, 0, stream, a, ws)
-    if (rows > 0) {
-        if (c == 1) { NORM(1); } else if (c == 2) { NORM(2); } else { NORM(4); }
-    }
-#undef NORM
+    const int nt = (int)threads(a.hidden, 1), groups = row_groups(a.hidden);
+    const int rows = norm_backward_blocks(a.num_tokens, a.hidden);
     const int n = norm_sums(a);
-    if (n)
-        hipLaunchKernelGGL(moe_norm_reduce, dim3((unsigned)(n * a.hidden + 63) / 64), dim3(256), 0,
-                           stream, a, ws, rows);
+    float* ws = static_cast<float*>(a.workspace);
+    if (rows > 0) {
+        const auto go = [&](auto kernel) {
+            hipLaunchKernelGGL(kernel, dim3((unsigned)rows), dim3((unsigned)(nt * groups)), (unsigned)a.hidden * 12,
+                               stream, a, ws, nt);
+        };
+        const bool f = a.stream_type == MEGA_MOE_F32, full = a.gate_kind == MEGA_MOE_GATE_FULL;
+        if (full && f) go(moe_norm_backward<true, true>);
+        else if (full) go(moe_norm_backward<false, true>);
+        else if (f) go(moe_norm_backward<true, false>);
+        else go(moe_norm_backward<false, false>);
+    }
+    if (n) {
+        float* outs[3];
+        int k = 0;
+        if (a.dpre_weight) outs[k++] = a.dpre_weight;
+        if (a.dpost_weight) outs[k++] = a.dpost_weight;
+        if (a.gate_kind == MEGA_MOE_GATE_CHANNEL && a.dgate) outs[k++] = static_cast<float*>(a.dgate);
+        hipLaunchKernelGGL(moe_norm_reduce, dim3((unsigned)(a.hidden + 63) / 64, (unsigned)n), dim3(512), 0, stream, ws,
+                           outs[0], n > 1 ? outs[1] : nullptr, n > 2 ? outs[2] : nullptr, a.hidden, rows);
+    }
 }
 
 }  // namespace mega_moe

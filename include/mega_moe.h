@@ -390,7 +390,7 @@ int mega_moe_profile_end(mega_moe_handle* h, float* ms_out, int32_t capacity, in
  */
 typedef struct mega_moe_norm_args {
     int32_t num_tokens;       /* T; 0 is a no-op                                 */
-    int32_t hidden;           /* H, a multiple of 8 up to 16384 (128 with q)     */
+    int32_t hidden;           /* H, a multiple of 8 up to 8192 (of 128 with q)   */
     int32_t stream_type;      /* type of h and r: MEGA_MOE_BF16 or MEGA_MOE_F32  */
     int32_t weight_type;      /* type of post_weight and pre_weight              */
     int32_t gate_kind;        /* MEGA_MOE_GATE_*                                 */
@@ -460,7 +460,7 @@ int64_t mega_moe_norm_workspace_bytes(const mega_moe_norm_backward_args* a);
  */
 typedef struct mega_moe_router_logits_args {
     int32_t num_tokens;       /* T                                               */
-    int32_t hidden;           /* H, a multiple of 8 up to 16384                  */
+    int32_t hidden;           /* H, a multiple of 8 up to 8192                   */
     int32_t num_experts;      /* E in [1, 1024]                                  */
     int32_t weight_type;      /* type of w                                       */
     const uint16_t* x;        /* [T, H] BF16                                     */

@@ -94,7 +94,7 @@ def _router_backward(**kw):
 SIZES = [dict(num_tokens=-1), dict(num_tokens=(1 << 21) + 1)]
 REFUSED = {
     "mega_moe_norm": (_norm, SIZES + [
-        dict(hidden=0), dict(hidden=260), dict(hidden=264), dict(hidden=16392), dict(stream_type=2), dict(weight_type=-1),
+        dict(hidden=0), dict(hidden=260), dict(hidden=264), dict(stream_type=2), dict(weight_type=-1),
         dict(gate_type=5), dict(gate_kind=4), dict(gate_kind=-1), dict(reserved=1), dict(post_eps=-1.0),
         dict(pre_eps=float("nan")), dict(pre_eps=float("inf")), dict(residual_scale=float("inf")),
         dict(gate=9 * M), dict(gate_kind=1), dict(y=None), dict(y=None, post_weight=None, residual_scale=0.5),
@@ -112,7 +112,7 @@ REFUSED = {
         dict(workspace=7 * M), dict(dr_stride=100), dict(dpre_weight=10 * M + 4),
         dict(gate_kind=1, gate=12 * M, dgate=13 * M + 2), dict(gate_kind=2, gate=12 * M, dgate=13 * M + 4)]),
     "mega_moe_router_logits": (_logits, SIZES + [
-        dict(hidden=4), dict(hidden=16392), dict(num_experts=0), dict(num_experts=1025), dict(weight_type=3), dict(x=None),
+        dict(hidden=4), dict(num_experts=0), dict(num_experts=1025), dict(weight_type=3), dict(x=None),
         dict(w=None), dict(logits=None), dict(x=M + 2), dict(w=2 * M + 8), dict(logits=3 * M + 1), dict(x_stride=255),
         dict(x_stride=260), dict(logits_stride=7), dict(logits=M), dict(logits=2 * M + 64)]),
     "mega_moe_router_logits_backward": (_logits, SIZES + [
@@ -149,6 +149,13 @@ def test_call_is_refused(name, change):
         getattr(B, name)(make(**change), None)
     assert ei.value.code == B.MEGA_MOE_ERR_INVALID_ARG
     assert B.mega_moe_last_error()
+
+
+@pytest.mark.parametrize("name", [n for n in REFUSED if "norm" in n or "logits" in n])
+def test_hidden_beyond_what_is_built_is_unsupported(name):
+    with pytest.raises(B.MegaMoEError) as ei:
+        getattr(B, name)(REFUSED[name][0](hidden=8320), None)
+    assert ei.value.code == B.MEGA_MOE_ERR_UNSUPPORTED
 
 
 @pytest.mark.parametrize("name", list(REFUSED))

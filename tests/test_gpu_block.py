@@ -33,8 +33,8 @@ NORM = [
     (17, 2048, BF16, F32, "full", BF16, False, 128),
     (7, 2056, BF16, F32, "token", F32, True, 0),
     (4, 8192, F32, BF16, "channel", F32, True, 0),
-    (3, 8200, BF16, BF16, "channel", F32, False, 8),
-    (2, 16384, BF16, F32, "full", BF16, True, 0),
+    (3, 8184, BF16, BF16, "channel", F32, False, 8),
+    (2, 8192, F32, F32, "full", BF16, True, 0),
     (1030, 384, BF16, F32, "channel", F32, True, 0),
     (577, 4096, F32, F32, "token", F32, False, 0),
 ]
