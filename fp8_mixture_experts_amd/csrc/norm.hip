@@ -147,7 +147,7 @@ moe_norm_backward(mega_moe_norm_backward_args a, float* ws, int nt) {
     const bool normed = a.y && a.post_weight;
     constexpr int SW = SF32 ? 2 : 1;
     const u32x4_t none = {0u, 0u, 0u, 0u};
-    u32x4_t raw_r[SW], raw_dr[SW], raw_dn, raw_y, raw_g[2];
+    u32x4_t raw_r[SW], raw_dr[SW], raw_dn, raw_y;
     float raw_tg = 1.0f;
 
     const auto fetch = [&](int64_t t) {
@@ -156,20 +156,12 @@ moe_norm_backward(mega_moe_norm_backward_args a, float* ws, int nt) {
         for (int i = 0; i < SW; ++i) {
             raw_r[i] = raw_dr[i] = none;
             if (live && a.dn) raw_r[i] = raw8<SF32>(a.r, t * a.r_stride + col)[i];
-            if (live && a.dr) raw_dr[i] = raw8<SF32>(a.dr, t * a.dr_stride + col)[i];
+            if (live && a.dr && !SF32) raw_dr[i] = raw8<SF32>(a.dr, t * a.dr_stride + col)[i];
         }
         raw_dn = raw_y = none;
         if (live && a.dn) raw_dn = raw8<false>(a.dn, t * a.dn_stride + col)[0];
         if (live && a.y) raw_y = raw8<false>(a.y, t * a.y_stride + col)[0];
-        if constexpr (FULL) {
-            raw_g[0] = raw_g[1] = none;
-            if (live && a.gate_type == MEGA_MOE_F32) {
-                raw_g[0] = raw8<true>(a.gate, t * a.gate_stride + col)[0];
-                raw_g[1] = raw8<true>(a.gate, t * a.gate_stride + col)[1];
-            } else if (live) {
-                raw_g[0] = raw8<false>(a.gate, t * a.gate_stride + col)[0];
-            }
-        } else if (a.gate_kind == MEGA_MOE_GATE_TOKEN && t < a.num_tokens) {
+        if (!FULL && a.gate_kind == MEGA_MOE_GATE_TOKEN && t < a.num_tokens) {
             raw_tg = a.gate_type == MEGA_MOE_F32 ? static_cast<const float*>(a.gate)[t]
                                                  : bf16_value(static_cast<const uint16_t*>(a.gate)[t]);
         }
@@ -208,10 +200,18 @@ moe_norm_backward(mega_moe_norm_backward_args a, float* ws, int nt) {
 #pragma unroll
         for (int i = 0; i < SW; ++i) cur_r[i] = raw_r[i];
         const u32x4_t cur_dn = raw_dn, cur_y = raw_y;
-        if constexpr (FULL) {
-            cur_g[0] = raw_g[0];
-            cur_g[1] = raw_g[1];
+        // what is needed after the first sum only, and would not fit beside the
+        // next row's registers, is loaded now
+        cur_g[0] = cur_g[1] = none;
+        if (FULL && live) {
+            if (a.gate_type == MEGA_MOE_F32) {
+                cur_g[0] = raw8<true>(a.gate, t * a.gate_stride + col)[0];
+                cur_g[1] = raw8<true>(a.gate, t * a.gate_stride + col)[1];
+            } else {
+                cur_g[0] = raw8<false>(a.gate, t * a.gate_stride + col)[0];
+            }
         }
+        if (SF32 && live && a.dr) load8<true>(a.dr, t * a.dr_stride + col, g);
         const float tg = raw_tg;
         if (round + 1 < rounds) fetch(t + step);
         // the sums that both norms need: of r^2 and u r, and of y^2
