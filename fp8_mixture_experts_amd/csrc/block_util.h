@@ -95,23 +95,84 @@ __device__ __forceinline__ void store8(void* p, int type, size_t i, const float 
     else store8<false>(p, i, v);
 }
 
-// Every lane gets the wave's sum; the order is fixed.
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d, 64);
+// Another lane's value by a data-parallel move: 1 and 2 are xor within a quad,
+// 4 and 8 (mirrors of 8 and of 16 lanes) pair groups whose lanes agree.
+template <int D>
+__device__ __forceinline__ uint32_t lane_pair(uint32_t v) {
+    constexpr int ctrl = D == 1 ? 0xB1 : D == 2 ? 0x4E : D == 4 ? 0x141 : 0x140;
+    return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, ctrl, 0xf, 0xf, true);
+}
+
+// op over LANES neighbouring lanes (16 or 64); every lane gets the result, and
+// the order is fixed.  All steps are vector moves, none goes through LDS.
+template <int LANES, typename F>
+__device__ __forceinline__ uint32_t over_lanes(uint32_t v, F op) {
+    v = op(v, lane_pair<1>(v));
+    v = op(v, lane_pair<2>(v));
+    v = op(v, lane_pair<4>(v));
+    v = op(v, lane_pair<8>(v));
+    if constexpr (LANES == 64) {
+        auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        v = op(r[0], r[1]);
+        r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        v = op(r[0], r[1]);
+    }
     return v;
 }
+
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float v) {
+    return __uint_as_float(over_lanes<LANES>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+        return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+    }));
+}
+
+template <int LANES>
+__device__ __forceinline__ float lanes_max(float v) {
+    return __uint_as_float(over_lanes<LANES>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+        return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+    }));
+}
+
+template <int LANES>
+__device__ __forceinline__ uint32_t lanes_min(uint32_t v) {
+    return over_lanes<LANES>(v, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
+}
+
+// The same for a wave of float64 values, moved in halves.
+template <typename F>
+__device__ __forceinline__ double over_wave(double v, F op) {
+    const auto step = [&](auto move) {
+        const uint64_t b = __builtin_bit_cast(uint64_t, v);
+        uint32_t lo[2], hi[2];
+        move((uint32_t)b, lo);
+        move((uint32_t)(b >> 32), hi);
+        v = op(__builtin_bit_cast(double, (uint64_t)hi[0] << 32 | lo[0]),
+               __builtin_bit_cast(double, (uint64_t)hi[1] << 32 | lo[1]));
+    };
+    step([](uint32_t x, uint32_t (&o)[2]) { o[0] = x, o[1] = lane_pair<1>(x); });
+    step([](uint32_t x, uint32_t (&o)[2]) { o[0] = x, o[1] = lane_pair<2>(x); });
+    step([](uint32_t x, uint32_t (&o)[2]) { o[0] = x, o[1] = lane_pair<4>(x); });
+    step([](uint32_t x, uint32_t (&o)[2]) { o[0] = x, o[1] = lane_pair<8>(x); });
+    step([](uint32_t x, uint32_t (&o)[2]) {
+        const auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+        o[0] = r[0], o[1] = r[1];
+    });
+    step([](uint32_t x, uint32_t (&o)[2]) {
+        const auto r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+        o[0] = r[0], o[1] = r[1];
+    });
+    return v;
+}
+
+__device__ __forceinline__ float wave_sum(float v) { return lanes_sum<64>(v); }
+__device__ __forceinline__ float wave_max(float v) { return lanes_max<64>(v); }
 
 __device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d, 64);
-    return v;
+    return over_wave(v, [](double a, double b) { return a + b; });
 }
-
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) v = fmaxf(v, __shfl_xor(v, d, 64));
-    return v;
+__device__ __forceinline__ double wave_max(double v) {
+    return over_wave(v, [](double a, double b) { return fmax(a, b); });
 }
 
 // Sums of N values over the workgroup (up to 16 waves), the waves' sums added

@@ -1,157 +1,307 @@
-// The router's selection and the gradient of its logits: one wave per token.
+// The router's selection and the gradient of its logits.
 #include <hip/hip_runtime.h>
+
+#include <type_traits>
 
 #include "router.h"
 #include "router_row.h"
 
 namespace mega_moe {
 
-// The wave's largest key and the lowest index that has it.
-template <typename Key>
-__device__ __forceinline__ void wave_best(Key& key, int& idx) {
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) {
-        const Key k2 = __shfl_xor(key, d, 64);
-        const int i2 = __shfl_xor(idx, d, 64);
-        if (k2 > key || (k2 == key && i2 < idx)) {
-            key = k2;
-            idx = i2;
-        }
-    }
-}
-
 constexpr int NO_EXPERT = 0x7fffffff;
 
-// Key = float: order by the logits.  Key = double: order by score + bias.
-template <int NI, typename Key>
-__global__ void __launch_bounds__(256)
-moe_router_topk(mega_moe_router_topk_args a) {
+// ---------------------------------------------------------------------------
+// Selection.  A token's experts lie in 16 lanes (up to 64 experts, four tokens
+// to a wave) or in a wave.  k rounds each find the largest key and the lowest
+// index that has it, by moves between lanes.  What bounds it is that chain of
+// vector instructions: a token's logits are read once and are small.
+//
+// Without bias and groups the keys are the logits, which order the experts as
+// the scores do.  Otherwise the order is that of score + bias in float64, but
+// it is found in float32 first, with one round more than there are slots: a
+// float32 score is off by less than `close` (below), so where any two
+// neighbours of the order lie further apart than both their errors, the order
+// is the float64 one.  A token with nearer ones (one in some hundreds) goes
+// through exact_topk, which computes the same in float64.
+// ---------------------------------------------------------------------------
+
+// A bound on the error of a float32 key c = score + bias.  Sigmoid: exp, the
+// sum and the division give less than 2.5 half steps of 1, the bias one of c.
+// Softmax: the rounding of l - max moves a score by at most 0.4 half steps of
+// the largest one, the sum over lanes and exp by less than 40 of its own.
+__device__ __forceinline__ float key_error(float c, bool softmax, float largest) {
+    return 0x1p-22f * fabsf(c) + (softmax ? 0x1p-18f * largest : 0x1p-22f);
+}
+
+// The wave's largest key and the lowest index that has it (NO_EXPERT: none is
+// above -inf).
+template <int NI>
+__device__ __forceinline__ int wave_best(const double (&key)[NI], double& best) {
     const int lane = threadIdx.x & 63;
-    const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (t >= a.num_tokens) return;
-    const int E = a.num_experts, k = a.num_topk;
-    int32_t* idx_out = a.topk_idx + (size_t)t * k;
-    float* w_out = a.topk_weights + (size_t)t * k;
-    if (a.token_mask && a.token_mask[t] == 0) {
-        for (int j = lane; j < k; j += 64) {
-            idx_out[j] = -1;
-            w_out[j] = 0.0f;
-        }
-        return;
-    }
-    float l[NI], s[NI];
+    best = key[0];
+#pragma unroll
+    for (int i = 1; i < NI; ++i) best = fmax(best, key[i]);
+    best = wave_max(best);
+    if (!(best > -(double)INFINITY)) return NO_EXPERT;
+    uint32_t at = NO_EXPERT;
+#pragma unroll
+    for (int i = NI - 1; i >= 0; --i)
+        if (key[i] == best) at = i * 64 + lane;
+    return (int)lanes_min<64>(at);
+}
+
+// The selection of token t in float64, by a whole wave: slots j, j + 64, ...
+// of idx_out are written by lane j.  `kept`: the groups that stay, or 0 where
+// float32 could not tell them either.
+template <int NI>
+__device__ __forceinline__ void exact_topk(const mega_moe_router_topk_args& a, int64_t t, uint64_t kept,
+                                           int32_t* idx_out) {
+    const int lane = threadIdx.x & 63, E = a.num_experts;
+    float l[NI];
+    double key[NI];
     load_row<NI>(a.logits, a.logits_type, (size_t)t * a.logits_stride, E, l);
-    Key key[NI];
     if (a.score == MEGA_MOE_SCORE_SOFTMAX) {
-        float top, sum;
-        row_exp(l, s, top, sum);
-        const float inv = 1.0f / sum;
+        float top = l[0];
 #pragma unroll
-        for (int i = 0; i < NI; ++i) s[i] *= inv;
-        if constexpr (sizeof(Key) == 8) {
-            double dsum = 0.0;
-#pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                key[i] = exp((double)l[i] - (double)top);
-                dsum += key[i];
-            }
-            dsum = wave_sum(dsum);
-#pragma unroll
-            for (int i = 0; i < NI; ++i) key[i] /= dsum;
-        }
-    } else {
+        for (int i = 1; i < NI; ++i) top = fmaxf(top, l[i]);
+        top = wave_max(top);
+        double sum = 0.0;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-            s[i] = sigmoid(l[i]);
-            if constexpr (sizeof(Key) == 8) key[i] = 1.0 / (1.0 + exp(-(double)l[i]));
+            key[i] = exp((double)l[i] - (double)top);
+            sum += key[i];
         }
+        sum = wave_sum(sum);
+#pragma unroll
+        for (int i = 0; i < NI; ++i) key[i] /= sum;
+    } else {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) key[i] = 1.0 / (1.0 + exp(-(double)l[i]));
     }
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
         const int e = i * 64 + lane;
-        if constexpr (sizeof(Key) == 8) {
-            if (a.bias && e < E) key[i] += (double)a.bias[e];
-        } else {
-            key[i] = l[i];
-        }
+        if (a.bias && e < E) key[i] += (double)a.bias[e];
         // never taken: -inf, NaN, and what lies behind the last expert
-        if (!(l[i] > -INFINITY) || !(key[i] > (Key)-INFINITY)) key[i] = (Key)-INFINITY;
+        if (!(l[i] > -INFINITY) || !(key[i] > -(double)INFINITY)) key[i] = -INFINITY;
     }
-    if constexpr (sizeof(Key) == 8) {
-        if (a.num_groups > 1) {
-            const int size = E / a.num_groups;
-            double mine = -INFINITY;             // lane g holds group g's score
+    if (a.num_groups > 1) {
+        const int size = E / a.num_groups;
+        if (kept == 0) {
+            double mine[1] = {-INFINITY};        // lane g holds group g's score
             for (int g = 0; g < a.num_groups; ++g) {
-                double sum = 0.0;
-                int first = NO_EXPERT;
-                for (int r = 0; r < a.group_top; ++r) {
-                    double best = -INFINITY;
-                    int at = NO_EXPERT;
+                double of[NI], sum = 0.0;
 #pragma unroll
-                    for (int i = 0; i < NI; ++i) {
-                        const int e = i * 64 + lane;
-                        if (e >= g * size && e < (g + 1) * size && e != first && key[i] > best) {
-                            best = key[i];
-                            at = e;
-                        }
-                    }
-                    wave_best(best, at);
-                    sum += best;
-                    first = at;
+                for (int i = 0; i < NI; ++i) {
+                    const int e = i * 64 + lane;
+                    of[i] = e >= g * size && e < (g + 1) * size ? key[i] : -(double)INFINITY;
                 }
-                if (lane == g) mine = sum;
+                for (int r = 0; r < a.group_top; ++r) {
+                    double best;
+                    const int at = wave_best(of, best);
+                    sum += best;
+#pragma unroll
+                    for (int i = 0; i < NI; ++i)
+                        if (at == i * 64 + lane) of[i] = -INFINITY;
+                }
+                if (lane == g) mine[0] = sum;
             }
-            uint64_t kept = 0;
             for (int r = 0; r < a.topk_groups; ++r) {
-                double best = lane < a.num_groups && !(kept >> lane & 1) ? mine : -INFINITY;
-                int at = lane < a.num_groups && !(kept >> lane & 1) ? lane : NO_EXPERT;
-                wave_best(best, at);
-                if (at < 64) kept |= 1ull << at;     // none left: NaN scores
-            }
-#pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                const int e = i * 64 + lane;
-                if (e < E && !(kept >> (e / size) & 1)) key[i] = -INFINITY;
+                double best;
+                int at = wave_best(mine, best);
+                // only groups at -inf are left: the lowest of them
+                if (at == NO_EXPERT) at = __builtin_ctzll(~kept);
+                kept |= 1ull << at;
+                if (lane == at) mine[0] = -INFINITY;
             }
         }
-    }
-    // k rounds: the wave's best goes to lane j % 64, which writes it
-    float total = 0.0f, mine_w = 0.0f;
-    int mine_e = -1;
-    for (int j = 0; j < k; ++j) {
-        Key best = (Key)-INFINITY;
-        int at = NO_EXPERT;
-        float sc = 0.0f;
 #pragma unroll
-        for (int i = 0; i < NI; ++i)
-            if (key[i] > best) {
-                best = key[i];
-                at = i * 64 + lane;
-            }
-        wave_best(best, at);
-        const bool found = at != NO_EXPERT;
-#pragma unroll
-        for (int i = 0; i < NI; ++i)
-            if (at == i * 64 + lane) {
-                sc = s[i];
-                key[i] = (Key)-INFINITY;
-            }
-        sc = __shfl(sc, found ? at & 63 : 0, 64);
-        if (!found) sc = 0.0f;
-        total += sc;
-        if ((j & 63) == lane) {
-            mine_e = found ? at : -1;
-            mine_w = sc;
-            idx_out[j] = mine_e;
-            if (k > 64) w_out[j] = mine_w;
+        for (int i = 0; i < NI; ++i) {
+            const int e = i * 64 + lane;
+            if (e < E && !(kept >> (e / size) & 1)) key[i] = -INFINITY;
         }
     }
+    for (int j = 0; j < a.num_topk; ++j) {
+        double best;
+        const int at = wave_best(key, best);
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+            if (at == i * 64 + lane) key[i] = -INFINITY;
+        if ((j & 63) == lane) idx_out[j] = at != NO_EXPERT ? at : -1;
+    }
+}
+
+// SCORED: the keys are score + bias, else the logits.
+template <int LANES, int NI, bool SCORED>
+__global__ void __launch_bounds__(256)
+moe_router_topk(mega_moe_router_topk_args a) {
+    constexpr int ROWS = 64 / LANES;             // tokens per wave
+    __shared__ float s_key[SCORED ? 4 * ROWS : 1][LANES * NI];
+    __shared__ float s_group[SCORED ? 4 * ROWS : 1][ROUTER_MAX_GROUPS];
+    const int lane = threadIdx.x & (LANES - 1), row = threadIdx.x / LANES;
+    const int64_t t = (int64_t)blockIdx.x * (256 / LANES) + row;
+    const bool softmax = a.score == MEGA_MOE_SCORE_SOFTMAX;
+    const int E = a.num_experts, k = a.num_topk;
+    // rows that have nothing to do keep their lanes in step with the others
+    const bool in = t < a.num_tokens;
+    const bool live = in && (!a.token_mask || a.token_mask[t] != 0);
+    if (__builtin_amdgcn_ballot_w64(in) == 0) return;
+    const size_t at_row = (size_t)t * a.logits_stride;
+    float l[NI], key[NI];
+    if (live) {
+        load_row<NI, LANES>(a.logits, a.logits_type, at_row, E, l);
+    } else {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) l[i] = -INFINITY;
+    }
+    // the softmax of a score: exp(l - top) * inv
+    float top = 0.0f, sum = 1.0f;
+    if (softmax) row_exp<LANES>(l, key, top, sum);
+    const float inv = 1.0f / sum;
+    const float largest = softmax ? inv : 1.0f;      // of the scores
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        const int e = i * LANES + lane;
+        if constexpr (SCORED) {
+            key[i] = softmax ? key[i] * inv : sigmoid(l[i]);
+            if (a.bias && e < E) key[i] += a.bias[e];
+            // NaN, -inf, and what lies behind the last expert
+            if (!(l[i] > -INFINITY) || !(key[i] > -INFINITY)) key[i] = -INFINITY;
+        } else {
+            key[i] = l[i] > -INFINITY ? l[i] : -INFINITY;
+        }
+    }
+    bool near = false;
+    uint64_t groups_kept = 0;
+    if constexpr (SCORED) {
+        if (a.num_groups > 1) {
+            const int G = a.num_groups, size = E / G;
+            float* keys = s_key[row];
+            float* groups = s_group[row];
+#pragma unroll
+            for (int i = 0; i < NI; ++i) keys[i * LANES + lane] = key[i];
+            __builtin_amdgcn_wave_barrier();
+            // a lane per group; each starts elsewhere in its group, so that
+            // the lanes read different banks
+            for (int g = lane; g < G; g += LANES) {
+                float first = -INFINITY, second = -INFINITY;
+                int o = g % size;
+                for (int j = 0; j < size; ++j) {
+                    const float x = keys[g * size + o];
+                    second = fmaxf(second, fminf(first, x));
+                    first = fmaxf(first, x);
+                    if (++o == size) o = 0;
+                }
+                groups[g] = a.group_top == 2 ? first + second : first;
+            }
+            __builtin_amdgcn_wave_barrier();
+            uint64_t kept = 0;
+            float low = INFINITY, high = -INFINITY;      // the last one kept, the first one not
+            for (int g0 = 0; g0 < G; g0 += LANES) {
+                const int g = g0 + lane;
+                bool keep = false;
+                if (g < G) {
+                    const float x = groups[g];
+                    int before = 0;
+                    for (int h = 0; h < G; ++h) {
+                        const float y = groups[h];
+                        before += y > x || (y == x && h < g);
+                    }
+                    keep = before < a.topk_groups;
+                    if (keep) low = fminf(low, x);
+                    else high = fmaxf(high, x);
+                }
+                const uint64_t b = __builtin_amdgcn_ballot_w64(keep);
+                if constexpr (LANES == 64) kept = b;
+                else kept |= (b >> ((threadIdx.x & 63) - lane) & 0xffffull) << g0;
+            }
+            low = -lanes_max<LANES>(-low);
+            high = lanes_max<LANES>(high);
+            float widest = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+                if (key[i] > -INFINITY) widest = fmaxf(widest, fabsf(key[i]));
+            const float error = key_error(lanes_max<LANES>(widest), softmax, largest);
+            near = high > -INFINITY && !(low - high > 8.0f * error);
+            groups_kept = near ? 0 : kept;
+            const uint32_t mul = ((1u << 20) + size - 1) / size;     // e / size for e * size < 2^20
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+                if (!(kept >> ((uint32_t)(i * LANES + lane) * mul >> 20 & 63) & 1)) key[i] = -INFINITY;
+        }
+    }
+    // the rounds; lane j % LANES writes slot j
+    const int rounds = SCORED ? (k < E ? k + 1 : k) : k;
+    int32_t* idx_out = a.topk_idx + (size_t)t * k;
+    float before = 0.0f;
+    int mine = -1;
+    for (int j = 0; j < rounds; ++j) {
+        float best = key[0];
+#pragma unroll
+        for (int i = 1; i < NI; ++i) best = fmaxf(best, key[i]);
+        best = lanes_max<LANES>(best);
+        uint32_t at = NO_EXPERT;
+#pragma unroll
+        for (int i = NI - 1; i >= 0; --i)
+            if (key[i] == best) at = i * LANES + lane;
+        at = lanes_min<LANES>(at);
+        const bool found = best > -INFINITY;
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+            if (at == (uint32_t)(i * LANES + lane)) key[i] = -INFINITY;
+        if constexpr (SCORED) {
+            if (j > 0 && found && !(before - best > 2.0f * key_error(before, softmax, largest))) near = true;
+            before = best;
+        }
+        if (in && j < k && (j & (LANES - 1)) == lane) {
+            mine = found ? (int)at : -1;
+            idx_out[j] = mine;
+        }
+    }
+    if constexpr (SCORED) {
+        // the whole wave on each token whose order float32 cannot tell
+        uint64_t again = __builtin_amdgcn_ballot_w64(near && live);
+        const int64_t t0 = t - (threadIdx.x & 63) / LANES;
+#pragma unroll 1
+        for (int r = 0; r < ROWS; ++r) {
+            const uint64_t mask = LANES == 64 ? ~0ull : 0xffffull << (r * 16);
+            if (!(again & mask)) continue;
+            const uint64_t kept = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(groups_kept >> 32), r * LANES) << 32 |
+                                  (uint32_t)__builtin_amdgcn_readlane((int)groups_kept, r * LANES);
+            exact_topk<(LANES * NI + 63) / 64>(a, t0 + r, kept, a.topk_idx + (size_t)(t0 + r) * k);
+        }
+        if (again && live && lane < k) {
+            __threadfence_block();
+            mine = idx_out[lane];
+        }
+    }
+    // the weights of the slots, from their own logits
+    if (!in) return;
+    float* w_out = a.topk_weights + (size_t)t * k;
+    const auto score_of = [&](int e) {
+        if (e < 0) return 0.0f;
+        const float x = a.logits_type == MEGA_MOE_F32
+                            ? static_cast<const float*>(a.logits)[at_row + e]
+                            : bf16_value(static_cast<const uint16_t*>(a.logits)[at_row + e]);
+        return softmax ? expf(x - top) * inv : sigmoid(x);
+    };
+    float w = 0.0f, total = 0.0f;
+    if (k <= LANES) {
+        total = w = score_of(mine);
+    } else {
+        for (int j = lane; j < k; j += LANES) {
+            w = score_of(idx_out[j]);
+            w_out[j] = w;
+            total += w;
+        }
+    }
+    total = lanes_sum<LANES>(total);
     float scale = a.weight_scale;
     if (a.renormalize) scale = total == 0.0f ? 0.0f : scale / total;
-    if (k <= 64) {
-        if (lane < k) w_out[lane] = mine_w * scale;
+    if (k <= LANES) {
+        if (lane < k) w_out[lane] = w * scale;
     } else {
-        for (int j = lane; j < k; j += 64) w_out[j] *= scale;
+        for (int j = lane; j < k; j += LANES) w_out[j] *= scale;
     }
 }
 
@@ -169,11 +319,12 @@ __device__ __forceinline__ int sequence_of(const int32_t* cu, int B, int64_t t) 
     return lo;
 }
 
-template <int NI>
+// The gradient of a token's logits, its experts in 16 lanes or a wave.
+template <int LANES, int NI>
 __global__ void __launch_bounds__(256)
 moe_router_backward(mega_moe_router_backward_args a) {
-    const int lane = threadIdx.x & 63;
-    const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int lane = threadIdx.x & (LANES - 1);
+    const int64_t t = (int64_t)blockIdx.x * (256 / LANES) + threadIdx.x / LANES;
     if (t >= a.num_tokens) return;
     const int E = a.num_experts, k = a.num_topk;
     float* out = a.dlogits + (size_t)t * a.dlogits_stride;
@@ -182,9 +333,9 @@ moe_router_backward(mega_moe_router_backward_args a) {
     for (int i = 0; i < NI; ++i) d[i] = 0.0f;
     if (!a.token_mask || a.token_mask[t] != 0) {
         float l[NI], s[NI], ex[NI];
-        load_row<NI>(a.logits, a.logits_type, (size_t)t * a.logits_stride, E, l);
+        load_row<NI, LANES>(a.logits, a.logits_type, (size_t)t * a.logits_stride, E, l);
         float top, sum;
-        row_exp(l, ex, top, sum);
+        row_exp<LANES>(l, ex, top, sum);
         const bool softmax = a.score == MEGA_MOE_SCORE_SOFTMAX;
         const float inv = sum > 0.0f ? 1.0f / sum : sum;
 #pragma unroll
@@ -199,13 +350,13 @@ moe_router_backward(mega_moe_router_backward_args a) {
                 const float g = dw[j];
 #pragma unroll
                 for (int i = 0; i < NI; ++i)
-                    if (e == i * 64 + lane && e < E) {
+                    if (e == i * LANES + lane && e < E) {
                         total += s[i];
                         dot += g * s[i];
                     }
             }
-            total = wave_sum(total);
-            dot = wave_sum(dot);
+            total = lanes_sum<LANES>(total);
+            dot = lanes_sum<LANES>(dot);
             const bool renorm = a.renormalize != 0;
             const float scale = renorm ? (total == 0.0f ? 0.0f : a.weight_scale / total) : a.weight_scale;
             const float mean = renorm && total != 0.0f ? dot / total : 0.0f;
@@ -217,13 +368,13 @@ moe_router_backward(mega_moe_router_backward_args a) {
                 const float g = scale * (dw[j] - mean);
 #pragma unroll
                 for (int i = 0; i < NI; ++i)
-                    if (e == i * 64 + lane && e < E) ds[i] += g;
+                    if (e == i * LANES + lane && e < E) ds[i] += g;
             }
             if (softmax) {
                 float c = 0.0f;
 #pragma unroll
                 for (int i = 0; i < NI; ++i) c += ds[i] * s[i];
-                c = wave_sum(c);
+                c = lanes_sum<LANES>(c);
 #pragma unroll
                 for (int i = 0; i < NI; ++i) d[i] += s[i] * (ds[i] - c);
             } else {
@@ -241,14 +392,14 @@ moe_router_backward(mega_moe_router_backward_args a) {
             float f[NI], den = 0.0f, c = 0.0f;
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
-                const int e = i * 64 + lane;
+                const int e = i * LANES + lane;
                 f[i] = e < E ? scale * (float)a.counts[(size_t)b * E + e] : 0.0f;
                 den += s[i];
                 c += s[i] * f[i];
             }
-            den = softmax ? 1.0f : wave_sum(den);
+            den = softmax ? 1.0f : lanes_sum<LANES>(den);
             const float id = den > 0.0f ? 1.0f / den : den;
-            c = wave_sum(c) * id;
+            c = lanes_sum<LANES>(c) * id;
             const float lse = a.dloss[1] * a.z_coeff * 2.0f / (float)max(n, 1) * row_lse(top, sum) * inv;
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
@@ -259,7 +410,7 @@ moe_router_backward(mega_moe_router_backward_args a) {
     }
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-        const int e = i * 64 + lane;
+        const int e = i * LANES + lane;
         if (e < E) out[e] = d[i];
     }
 }
@@ -268,29 +419,32 @@ namespace {
 // The smallest instance that holds E experts.
 template <typename F>
 void by_experts(int E, F&& go) {
-    if (E <= 64) go(std::integral_constant<int, 1>{});
-    else if (E <= 128) go(std::integral_constant<int, 2>{});
-    else if (E <= 256) go(std::integral_constant<int, 4>{});
-    else if (E <= 512) go(std::integral_constant<int, 8>{});
-    else go(std::integral_constant<int, 16>{});
+    using std::integral_constant;
+    if (E <= 16) go(integral_constant<int, 16>{}, integral_constant<int, 1>{});
+    else if (E <= 32) go(integral_constant<int, 16>{}, integral_constant<int, 2>{});
+    else if (E <= 64) go(integral_constant<int, 16>{}, integral_constant<int, 4>{});
+    else if (E <= 128) go(integral_constant<int, 64>{}, integral_constant<int, 2>{});
+    else if (E <= 256) go(integral_constant<int, 64>{}, integral_constant<int, 4>{});
+    else if (E <= 512) go(integral_constant<int, 64>{}, integral_constant<int, 8>{});
+    else go(integral_constant<int, 64>{}, integral_constant<int, 16>{});
 }
+unsigned workgroups(int tokens, int lanes) { return (unsigned)(((int64_t)tokens * lanes + 255) / 256); }
 }  // namespace
 
 void launch_router_topk(const mega_moe_router_topk_args& a, hipStream_t stream) {
-    const dim3 grid((unsigned)(((int64_t)a.num_tokens + 3) / 4));
-    const bool wide = a.bias || a.num_groups > 1;
-    by_experts(a.num_experts, [&](auto ni) {
-        constexpr int NI = decltype(ni)::value;
-        if (wide) hipLaunchKernelGGL((moe_router_topk<NI, double>), grid, dim3(256), 0, stream, a);
-        else hipLaunchKernelGGL((moe_router_topk<NI, float>), grid, dim3(256), 0, stream, a);
+    const bool scored = a.bias || a.num_groups > 1;
+    by_experts(a.num_experts, [&](auto lanes, auto ni) {
+        constexpr int L = decltype(lanes)::value, NI = decltype(ni)::value;
+        const dim3 grid(workgroups(a.num_tokens, L));
+        if (scored) hipLaunchKernelGGL((moe_router_topk<L, NI, true>), grid, dim3(256), 0, stream, a);
+        else hipLaunchKernelGGL((moe_router_topk<L, NI, false>), grid, dim3(256), 0, stream, a);
     });
 }
 
 void launch_router_backward(const mega_moe_router_backward_args& a, hipStream_t stream) {
-    const dim3 grid((unsigned)(((int64_t)a.num_tokens + 3) / 4));
-    by_experts(a.num_experts, [&](auto ni) {
-        constexpr int NI = decltype(ni)::value;
-        hipLaunchKernelGGL((moe_router_backward<NI>), grid, dim3(256), 0, stream, a);
+    by_experts(a.num_experts, [&](auto lanes, auto ni) {
+        constexpr int L = decltype(lanes)::value, NI = decltype(ni)::value;
+        hipLaunchKernelGGL((moe_router_backward<L, NI>), dim3(workgroups(a.num_tokens, L)), dim3(256), 0, stream, a);
     });
 }
 

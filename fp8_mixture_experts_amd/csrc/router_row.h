@@ -1,16 +1,17 @@
-// One token's logits in a wave: lane l holds experts l, l + 64, ...
+// One token's logits in LANES neighbouring lanes (16 or a whole wave): lane l
+// holds experts l, l + LANES, ...
 #pragma once
 
 #include "block_util.h"
 
 namespace mega_moe {
 
-template <int NI>
+template <int NI, int LANES = 64>
 __device__ __forceinline__ void load_row(const void* logits, int type, size_t row, int E, float (&l)[NI]) {
-    const int lane = threadIdx.x & 63;
+    const int lane = threadIdx.x & (LANES - 1);
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-        const int e = i * 64 + lane;
+        const int e = i * LANES + lane;
         l[i] = -INFINITY;
         if (e < E)
             l[i] = type == MEGA_MOE_F32 ? static_cast<const float*>(logits)[row + e]
@@ -20,12 +21,12 @@ __device__ __forceinline__ void load_row(const void* logits, int type, size_t ro
 
 // The largest logit of the row, and the sum of exp(logit - largest).  A row of
 // -inf alone has sum 0.  An infinity or NaN among the logits makes the sum NaN.
-template <int NI>
+template <int LANES = 64, int NI>
 __device__ __forceinline__ void row_exp(const float (&l)[NI], float (&ex)[NI], float& top, float& sum) {
     top = l[0];
 #pragma unroll
     for (int i = 1; i < NI; ++i) top = fmaxf(top, l[i]);
-    top = wave_max(top);
+    top = lanes_max<LANES>(top);
     const float at = top == -INFINITY ? 0.0f : top;
     sum = 0.0f;
 #pragma unroll
@@ -33,7 +34,7 @@ __device__ __forceinline__ void row_exp(const float (&l)[NI], float (&ex)[NI], f
         ex[i] = expf(l[i] - at);
         sum += ex[i];
     }
-    sum = wave_sum(sum);
+    sum = lanes_sum<LANES>(sum);
 }
 
 // log sum exp of the row; 0 for a row of -inf alone, so that a token without
