@@ -103,7 +103,7 @@ __device__ __forceinline__ uint32_t lane_pair(uint32_t v) {
     return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, ctrl, 0xf, 0xf, true);
 }
 
-// op over LANES neighbouring lanes (16 or 64); every lane gets the result, and
+// op over LANES neighbouring lanes (16, 32 or 64); every lane gets the result, and
 // the order is fixed.  All steps are vector moves, none goes through LDS.
 template <int LANES, typename F>
 __device__ __forceinline__ uint32_t over_lanes(uint32_t v, F op) {
@@ -111,10 +111,12 @@ __device__ __forceinline__ uint32_t over_lanes(uint32_t v, F op) {
     v = op(v, lane_pair<2>(v));
     v = op(v, lane_pair<4>(v));
     v = op(v, lane_pair<8>(v));
-    if constexpr (LANES == 64) {
-        auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    if constexpr (LANES >= 32) {
+        const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
         v = op(r[0], r[1]);
-        r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    }
+    if constexpr (LANES == 64) {
+        const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
         v = op(r[0], r[1]);
     }
     return v;

@@ -11,8 +11,8 @@ namespace mega_moe {
 constexpr int NO_EXPERT = 0x7fffffff;
 
 // ---------------------------------------------------------------------------
-// Selection.  A token's experts lie in 16 lanes (up to 64 experts, four tokens
-// to a wave) or in a wave.  k rounds each find the largest key and the lowest
+// Selection.  A token's experts lie in 16 lanes (up to 256 experts, four tokens
+// to a wave), in 32 (512) or in a wave.  k rounds each find the largest key and the lowest
 // index that has it, by moves between lanes.  What bounds it is that chain of
 // vector instructions: a token's logits are read once and are small.
 //
@@ -21,16 +21,26 @@ constexpr int NO_EXPERT = 0x7fffffff;
 // it is found in float32 first, with one round more than there are slots: a
 // float32 score is off by less than `close` (below), so where any two
 // neighbours of the order lie further apart than both their errors, the order
-// is the float64 one.  A token with nearer ones (one in some hundreds) goes
-// through exact_topk, which computes the same in float64.
+// is the float64 one.  Nearer ones (in one token of some hundreds) are ordered
+// again by their float64 keys, one candidate to a lane; where that is not
+// enough (softmax, whose float64 sum takes every expert; a near tie of groups,
+// or of three at the last slot; more slots than lanes) the token goes through
+// exact_topk, which computes all of it in float64.
 // ---------------------------------------------------------------------------
 
-// A bound on the error of a float32 key c = score + bias.  Sigmoid: exp, the
-// sum and the division give less than 2.5 half steps of 1, the bias one of c.
+// The score as a key: hardware exp2 and reciprocal.
+__device__ __forceinline__ float sigmoid_key(float x) {
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -1.44269504f));
+}
+
+// A bound on the error of a float32 key c = score + bias, in half steps of 1
+// (2^-24).  Sigmoid: the exponent's two roundings and exp2's step move the
+// score by s (1 - s) (2.9 |x| + 2) < 1.2, the sum by 1, the reciprocal by 2,
+// the bias by |c|: less than 4.2 + |c|.
 // Softmax: the rounding of l - max moves a score by at most 0.4 half steps of
 // the largest one, the sum over lanes and exp by less than 40 of its own.
 __device__ __forceinline__ float key_error(float c, bool softmax, float largest) {
-    return 0x1p-22f * fabsf(c) + (softmax ? 0x1p-18f * largest : 0x1p-22f);
+    return 0x1p-23f * fabsf(c) + (softmax ? 0x1p-18f * largest : 0x1.4p-22f);
 }
 
 // The wave's largest key and the lowest index that has it (NO_EXPERT: none is
@@ -131,6 +141,32 @@ __device__ __forceinline__ void exact_topk(const mega_moe_router_topk_args& a, i
     }
 }
 
+// The two largest of the lanes' pairs first >= second.
+template <int LANES>
+__device__ __forceinline__ void lanes_top2(float& first, float& second) {
+    const auto join = [&](uint32_t f1, uint32_t s1, uint32_t f2, uint32_t s2) {
+        const float a = __uint_as_float(f1), b = __uint_as_float(f2);
+        second = fmaxf(fminf(a, b), fmaxf(__uint_as_float(s1), __uint_as_float(s2)));
+        first = fmaxf(a, b);
+    };
+    const auto f = [&] { return __float_as_uint(first); };
+    const auto s = [&] { return __float_as_uint(second); };
+    join(f(), s(), lane_pair<1>(f()), lane_pair<1>(s()));
+    join(f(), s(), lane_pair<2>(f()), lane_pair<2>(s()));
+    join(f(), s(), lane_pair<4>(f()), lane_pair<4>(s()));
+    join(f(), s(), lane_pair<8>(f()), lane_pair<8>(s()));
+    if constexpr (LANES >= 32) {
+        const auto x = __builtin_amdgcn_permlane16_swap(f(), f(), false, false);
+        const auto y = __builtin_amdgcn_permlane16_swap(s(), s(), false, false);
+        join(x[0], y[0], x[1], y[1]);
+    }
+    if constexpr (LANES == 64) {
+        const auto x = __builtin_amdgcn_permlane32_swap(f(), f(), false, false);
+        const auto y = __builtin_amdgcn_permlane32_swap(s(), s(), false, false);
+        join(x[0], y[0], x[1], y[1]);
+    }
+}
+
 // SCORED: the keys are score + bias, else the logits.
 template <int LANES, int NI, bool SCORED>
 __global__ void __launch_bounds__(256)
@@ -163,7 +199,7 @@ moe_router_topk(mega_moe_router_topk_args a) {
     for (int i = 0; i < NI; ++i) {
         const int e = i * LANES + lane;
         if constexpr (SCORED) {
-            key[i] = softmax ? key[i] * inv : sigmoid(l[i]);
+            key[i] = softmax ? key[i] * inv : sigmoid_key(l[i]);
             if (a.bias && e < E) key[i] += a.bias[e];
             // NaN, -inf, and what lies behind the last expert
             if (!(l[i] > -INFINITY) || !(key[i] > -INFINITY)) key[i] = -INFINITY;
@@ -176,23 +212,42 @@ moe_router_topk(mega_moe_router_topk_args a) {
     if constexpr (SCORED) {
         if (a.num_groups > 1) {
             const int G = a.num_groups, size = E / G;
-            float* keys = s_key[row];
             float* groups = s_group[row];
-#pragma unroll
-            for (int i = 0; i < NI; ++i) keys[i * LANES + lane] = key[i];
-            __builtin_amdgcn_wave_barrier();
-            // a lane per group; each starts elsewhere in its group, so that
-            // the lanes read different banks
-            for (int g = lane; g < G; g += LANES) {
+            if (size % LANES == 0) {
+                // whole rounds of the lanes: the two largest by moves
                 float first = -INFINITY, second = -INFINITY;
-                int o = g % size;
-                for (int j = 0; j < size; ++j) {
-                    const float x = keys[g * size + o];
-                    second = fmaxf(second, fminf(first, x));
-                    first = fmaxf(first, x);
-                    if (++o == size) o = 0;
+                int g = 0, left = size;
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    if (i * LANES >= E) break;
+                    second = fmaxf(second, fminf(first, key[i]));
+                    first = fmaxf(first, key[i]);
+                    if ((left -= LANES) > 0) continue;
+                    lanes_top2<LANES>(first, second);
+                    if (lane == 0) groups[g] = a.group_top == 2 ? first + second : first;
+                    first = second = -INFINITY;
+                    left = size;
+                    ++g;
                 }
-                groups[g] = a.group_top == 2 ? first + second : first;
+            } else {
+                // through LDS, a lane per group; each starts elsewhere in its
+                // group, so that the lanes read different banks
+                float* keys = s_key[row];
+#pragma unroll
+                for (int i = 0; i < NI; ++i) keys[i * LANES + lane] = key[i];
+                __builtin_amdgcn_wave_barrier();
+                for (int g = lane; g < G; g += LANES) {
+                    float first = -INFINITY, second = -INFINITY;
+                    int o = g % size;
+#pragma unroll 4
+                    for (int j = 0; j < size; ++j) {
+                        const float x = keys[g * size + o];
+                        second = fmaxf(second, fminf(first, x));
+                        first = fmaxf(first, x);
+                        if (++o == size) o = 0;
+                    }
+                    groups[g] = a.group_top == 2 ? first + second : first;
+                }
             }
             __builtin_amdgcn_wave_barrier();
             uint64_t kept = 0;
@@ -213,7 +268,7 @@ moe_router_topk(mega_moe_router_topk_args a) {
                 }
                 const uint64_t b = __builtin_amdgcn_ballot_w64(keep);
                 if constexpr (LANES == 64) kept = b;
-                else kept |= (b >> ((threadIdx.x & 63) - lane) & 0xffffull) << g0;
+                else kept |= (b >> ((threadIdx.x & 63) - lane) & ((1ull << (LANES & 63)) - 1)) << g0;
             }
             low = -lanes_max<LANES>(-low);
             high = lanes_max<LANES>(high);
@@ -230,11 +285,14 @@ moe_router_topk(mega_moe_router_topk_args a) {
                 if (!(kept >> ((uint32_t)(i * LANES + lane) * mul >> 20 & 63) & 1)) key[i] = -INFINITY;
         }
     }
-    // the rounds; lane j % LANES writes slot j
-    const int rounds = SCORED ? (k < E ? k + 1 : k) : k;
+    // the rounds; slot j belongs to lane j % LANES.  One more candidate than
+    // slots, and another to see whether that one has near ties
+    const int rounds = SCORED ? (k + 2 < E ? k + 2 : E) : k;
+    const bool one_each = k < LANES;             // every candidate has a lane
     int32_t* idx_out = a.topk_idx + (size_t)t * k;
     float before = 0.0f;
     int mine = -1;
+    bool tie = false, tie_at_k = false, full = near;
     for (int j = 0; j < rounds; ++j) {
         float best = key[0];
 #pragma unroll
@@ -250,44 +308,70 @@ moe_router_topk(mega_moe_router_topk_args a) {
         for (int i = 0; i < NI; ++i)
             if (at == (uint32_t)(i * LANES + lane)) key[i] = -INFINITY;
         if constexpr (SCORED) {
-            if (j > 0 && found && !(before - best > 2.0f * key_error(before, softmax, largest))) near = true;
+            const bool close = j > 0 && found && !(before - best > 2.0f * key_error(before, softmax, largest));
+            if (j <= k) tie = tie || close;
+            if (j == k) tie_at_k = close;
+            if (j == k + 1) full = full || (close && tie_at_k);
             before = best;
         }
-        if (in && j < k && (j & (LANES - 1)) == lane) {
+        if ((j & (LANES - 1)) == lane && (j < k || (one_each && j == k))) {
             mine = found ? (int)at : -1;
-            idx_out[j] = mine;
+            if (!one_each && in) idx_out[j] = mine;
         }
     }
+    const auto logit = [&](int e) {
+        return a.logits_type == MEGA_MOE_F32 ? static_cast<const float*>(a.logits)[at_row + e]
+                                             : bf16_value(static_cast<const uint16_t*>(a.logits)[at_row + e]);
+    };
     if constexpr (SCORED) {
-        // the whole wave on each token whose order float32 cannot tell
-        uint64_t again = __builtin_amdgcn_ballot_w64(near && live);
-        const int64_t t0 = t - (threadIdx.x & 63) / LANES;
+        const bool by_lane = one_each && !softmax;
+        if (!by_lane) full = full || tie;
+        if (by_lane && __builtin_amdgcn_ballot_w64(tie) != 0) {
+            // candidates by their float64 keys; those without an expert last
+            const bool cand = lane <= k && mine >= 0;
+            double c = -INFINITY;
+            if (cand) c = 1.0 / (1.0 + exp(-(double)logit(mine))) + (a.bias ? (double)a.bias[mine] : 0.0);
+            const int order = cand ? mine : NO_EXPERT - LANES + lane;
+            int rank = 0;
+            for (int i = 0; i <= k; ++i) {
+                const double ci = __shfl(c, i, LANES);
+                const int oi = __shfl(order, i, LANES);
+                rank += ci > c || (ci == c && oi < order);
+            }
+            // lanes behind the candidates stay where they are
+            if (lane > k) rank = lane;
+            mine = __builtin_amdgcn_ds_permute((int)(((threadIdx.x & 63) - lane + rank) * 4), mine);
+        }
+        if (one_each && in && lane < k) idx_out[lane] = mine;
+        // the whole wave on each token that needs all of it
+        const uint64_t again = __builtin_amdgcn_ballot_w64(full && live);
+        if (again) {
+            const int64_t t0 = t - (threadIdx.x & 63) / LANES;
 #pragma unroll 1
-        for (int r = 0; r < ROWS; ++r) {
-            const uint64_t mask = LANES == 64 ? ~0ull : 0xffffull << (r * 16);
-            if (!(again & mask)) continue;
-            const uint64_t kept = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(groups_kept >> 32), r * LANES) << 32 |
-                                  (uint32_t)__builtin_amdgcn_readlane((int)groups_kept, r * LANES);
-            exact_topk<(LANES * NI + 63) / 64>(a, t0 + r, kept, a.topk_idx + (size_t)(t0 + r) * k);
-        }
-        if (again && live && lane < k) {
+            for (int r = 0; r < ROWS; ++r) {
+                const uint64_t mask = LANES == 64 ? ~0ull : ((1ull << (LANES & 63)) - 1) << (r * LANES);
+                if (!(again & mask)) continue;
+                const uint64_t kept = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(groups_kept >> 32), r * LANES) << 32 |
+                                      (uint32_t)__builtin_amdgcn_readlane((int)groups_kept, r * LANES);
+                exact_topk<(LANES * NI + 63) / 64>(a, t0 + r, kept, a.topk_idx + (size_t)(t0 + r) * k);
+            }
             __threadfence_block();
-            mine = idx_out[lane];
+            if (live && one_each && lane < k) mine = idx_out[lane];
         }
+    } else {
+        if (one_each && in && lane < k) idx_out[lane] = mine;
     }
     // the weights of the slots, from their own logits
     if (!in) return;
     float* w_out = a.topk_weights + (size_t)t * k;
     const auto score_of = [&](int e) {
         if (e < 0) return 0.0f;
-        const float x = a.logits_type == MEGA_MOE_F32
-                            ? static_cast<const float*>(a.logits)[at_row + e]
-                            : bf16_value(static_cast<const uint16_t*>(a.logits)[at_row + e]);
+        const float x = logit(e);
         return softmax ? expf(x - top) * inv : sigmoid(x);
     };
     float w = 0.0f, total = 0.0f;
-    if (k <= LANES) {
-        total = w = score_of(mine);
+    if (one_each) {
+        if (lane < k) total = w = score_of(mine);
     } else {
         for (int j = lane; j < k; j += LANES) {
             w = score_of(idx_out[j]);
@@ -298,7 +382,7 @@ moe_router_topk(mega_moe_router_topk_args a) {
     total = lanes_sum<LANES>(total);
     float scale = a.weight_scale;
     if (a.renormalize) scale = total == 0.0f ? 0.0f : scale / total;
-    if (k <= LANES) {
+    if (one_each) {
         if (lane < k) w_out[lane] = w * scale;
     } else {
         for (int j = lane; j < k; j += LANES) w_out[j] *= scale;
@@ -319,7 +403,7 @@ __device__ __forceinline__ int sequence_of(const int32_t* cu, int B, int64_t t) 
     return lo;
 }
 
-// The gradient of a token's logits, its experts in 16 lanes or a wave.
+// The gradient of a token's logits, its experts in 16, 32 or 64 lanes.
 template <int LANES, int NI>
 __global__ void __launch_bounds__(256)
 moe_router_backward(mega_moe_router_backward_args a) {
@@ -423,9 +507,9 @@ void by_experts(int E, F&& go) {
     if (E <= 16) go(integral_constant<int, 16>{}, integral_constant<int, 1>{});
     else if (E <= 32) go(integral_constant<int, 16>{}, integral_constant<int, 2>{});
     else if (E <= 64) go(integral_constant<int, 16>{}, integral_constant<int, 4>{});
-    else if (E <= 128) go(integral_constant<int, 64>{}, integral_constant<int, 2>{});
-    else if (E <= 256) go(integral_constant<int, 64>{}, integral_constant<int, 4>{});
-    else if (E <= 512) go(integral_constant<int, 64>{}, integral_constant<int, 8>{});
+    else if (E <= 128) go(integral_constant<int, 16>{}, integral_constant<int, 8>{});
+    else if (E <= 256) go(integral_constant<int, 16>{}, integral_constant<int, 16>{});
+    else if (E <= 512) go(integral_constant<int, 32>{}, integral_constant<int, 16>{});
     else go(integral_constant<int, 64>{}, integral_constant<int, 16>{});
 }
 unsigned workgroups(int tokens, int lanes) { return (unsigned)(((int64_t)tokens * lanes + 255) / 256); }

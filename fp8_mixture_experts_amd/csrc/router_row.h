@@ -1,4 +1,4 @@
-// One token's logits in LANES neighbouring lanes (16 or a whole wave): lane l
+// One token's logits in LANES neighbouring lanes (16, 32 or 64): lane l
 // holds experts l, l + LANES, ...
 #pragma once
 
