@@ -9,14 +9,19 @@ namespace mega_moe {
 template <int NI, int LANES = 64>
 __device__ __forceinline__ void load_row(const void* logits, int type, size_t row, int E, float (&l)[NI]) {
     const int lane = threadIdx.x & (LANES - 1);
+    // lanes behind the last expert read it once more and drop it: no branches
+    // between the loads
+    if (type == MEGA_MOE_F32) {
+        const float* p = static_cast<const float*>(logits) + row;
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-        const int e = i * LANES + lane;
-        l[i] = -INFINITY;
-        if (e < E)
-            l[i] = type == MEGA_MOE_F32 ? static_cast<const float*>(logits)[row + e]
-                                        : bf16_value(static_cast<const uint16_t*>(logits)[row + e]);
+        for (int i = 0; i < NI; ++i) l[i] = p[min(i * LANES + lane, E - 1)];
+    } else {
+        const uint16_t* p = static_cast<const uint16_t*>(logits) + row;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) l[i] = bf16_value(p[min(i * LANES + lane, E - 1)]);
     }
+#pragma unroll
+    for (int i = 0; i < NI; ++i) l[i] = i * LANES + lane < E ? l[i] : -INFINITY;
 }
 
 // The largest logit of the row, and the sum of exp(logit - largest).  A row of
@@ -41,11 +46,14 @@ __device__ __forceinline__ void row_exp(const float (&l)[NI], float (&ex)[NI], f
 // any expert adds nothing to a loss.
 __device__ __forceinline__ float row_lse(float top, float sum) { return sum == 0.0f ? 0.0f : logf(sum) + top; }
 
-// The derivative comes from exp(-|x|): s (1 - s) would cancel where s is near 1.
 __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
-__device__ __forceinline__ float sigmoid_slope(float x) {
+
+// sigmoid(x) and its derivative, from exp(-|x|): s (1 - s) would cancel where s
+// is near 1.
+__device__ __forceinline__ void sigmoid_slope(float x, float& s, float& slope) {
     const float e = expf(-fabsf(x)), d = 1.0f / (1.0f + e);
-    return e * d * d;
+    s = x >= 0.0f ? d : e * d;
+    slope = e * d * d;
 }
 
 }  // namespace mega_moe
