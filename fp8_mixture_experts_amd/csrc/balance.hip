@@ -1,5 +1,19 @@
-// Per-expert route counts and the router's losses.
+// Per-expert route counts and the router's losses, in two launches.
+//
+// moe_balance_part takes the tokens in chunks of 32, one per workgroup, and
+// writes a record (sums of p and counts per expert, sum of lse^2, tokens) for
+// every sequence that has tokens in the chunk: chunk c and sequence b have
+// record c + b, which no other pair has, since both grow along the tokens; a
+// sequence's records lie next to each other.  The lengths of the sequences,
+// which the host does not know, thus never unbalance the work.
+// moe_balance_finish adds up every sequence's records in order, 32 experts per
+// workgroup; the workgroup that ends last adds up the losses.
+//
+// The logits are read once (8 MB at 8192 x 256: 2 us); what bounds it is the
+// chain of a token's loads, exponentials and sums, and the two launches.
 #include <hip/hip_runtime.h>
+
+#include <type_traits>
 
 #include "moe_args.h"
 #include "router.h"
@@ -7,36 +21,40 @@
 
 namespace mega_moe {
 
-// Workspace, for B sequences in S parts each: [B][S][E] floats (sums of p),
-// [B][S][E] ints (counts), [B][S] floats (sums of lse^2), [B][S] ints (tokens),
-// then [B] floats each: a sequence's balance term, its sum of lse^2.
+constexpr int CHUNK = 32;             // tokens per chunk
+constexpr int SLICE = 32;             // experts per workgroup of the second launch
+
 struct BalanceWs {
-    float* p;
-    int32_t* count;
-    float* z;
-    int32_t* n;
-    float* seq_loss;
-    float* seq_z;
+    float* p;             // [records][E]
+    int32_t* count;       // [records][E]
+    float* z;             // [records]
+    int32_t* n;           // [records]
+    float* seq_loss;      // [B][slices] a sequence's balance term
+    float* seq_z;         // [B] its sum of lse^2
+    uint32_t* done;       // workgroups of the second launch that have ended
 };
 
-__host__ __device__ inline size_t balance_layout(int64_t B, int64_t S, int64_t E, char* base, BalanceWs& w) {
+__host__ __device__ inline int64_t balance_chunks(int64_t T) { return (T + CHUNK - 1) / CHUNK; }
+
+__host__ __device__ inline size_t balance_layout(int64_t T, int64_t B, int64_t E, char* base, BalanceWs& w) {
+    const int64_t records = balance_chunks(T) + B;
     size_t o = 0;
     const auto take = [&](size_t n) {
         char* p = base + o;
         o += (n + 15) / 16 * 16;
         return p;
     };
-    w.p = (float*)take((size_t)(B * S * E) * 4);
-    w.count = (int32_t*)take((size_t)(B * S * E) * 4);
-    w.z = (float*)take((size_t)(B * S) * 4);
-    w.n = (int32_t*)take((size_t)(B * S) * 4);
-    w.seq_loss = (float*)take((size_t)B * 4);
+    w.p = (float*)take((size_t)(records * E) * 4);
+    w.count = (int32_t*)take((size_t)(records * E) * 4);
+    w.z = (float*)take((size_t)records * 4);
+    w.n = (int32_t*)take((size_t)records * 4);
+    w.seq_loss = (float*)take((size_t)(B * ((E + SLICE - 1) / SLICE)) * 4);
     w.seq_z = (float*)take((size_t)B * 4);
+    w.done = (uint32_t*)take(4);
     return o;
 }
 
-constexpr int BALANCE_ROWS = 32;      // tokens per part, about
-
+// Sequence b's tokens, within [0, T) whatever cu_seqlens holds.
 __device__ __forceinline__ void sequence_span(const mega_moe_balance_loss_args& a, int b, int& lo, int& hi) {
     lo = 0;
     hi = a.num_tokens;
@@ -46,157 +64,232 @@ __device__ __forceinline__ void sequence_span(const mega_moe_balance_loss_args& 
     }
 }
 
-// One part of one sequence per workgroup: a wave per token, its lanes keeping
-// the sums of their experts; counts meet in LDS.
-template <int NI>
-__global__ void __launch_bounds__(256)
-moe_balance_part(mega_moe_balance_loss_args a, BalanceWs ws, int S) {
-    __shared__ int count[MAX_EXPERTS];
-    __shared__ float sums[4][NI * 64];
-    __shared__ float zs[4];
-    __shared__ int ns[4];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+// A token's experts lie in LANES lanes; the 512 / LANES groups of lanes take
+// the tokens in turn, each lane keeping the sums of its experts.
+template <int LANES, int NI>
+__global__ void __launch_bounds__(512)
+moe_balance_part(mega_moe_balance_loss_args a, BalanceWs ws, int B) {
+    constexpr int GROUPS = 512 / LANES;
+    __shared__ int count[LANES * NI];
+    __shared__ float sums[8][LANES * NI];
+    __shared__ float zs[8];
+    __shared__ int ns[8];
+    const int tid = threadIdx.x, lane = tid & (LANES - 1), group = tid / LANES, wave = tid >> 6;
     const int E = a.num_experts, k = a.num_topk;
-    const int b = blockIdx.x / S, part = blockIdx.x - b * S;
-    int lo, hi;
-    sequence_span(a, b, lo, hi);
-    const int64_t len = hi - lo;
-    const int first = lo + (int)(len * part / S), last = lo + (int)(len * (part + 1) / S);
-    for (int e = tid; e < E; e += 256) count[e] = 0;
-    __syncthreads();
-    float acc[NI], z = 0.0f;
-    int n = 0;
+    const int c0 = blockIdx.x * CHUNK, c1 = min(c0 + CHUNK, a.num_tokens);
+    if (blockIdx.x == 0 && tid == 0) *ws.done = 0;
+    int p = c0;
+    while (p < c1) {
+        const int b = sequence_of<64>(a.cu_seqlens, B, p);
+        if (b < 0) {
+            // before the first sequence, or behind the last
+            if (p >= a.cu_seqlens[0]) break;
+            p = a.cu_seqlens[0];
+            continue;
+        }
+        int lo, hi;
+        sequence_span(a, b, lo, hi);
+        if (hi <= p) break;                      // cu_seqlens decreases
+        const int end = min(hi, c1);
+        for (int e = tid; e < LANES * NI; e += 512) count[e] = 0;
+        __syncthreads();
+        float acc[NI], z = 0.0f;
+        int n = 0;
 #pragma unroll
-    for (int i = 0; i < NI; ++i) acc[i] = 0.0f;
-    for (int t = first + wave; t < last; t += 4) {
-        if (a.token_mask && a.token_mask[t] == 0) continue;
-        ++n;
-        float l[NI], ex[NI], top, sum;
-        load_row<NI>(a.logits, a.logits_type, (size_t)t * a.logits_stride, E, l);
-        row_exp(l, ex, top, sum);
-        const float lse = row_lse(top, sum);
-        z += lse * lse;
-        if (a.score == MEGA_MOE_SCORE_SIGMOID) {
+        for (int i = 0; i < NI; ++i) acc[i] = 0.0f;
+        for (int t = p + group; t < end; t += GROUPS) {
+            const bool live = !a.token_mask || a.token_mask[t] != 0;
+            int e0 = lane < k ? a.topk_idx[(size_t)t * k + lane] : -1;
+            float l[NI], ex[NI], top, sum;
+            load_row<NI, LANES>(a.logits, a.logits_type, (size_t)t * a.logits_stride, E, l);
+            if (!live) continue;
+            ++n;
+            row_exp<LANES>(l, ex, top, sum);
+            const float lse = row_lse(top, sum);
+            z += lse * lse;
+            if (a.score == MEGA_MOE_SCORE_SIGMOID) {
+                float s = 0.0f;
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    ex[i] = sigmoid(l[i]);
+                    s += ex[i];
+                }
+                sum = lanes_sum<LANES>(s);
+            }
+            const float inv = sum > 0.0f ? 1.0f / sum : sum;
+#pragma unroll
+            for (int i = 0; i < NI; ++i) acc[i] += ex[i] * inv;
+            if (e0 >= 0 && e0 < E) atomicAdd(&count[e0], 1);
+            for (int j = lane + LANES; j < k; j += LANES) {
+                e0 = a.topk_idx[(size_t)t * k + j];
+                if (e0 >= 0 && e0 < E) atomicAdd(&count[e0], 1);
+            }
+        }
+        // the wave's groups of lanes, then the waves, in order
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            if constexpr (LANES <= 16) acc[i] += __shfl_xor(acc[i], 16, 64);
+            if constexpr (LANES <= 32) acc[i] += __shfl_xor(acc[i], 32, 64);
+            if ((tid & 63) < LANES) sums[wave][i * LANES + lane] = acc[i];
+        }
+        if constexpr (LANES <= 16) z += __shfl_xor(z, 16, 64), n += __shfl_xor(n, 16, 64);
+        if constexpr (LANES <= 32) z += __shfl_xor(z, 32, 64), n += __shfl_xor(n, 32, 64);
+        if ((tid & 63) == 0) {
+            zs[wave] = z;
+            ns[wave] = n;
+        }
+        __syncthreads();
+        const size_t rec = (size_t)blockIdx.x + b;
+        for (int e = tid; e < E; e += 512) {
             float s = 0.0f;
 #pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                ex[i] = sigmoid(l[i]);
-                s += ex[i];
+            for (int w = 0; w < 8; ++w) s += sums[w][e];
+            ws.p[rec * E + e] = s;
+            ws.count[rec * E + e] = count[e];
+        }
+        if (tid == 0) {
+            float zt = 0.0f;
+            int nt = 0;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) {
+                zt += zs[w];
+                nt += ns[w];
             }
-            sum = wave_sum(s);
+            ws.z[rec] = zt;
+            ws.n[rec] = nt;
         }
-        const float inv = sum > 0.0f ? 1.0f / sum : sum;
-#pragma unroll
-        for (int i = 0; i < NI; ++i) acc[i] += ex[i] * inv;
-        for (int j = lane; j < k; j += 64) {
-            const int e = a.topk_idx[(size_t)t * k + j];
-            if (e >= 0 && e < E) atomicAdd(&count[e], 1);
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < NI; ++i) sums[wave][i * 64 + lane] = acc[i];
-    if (lane == 0) {
-        zs[wave] = z;
-        ns[wave] = n;
-    }
-    __syncthreads();
-    for (int e = tid; e < E; e += 256) {
-        ws.p[(size_t)blockIdx.x * E + e] = (sums[0][e] + sums[1][e]) + (sums[2][e] + sums[3][e]);
-        ws.count[(size_t)blockIdx.x * E + e] = count[e];
-    }
-    if (tid == 0) {
-        ws.z[blockIdx.x] = (zs[0] + zs[1]) + (zs[2] + zs[3]);
-        ws.n[blockIdx.x] = ns[0] + ns[1] + ns[2] + ns[3];
+        __syncthreads();
+        p = end;
     }
 }
 
-// One sequence per workgroup: its parts added up in order.
-__global__ void __launch_bounds__(256)
-moe_balance_sequence(mega_moe_balance_loss_args a, BalanceWs ws, int S) {
-    __shared__ float part[16][1];
-    const int b = blockIdx.x, tid = threadIdx.x, E = a.num_experts;
-    int n = 0;
-    float z = 0.0f;
-    for (int s = 0; s < S; ++s) {
-        n += ws.n[(size_t)b * S + s];
-        z += ws.z[(size_t)b * S + s];
+// Workgroup (b, slice): GROUPS groups of 32 threads add up every GROUPS-th
+// record of sequence b for 32 experts, and meet in LDS.
+template <int GROUPS>
+__global__ void __launch_bounds__(GROUPS * SLICE)
+moe_balance_finish(mega_moe_balance_loss_args a, BalanceWs ws, int B) {
+    __shared__ float sp[GROUPS][SLICE];
+    __shared__ int sc[GROUPS][SLICE], n_part[16], live_part[16];
+    __shared__ float z_part[16][1], loss_part[16][2];
+    __shared__ bool last;
+    const int tid = threadIdx.x, x = tid & (SLICE - 1), g = tid / SLICE, wave = tid >> 6;
+    constexpr int WAVES = (GROUPS * SLICE + 63) / 64;
+    const int E = a.num_experts, slices = (E + SLICE - 1) / SLICE;
+    const int b = blockIdx.x / slices, slice = blockIdx.x - b * slices, e = slice * SLICE + x;
+    int lo, hi;
+    sequence_span(a, b, lo, hi);
+    const size_t first = (size_t)(lo / CHUNK) + b;
+    const int records = hi > lo ? (hi - 1) / CHUNK - lo / CHUNK + 1 : 0;
+    float p = 0.0f, z[1] = {0.0f};
+    int c = 0, n = 0;
+    if (e < E) {
+#pragma unroll 8
+        for (int r = g; r < records; r += GROUPS) {
+            p += ws.p[(first + r) * E + e];
+            c += ws.count[(first + r) * E + e];
+        }
     }
+    for (int r = tid; r < records; r += GROUPS * SLICE) {
+        n += ws.n[first + r];
+        z[0] += ws.z[first + r];
+    }
+    sp[g][x] = p;
+    sc[g][x] = c;
+    n = (int)over_lanes<64>((uint32_t)n, [](uint32_t u, uint32_t v) { return u + v; });
+    if ((tid & 63) == 0) n_part[wave] = n;
+    block_sum(z, z_part);
+    __syncthreads();
+    n = 0;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) n += n_part[w];
     const float inv = n > 0 ? 1.0f / (float)n : 0.0f;
-    float dot[1] = {0.0f};
-    for (int e = tid; e < E; e += 256) {
-        float p = 0.0f;
-        int c = 0;
-        for (int s = 0; s < S; ++s) {
-            p += ws.p[((size_t)b * S + s) * E + e];
-            c += ws.count[((size_t)b * S + s) * E + e];
+    if (tid < 64) {
+        float dot = 0.0f;
+        if (tid < SLICE && e < E) {
+            p = 0.0f;
+            c = 0;
+#pragma unroll
+            for (int q = 0; q < GROUPS; ++q) {
+                p += sp[q][x];
+                c += sc[q][x];
+            }
+            p *= inv;
+            a.counts[(size_t)b * E + e] = c;
+            if (a.probs) a.probs[(size_t)b * E + e] = p;
+            dot = (float)c * p;
         }
-        p *= inv;
-        a.counts[(size_t)b * E + e] = c;
-        if (a.probs) a.probs[(size_t)b * E + e] = p;
-        dot[0] += (float)c * p;
+        dot = wave_sum(dot);
+        if (tid == 0) {
+            // read by the last workgroup, from another die perhaps: past its L2
+            __hip_atomic_store(ws.seq_loss + (size_t)b * slices + slice, dot * ((float)E / (float)a.num_topk) * inv,
+                               __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            if (slice == 0) {
+                __hip_atomic_store(ws.seq_z + b, z[0], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                __hip_atomic_store(a.tokens + b, n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            }
+            last = __hip_atomic_fetch_add(ws.done, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
+        }
     }
-    block_sum(dot, part);
-    if (tid == 0) {
-        ws.seq_loss[b] = dot[0] * ((float)E / (float)a.num_topk) * inv;
-        ws.seq_z[b] = z;
-        a.tokens[b] = n;
-    }
-}
-
-// The losses of all sequences.
-__global__ void __launch_bounds__(256)
-moe_balance_total(mega_moe_balance_loss_args a, BalanceWs ws, int B) {
-    __shared__ float part[16][2];
-    __shared__ int n_all, live_all;
-    if (threadIdx.x == 0) n_all = live_all = 0;
     __syncthreads();
+    if (!last) return;
     float v[2] = {0.0f, 0.0f};
-    int n = 0, live = 0;
-    for (int b = threadIdx.x; b < B; b += 256) {
-        v[0] += ws.seq_loss[b];
-        v[1] += ws.seq_z[b];
-        n += a.tokens[b];
-        live += a.tokens[b] > 0;
+    int all = 0, live = 0;
+    for (int64_t i = tid; i < (int64_t)B * slices; i += GROUPS * SLICE)
+        v[0] += __hip_atomic_load(ws.seq_loss + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    for (int i = tid; i < B; i += GROUPS * SLICE) {
+        v[1] += __hip_atomic_load(ws.seq_z + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        const int m = __hip_atomic_load(a.tokens + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        all += m;
+        live += m > 0;
     }
-    atomicAdd(&n_all, n);
-    atomicAdd(&live_all, live);
-    block_sum(v, part);
-    if (threadIdx.x == 0) {
-        a.loss[0] = live_all ? a.balance_coeff * v[0] / (float)live_all : 0.0f;
-        a.loss[1] = n_all ? a.z_coeff * v[1] / (float)n_all : 0.0f;
-        a.tokens[B] = n_all;
-        a.tokens[B + 1] = live_all;
+    const auto add = [](uint32_t u, uint32_t w) { return u + w; };
+    all = (int)over_lanes<64>((uint32_t)all, add);
+    live = (int)over_lanes<64>((uint32_t)live, add);
+    if ((tid & 63) == 0) {
+        n_part[wave] = all;
+        live_part[wave] = live;
+    }
+    block_sum(v, loss_part);
+    __syncthreads();
+    if (tid == 0) {
+        all = live = 0;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) {
+            all += n_part[w];
+            live += live_part[w];
+        }
+        a.loss[0] = live ? a.balance_coeff * v[0] / (float)live : 0.0f;
+        a.loss[1] = all ? a.z_coeff * v[1] / (float)all : 0.0f;
+        a.tokens[B] = all;
+        a.tokens[B + 1] = live;
     }
 }
 
 namespace {
 int sequences(const mega_moe_balance_loss_args& a) { return a.cu_seqlens ? a.num_sequences : 1; }
-// Parts per sequence: the host knows the sequences' average length only.
-int parts(const mega_moe_balance_loss_args& a) {
-    const int64_t B = sequences(a);
-    const int64_t per = ((int64_t)a.num_tokens + B - 1) / B;
-    const int64_t s = (per + BALANCE_ROWS - 1) / BALANCE_ROWS;
-    return (int)(s < 1 ? 1 : s > 256 ? 256 : s);
-}
 }  // namespace
 
 int64_t balance_loss_workspace(const mega_moe_balance_loss_args& a) {
     BalanceWs w;
-    return (int64_t)balance_layout(sequences(a), parts(a), a.num_experts, nullptr, w);
+    return (int64_t)balance_layout(a.num_tokens, sequences(a), a.num_experts, nullptr, w);
 }
 
 void launch_balance_loss(const mega_moe_balance_loss_args& a, hipStream_t stream) {
-    const int B = sequences(a), S = parts(a), E = a.num_experts;
+    const int B = sequences(a), E = a.num_experts;
     BalanceWs w;
-    balance_layout(B, S, E, static_cast<char*>(a.workspace), w);
-    const dim3 grid((unsigned)(B * S)), block(256);
-    if (E <= 64) hipLaunchKernelGGL((moe_balance_part<1>), grid, block, 0, stream, a, w, S);
-    else if (E <= 128) hipLaunchKernelGGL((moe_balance_part<2>), grid, block, 0, stream, a, w, S);
-    else if (E <= 256) hipLaunchKernelGGL((moe_balance_part<4>), grid, block, 0, stream, a, w, S);
-    else if (E <= 512) hipLaunchKernelGGL((moe_balance_part<8>), grid, block, 0, stream, a, w, S);
-    else hipLaunchKernelGGL((moe_balance_part<16>), grid, block, 0, stream, a, w, S);
-    hipLaunchKernelGGL(moe_balance_sequence, dim3((unsigned)B), block, 0, stream, a, w, S);
-    hipLaunchKernelGGL(moe_balance_total, dim3(1), block, 0, stream, a, w, B);
+    balance_layout(a.num_tokens, B, E, static_cast<char*>(a.workspace), w);
+    const int64_t chunks = balance_chunks(a.num_tokens);
+    const dim3 grid((unsigned)(chunks > 0 ? chunks : 1)), block(512);
+    if (E <= 16) hipLaunchKernelGGL((moe_balance_part<16, 1>), grid, block, 0, stream, a, w, B);
+    else if (E <= 32) hipLaunchKernelGGL((moe_balance_part<16, 2>), grid, block, 0, stream, a, w, B);
+    else if (E <= 64) hipLaunchKernelGGL((moe_balance_part<16, 4>), grid, block, 0, stream, a, w, B);
+    else if (E <= 128) hipLaunchKernelGGL((moe_balance_part<32, 4>), grid, block, 0, stream, a, w, B);
+    else if (E <= 256) hipLaunchKernelGGL((moe_balance_part<32, 8>), grid, block, 0, stream, a, w, B);
+    else if (E <= 512) hipLaunchKernelGGL((moe_balance_part<64, 8>), grid, block, 0, stream, a, w, B);
+    else hipLaunchKernelGGL((moe_balance_part<64, 16>), grid, block, 0, stream, a, w, B);
+    const dim3 finish((unsigned)(B * ((E + SLICE - 1) / SLICE)));
+    if (chunks / B >= 16) hipLaunchKernelGGL((moe_balance_finish<32>), finish, dim3(1024), 0, stream, a, w, B);
+    else hipLaunchKernelGGL((moe_balance_finish<8>), finish, dim3(256), 0, stream, a, w, B);
 }
 
 }  // namespace mega_moe

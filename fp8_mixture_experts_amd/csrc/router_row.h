@@ -56,4 +56,27 @@ __device__ __forceinline__ void sigmoid_slope(float x, float& s, float& slope) {
     slope = e * d * d;
 }
 
+// The sequence of token t: the last b with cu[b] <= t, if t < cu[b + 1]; -1 if
+// there is none.  Empty sequences are passed over.
+template <int LANES>
+__device__ __forceinline__ int sequence_of(const int32_t* cu, int B, int64_t t) {
+    if (!cu) return 0;
+    const int lane = threadIdx.x & (LANES - 1);
+    if (B <= 2 * LANES) {
+        // how many sequences end at t or before: loads that do not wait for each other
+        int n = 0;
+        for (int b = lane; b < B; b += LANES) n += cu[b + 1] <= t;
+        n = (int)over_lanes<LANES>((uint32_t)n, [](uint32_t x, uint32_t y) { return x + y; });
+        return t < cu[0] || n >= B ? -1 : n;
+    }
+    int lo = 0, hi = B;                      // cu[lo] <= t < cu[hi], if any
+    if (t < cu[0] || t >= cu[B]) return -1;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (cu[mid] <= t) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
 }  // namespace mega_moe
