@@ -64,20 +64,41 @@ __device__ __forceinline__ void sequence_span(const mega_moe_balance_loss_args& 
     }
 }
 
-// A token's experts lie in LANES lanes; the 512 / LANES groups of lanes take
-// the tokens in turn, each lane keeping the sums of its experts.
+// A token's experts lie in LANES lanes; the groups of lanes take the tokens in
+// turn, each lane keeping the sums of its experts.  The whole
+// chunk is loaded before the sequences are looked up, so that the two chains
+// of loads run side by side.
+constexpr int part_threads(int lanes) { return lanes == 32 ? 1024 : 512; }
+
 template <int LANES, int NI>
-__global__ void __launch_bounds__(512)
+__global__ void __launch_bounds__(part_threads(LANES))
 moe_balance_part(mega_moe_balance_loss_args a, BalanceWs ws, int B) {
-    constexpr int GROUPS = 512 / LANES;
+    constexpr int THREADS = part_threads(LANES), WAVES = THREADS / 64, GROUPS = THREADS / LANES;
     __shared__ int count[LANES * NI];
-    __shared__ float sums[8][LANES * NI];
-    __shared__ float zs[8];
-    __shared__ int ns[8];
+    __shared__ float sums[WAVES][LANES * NI];
+    __shared__ float zs[WAVES];
+    __shared__ int ns[WAVES];
     const int tid = threadIdx.x, lane = tid & (LANES - 1), group = tid / LANES, wave = tid >> 6;
     const int E = a.num_experts, k = a.num_topk;
     const int c0 = blockIdx.x * CHUNK, c1 = min(c0 + CHUNK, a.num_tokens);
     if (blockIdx.x == 0 && tid == 0) *ws.done = 0;
+    constexpr int ROWS = CHUNK / GROUPS;         // tokens per group
+    const bool sigmoids = a.score == MEGA_MOE_SCORE_SIGMOID;
+    float l[ROWS][NI];
+    int slot[ROWS];
+    bool live[ROWS];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+        const int t = c0 + r * GROUPS + group;
+        live[r] = t < c1 && (!a.token_mask || a.token_mask[t] != 0);
+        slot[r] = t < c1 && lane < k ? a.topk_idx[(size_t)t * k + lane] : -1;
+        if (t < c1) {
+            load_row<NI, LANES>(a.logits, a.logits_type, (size_t)t * a.logits_stride, E, l[r]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < NI; ++i) l[r][i] = 0.0f;
+        }
+    }
     int p = c0;
     while (p < c1) {
         const int b = sequence_of<64>(a.cu_seqlens, B, p);
@@ -91,38 +112,39 @@ moe_balance_part(mega_moe_balance_loss_args a, BalanceWs ws, int B) {
         sequence_span(a, b, lo, hi);
         if (hi <= p) break;                      // cu_seqlens decreases
         const int end = min(hi, c1);
-        for (int e = tid; e < LANES * NI; e += 512) count[e] = 0;
+        for (int e = tid; e < LANES * NI; e += THREADS) count[e] = 0;
         __syncthreads();
         float acc[NI], z = 0.0f;
         int n = 0;
 #pragma unroll
         for (int i = 0; i < NI; ++i) acc[i] = 0.0f;
-        for (int t = p + group; t < end; t += GROUPS) {
-            const bool live = !a.token_mask || a.token_mask[t] != 0;
-            int e0 = lane < k ? a.topk_idx[(size_t)t * k + lane] : -1;
-            float l[NI], ex[NI], top, sum;
-            load_row<NI, LANES>(a.logits, a.logits_type, (size_t)t * a.logits_stride, E, l);
-            if (!live) continue;
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+            const int t = c0 + r * GROUPS + group;
+            if (!live[r] || t < p || t >= end) continue;
             ++n;
-            row_exp<LANES>(l, ex, top, sum);
-            const float lse = row_lse(top, sum);
-            z += lse * lse;
-            if (a.score == MEGA_MOE_SCORE_SIGMOID) {
-                float s = 0.0f;
+            float ex[NI], top, sum = 0.0f;
+            if (!sigmoids || a.z_coeff != 0.0f) {
+                row_exp<LANES>(l[r], ex, top, sum);
+                const float lse = row_lse(top, sum);
+                z += lse * lse;
+            }
+            if (sigmoids) {
+                sum = 0.0f;
 #pragma unroll
                 for (int i = 0; i < NI; ++i) {
-                    ex[i] = sigmoid(l[i]);
-                    s += ex[i];
+                    ex[i] = sigmoid(l[r][i]);
+                    sum += ex[i];
                 }
-                sum = lanes_sum<LANES>(s);
+                sum = lanes_sum<LANES>(sum);
             }
             const float inv = sum > 0.0f ? 1.0f / sum : sum;
 #pragma unroll
             for (int i = 0; i < NI; ++i) acc[i] += ex[i] * inv;
-            if (e0 >= 0 && e0 < E) atomicAdd(&count[e0], 1);
+            if (slot[r] >= 0 && slot[r] < E) atomicAdd(&count[slot[r]], 1);
             for (int j = lane + LANES; j < k; j += LANES) {
-                e0 = a.topk_idx[(size_t)t * k + j];
-                if (e0 >= 0 && e0 < E) atomicAdd(&count[e0], 1);
+                const int e = a.topk_idx[(size_t)t * k + j];
+                if (e >= 0 && e < E) atomicAdd(&count[e], 1);
             }
         }
         // the wave's groups of lanes, then the waves, in order
@@ -140,10 +162,10 @@ moe_balance_part(mega_moe_balance_loss_args a, BalanceWs ws, int B) {
         }
         __syncthreads();
         const size_t rec = (size_t)blockIdx.x + b;
-        for (int e = tid; e < E; e += 512) {
+        for (int e = tid; e < E; e += THREADS) {
             float s = 0.0f;
 #pragma unroll
-            for (int w = 0; w < 8; ++w) s += sums[w][e];
+            for (int w = 0; w < WAVES; ++w) s += sums[w][e];
             ws.p[rec * E + e] = s;
             ws.count[rec * E + e] = count[e];
         }
@@ -151,7 +173,7 @@ moe_balance_part(mega_moe_balance_loss_args a, BalanceWs ws, int B) {
             float zt = 0.0f;
             int nt = 0;
 #pragma unroll
-            for (int w = 0; w < 8; ++w) {
+            for (int w = 0; w < WAVES; ++w) {
                 zt += zs[w];
                 nt += ns[w];
             }
@@ -219,7 +241,14 @@ moe_balance_finish(mega_moe_balance_loss_args a, BalanceWs ws, int B) {
             dot = (float)c * p;
         }
         dot = wave_sum(dot);
-        if (tid == 0) {
+        if (tid == 0 && gridDim.x == 1) {
+            // nothing to wait for
+            a.loss[0] = n > 0 ? a.balance_coeff * (dot * ((float)E / (float)a.num_topk) * inv) : 0.0f;
+            a.loss[1] = n > 0 ? a.z_coeff * z[0] / (float)n : 0.0f;
+            a.tokens[0] = a.tokens[1] = n;
+            a.tokens[2] = n > 0;
+            last = false;
+        } else if (tid == 0) {
             // read by the last workgroup, from another die perhaps: past its L2
             __hip_atomic_store(ws.seq_loss + (size_t)b * slices + slice, dot * ((float)E / (float)a.num_topk) * inv,
                                __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -279,14 +308,19 @@ void launch_balance_loss(const mega_moe_balance_loss_args& a, hipStream_t stream
     BalanceWs w;
     balance_layout(a.num_tokens, B, E, static_cast<char*>(a.workspace), w);
     const int64_t chunks = balance_chunks(a.num_tokens);
-    const dim3 grid((unsigned)(chunks > 0 ? chunks : 1)), block(512);
-    if (E <= 16) hipLaunchKernelGGL((moe_balance_part<16, 1>), grid, block, 0, stream, a, w, B);
-    else if (E <= 32) hipLaunchKernelGGL((moe_balance_part<16, 2>), grid, block, 0, stream, a, w, B);
-    else if (E <= 64) hipLaunchKernelGGL((moe_balance_part<16, 4>), grid, block, 0, stream, a, w, B);
-    else if (E <= 128) hipLaunchKernelGGL((moe_balance_part<32, 4>), grid, block, 0, stream, a, w, B);
-    else if (E <= 256) hipLaunchKernelGGL((moe_balance_part<32, 8>), grid, block, 0, stream, a, w, B);
-    else if (E <= 512) hipLaunchKernelGGL((moe_balance_part<64, 8>), grid, block, 0, stream, a, w, B);
-    else hipLaunchKernelGGL((moe_balance_part<64, 16>), grid, block, 0, stream, a, w, B);
+    const dim3 grid((unsigned)(chunks > 0 ? chunks : 1));
+    const auto part = [&](auto lanes, auto ni) {
+        constexpr int L = decltype(lanes)::value, NI = decltype(ni)::value;
+        hipLaunchKernelGGL((moe_balance_part<L, NI>), grid, dim3(part_threads(L)), 0, stream, a, w, B);
+    };
+    using std::integral_constant;
+    if (E <= 16) part(integral_constant<int, 16>{}, integral_constant<int, 1>{});
+    else if (E <= 32) part(integral_constant<int, 16>{}, integral_constant<int, 2>{});
+    else if (E <= 64) part(integral_constant<int, 16>{}, integral_constant<int, 4>{});
+    else if (E <= 128) part(integral_constant<int, 32>{}, integral_constant<int, 4>{});
+    else if (E <= 256) part(integral_constant<int, 32>{}, integral_constant<int, 8>{});
+    else if (E <= 512) part(integral_constant<int, 64>{}, integral_constant<int, 8>{});
+    else part(integral_constant<int, 64>{}, integral_constant<int, 16>{});
     const dim3 finish((unsigned)(B * ((E + SLICE - 1) / SLICE)));
     if (chunks / B >= 16) hipLaunchKernelGGL((moe_balance_finish<32>), finish, dim3(1024), 0, stream, a, w, B);
     else hipLaunchKernelGGL((moe_balance_finish<8>), finish, dim3(256), 0, stream, a, w, B);

@@ -46,12 +46,14 @@ __device__ __forceinline__ void row_exp(const float (&l)[NI], float (&ex)[NI], f
 // any expert adds nothing to a loss.
 __device__ __forceinline__ float row_lse(float top, float sum) { return sum == 0.0f ? 0.0f : logf(sum) + top; }
 
-__device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
+// The hardware reciprocal is within one step of the quotient, and its argument
+// is at least 1.
+__device__ __forceinline__ float sigmoid(float x) { return __builtin_amdgcn_rcpf(1.0f + expf(-x)); }
 
 // sigmoid(x) and its derivative, from exp(-|x|): s (1 - s) would cancel where s
 // is near 1.
 __device__ __forceinline__ void sigmoid_slope(float x, float& s, float& slope) {
-    const float e = expf(-fabsf(x)), d = 1.0f / (1.0f + e);
+    const float e = expf(-fabsf(x)), d = __builtin_amdgcn_rcpf(1.0f + e);
     s = x >= 0.0f ? d : e * d;
     slope = e * d * d;
 }
