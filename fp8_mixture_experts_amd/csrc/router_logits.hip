@@ -30,53 +30,71 @@ __device__ __forceinline__ void split_bf16(const float (&v)[8], u32x4_t (&p)[3])
     }
 }
 
-// A tile of 16 tokens x 16 experts per workgroup; its four waves take the K
-// steps of 32 in turn and their sums meet in LDS.
+// Small batches.  A tile of up to 16 tokens x 16 experts per workgroup; its 16
+// waves take the K steps of 32 in turn, straight from memory, and their sums
+// meet in LDS.  What bounds it is how fast one compute unit takes in its rows
+// (about 40 GB/s, whatever the others do), so the tile is the one that leaves
+// the fewest bytes to each (small_tile below) and fills the rest of the matrix
+// instruction with zeros, and each wave has the loads of STEPS steps in flight
+// (H = 7168: its 14 steps in two rounds).  128 x 7168 x 32: 14 us with whole
+// tiles on 16 compute units, 6.5 us with 4 x 4 on 256.
 template <bool WF32>
-__global__ void __launch_bounds__(256)
-moe_router_logits(mega_moe_router_logits_args a) {
-    __shared__ float part[4][16][17];
+__global__ void __launch_bounds__(1024)
+moe_router_logits(mega_moe_router_logits_args a, int tile_t, int tile_e) {
+    constexpr int STEPS = 7;
+    __shared__ float part[16][16][17];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int r = lane & 15, kq = (lane >> 4) * 8;
-    const int e_tiles = (a.num_experts + 15) / 16;
-    const int e0 = (int)(blockIdx.x % e_tiles) * 16;
-    const int64_t t0 = (int64_t)(blockIdx.x / e_tiles) * 16;
-    const int e = e0 + r;
-    const int64_t t = t0 + r;
     const int H = a.hidden, E = a.num_experts;
+    const int e_tiles = (E + tile_e - 1) / tile_e;
+    const int e0 = (int)(blockIdx.x % e_tiles) * tile_e;
+    const int t0 = (int)(blockIdx.x / e_tiles) * tile_t;
+    const bool has_t = r < tile_t && t0 + r < a.num_tokens, has_e = r < tile_e && e0 + r < E;
+    const uint16_t* x = a.x + (int64_t)(t0 + r) * a.x_stride;
+    const size_t w_row = (size_t)(e0 + r) * H;
     f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int k0 = wave * 32; k0 < H; k0 += 128) {
-        const int k = k0 + kq;
-        u32x4_t xv = {0u, 0u, 0u, 0u};
-        if (t < a.num_tokens && k < H)
-            xv = *reinterpret_cast<const u32x4_t*>(a.x + t * a.x_stride + k);
-        const bf16x8_t xb = __builtin_bit_cast(bf16x8_t, xv);
-        if constexpr (WF32) {
-            float w[8];
+    for (int k0 = wave * 32; k0 < H; k0 += 512 * STEPS) {
+        u32x4_t xv[STEPS], wv[STEPS][WF32 ? 2 : 1];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = 0.0f;
-            if (e < E && k < H) load8<true>(a.w, (size_t)e * H + k, w);
-            u32x4_t p[3];
-            split_bf16<3>(w, p);
+        for (int s = 0; s < STEPS; ++s) {
+            const int k = k0 + s * 512 + kq;
+            const u32x4_t none = {0u, 0u, 0u, 0u};
+            xv[s] = none;
 #pragma unroll
-            for (int q = 2; q >= 0; --q)
-                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, p[q]), xb, acc, 0, 0, 0);
-        } else {
-            u32x4_t wv = {0u, 0u, 0u, 0u};
-            if (e < E && k < H)
-                wv = *reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(a.w) + (size_t)e * H + k);
-            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, wv), xb, acc, 0, 0, 0);
+            for (int i = 0; i < (WF32 ? 2 : 1); ++i) wv[s][i] = none;
+            if (has_t && k < H) xv[s] = *reinterpret_cast<const u32x4_t*>(x + k);
+            if (has_e && k < H) {
+#pragma unroll
+                for (int i = 0; i < (WF32 ? 2 : 1); ++i) wv[s][i] = raw8<WF32>(a.w, w_row + k)[i];
+            }
+        }
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+            const bf16x8_t xb = __builtin_bit_cast(bf16x8_t, xv[s]);
+            if constexpr (WF32) {
+                float w[8];
+                values8<true>(wv[s], w);
+                u32x4_t p[3];
+                split_bf16<3>(w, p);
+#pragma unroll
+                for (int q = 2; q >= 0; --q)
+                    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, p[q]), xb, acc, 0, 0, 0);
+            } else {
+                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, wv[s][0]), xb, acc, 0, 0, 0);
+            }
         }
     }
     // lane l holds experts 4 (l / 16) .. + 3 of token l % 16
 #pragma unroll
     for (int i = 0; i < 4; ++i) part[wave][r][(lane >> 4) * 4 + i] = acc[i];
     __syncthreads();
+    if (threadIdx.x >= 256) return;
     const int to = threadIdx.x >> 4, eo = threadIdx.x & 15;
-    const float s = (part[0][to][eo] + part[1][to][eo]) + (part[2][to][eo] + part[3][to][eo]);
-    const int64_t tt = t0 + to;
-    const int ee = e0 + eo;
-    if (tt < a.num_tokens && ee < E) a.logits[tt * a.logits_stride + ee] = s;
+    float s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) s += part[w][to][eo];
+    if (to < tile_t && eo < tile_e && t0 + to < a.num_tokens && e0 + eo < E)
+        a.logits[(int64_t)(t0 + to) * a.logits_stride + e0 + eo] = s;
 }
 
 // ---------------------------------------------------------------------------
@@ -376,6 +394,24 @@ Split split_for(int64_t tiles, int64_t K) {
 int columns(int64_t E) { return E <= 32 ? 32 : E <= 64 ? 64 : 128; }
 int64_t tiles(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// The tile of a small batch: the fewest rows, by their bytes, for one compute
+// unit of 256, in as many turns as the tiles take.
+struct SmallTile {
+    int t, e;
+};
+SmallTile small_tile(const mega_moe_router_logits_args& a) {
+    const int w_bytes = a.weight_type == MEGA_MOE_F32 ? 4 : 2;
+    SmallTile best{16, 16};
+    int64_t least = INT64_MAX;
+    for (int t = 16; t >= 1; t /= 2)
+        for (int e = 16; e >= 1; e /= 2) {
+            const int64_t turns = tiles(tiles(a.num_tokens, t) * tiles(a.num_experts, e), 256);
+            const int64_t bytes = turns * (t * 2 + e * w_bytes);
+            if (bytes < least) least = bytes, best = SmallTile{t, e};
+        }
+    return best;
+}
+
 Split forward_split(const mega_moe_router_logits_args& a) {
     return split_for(tiles(a.num_tokens, 128) * tiles(a.num_experts, columns(a.num_experts)), a.hidden);
 }
@@ -426,9 +462,10 @@ void launch_router_logits(const mega_moe_router_logits_args& a, hipStream_t stre
         }
         return;
     }
-    const dim3 grid((unsigned)((a.num_experts + 15) / 16) * (unsigned)((a.num_tokens + 15) / 16));
-    if (f) hipLaunchKernelGGL((moe_router_logits<true>), grid, dim3(256), 0, stream, a);
-    else hipLaunchKernelGGL((moe_router_logits<false>), grid, dim3(256), 0, stream, a);
+    const SmallTile s = small_tile(a);
+    const dim3 grid((unsigned)(tiles(a.num_tokens, s.t) * tiles(a.num_experts, s.e)));
+    if (f) hipLaunchKernelGGL((moe_router_logits<true>), grid, dim3(1024), 0, stream, a, s.t, s.e);
+    else hipLaunchKernelGGL((moe_router_logits<false>), grid, dim3(1024), 0, stream, a, s.t, s.e);
 }
 
 void launch_router_logits_backward(const mega_moe_router_logits_args& a, hipStream_t stream) {
