@@ -231,13 +231,16 @@ struct Result {
 };
 
 template <bool AF32, Lay AL, int PA, bool BF32, Lay BL, int PB, int BM, int BN, bool OUT_BF16>
-__global__ void __launch_bounds__(256, 2)
+__global__ void __launch_bounds__(256)
 moe_router_product(Operand A, Operand Bo, Result out, int64_t k_split, int splits) {
-    __shared__ u32x4_t lds[(PA * BM + PB * BN) * 8];
+    // BF16 results go out through LDS, as rows of floats
+    constexpr int PITCH = BN + 4;
+    constexpr int STAGE = (PA * BM + PB * BN) * 8, OUT = OUT_BF16 ? BM * PITCH / 4 : 0;
+    __shared__ u32x4_t lds[STAGE > OUT ? STAGE : OUT];
     u32x4_t* la = lds;
     u32x4_t* lb = lds + PA * BM * 8;
     // waves over the tile: 2 x 2 where it is wide, else all along M
-    constexpr int WN = BN >= 128 ? 2 : 1, WM = 4 / WN;
+    constexpr int WN = BN >= 128 || BM < 128 ? 2 : 1, WM = 4 / WN;
     constexpr int TM = BM / WM / 32, TN = BN / WN / 32;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int wm = wave / WN * (TM * 32), wn = wave % WN * (TN * 32);
@@ -303,31 +306,50 @@ moe_router_product(Operand A, Operand Bo, Result out, int64_t k_split, int split
     }
 
     // lane l holds row m = l % 32 and columns n = 8 g + 4 (l / 32) .. + 3, g < 4
+    if constexpr (OUT_BF16) {
+        float* rows = reinterpret_cast<float*>(lds);
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
-        const int64_t m = m0 + wm + i * 32 + (lane & 31);
-        if (m >= A.rows) continue;
+        for (int i = 0; i < TM; ++i)
 #pragma unroll
-        for (int j = 0; j < TN; ++j)
+            for (int j = 0; j < TN; ++j)
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const int64_t n = n0 + wn + j * 32 + g * 8 + (lane >> 5) * 4;
-                if (n >= Bo.rows) continue;
-                float v[4];
+                for (int g = 0; g < 4; ++g) {
+                    u32x4_t d;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) v[q] = acc[i][j][g * 4 + q];
-                if constexpr (OUT_BF16) {
-                    // the rows come in eights
-                    if (out.add) {
-                        const uint2 d = *reinterpret_cast<const uint2*>(out.add + m * out.add_stride + n);
-                        v[0] += __uint_as_float(d.x << 16);
-                        v[1] += __uint_as_float(d.x & 0xffff0000u);
-                        v[2] += __uint_as_float(d.y << 16);
-                        v[3] += __uint_as_float(d.y & 0xffff0000u);
-                    }
-                    *reinterpret_cast<uint2*>(out.bf16 + m * out.stride + n) =
-                        uint2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
-                } else {
+                    for (int q = 0; q < 4; ++q) d[q] = __float_as_uint(acc[i][j][g * 4 + q]);
+                    lds[((wm + i * 32 + (lane & 31)) * PITCH + wn + j * 32 + g * 8 + (lane >> 5) * 4) / 4] = d;
+                }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < BM * BN / 8 / 256; ++i) {
+            const int id = i * 256 + (int)threadIdx.x;
+            const int r = id / (BN / 8), c = id % (BN / 8) * 8;
+            const int64_t m = m0 + r, n = n0 + c;
+            if (m >= A.rows || n >= Bo.rows) continue;      // the rows come in eights
+            float v[8];
+            load8<true>(rows, (size_t)r * PITCH + c, v);
+            if (out.add) {
+                float d[8];
+                load8<false>(out.add, m * out.add_stride + n, d);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) v[q] += d[q];
+            }
+            store8<false>(out.bf16, m * out.stride + n, v);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+            const int64_t m = m0 + wm + i * 32 + (lane & 31);
+            if (m >= A.rows) continue;
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const int64_t n = n0 + wn + j * 32 + g * 8 + (lane >> 5) * 4;
+                    if (n >= Bo.rows) continue;
+                    float v[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) v[q] = acc[i][j][g * 4 + q];
                     float* o = out.f32 + (splits > 1 ? split * A.rows * Bo.rows + m * Bo.rows : m * out.stride) + n;
                     if (n + 4 <= Bo.rows) {
                         u32x4a_t d;
@@ -340,7 +362,7 @@ moe_router_product(Operand A, Operand Bo, Result out, int64_t k_split, int split
                             if (n + q < Bo.rows) o[q] = v[q];
                     }
                 }
-            }
+        }
     }
 }
 
@@ -416,7 +438,7 @@ Split forward_split(const mega_moe_router_logits_args& a) {
     return split_for(tiles(a.num_tokens, 128) * tiles(a.num_experts, columns(a.num_experts)), a.hidden);
 }
 Split dw_split(const mega_moe_router_logits_args& a) {
-    return split_for(tiles(a.num_experts, 64) * tiles(a.hidden, 128), a.num_tokens);
+    return split_for(tiles(a.num_experts, 64) * tiles(a.hidden, 64), a.num_tokens);
 }
 
 void launch_join(const mega_moe_router_logits_args& a, float* out, int64_t M, int64_t N, int64_t stride, int splits,
@@ -473,20 +495,20 @@ void launch_router_logits_backward(const mega_moe_router_logits_args& a, hipStre
     if (a.dx && T > 0) {
         const Operand D{a.dlogits, a.dlogits_stride, T, E}, W{a.w, H, H, E};
         const Result out{nullptr, a.dx_stride, a.dx, a.dx_add, a.dx_add_stride};
-        const dim3 grid((unsigned)(tiles(T, 128) * tiles(H, 128)));
+        const dim3 grid((unsigned)(tiles(T, 64) * tiles(H, 128)));
         if (a.weight_type == MEGA_MOE_F32)
-            hipLaunchKernelGGL((moe_router_product<true, Lay::k_major, 2, true, Lay::row_major, 2, 128, 128, true>), grid,
+            hipLaunchKernelGGL((moe_router_product<true, Lay::k_major, 2, true, Lay::row_major, 2, 64, 128, true>), grid,
                                dim3(256), 0, stream, D, W, out, (E + 63) / 64 * 64, 1);
         else
-            hipLaunchKernelGGL((moe_router_product<true, Lay::k_major, 2, false, Lay::row_major, 1, 128, 128, true>), grid,
+            hipLaunchKernelGGL((moe_router_product<true, Lay::k_major, 2, false, Lay::row_major, 1, 64, 128, true>), grid,
                                dim3(256), 0, stream, D, W, out, (E + 63) / 64 * 64, 1);
     }
     if (a.dw) {
         const Split s = dw_split(a);
         const Operand D{a.dlogits, a.dlogits_stride, E, T}, X{a.x, a.x_stride, H, T};
         const Result out{s.n > 1 ? static_cast<float*>(a.workspace) : a.dw, H, nullptr, nullptr, 0};
-        hipLaunchKernelGGL((moe_router_product<true, Lay::row_major, 3, false, Lay::row_major, 1, 64, 128, false>),
-                           dim3((unsigned)(tiles(E, 64) * tiles(H, 128) * s.n)), dim3(256), 0, stream, D, X, out, s.k, s.n);
+        hipLaunchKernelGGL((moe_router_product<true, Lay::row_major, 3, false, Lay::row_major, 1, 64, 64, false>),
+                           dim3((unsigned)(tiles(E, 64) * tiles(H, 64) * s.n)), dim3(256), 0, stream, D, X, out, s.k, s.n);
         if (s.n > 1) launch_join(a, a.dw, E, H, H, s.n, stream);
     }
 }
