@@ -20,6 +20,7 @@ namespace {
 
 constexpr int32_t MAX_HIDDEN = 8192;        // as the layer
 constexpr int32_t MAX_TOKENS = 1 << 21;     // one workgroup of up to 1024 threads per token
+constexpr int64_t MAX_X_STRIDE = 1 << 22;       // a tile's rows of x within 32-bit byte offsets
 constexpr int MAX_DEVICES = 64;
 
 int bad(const char* what) { return fail(MEGA_MOE_ERR_INVALID_ARG, "%s", what); }
@@ -218,6 +219,8 @@ int logits_strides(mega_moe_router_logits_args& a) {
     a.dx_stride = stride_of(a.dx_stride, a.hidden, 8);
     a.logits_stride = stride_of(a.logits_stride, a.num_experts, 1);
     a.dlogits_stride = stride_of(a.dlogits_stride, a.num_experts, 1);
+    if (a.x_stride > MAX_X_STRIDE)
+        return fail(MEGA_MOE_ERR_UNSUPPORTED, "built for x_stride <= %lld", (long long)MAX_X_STRIDE);
     if (a.x_stride < 0 || a.dx_add_stride < 0 || a.dx_stride < 0 || a.logits_stride < 0 || a.dlogits_stride < 0)
         return bad("a stride is shorter than its row, or not a multiple of 8");
     return MEGA_MOE_OK;

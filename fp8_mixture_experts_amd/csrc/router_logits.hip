@@ -9,24 +9,20 @@ namespace mega_moe {
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
-// Eight finite floats as the sum of P BF16 vectors.  Each term but the last is
-// the leading eight significant bits of what is left (cut off, so it never
-// overflows); with P = 3 the last holds the remaining eight bits, so the sum
-// is exact, with P = 2 it is rounded to nearest: off by 2^-16 of the value.
+// Eight floats as the sum of P BF16 vectors: each term is what is left, rounded
+// to nearest.  Two leave 2^-18 of the value, three nothing (24 bits).  Finite
+// values below BF16's largest; an infinity becomes NaN.
 template <int P>
-__device__ __forceinline__ void split_bf16(const float (&v)[8], u32x4_t (&p)[3]) {
+__device__ __forceinline__ void split_bf16(const float (&v)[8], u32x4_t (&p)[P]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        float r[2] = {v[2 * i], v[2 * i + 1]};
+        float r0 = v[2 * i], r1 = v[2 * i + 1];
 #pragma unroll
-        for (int q = 0; q + 1 < P; ++q) {
-            const uint32_t a = __float_as_uint(r[0]), b = __float_as_uint(r[1]);
-            p[q][i] = __builtin_amdgcn_perm(b, a, 0x07060302u);      // the upper halves
-            r[0] -= __uint_as_float(a & 0xffff0000u);
-            r[1] -= __uint_as_float(b & 0xffff0000u);
+        for (int q = 0; q < P; ++q) {
+            p[q][i] = bf16_pair(r0, r1);
+            r0 -= __uint_as_float(p[q][i] << 16);
+            r1 -= __uint_as_float(p[q][i] & 0xffff0000u);
         }
-        p[P - 1][i] = P == 3 ? __builtin_amdgcn_perm(__float_as_uint(r[1]), __float_as_uint(r[0]), 0x07060302u)
-                             : bf16_pair(r[0], r[1]);
     }
 }
 
@@ -100,129 +96,143 @@ moe_router_logits(mega_moe_router_logits_args a, int tile_t, int tile_e) {
 // ---------------------------------------------------------------------------
 // Tiles through LDS, for batches of tokens and for the gradients.
 // C[m, n] = sum over k of A[m, k] B[n, k] on 32 x 32 x 16 BF16 matrix
-// instructions.  A workgroup of four waves computes BM x BN; every
-// K step of 64 goes through registers into LDS, as one to three BF16 planes
-// per operand (a float32 operand is split there), and the planes' products add
-// into the same accumulators, the small ones first.
+// instructions, each operand as one to three BF16 planes whose products add
+// into the same accumulators, the small ones first.  float32 operands are
+// split into planes in the workspace by moe_router_split beforehand: a tile's
+// values are used by many workgroups, which would each split them again.
 //
-// LDS: a plane is [rows][64] BF16, 128 bytes a row in eight 16-byte chunks;
-// chunk c of row r lies at c ^ (r & 7), so that the 16-byte reads of eight
-// rows at one k spread over all banks.
+// A workgroup of four waves computes BM x BN.  Steps of 64 k go from memory
+// straight into LDS (16 bytes a lane, no registers), STAGES - 1 of them ahead
+// of the one that is multiplied.  An operand lies in memory, and in LDS, in
+// one of two ways:
+//   k_major    rows of k: a fragment's eight k are one 16-byte read
+//   row_major  k after k, each a row of m (or n): the LDS reads that turn
+//              4 x 16 values around give four k of a lane's row at a time
+// Lanes that point outside an operand read zeros.
+//
+// LDS holds 16-byte chunks in the order in which they are loaded; where a
+// chunk comes from is permuted within its row, so that the reads of a fragment
+// spread over all banks: chunk c of a k_major row r lies at c ^ (r & 7); of a
+// row_major row the pairs of chunks (16 columns, one turned read) are permuted
+// by the bits in which the eight rows of a read differ.
 // ---------------------------------------------------------------------------
 
-// How an operand lies in memory: K contiguous ([rows][K], a chunk of eight k
-// is one or two 16-byte loads) or rows contiguous ([K][rows], eight k of two
-// rows are eight loads that the registers turn around).
 enum class Lay { k_major, row_major };
 
 struct Operand {
-    const void* p;
-    int64_t stride;        // elements from one row (k_major) or k (row_major) to the next
-    int64_t rows, k;       // valid extents
+    const uint16_t* p;
+    int64_t plane;         // elements from one plane to the next
+    int64_t stride;        // elements from one row to the next, in memory
+    int64_t rows, k;       // extents: of m or n, and of k (rows in memory: of m or n
+                           // for k_major, of k for row_major)
 };
 
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4a_t __attribute__((ext_vector_type(4), aligned(4)));
-typedef uint32_t u32x2a_t __attribute__((ext_vector_type(2), aligned(4)));
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+#define LDS_PTR __attribute__((address_space(3)))
 
-// One operand's share of a K step in this thread's registers.
-template <bool F32, Lay L, int R>
-struct Staged {
-    // k_major: R / 32 chunks; row_major: R / 64 units of 8 k x 2 rows
-    static constexpr int N = L == Lay::k_major ? R / 32 : R / 64;
-    static constexpr int W = L == Lay::k_major ? (F32 ? 8 : 4) : (F32 ? 16 : 8);
-    uint32_t v[N][W];
+constexpr int STEP = 64;
+constexpr uint32_t OUTSIDE = 0x7fffff00u;      // beyond every buffer's bytes
 
-    __device__ __forceinline__ void load(const Operand& o, int64_t row0, int64_t k0, int64_t k_end) {
-        const int tid = threadIdx.x;
+// `bytes` bytes at `base`; both are the same for the whole wave.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* base, int64_t bytes) {
+    const uint64_t p = (uint64_t)(uintptr_t)base;
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)p);
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(p >> 32));
+    const int n = __builtin_amdgcn_readfirstlane((int)(bytes < 0 ? 0 : bytes));
+    return __builtin_amdgcn_make_buffer_rsrc((void*)(uintptr_t)((uint64_t)hi << 32 | lo), 0, n, 0x00020000);
+}
+
+// The pairs of chunks of a row_major row of R columns, permuted.
+template <int R>
+__device__ __forceinline__ int pair_swizzle(int row) {
+    return R >= 128 ? (row & 3) | (row >> 1 & 4) : (row >> 1 & 1) | (row >> 2 & 2);
+}
+
+// One operand's planes of a step: R rows of m (or n) by 64 k.
+template <Lay L, int P, int R>
+struct Tile {
+    static constexpr int CHUNKS = R * 8;                 // of a plane
+    static constexpr int LOADS = P * CHUNKS / 256;       // per lane and step
+    static constexpr int WIDTH = L == Lay::k_major ? 8 : R / 8;      // chunks of a row
+
+    // Byte offset of this lane's chunk of load i of a plane, from the tile's
+    // first element, or OUTSIDE where its columns are.
+    uint32_t at[CHUNKS / 256];
+
+    __device__ __forceinline__ void place(const Operand& o, int64_t row0) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int id = i * 256 + tid;
+        for (int i = 0; i < CHUNKS / 256; ++i) {
+            const int id = i * 256 + (int)threadIdx.x, r = id / WIDTH;
+            const int c = L == Lay::k_major ? (id % WIDTH) ^ (r & 7) : (id % WIDTH) ^ (pair_swizzle<R>(r) << 1);
+            const bool in = L == Lay::k_major ? row0 + r < o.rows : row0 + c * 8 < o.rows;
+            at[i] = in ? (uint32_t)((r * o.stride + c * 8) * 2) : OUTSIDE;
+        }
+    }
+
+    // Starts the loads of the step at k0; from k_end on, or the operand's own
+    // end, they bring zeros.
+    __device__ __forceinline__ void load(const Operand& o, int64_t row0, int64_t k0, int64_t k_end, u32x4_t* lds) const {
+        const int64_t left = (k_end < o.k ? k_end : o.k) - k0;
+        const int wave = threadIdx.x >> 6;
 #pragma unroll
-            for (int j = 0; j < W; ++j) v[i][j] = 0u;
-            if constexpr (L == Lay::k_major) {
-                const int64_t r = row0 + (id >> 3), k = k0 + (id & 7) * 8;
-                if (r >= o.rows || k >= k_end) continue;
-                if constexpr (F32) {
-                    const uint32_t* q = static_cast<const uint32_t*>(o.p) + r * o.stride + k;
-                    if (k + 8 <= k_end) {
-                        const u32x4a_t a = *reinterpret_cast<const u32x4a_t*>(q);
-                        const u32x4a_t b = *reinterpret_cast<const u32x4a_t*>(q + 4);
+        for (int p = 0; p < P; ++p) {
+            // rows past the last lie outside of the buffer; a k_major row's
+            // chunks past its last k must be pointed there
+            const int64_t n = L == Lay::k_major ? o.rows - row0 : left < STEP ? left : STEP;
+            const int64_t width = L == Lay::k_major ? left : o.rows - row0;
+            const auto buf = buffer_of(o.p + p * o.plane + (L == Lay::k_major ? row0 * o.stride + k0 : k0 * o.stride + row0),
+                                       left > 0 ? (((n < R ? n : R) - 1) * o.stride + width) * 2 : 0);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) v[i][j] = a[j], v[i][4 + j] = b[j];
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            if (k + j < k_end) v[i][j] = q[j];
-                    }
-                } else {
-                    // BF16 rows are whole chunks of eight
-                    const u32x4_t a = *reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(o.p) + r * o.stride + k);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) v[i][j] = a[j];
+            for (int i = 0; i < CHUNKS / 256; ++i) {
+                uint32_t off = at[i];
+                if (L == Lay::k_major && left < STEP) {
+                    const int id = i * 256 + (int)threadIdx.x;
+                    if (((id & 7) ^ (id >> 3 & 7)) * 8 >= left) off = OUTSIDE;
                 }
-            } else {
-                const int64_t r = row0 + (id % (R / 2)) * 2, k = k0 + (id / (R / 2)) * 8;
-                if (r >= o.rows) continue;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    if (k + j >= k_end) break;
-                    if constexpr (F32) {
-                        const uint32_t* q = static_cast<const uint32_t*>(o.p) + (k + j) * o.stride + r;
-                        if (r + 1 < o.rows) {
-                            const u32x2a_t a = *reinterpret_cast<const u32x2a_t*>(q);
-                            v[i][2 * j] = a[0];
-                            v[i][2 * j + 1] = a[1];
-                        } else {
-                            v[i][2 * j] = q[0];
-                        }
-                    } else {
-                        // the rows come in eights
-                        v[i][j] = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(o.p) + (k + j) * o.stride + r);
-                    }
-                }
+                u32x4_t* to = lds + p * CHUNKS + i * 256 + __builtin_amdgcn_readfirstlane(wave) * 64;
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (LDS_PTR void*)to, 16, (int)off, 0, 0, 0);
             }
         }
     }
 
-    // Writes the chunks as P planes (1: BF16 as it is).
-    template <int P>
-    __device__ __forceinline__ void store(u32x4_t* lds) const {
-        const int tid = threadIdx.x;
+    // The fragment of rows r0 .. r0 + 31 and k 16 kk .. + 15 of a plane: lane l
+    // holds row r0 + l % 32, k 8 (l / 32) .. + 7 of them.
+    __device__ __forceinline__ static bf16x8_t fragment(const u32x4_t* lds, int p, int r0, int kk) {
+        const int lane = threadIdx.x & 63;
+        if constexpr (L == Lay::k_major) {
+            const int r = r0 + (lane & 31), c = kk * 2 + (lane >> 5);
+            return __builtin_bit_cast(bf16x8_t, lds[p * CHUNKS + r * 8 + (c ^ (r & 7))]);
+        } else {
+            // 16 lanes turn a block of 4 k x 16 rows around: lane i of them
+            // brings rows 4 (i % 4) .. + 3 of k i / 4 and takes row i
+            const int i = lane & 15, col = r0 + (lane >> 4 & 1) * 16 + (i & 3) * 4;
+            s16x4_t v[2];
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int id = i * 256 + tid;
-#pragma unroll
-            for (int h = 0; h < (L == Lay::k_major ? 1 : 2); ++h) {
-                const int r = L == Lay::k_major ? id >> 3 : (id % (R / 2)) * 2 + h;
-                const int c = L == Lay::k_major ? id & 7 : id / (R / 2);
-                u32x4_t* at = lds + r * 8 + (c ^ (r & 7));
-                if constexpr (F32) {
-                    float x[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(L == Lay::k_major ? v[i][j] : v[i][2 * j + h]);
-                    u32x4_t p[3];
-                    split_bf16<P>(x, p);
-#pragma unroll
-                    for (int q = 0; q < P; ++q) at[q * R * 8] = p[q];
-                } else if constexpr (L == Lay::k_major) {
-                    *at = u32x4_t{v[i][0], v[i][1], v[i][2], v[i][3]};
-                } else {
-                    u32x4_t p;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        p[j] = h == 0 ? (v[i][2 * j] & 0xffffu) | (v[i][2 * j + 1] << 16)
-                                      : (v[i][2 * j] >> 16) | (v[i][2 * j + 1] & 0xffff0000u);
-                    *at = p;
-                }
+            for (int h = 0; h < 2; ++h) {
+                const int row = kk * 16 + (lane >> 5) * 8 + h * 4 + (i >> 2);
+                const u32x4_t* chunk = lds + p * CHUNKS + row * WIDTH + (col / 8 ^ (pair_swizzle<R>(row) << 1));
+                v[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_PTR s16x4_t*)chunk + (col >> 2 & 1));
             }
+            typedef short s16x8_t __attribute__((ext_vector_type(8)));
+            return __builtin_bit_cast(bf16x8_t, s16x8_t{v[0][0], v[0][1], v[0][2], v[0][3],
+                                                        v[1][0], v[1][1], v[1][2], v[1][3]});
         }
     }
 };
 
+// Waits until this wave has at most N loads in flight, then for the others.
+template <int N>
+__device__ __forceinline__ void arrived() {
+    static_assert(N < 64, "the counter's range");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
 // Where a product goes: float32 rows (the result, or one split's part of it in
 // the workspace, [split][M][N]), or BF16 rows with something added.
 struct Result {
+    int64_t rows, cols;
     float* f32;
     int64_t stride;
     uint16_t* bf16;
@@ -230,16 +240,16 @@ struct Result {
     int64_t add_stride;
 };
 
-template <bool AF32, Lay AL, int PA, bool BF32, Lay BL, int PB, int BM, int BN, bool OUT_BF16>
+template <Lay LA, int PA, Lay LB, int PB, int BM, int BN, int STAGES, bool OUT_BF16>
 __global__ void __launch_bounds__(256)
 moe_router_product(Operand A, Operand Bo, Result out, int64_t k_split, int splits) {
+    using TA = Tile<LA, PA, BM>;
+    using TB = Tile<LB, PB, BN>;
     // BF16 results go out through LDS, as rows of floats
     constexpr int PITCH = BN + 4;
-    constexpr int STAGE = (PA * BM + PB * BN) * 8, OUT = OUT_BF16 ? BM * PITCH / 4 : 0;
-    __shared__ u32x4_t lds[STAGE > OUT ? STAGE : OUT];
-    u32x4_t* la = lds;
-    u32x4_t* lb = lds + PA * BM * 8;
-    // waves over the tile: 2 x 2 where it is wide, else all along M
+    constexpr int STAGE = PA * TA::CHUNKS + PB * TB::CHUNKS, OUT = OUT_BF16 ? BM * PITCH / 4 : 0;
+    __shared__ u32x4_t lds[STAGE * STAGES > OUT ? STAGE * STAGES : OUT];
+    // waves over the tile: 2 x 2, or all along M
     constexpr int WN = BN >= 128 || BM < 128 ? 2 : 1, WM = 4 / WN;
     constexpr int TM = BM / WM / 32, TN = BN / WN / 32;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -259,34 +269,43 @@ moe_router_product(Operand A, Operand Bo, Result out, int64_t k_split, int split
 #pragma unroll
             for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.0f;
 
-    Staged<AF32, AL, BM> sa;
-    Staged<BF32, BL, BN> sb;
-    if (k_first < k_end) {
-        sa.load(A, m0, k_first, k_end);
-        sb.load(Bo, n0, k_first, k_end);
-    }
-    for (int64_t k0 = k_first; k0 < k_end; k0 += 64) {
-        sa.template store<PA>(la);
-        sb.template store<PB>(lb);
-        __syncthreads();
-        if (k0 + 64 < k_end) {
-            sa.load(A, m0, k0 + 64, k_end);
-            sb.load(Bo, n0, k0 + 64, k_end);
-        }
+    TA ta;
+    TB tb;
+    ta.place(A, m0);
+    tb.place(Bo, n0);
+    const auto load = [&](int64_t k0, int stage) {
+        ta.load(A, m0, k0, k_end, lds + stage * STAGE);
+        tb.load(Bo, n0, k0, k_end, lds + stage * STAGE + PA * TA::CHUNKS);
+    };
+    constexpr int LOADS = TA::LOADS + TB::LOADS;
+    // steps past the last load nothing but zeros, so that the count of loads in
+    // flight is the same in every round
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-            const int c = kk * 2 + (lane >> 5), r = lane & 31;
+    for (int s = 0; s + 1 < STAGES; ++s) load(k_first + s * STEP, s);
+    int stage = 0;
+    for (int64_t k0 = k_first; k0 < k_end; k0 += STEP) {
+        if constexpr (STAGES == 1) {
+            load(k0, 0);
+            arrived<0>();
+        } else {
+            // this step is there, and every wave has left the one before it,
+            // whose place the newest load takes
+            arrived<(STAGES - 2) * LOADS>();
+            load(k0 + (STAGES - 1) * STEP, stage == 0 ? STAGES - 1 : stage - 1);
+        }
+        const u32x4_t* la = lds + stage * STAGE;
+        const u32x4_t* lb = la + PA * TA::CHUNKS;
+#pragma unroll
+        for (int kk = 0; kk < STEP / 16; ++kk) {
             bf16x8_t fa[PA][TM], fb[PB][TN];
 #pragma unroll
             for (int p = 0; p < PA; ++p)
 #pragma unroll
-                for (int i = 0; i < TM; ++i)
-                    fa[p][i] = __builtin_bit_cast(bf16x8_t, la[(p * BM + wm + i * 32 + r) * 8 + (c ^ (r & 7))]);
+                for (int i = 0; i < TM; ++i) fa[p][i] = TA::fragment(la, p, wm + i * 32, kk);
 #pragma unroll
             for (int p = 0; p < PB; ++p)
 #pragma unroll
-                for (int j = 0; j < TN; ++j)
-                    fb[p][j] = __builtin_bit_cast(bf16x8_t, lb[(p * BN + wn + j * 32 + r) * 8 + (c ^ (r & 7))]);
+                for (int j = 0; j < TN; ++j) fb[p][j] = TB::fragment(lb, p, wn + j * 32, kk);
             // the planes' products, the smallest first; beyond the last plane's
             // weight they are dropped
 #pragma unroll
@@ -302,9 +321,11 @@ moe_router_product(Operand A, Operand Bo, Result out, int64_t k_split, int split
                             acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[q][j], fa[p][i], acc[i][j], 0, 0, 0);
                 }
         }
-        __syncthreads();
+        if constexpr (STAGES == 1) __syncthreads();
+        else stage = stage + 1 == STAGES ? 0 : stage + 1;
     }
 
+    arrived<0>();        // nothing is on its way into LDS any more
     // lane l holds row m = l % 32 and columns n = 8 g + 4 (l / 32) .. + 3, g < 4
     if constexpr (OUT_BF16) {
         float* rows = reinterpret_cast<float*>(lds);
@@ -325,7 +346,7 @@ moe_router_product(Operand A, Operand Bo, Result out, int64_t k_split, int split
             const int id = i * 256 + (int)threadIdx.x;
             const int r = id / (BN / 8), c = id % (BN / 8) * 8;
             const int64_t m = m0 + r, n = n0 + c;
-            if (m >= A.rows || n >= Bo.rows) continue;      // the rows come in eights
+            if (m >= out.rows || n >= out.cols) continue;      // the rows come in eights
             float v[8];
             load8<true>(rows, (size_t)r * PITCH + c, v);
             if (out.add) {
@@ -340,18 +361,18 @@ moe_router_product(Operand A, Operand Bo, Result out, int64_t k_split, int split
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
             const int64_t m = m0 + wm + i * 32 + (lane & 31);
-            if (m >= A.rows) continue;
+            if (m >= out.rows) continue;
 #pragma unroll
             for (int j = 0; j < TN; ++j)
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
                     const int64_t n = n0 + wn + j * 32 + g * 8 + (lane >> 5) * 4;
-                    if (n >= Bo.rows) continue;
+                    if (n >= out.cols) continue;
                     float v[4];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) v[q] = acc[i][j][g * 4 + q];
-                    float* o = out.f32 + (splits > 1 ? split * A.rows * Bo.rows + m * Bo.rows : m * out.stride) + n;
-                    if (n + 4 <= Bo.rows) {
+                    float* o = out.f32 + (splits > 1 ? (split * out.rows + m) * out.cols : m * out.stride) + n;
+                    if (n + 4 <= out.cols) {
                         u32x4a_t d;
 #pragma unroll
                         for (int q = 0; q < 4; ++q) d[q] = __float_as_uint(v[q]);
@@ -359,10 +380,41 @@ moe_router_product(Operand A, Operand Bo, Result out, int64_t k_split, int split
                     } else {
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
-                            if (n + q < Bo.rows) o[q] = v[q];
+                            if (n + q < out.cols) o[q] = v[q];
                     }
                 }
         }
+    }
+}
+
+// float32 rows as P BF16 planes, [P][rows][width]; columns behind the last are 0.
+struct Planes {
+    const float* from;
+    int64_t stride, rows, cols;
+    uint16_t* to;
+    int64_t width;         // a multiple of 8
+    int planes;            // 2 or 3
+};
+
+__device__ __forceinline__ void split_row_part(const Planes& s, int64_t unit) {
+    const int64_t units = s.width / 8, r = unit / units, c = (unit - r * units) * 8;
+    const float* q = s.from + r * s.stride + c;
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = c + i < s.cols ? q[i] : 0.0f;
+    u32x4_t p[3];
+    split_bf16<3>(v, p);
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+        if (i < s.planes) *reinterpret_cast<u32x4_t*>(s.to + ((int64_t)i * s.rows + r) * s.width + c) = p[i];
+}
+
+__global__ void __launch_bounds__(256)
+moe_router_split(Planes s0, Planes s1) {
+    const int64_t n0 = s0.rows * (s0.width / 8), n = n0 + s1.rows * (s1.width / 8);
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        if (i < n0) split_row_part(s0, i);
+        else split_row_part(s1, i - n0);
     }
 }
 
@@ -413,7 +465,6 @@ Split split_for(int64_t tiles, int64_t K) {
     return Split{n, (steps + n - 1) / n * 64};
 }
 
-int columns(int64_t E) { return E <= 32 ? 32 : E <= 64 ? 64 : 128; }
 int64_t tiles(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // The tile of a small batch: the fewest rows, by their bytes, for one compute
@@ -434,39 +485,76 @@ SmallTile small_tile(const mega_moe_router_logits_args& a) {
     return best;
 }
 
-Split forward_split(const mega_moe_router_logits_args& a) {
-    return split_for(tiles(a.num_tokens, 128) * tiles(a.num_experts, columns(a.num_experts)), a.hidden);
-}
-Split dw_split(const mega_moe_router_logits_args& a) {
-    return split_for(tiles(a.num_experts, 64) * tiles(a.hidden, 64), a.num_tokens);
+int columns(int64_t E) { return E <= 32 ? 32 : E <= 64 ? 64 : 128; }
+
+// The workspace: the planes of what is split, then the parts of a split K.
+struct Plan {
+    Split split;
+    int64_t w_planes, d_planes, parts, total;   // byte offsets, and bytes in all
+};
+
+int64_t padded(int64_t E) { return (E + 63) / 64 * 64; }
+
+Plan forward_plan(const mega_moe_router_logits_args& a) {
+    const int64_t T = a.num_tokens, E = a.num_experts, H = a.hidden;
+    Plan p{};
+    if (T <= SMALL_TOKENS) return p;
+    p.split = split_for(tiles(T, 128) * tiles(E, columns(E)), H);
+    p.parts = a.weight_type == MEGA_MOE_F32 ? 3 * E * H * 2 : 0;
+    p.total = p.parts + (p.split.n > 1 ? p.split.n * T * E * 4 : 0);
+    return p;
 }
 
-void launch_join(const mega_moe_router_logits_args& a, float* out, int64_t M, int64_t N, int64_t stride, int splits,
-                 hipStream_t stream) {
+Plan backward_plan(const mega_moe_router_logits_args& a) {
+    const int64_t T = a.num_tokens, E = a.num_experts, H = a.hidden;
+    Plan p{};
+    p.split = split_for(tiles(E, 64) * tiles(H, 128), T);
+    p.d_planes = a.weight_type == MEGA_MOE_F32 ? 2 * E * H * 2 : 0;
+    p.parts = p.d_planes + 3 * T * padded(E) * 2;
+    p.total = p.parts + (p.split.n > 1 ? p.split.n * E * H * 4 : 0);
+    return p;
+}
+
+uint8_t* at(const mega_moe_router_logits_args& a, int64_t offset) { return static_cast<uint8_t*>(a.workspace) + offset; }
+
+void launch_split(const Planes& s0, const Planes& s1, hipStream_t stream) {
+    const int64_t blocks = tiles(s0.rows * (s0.width / 8) + s1.rows * (s1.width / 8), 256);
+    if (blocks > 0)
+        hipLaunchKernelGGL(moe_router_split, dim3((unsigned)(blocks > 65536 ? 65536 : blocks)), dim3(256), 0, stream, s0, s1);
+}
+
+void launch_join(const float* parts, float* out, int64_t M, int64_t N, int64_t stride, int splits, hipStream_t stream) {
     const int64_t blocks = tiles(M * N, 1024);
     hipLaunchKernelGGL(moe_router_product_join, dim3((unsigned)(blocks > 65536 ? 65536 : blocks)), dim3(256), 0, stream,
-                       static_cast<const float*>(a.workspace), out, M, N, stride, splits);
+                       parts, out, M, N, stride, splits);
 }
 
-template <bool WF32, int BN>
+template <int PW, int BN>
 void launch_logits(const mega_moe_router_logits_args& a, hipStream_t stream) {
-    const Split s = forward_split(a);
+    const Plan p = forward_plan(a);
     const int64_t T = a.num_tokens, H = a.hidden, E = a.num_experts;
-    const Operand A{a.x, a.x_stride, T, H}, W{a.w, H, E, H};
-    const Result out{s.n > 1 ? static_cast<float*>(a.workspace) : a.logits, a.logits_stride, nullptr, nullptr, 0};
-    hipLaunchKernelGGL((moe_router_product<false, Lay::k_major, 1, WF32, Lay::k_major, WF32 ? 3 : 1, 128, BN, false>),
-                       dim3((unsigned)(tiles(T, 128) * tiles(E, BN) * s.n)), dim3(256), 0, stream, A, W, out, s.k, s.n);
-    if (s.n > 1) launch_join(a, a.logits, T, E, a.logits_stride, s.n, stream);
+    const Operand A{a.x, 0, a.x_stride, T, H};
+    Operand W{static_cast<const uint16_t*>(a.w), 0, H, E, H};
+    if (PW == 3) {
+        launch_split(Planes{static_cast<const float*>(a.w), H, E, H, reinterpret_cast<uint16_t*>(at(a, p.w_planes)), H, 3},
+                     Planes{}, stream);
+        W.p = reinterpret_cast<uint16_t*>(at(a, p.w_planes));
+        W.plane = E * H;
+    }
+    float* parts = reinterpret_cast<float*>(at(a, p.parts));
+    const Result out{T, E, p.split.n > 1 ? parts : a.logits, a.logits_stride, nullptr, nullptr, 0};
+    constexpr int STAGES = PW == 3 ? 1 : 2;
+    hipLaunchKernelGGL((moe_router_product<Lay::k_major, 1, Lay::k_major, PW, 128, BN, STAGES, false>),
+                       dim3((unsigned)(tiles(T, 128) * tiles(E, BN) * p.split.n)), dim3(256), 0, stream, A, W, out, p.split.k,
+                       p.split.n);
+    if (p.split.n > 1) launch_join(parts, a.logits, T, E, a.logits_stride, p.split.n, stream);
 }
 
 }  // namespace
 
 int64_t router_logits_workspace(const mega_moe_router_logits_args& a) {
-    const int64_t T = a.num_tokens, E = a.num_experts, H = a.hidden;
-    const Split f = forward_split(a), d = dw_split(a);
-    const int64_t forward = T > SMALL_TOKENS && f.n > 1 ? f.n * T * E * 4 : 0;
-    const int64_t backward = d.n > 1 ? d.n * E * H * 4 : 0;
-    return forward > backward ? forward : backward;
+    const int64_t f = forward_plan(a).total, b = backward_plan(a).total;
+    return f > b ? f : b;
 }
 
 void launch_router_logits(const mega_moe_router_logits_args& a, hipStream_t stream) {
@@ -474,13 +562,13 @@ void launch_router_logits(const mega_moe_router_logits_args& a, hipStream_t stre
     if (a.num_tokens > SMALL_TOKENS) {
         const int bn = columns(a.num_experts);
         if (f) {
-            if (bn == 32) launch_logits<true, 32>(a, stream);
-            else if (bn == 64) launch_logits<true, 64>(a, stream);
-            else launch_logits<true, 128>(a, stream);
+            if (bn == 32) launch_logits<3, 32>(a, stream);
+            else if (bn == 64) launch_logits<3, 64>(a, stream);
+            else launch_logits<3, 128>(a, stream);
         } else {
-            if (bn == 32) launch_logits<false, 32>(a, stream);
-            else if (bn == 64) launch_logits<false, 64>(a, stream);
-            else launch_logits<false, 128>(a, stream);
+            if (bn == 32) launch_logits<1, 32>(a, stream);
+            else if (bn == 64) launch_logits<1, 64>(a, stream);
+            else launch_logits<1, 128>(a, stream);
         }
         return;
     }
@@ -491,25 +579,33 @@ void launch_router_logits(const mega_moe_router_logits_args& a, hipStream_t stre
 }
 
 void launch_router_logits_backward(const mega_moe_router_logits_args& a, hipStream_t stream) {
-    const int64_t T = a.num_tokens, H = a.hidden, E = a.num_experts;
+    const int64_t T = a.num_tokens, H = a.hidden, E = a.num_experts, Ep = padded(E);
+    const Plan p = backward_plan(a);
+    const bool f = a.weight_type == MEGA_MOE_F32;
+    uint16_t* dp = reinterpret_cast<uint16_t*>(at(a, p.d_planes));
+    uint16_t* wp = reinterpret_cast<uint16_t*>(at(a, p.w_planes));
+    launch_split(Planes{a.dlogits, a.dlogits_stride, T, E, dp, Ep, a.dw ? 3 : 2},
+                 a.dx && f ? Planes{static_cast<const float*>(a.w), H, E, H, wp, H, 2} : Planes{}, stream);
     if (a.dx && T > 0) {
-        const Operand D{a.dlogits, a.dlogits_stride, T, E}, W{a.w, H, H, E};
-        const Result out{nullptr, a.dx_stride, a.dx, a.dx_add, a.dx_add_stride};
+        const Operand D{dp, T * Ep, Ep, T, Ep};
+        const Operand W{f ? wp : static_cast<const uint16_t*>(a.w), E * H, H, H, E};
+        const Result out{T, H, nullptr, a.dx_stride, a.dx, a.dx_add, a.dx_add_stride};
         const dim3 grid((unsigned)(tiles(T, 64) * tiles(H, 128)));
-        if (a.weight_type == MEGA_MOE_F32)
-            hipLaunchKernelGGL((moe_router_product<true, Lay::k_major, 2, true, Lay::row_major, 2, 64, 128, true>), grid,
-                               dim3(256), 0, stream, D, W, out, (E + 63) / 64 * 64, 1);
+        if (f)
+            hipLaunchKernelGGL((moe_router_product<Lay::k_major, 2, Lay::row_major, 2, 64, 128, 1, true>), grid, dim3(256), 0,
+                               stream, D, W, out, Ep, 1);
         else
-            hipLaunchKernelGGL((moe_router_product<true, Lay::k_major, 2, false, Lay::row_major, 1, 64, 128, true>), grid,
-                               dim3(256), 0, stream, D, W, out, (E + 63) / 64 * 64, 1);
+            hipLaunchKernelGGL((moe_router_product<Lay::k_major, 2, Lay::row_major, 1, 64, 128, 1, true>), grid, dim3(256), 0,
+                               stream, D, W, out, Ep, 1);
     }
     if (a.dw) {
-        const Split s = dw_split(a);
-        const Operand D{a.dlogits, a.dlogits_stride, E, T}, X{a.x, a.x_stride, H, T};
-        const Result out{s.n > 1 ? static_cast<float*>(a.workspace) : a.dw, H, nullptr, nullptr, 0};
-        hipLaunchKernelGGL((moe_router_product<true, Lay::row_major, 3, false, Lay::row_major, 1, 64, 64, false>),
-                           dim3((unsigned)(tiles(E, 64) * tiles(H, 64) * s.n)), dim3(256), 0, stream, D, X, out, s.k, s.n);
-        if (s.n > 1) launch_join(a, a.dw, E, H, H, s.n, stream);
+        const Operand D{dp, T * Ep, Ep, Ep, T}, X{a.x, 0, a.x_stride, H, T};
+        float* parts = reinterpret_cast<float*>(at(a, p.parts));
+        const Result out{E, H, p.split.n > 1 ? parts : a.dw, H, nullptr, nullptr, 0};
+        hipLaunchKernelGGL((moe_router_product<Lay::row_major, 3, Lay::row_major, 1, 64, 128, 3, false>),
+                           dim3((unsigned)(tiles(E, 64) * tiles(H, 128) * p.split.n)), dim3(256), 0, stream, D, X, out,
+                           p.split.k, p.split.n);
+        if (p.split.n > 1) launch_join(parts, a.dw, E, H, H, p.split.n, stream);
     }
 }
 

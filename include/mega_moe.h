@@ -455,8 +455,8 @@ int64_t mega_moe_norm_workspace_bytes(const mega_moe_norm_backward_args* a);
  *   dx = dlogits . w (+ dx_add),   dw = dlogits^T . x.
  * The products run on the BF16 matrix cores.  A float32 operand is split into
  * BF16 terms: three where the result is float32 (the split is exact), two
- * where it is rounded to BF16 (dx).  x, dlogits and w must be finite (an
- * infinity may come out as NaN).
+ * where it is rounded to BF16 (dx).  x, dlogits and w must be finite and below
+ * BF16's largest value (an infinity may come out as NaN).
  */
 typedef struct mega_moe_router_logits_args {
     int32_t num_tokens;       /* T                                               */
@@ -473,7 +473,7 @@ typedef struct mega_moe_router_logits_args {
     float* dw;                /* [E, H] float, dense, or NULL; 0 with T = 0      */
     void* workspace;          /* may be NULL where the bytes needed are 0        */
     int64_t workspace_bytes;
-    int64_t x_stride, dx_add_stride, dx_stride;      /* >= H, of 8               */
+    int64_t x_stride, dx_add_stride, dx_stride;      /* >= H, of 8; x_stride up to 2^22 */
     int64_t logits_stride, dlogits_stride;           /* >= E                     */
 } mega_moe_router_logits_args;
 int mega_moe_router_logits(const mega_moe_router_logits_args* a, void* stream);

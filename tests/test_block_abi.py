@@ -158,6 +158,13 @@ def test_hidden_beyond_what_is_built_is_unsupported(name):
     assert ei.value.code == B.MEGA_MOE_ERR_UNSUPPORTED
 
 
+@pytest.mark.parametrize("name", ["mega_moe_router_logits", "mega_moe_router_logits_backward"])
+def test_rows_of_x_too_far_apart_are_unsupported(name):
+    with pytest.raises(B.MegaMoEError) as ei:
+        getattr(B, name)(_logits(x_stride=(1 << 22) + 8, num_tokens=1), None)
+    assert ei.value.code == B.MEGA_MOE_ERR_UNSUPPORTED
+
+
 @pytest.mark.parametrize("name", list(REFUSED))
 def test_call_without_a_block_is_refused_and_without_tokens_is_none(name):
     with pytest.raises(B.MegaMoEError) as ei:
