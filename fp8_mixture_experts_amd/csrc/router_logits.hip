@@ -1,6 +1,8 @@
 // The router's product, logits = x . w^T, and its gradients.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "block_util.h"
 #include "router_logits.h"
 
@@ -197,36 +199,101 @@ struct Tile {
         }
     }
 
-    // The fragment of rows r0 .. r0 + 31 and k 16 kk .. + 15 of a plane: lane l
-    // holds row r0 + l % 32, k 8 (l / 32) .. + 7 of them.
+    // The fragment of rows r0 .. r0 + 31 and k 16 kk .. + 15 of a plane of a
+    // k_major tile: lane l holds row r0 + l % 32, k 8 (l / 32) .. + 7 of them.
     __device__ __forceinline__ static bf16x8_t fragment(const u32x4_t* lds, int p, int r0, int kk) {
-        const int lane = threadIdx.x & 63;
-        if constexpr (L == Lay::k_major) {
-            const int r = r0 + (lane & 31), c = kk * 2 + (lane >> 5);
-            return __builtin_bit_cast(bf16x8_t, lds[p * CHUNKS + r * 8 + (c ^ (r & 7))]);
-        } else {
-            // 16 lanes turn a block of 4 k x 16 rows around: lane i of them
-            // brings rows 4 (i % 4) .. + 3 of k i / 4 and takes row i
-            const int i = lane & 15, col = r0 + (lane >> 4 & 1) * 16 + (i & 3) * 4;
-            s16x4_t v[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int row = kk * 16 + (lane >> 5) * 8 + h * 4 + (i >> 2);
-                const u32x4_t* chunk = lds + p * CHUNKS + row * WIDTH + (col / 8 ^ (pair_swizzle<R>(row) << 1));
-                v[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LDS_PTR s16x4_t*)chunk + (col >> 2 & 1));
-            }
-            typedef short s16x8_t __attribute__((ext_vector_type(8)));
-            return __builtin_bit_cast(bf16x8_t, s16x8_t{v[0][0], v[0][1], v[0][2], v[0][3],
-                                                        v[1][0], v[1][1], v[1][2], v[1][3]});
-        }
+        const int lane = threadIdx.x & 63, r = r0 + (lane & 31), c = kk * 2 + (lane >> 5);
+        return __builtin_bit_cast(bf16x8_t, lds[p * CHUNKS + r * 8 + (c ^ (r & 7))]);
     }
+
+    // Of a row_major tile: where this lane's part of it starts, as an LDS byte
+    // address, at kk = 0.  16 lanes turn a block of 4 k x 16 rows around: lane
+    // i of them brings rows 4 (i % 4) .. + 3 of k i / 4 and takes row i; a
+    // fragment is two such reads, of k 8 (l / 32) .. + 3 and of the next four.
+    __device__ __forceinline__ static uint32_t turned_at(const u32x4_t* lds, int r0) {
+        const int lane = threadIdx.x & 63, i = lane & 15, col = r0 + (lane >> 4 & 1) * 16 + (i & 3) * 4;
+        const int row = (lane >> 5) * 8 + (i >> 2);
+        const u32x4_t* chunk = lds + row * WIDTH + (col / 8 ^ (pair_swizzle<R>(row) << 1));
+        return (uint32_t)(uintptr_t)(LDS_PTR const void*)chunk + (col >> 2 & 1) * 8;
+    }
+    // Bytes on from there: to the next 16 k, the other four k, the next plane.
+    static constexpr int NEXT_KK = 16 * WIDTH * 16, NEXT_HALF = 4 * WIDTH * 16, NEXT_PLANE = CHUNKS * 16;
 };
+
+// The turned reads of one kk, with the wait for them: the compiler would wait
+// for the loads into LDS in flight before each.  N0 planes from at0, N1 from
+// at1 and from at2 (one tile's two fragments).
+typedef uint64_t Half;
+__device__ __forceinline__ bf16x8_t halves(Half a, Half b) {
+    struct Two { Half v[2]; };
+    return __builtin_bit_cast(bf16x8_t, Two{{a, b}});
+}
+
+#define TURN(dst, at, off) "ds_read_b64_tr_b16 %" dst ", %" at " offset:%" off "\n\t"
+
+// Fragments f1[j] of tile columns at1, at2: P = 1.
+template <int OFF, int HALF>
+__device__ __forceinline__ void turned(uint32_t at1, uint32_t at2, bf16x8_t (&f)[1][2]) {
+    Half a, b, c, d;
+    asm volatile(TURN("0", "4", "6") TURN("1", "4", "7") TURN("2", "5", "6") TURN("3", "5", "7")
+                 "s_waitcnt lgkmcnt(0)"
+                 : "=&v"(a), "=&v"(b), "=&v"(c), "=&v"(d)
+                 : "v"(at1), "v"(at2), "n"(OFF), "n"(OFF + HALF)
+                 : "memory");
+    f[0][0] = halves(a, b);
+    f[0][1] = halves(c, d);
+}
+
+// The same with two planes.
+template <int OFF, int HALF, int PLANE>
+__device__ __forceinline__ void turned(uint32_t at1, uint32_t at2, bf16x8_t (&f)[2][2]) {
+    Half a, b, c, d, e, g, h, i;
+    asm volatile(TURN("0", "8", "10") TURN("1", "8", "11") TURN("2", "9", "10") TURN("3", "9", "11")
+                 TURN("4", "8", "12") TURN("5", "8", "13") TURN("6", "9", "12") TURN("7", "9", "13")
+                 "s_waitcnt lgkmcnt(0)"
+                 : "=&v"(a), "=&v"(b), "=&v"(c), "=&v"(d), "=&v"(e), "=&v"(g), "=&v"(h), "=&v"(i)
+                 : "v"(at1), "v"(at2), "n"(OFF), "n"(OFF + HALF), "n"(OFF + PLANE), "n"(OFF + PLANE + HALF)
+                 : "memory");
+    f[0][0] = halves(a, b);
+    f[0][1] = halves(c, d);
+    f[1][0] = halves(e, g);
+    f[1][1] = halves(h, i);
+}
+
+// Three planes of one fragment of A, and one of two fragments of B.
+template <int AOFF, int AHALF, int APLANE, int BOFF, int BHALF>
+__device__ __forceinline__ void turned(uint32_t at0, bf16x8_t (&fa)[3][1], uint32_t at1, uint32_t at2, bf16x8_t (&fb)[1][2]) {
+    Half a, b, c, d, e, g, h, i, j, k;
+    asm volatile(TURN("0", "10", "13") TURN("1", "10", "14") TURN("2", "10", "15") TURN("3", "10", "16")
+                 TURN("4", "10", "17") TURN("5", "10", "18") TURN("6", "11", "19") TURN("7", "11", "20")
+                 TURN("8", "12", "19") TURN("9", "12", "20")
+                 "s_waitcnt lgkmcnt(0)"
+                 : "=&v"(a), "=&v"(b), "=&v"(c), "=&v"(d), "=&v"(e), "=&v"(g), "=&v"(h), "=&v"(i), "=&v"(j), "=&v"(k)
+                 : "v"(at0), "v"(at1), "v"(at2), "n"(AOFF), "n"(AOFF + AHALF), "n"(AOFF + APLANE),
+                   "n"(AOFF + APLANE + AHALF), "n"(AOFF + 2 * APLANE), "n"(AOFF + 2 * APLANE + AHALF), "n"(BOFF),
+                   "n"(BOFF + BHALF)
+                 : "memory");
+    fa[0][0] = halves(a, b);
+    fa[1][0] = halves(c, d);
+    fa[2][0] = halves(e, g);
+    fb[0][0] = halves(h, i);
+    fb[0][1] = halves(j, k);
+}
 
 // Waits until this wave has at most N loads in flight, then for the others.
 template <int N>
 __device__ __forceinline__ void arrived() {
     static_assert(N < 64, "the counter's range");
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+template <typename F>
+__device__ __forceinline__ void over_kk(F&& f) {
+    static_assert(STEP == 64, "four instructions' k to a step");
+    f(std::integral_constant<int, 0>{});
+    f(std::integral_constant<int, 1>{});
+    f(std::integral_constant<int, 2>{});
+    f(std::integral_constant<int, 3>{});
 }
 
 // Where a product goes: float32 rows (the result, or one split's part of it in
@@ -295,17 +362,35 @@ moe_router_product(Operand A, Operand Bo, Result out, int64_t k_split, int split
         }
         const u32x4_t* la = lds + stage * STAGE;
         const u32x4_t* lb = la + PA * TA::CHUNKS;
-#pragma unroll
-        for (int kk = 0; kk < STEP / 16; ++kk) {
+        uint32_t at[3] = {0, 0, 0};
+        if constexpr (LA == Lay::row_major) at[0] = TA::turned_at(la, wm);
+        if constexpr (LB == Lay::row_major) {
+            static_assert(TN == 2, "two fragments to a turned read");
+            at[1] = TB::turned_at(lb, wn);
+            at[2] = TB::turned_at(lb, wn + 32);
+        }
+        over_kk([&](auto step) {
+            constexpr int kk = decltype(step)::value;
             bf16x8_t fa[PA][TM], fb[PB][TN];
+            if constexpr (LA == Lay::k_major) {
 #pragma unroll
-            for (int p = 0; p < PA; ++p)
+                for (int p = 0; p < PA; ++p)
 #pragma unroll
-                for (int i = 0; i < TM; ++i) fa[p][i] = TA::fragment(la, p, wm + i * 32, kk);
+                    for (int i = 0; i < TM; ++i) fa[p][i] = TA::fragment(la, p, wm + i * 32, kk);
+            }
+            if constexpr (LB == Lay::k_major) {
 #pragma unroll
-            for (int p = 0; p < PB; ++p)
+                for (int p = 0; p < PB; ++p)
 #pragma unroll
-                for (int j = 0; j < TN; ++j) fb[p][j] = TB::fragment(lb, p, wn + j * 32, kk);
+                    for (int j = 0; j < TN; ++j) fb[p][j] = TB::fragment(lb, p, wn + j * 32, kk);
+            } else if constexpr (LA == Lay::row_major) {
+                turned<kk * TA::NEXT_KK, TA::NEXT_HALF, TA::NEXT_PLANE, kk * TB::NEXT_KK, TB::NEXT_HALF>(at[0], fa, at[1],
+                                                                                                         at[2], fb);
+            } else if constexpr (PB == 1) {
+                turned<kk * TB::NEXT_KK, TB::NEXT_HALF>(at[1], at[2], fb);
+            } else {
+                turned<kk * TB::NEXT_KK, TB::NEXT_HALF, TB::NEXT_PLANE>(at[1], at[2], fb);
+            }
             // the planes' products, the smallest first; beyond the last plane's
             // weight they are dropped
 #pragma unroll
@@ -320,7 +405,7 @@ moe_router_product(Operand A, Operand Bo, Result out, int64_t k_split, int split
                         for (int j = 0; j < TN; ++j)
                             acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[q][j], fa[p][i], acc[i][j], 0, 0, 0);
                 }
-        }
+        });
         if constexpr (STAGES == 1) __syncthreads();
         else stage = stage + 1 == STAGES ? 0 : stage + 1;
     }
@@ -456,11 +541,11 @@ struct Split {
     int64_t k;           // K of a part, whole steps of 64
 };
 
-// Parts of K for a product of `tiles` tiles: enough to give every compute unit
-// two workgroups, each with four steps or more.
-Split split_for(int64_t tiles, int64_t K) {
+// Parts of K for a product of `tiles` tiles: enough for `want` workgroups, each
+// with four steps or more.
+Split split_for(int64_t tiles, int64_t K, int64_t want) {
     int n = 1;
-    while (n < 16 && tiles * n < 512 && K / (2 * n) >= 256) n *= 2;
+    while (n < 16 && tiles * n < want && K / (2 * n) >= 256) n *= 2;
     const int64_t steps = (K + 63) / 64;
     return Split{n, (steps + n - 1) / n * 64};
 }
@@ -499,7 +584,7 @@ Plan forward_plan(const mega_moe_router_logits_args& a) {
     const int64_t T = a.num_tokens, E = a.num_experts, H = a.hidden;
     Plan p{};
     if (T <= SMALL_TOKENS) return p;
-    p.split = split_for(tiles(T, 128) * tiles(E, columns(E)), H);
+    p.split = split_for(tiles(T, 128) * tiles(E, columns(E)), H, 512);     // two to a compute unit
     p.parts = a.weight_type == MEGA_MOE_F32 ? 3 * E * H * 2 : 0;
     p.total = p.parts + (p.split.n > 1 ? p.split.n * T * E * 4 : 0);
     return p;
@@ -508,7 +593,7 @@ Plan forward_plan(const mega_moe_router_logits_args& a) {
 Plan backward_plan(const mega_moe_router_logits_args& a) {
     const int64_t T = a.num_tokens, E = a.num_experts, H = a.hidden;
     Plan p{};
-    p.split = split_for(tiles(E, 64) * tiles(H, 128), T);
+    p.split = split_for(tiles(E, 64) * tiles(H, 128), T, 256);     // one: its LDS holds three steps
     p.d_planes = a.weight_type == MEGA_MOE_F32 ? 2 * E * H * 2 : 0;
     p.parts = p.d_planes + 3 * T * padded(E) * 2;
     p.total = p.parts + (p.split.n > 1 ? p.split.n * E * H * 4 : 0);
