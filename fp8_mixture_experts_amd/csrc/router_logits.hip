@@ -307,23 +307,46 @@ struct Result {
     int64_t add_stride;
 };
 
-template <Lay LA, int PA, Lay LB, int PB, int BM, int BN, int STAGES, bool OUT_BF16>
-__global__ void __launch_bounds__(256)
-moe_router_product(Operand A, Operand Bo, Result out, int64_t k_split, int splits) {
+// One product's operands, result and split of K.
+struct Product {
+    Operand a, b;
+    Result out;
+    int64_t k_split;
+    int splits;
+};
+
+// The kind of a product, and what it needs of LDS (in chunks).
+template <Lay LA_, int PA_, Lay LB_, int PB_, int BM_, int BN_, int STAGES_, bool OUT_BF16_>
+struct Kind {
+    static constexpr Lay LA = LA_, LB = LB_;
+    static constexpr int PA = PA_, PB = PB_, BM = BM_, BN = BN_, STAGES = STAGES_;
+    static constexpr bool OUT_BF16 = OUT_BF16_;
+    static constexpr int PITCH = BN + 4;         // BF16 results go out through LDS, as rows of floats
+    static constexpr int STAGE = PA * Tile<LA, PA, BM>::CHUNKS + PB * Tile<LB, PB, BN>::CHUNKS;
+    static constexpr int OUT = OUT_BF16 ? BM * PITCH / 4 : 0;
+    static constexpr int LDS = STAGE * STAGES > OUT ? STAGE * STAGES : OUT;
+};
+
+// Workgroup `block` of a product.
+template <typename K>
+__device__ __forceinline__ void product(u32x4_t* lds, const Product& x, unsigned block) {
+    constexpr Lay LA = K::LA, LB = K::LB;
+    constexpr int PA = K::PA, PB = K::PB, BM = K::BM, BN = K::BN, STAGES = K::STAGES, STAGE = K::STAGE, PITCH = K::PITCH;
+    constexpr bool OUT_BF16 = K::OUT_BF16;
     using TA = Tile<LA, PA, BM>;
     using TB = Tile<LB, PB, BN>;
-    // BF16 results go out through LDS, as rows of floats
-    constexpr int PITCH = BN + 4;
-    constexpr int STAGE = PA * TA::CHUNKS + PB * TB::CHUNKS, OUT = OUT_BF16 ? BM * PITCH / 4 : 0;
-    __shared__ u32x4_t lds[STAGE * STAGES > OUT ? STAGE * STAGES : OUT];
+    const Operand &A = x.a, &Bo = x.b;
+    const Result& out = x.out;
+    const int splits = x.splits;
+    const int64_t k_split = x.k_split;
     // waves over the tile: 2 x 2, or all along M
     constexpr int WN = BN >= 128 || BM < 128 ? 2 : 1, WM = 4 / WN;
     constexpr int TM = BM / WM / 32, TN = BN / WN / 32;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int wm = wave / WN * (TM * 32), wn = wave % WN * (TN * 32);
     const int n_tiles = (int)((Bo.rows + BN - 1) / BN);
-    const int split = blockIdx.x % splits;
-    const int64_t tile = blockIdx.x / splits;
+    const int split = block % splits;
+    const int64_t tile = block / splits;
     const int64_t m0 = tile / n_tiles * BM, n0 = tile % n_tiles * BN;
     const int64_t k_first = split * k_split;
     const int64_t k_end = k_first + k_split < A.k ? k_first + k_split : A.k;
@@ -472,6 +495,23 @@ moe_router_product(Operand A, Operand Bo, Result out, int64_t k_split, int split
     }
 }
 
+template <typename K>
+__global__ void __launch_bounds__(256)
+moe_router_product(Product x) {
+    __shared__ u32x4_t lds[K::LDS];
+    product<K>(lds, x, blockIdx.x);
+}
+
+// Both gradients in one launch: workgroups of dw, which are few and long, and
+// then those of dx, which fill up what is left.
+template <typename KW, typename KX>
+__global__ void __launch_bounds__(256)
+moe_router_gradients(Product w, unsigned w_blocks, Product x) {
+    __shared__ u32x4_t lds[KW::LDS > KX::LDS ? KW::LDS : KX::LDS];
+    if (blockIdx.x < w_blocks) product<KW>(lds, w, blockIdx.x);
+    else product<KX>(lds, x, blockIdx.x - w_blocks);
+}
+
 // float32 rows as P BF16 planes, [P][rows][width]; columns behind the last are 0.
 struct Planes {
     const float* from;
@@ -534,6 +574,7 @@ moe_router_product_join(const float* ws, float* out, int64_t M, int64_t N, int64
 
 namespace {
 
+constexpr int DW_STAGES = 2;
 constexpr int64_t SMALL_TOKENS = 256;    // up to here the 16 x 16 tiles compute the logits
 
 struct Split {
@@ -628,10 +669,9 @@ void launch_logits(const mega_moe_router_logits_args& a, hipStream_t stream) {
     }
     float* parts = reinterpret_cast<float*>(at(a, p.parts));
     const Result out{T, E, p.split.n > 1 ? parts : a.logits, a.logits_stride, nullptr, nullptr, 0};
-    constexpr int STAGES = PW == 3 ? 1 : 2;
-    hipLaunchKernelGGL((moe_router_product<Lay::k_major, 1, Lay::k_major, PW, 128, BN, STAGES, false>),
-                       dim3((unsigned)(tiles(T, 128) * tiles(E, BN) * p.split.n)), dim3(256), 0, stream, A, W, out, p.split.k,
-                       p.split.n);
+    using K = Kind<Lay::k_major, 1, Lay::k_major, PW, 128, BN, PW == 3 ? 1 : 2, false>;
+    hipLaunchKernelGGL((moe_router_product<K>), dim3((unsigned)(tiles(T, 128) * tiles(E, BN) * p.split.n)), dim3(256), 0,
+                       stream, Product{A, W, out, p.split.k, p.split.n});
     if (p.split.n > 1) launch_join(parts, a.logits, T, E, a.logits_stride, p.split.n, stream);
 }
 
@@ -671,27 +711,21 @@ void launch_router_logits_backward(const mega_moe_router_logits_args& a, hipStre
     uint16_t* wp = reinterpret_cast<uint16_t*>(at(a, p.w_planes));
     launch_split(Planes{a.dlogits, a.dlogits_stride, T, E, dp, Ep, a.dw ? 3 : 2},
                  a.dx && f ? Planes{static_cast<const float*>(a.w), H, E, H, wp, H, 2} : Planes{}, stream);
-    if (a.dx && T > 0) {
-        const Operand D{dp, T * Ep, Ep, T, Ep};
-        const Operand W{f ? wp : static_cast<const uint16_t*>(a.w), E * H, H, H, E};
-        const Result out{T, H, nullptr, a.dx_stride, a.dx, a.dx_add, a.dx_add_stride};
-        const dim3 grid((unsigned)(tiles(T, 64) * tiles(H, 128)));
-        if (f)
-            hipLaunchKernelGGL((moe_router_product<Lay::k_major, 2, Lay::row_major, 2, 64, 128, 1, true>), grid, dim3(256), 0,
-                               stream, D, W, out, Ep, 1);
-        else
-            hipLaunchKernelGGL((moe_router_product<Lay::k_major, 2, Lay::row_major, 1, 64, 128, 1, true>), grid, dim3(256), 0,
-                               stream, D, W, out, Ep, 1);
-    }
-    if (a.dw) {
-        const Operand D{dp, T * Ep, Ep, Ep, T}, X{a.x, 0, a.x_stride, H, T};
-        float* parts = reinterpret_cast<float*>(at(a, p.parts));
-        const Result out{E, H, p.split.n > 1 ? parts : a.dw, H, nullptr, nullptr, 0};
-        hipLaunchKernelGGL((moe_router_product<Lay::row_major, 3, Lay::row_major, 1, 64, 128, 3, false>),
-                           dim3((unsigned)(tiles(E, 64) * tiles(H, 128) * p.split.n)), dim3(256), 0, stream, D, X, out,
-                           p.split.k, p.split.n);
-        if (p.split.n > 1) launch_join(parts, a.dw, E, H, H, p.split.n, stream);
-    }
+    const Product x{Operand{dp, T * Ep, Ep, T, Ep}, Operand{f ? wp : static_cast<const uint16_t*>(a.w), E * H, H, H, E},
+                    Result{T, H, nullptr, a.dx_stride, a.dx, a.dx_add, a.dx_add_stride}, Ep, 1};
+    float* parts = reinterpret_cast<float*>(at(a, p.parts));
+    const Product w{Operand{dp, T * Ep, Ep, Ep, T}, Operand{a.x, 0, a.x_stride, H, T},
+                    Result{E, H, p.split.n > 1 ? parts : a.dw, H, nullptr, nullptr, 0}, p.split.k, p.split.n};
+    const unsigned w_blocks = a.dw ? (unsigned)(tiles(E, 64) * tiles(H, 128) * p.split.n) : 0;
+    const unsigned x_blocks = a.dx ? (unsigned)(tiles(T, 64) * tiles(H, 128)) : 0;
+    using KW = Kind<Lay::row_major, 3, Lay::row_major, 1, 64, 128, DW_STAGES, false>;
+    using KX1 = Kind<Lay::k_major, 2, Lay::row_major, 1, 64, 128, 1, true>;
+    using KX2 = Kind<Lay::k_major, 2, Lay::row_major, 2, 64, 128, 1, true>;
+    if (f)
+        hipLaunchKernelGGL((moe_router_gradients<KW, KX2>), dim3(w_blocks + x_blocks), dim3(256), 0, stream, w, w_blocks, x);
+    else
+        hipLaunchKernelGGL((moe_router_gradients<KW, KX1>), dim3(w_blocks + x_blocks), dim3(256), 0, stream, w, w_blocks, x);
+    if (a.dw && p.split.n > 1) launch_join(parts, a.dw, E, H, H, p.split.n, stream);
 }
 
 }  // namespace mega_moe
