@@ -574,7 +574,6 @@ moe_router_product_join(const float* ws, float* out, int64_t M, int64_t N, int64
 
 namespace {
 
-constexpr int DW_STAGES = 2;
 constexpr int64_t SMALL_TOKENS = 256;    // up to here the 16 x 16 tiles compute the logits
 
 struct Split {
@@ -634,7 +633,7 @@ Plan forward_plan(const mega_moe_router_logits_args& a) {
 Plan backward_plan(const mega_moe_router_logits_args& a) {
     const int64_t T = a.num_tokens, E = a.num_experts, H = a.hidden;
     Plan p{};
-    p.split = split_for(tiles(E, 64) * tiles(H, 128), T, 256);     // one: its LDS holds three steps
+    p.split = split_for(tiles(E, 64) * tiles(H, 128), T, 256);     // few: they are joined again
     p.d_planes = a.weight_type == MEGA_MOE_F32 ? 2 * E * H * 2 : 0;
     p.parts = p.d_planes + 3 * T * padded(E) * 2;
     p.total = p.parts + (p.split.n > 1 ? p.split.n * E * H * 4 : 0);
@@ -718,7 +717,7 @@ void launch_router_logits_backward(const mega_moe_router_logits_args& a, hipStre
                     Result{E, H, p.split.n > 1 ? parts : a.dw, H, nullptr, nullptr, 0}, p.split.k, p.split.n};
     const unsigned w_blocks = a.dw ? (unsigned)(tiles(E, 64) * tiles(H, 128) * p.split.n) : 0;
     const unsigned x_blocks = a.dx ? (unsigned)(tiles(T, 64) * tiles(H, 128)) : 0;
-    using KW = Kind<Lay::row_major, 3, Lay::row_major, 1, 64, 128, DW_STAGES, false>;
+    using KW = Kind<Lay::row_major, 3, Lay::row_major, 1, 64, 128, 1, false>;
     using KX1 = Kind<Lay::k_major, 2, Lay::row_major, 1, 64, 128, 1, true>;
     using KX2 = Kind<Lay::k_major, 2, Lay::row_major, 2, 64, 128, 1, true>;
     if (f)
