@@ -103,8 +103,8 @@ moe_router_logits(mega_moe_router_logits_args a, int tile_t, int tile_e) {
 // split into planes in the workspace by moe_router_split beforehand: a tile's
 // values are used by many workgroups, which would each split them again.
 //
-// A workgroup of four waves computes BM x BN.  Steps of 64 k go from memory
-// straight into LDS (16 bytes a lane, no registers), STAGES - 1 of them ahead
+// A workgroup computes BM x BN.  Steps of 64 or 32 k go from memory straight
+// into LDS (16 bytes a lane, no registers), STAGES - 1 of them ahead
 // of the one that is multiplied.  An operand lies in memory, and in LDS, in
 // one of two ways:
 //   k_major    rows of k: a fragment's eight k are one 16-byte read
@@ -114,8 +114,8 @@ moe_router_logits(mega_moe_router_logits_args a, int tile_t, int tile_e) {
 //
 // LDS holds 16-byte chunks in the order in which they are loaded; where a
 // chunk comes from is permuted within its row, so that the reads of a fragment
-// spread over all banks: chunk c of a k_major row r lies at c ^ (r & 7); of a
-// row_major row the pairs of chunks (16 columns, one turned read) are permuted
+// spread over all banks: in a k_major row r chunk c lies at c ^ (r / 2) % 8 (of
+// 64 k; of 32 k at c ^ (r / 4) % 4); of a row_major row the pairs of chunks (16 columns, one turned read) are permuted
 // by the bits in which the eight rows of a read differ.
 // ---------------------------------------------------------------------------
 
@@ -134,7 +134,6 @@ typedef uint32_t u32x4a_t __attribute__((ext_vector_type(4), aligned(4)));
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 #define LDS_PTR __attribute__((address_space(3)))
 
-constexpr int STEP = 64;
 constexpr uint32_t OUTSIDE = 0x7fffff00u;      // beyond every buffer's bytes
 
 // `bytes` bytes at `base`; both are the same for the whole wave.
@@ -152,22 +151,29 @@ __device__ __forceinline__ int pair_swizzle(int row) {
     return R >= 128 ? (row & 3) | (row >> 1 & 4) : (row >> 1 & 1) | (row >> 2 & 2);
 }
 
-// One operand's planes of a step: R rows of m (or n) by 64 k.
-template <Lay L, int P, int R>
+// One operand's planes of a step: R rows of m (or n) by STEP k.
+template <Lay L, int P, int R, int STEP, int THREADS>
 struct Tile {
-    static constexpr int CHUNKS = R * 8;                 // of a plane
-    static constexpr int LOADS = P * CHUNKS / 256;       // per lane and step
-    static constexpr int WIDTH = L == Lay::k_major ? 8 : R / 8;      // chunks of a row
+    static constexpr int CHUNKS = R * STEP / 8;          // of a plane
+    static constexpr int PER_LANE = CHUNKS / THREADS;
+    static constexpr int LOADS = P * PER_LANE;           // per lane and step
+    static constexpr int WIDTH = L == Lay::k_major ? STEP / 8 : R / 8;       // chunks of a row
+    static_assert(CHUNKS % THREADS == 0, "whole loads");
+
+    __device__ __forceinline__ static int swizzle(int r) {
+        if constexpr (L == Lay::row_major) return pair_swizzle<R>(r) << 1;
+        else return STEP == 64 ? r >> 1 & 7 : r >> 2 & 3;
+    }
 
     // Byte offset of this lane's chunk of load i of a plane, from the tile's
     // first element, or OUTSIDE where its columns are.
-    uint32_t at[CHUNKS / 256];
+    uint32_t at[PER_LANE];
 
     __device__ __forceinline__ void place(const Operand& o, int64_t row0) {
 #pragma unroll
-        for (int i = 0; i < CHUNKS / 256; ++i) {
-            const int id = i * 256 + (int)threadIdx.x, r = id / WIDTH;
-            const int c = L == Lay::k_major ? (id % WIDTH) ^ (r & 7) : (id % WIDTH) ^ (pair_swizzle<R>(r) << 1);
+        for (int i = 0; i < PER_LANE; ++i) {
+            const int id = i * THREADS + (int)threadIdx.x, r = id / WIDTH;
+            const int c = (id % WIDTH) ^ swizzle(r);
             const bool in = L == Lay::k_major ? row0 + r < o.rows : row0 + c * 8 < o.rows;
             at[i] = in ? (uint32_t)((r * o.stride + c * 8) * 2) : OUTSIDE;
         }
@@ -187,13 +193,13 @@ struct Tile {
             const auto buf = buffer_of(o.p + p * o.plane + (L == Lay::k_major ? row0 * o.stride + k0 : k0 * o.stride + row0),
                                        left > 0 ? (((n < R ? n : R) - 1) * o.stride + width) * 2 : 0);
 #pragma unroll
-            for (int i = 0; i < CHUNKS / 256; ++i) {
+            for (int i = 0; i < PER_LANE; ++i) {
                 uint32_t off = at[i];
                 if (L == Lay::k_major && left < STEP) {
-                    const int id = i * 256 + (int)threadIdx.x;
-                    if (((id & 7) ^ (id >> 3 & 7)) * 8 >= left) off = OUTSIDE;
+                    const int id = i * THREADS + (int)threadIdx.x;
+                    if (((id % WIDTH) ^ swizzle(id / WIDTH)) * 8 >= left) off = OUTSIDE;
                 }
-                u32x4_t* to = lds + p * CHUNKS + i * 256 + __builtin_amdgcn_readfirstlane(wave) * 64;
+                u32x4_t* to = lds + p * CHUNKS + i * THREADS + __builtin_amdgcn_readfirstlane(wave) * 64;
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (LDS_PTR void*)to, 16, (int)off, 0, 0, 0);
             }
         }
@@ -203,7 +209,7 @@ struct Tile {
     // k_major tile: lane l holds row r0 + l % 32, k 8 (l / 32) .. + 7 of them.
     __device__ __forceinline__ static bf16x8_t fragment(const u32x4_t* lds, int p, int r0, int kk) {
         const int lane = threadIdx.x & 63, r = r0 + (lane & 31), c = kk * 2 + (lane >> 5);
-        return __builtin_bit_cast(bf16x8_t, lds[p * CHUNKS + r * 8 + (c ^ (r & 7))]);
+        return __builtin_bit_cast(bf16x8_t, lds[p * CHUNKS + r * WIDTH + (c ^ swizzle(r))]);
     }
 
     // Of a row_major tile: where this lane's part of it starts, as an LDS byte
@@ -213,7 +219,7 @@ struct Tile {
     __device__ __forceinline__ static uint32_t turned_at(const u32x4_t* lds, int r0) {
         const int lane = threadIdx.x & 63, i = lane & 15, col = r0 + (lane >> 4 & 1) * 16 + (i & 3) * 4;
         const int row = (lane >> 5) * 8 + (i >> 2);
-        const u32x4_t* chunk = lds + row * WIDTH + (col / 8 ^ (pair_swizzle<R>(row) << 1));
+        const u32x4_t* chunk = lds + row * WIDTH + (col / 8 ^ swizzle(row));
         return (uint32_t)(uintptr_t)(LDS_PTR const void*)chunk + (col >> 2 & 1) * 8;
     }
     // Bytes on from there: to the next 16 k, the other four k, the next plane.
@@ -287,13 +293,14 @@ __device__ __forceinline__ void arrived() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-template <typename F>
+template <int STEP, typename F>
 __device__ __forceinline__ void over_kk(F&& f) {
-    static_assert(STEP == 64, "four instructions' k to a step");
     f(std::integral_constant<int, 0>{});
     f(std::integral_constant<int, 1>{});
-    f(std::integral_constant<int, 2>{});
-    f(std::integral_constant<int, 3>{});
+    if constexpr (STEP == 64) {
+        f(std::integral_constant<int, 2>{});
+        f(std::integral_constant<int, 3>{});
+    }
 }
 
 // Where a product goes: float32 rows (the result, or one split's part of it in
@@ -316,13 +323,17 @@ struct Product {
 };
 
 // The kind of a product, and what it needs of LDS (in chunks).
-template <Lay LA_, int PA_, Lay LB_, int PB_, int BM_, int BN_, int STAGES_, bool OUT_BF16_>
+template <Lay LA_, int PA_, Lay LB_, int PB_, int BM_, int BN_, int STAGES_, bool OUT_BF16_, int STEP_ = 64, int WM_ = 2,
+          int WN_ = 2>
 struct Kind {
     static constexpr Lay LA = LA_, LB = LB_;
-    static constexpr int PA = PA_, PB = PB_, BM = BM_, BN = BN_, STAGES = STAGES_;
+    static constexpr int PA = PA_, PB = PB_, BM = BM_, BN = BN_, STAGES = STAGES_, STEP = STEP_;
+    static constexpr int WM = WM_, WN = WN_, THREADS = WM * WN * 64;     // waves over the tile
     static constexpr bool OUT_BF16 = OUT_BF16_;
     static constexpr int PITCH = BN + 4;         // BF16 results go out through LDS, as rows of floats
-    static constexpr int STAGE = PA * Tile<LA, PA, BM>::CHUNKS + PB * Tile<LB, PB, BN>::CHUNKS;
+    using TA = Tile<LA, PA, BM, STEP, THREADS>;
+    using TB = Tile<LB, PB, BN, STEP, THREADS>;
+    static constexpr int STAGE = PA * TA::CHUNKS + PB * TB::CHUNKS;
     static constexpr int OUT = OUT_BF16 ? BM * PITCH / 4 : 0;
     static constexpr int LDS = STAGE * STAGES > OUT ? STAGE * STAGES : OUT;
 };
@@ -333,14 +344,13 @@ __device__ __forceinline__ void product(u32x4_t* lds, const Product& x, unsigned
     constexpr Lay LA = K::LA, LB = K::LB;
     constexpr int PA = K::PA, PB = K::PB, BM = K::BM, BN = K::BN, STAGES = K::STAGES, STAGE = K::STAGE, PITCH = K::PITCH;
     constexpr bool OUT_BF16 = K::OUT_BF16;
-    using TA = Tile<LA, PA, BM>;
-    using TB = Tile<LB, PB, BN>;
+    constexpr int STEP = K::STEP, WM = K::WM, WN = K::WN, THREADS = K::THREADS;
+    using TA = typename K::TA;
+    using TB = typename K::TB;
     const Operand &A = x.a, &Bo = x.b;
     const Result& out = x.out;
     const int splits = x.splits;
     const int64_t k_split = x.k_split;
-    // waves over the tile: 2 x 2, or all along M
-    constexpr int WN = BN >= 128 || BM < 128 ? 2 : 1, WM = 4 / WN;
     constexpr int TM = BM / WM / 32, TN = BN / WN / 32;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int wm = wave / WN * (TM * 32), wn = wave % WN * (TN * 32);
@@ -392,7 +402,7 @@ __device__ __forceinline__ void product(u32x4_t* lds, const Product& x, unsigned
             at[1] = TB::turned_at(lb, wn);
             at[2] = TB::turned_at(lb, wn + 32);
         }
-        over_kk([&](auto step) {
+        over_kk<STEP>([&](auto step) {
             constexpr int kk = decltype(step)::value;
             bf16x8_t fa[PA][TM], fb[PB][TN];
             if constexpr (LA == Lay::k_major) {
@@ -450,8 +460,8 @@ __device__ __forceinline__ void product(u32x4_t* lds, const Product& x, unsigned
                 }
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < BM * BN / 8 / 256; ++i) {
-            const int id = i * 256 + (int)threadIdx.x;
+        for (int i = 0; i < BM * BN / 8 / THREADS; ++i) {
+            const int id = i * THREADS + (int)threadIdx.x;
             const int r = id / (BN / 8), c = id % (BN / 8) * 8;
             const int64_t m = m0 + r, n = n0 + c;
             if (m >= out.rows || n >= out.cols) continue;      // the rows come in eights
@@ -496,7 +506,7 @@ __device__ __forceinline__ void product(u32x4_t* lds, const Product& x, unsigned
 }
 
 template <typename K>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(K::THREADS)
 moe_router_product(Product x) {
     __shared__ u32x4_t lds[K::LDS];
     product<K>(lds, x, blockIdx.x);
@@ -525,8 +535,14 @@ __device__ __forceinline__ void split_row_part(const Planes& s, int64_t unit) {
     const int64_t units = s.width / 8, r = unit / units, c = (unit - r * units) * 8;
     const float* q = s.from + r * s.stride + c;
     float v[8];
+    if (c + 8 <= s.cols) {
+        const u32x4a_t a = *reinterpret_cast<const u32x4a_t*>(q), b = *reinterpret_cast<const u32x4a_t*>(q + 4);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = c + i < s.cols ? q[i] : 0.0f;
+        for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(a[i]), v[4 + i] = __uint_as_float(b[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = c + i < s.cols ? q[i] : 0.0f;
+    }
     u32x4_t p[3];
     split_bf16<3>(v, p);
 #pragma unroll
@@ -610,8 +626,6 @@ SmallTile small_tile(const mega_moe_router_logits_args& a) {
     return best;
 }
 
-int columns(int64_t E) { return E <= 32 ? 32 : E <= 64 ? 64 : 128; }
-
 // The workspace: the planes of what is split, then the parts of a split K.
 struct Plan {
     Split split;
@@ -624,7 +638,9 @@ Plan forward_plan(const mega_moe_router_logits_args& a) {
     const int64_t T = a.num_tokens, E = a.num_experts, H = a.hidden;
     Plan p{};
     if (T <= SMALL_TOKENS) return p;
-    p.split = split_for(tiles(T, 128) * tiles(E, columns(E)), H, 512);     // two to a compute unit
+    const bool f = a.weight_type == MEGA_MOE_F32;
+    const int bn = E <= 32 ? 32 : E <= 64 ? 64 : 128, bm = f && bn == 128 ? 256 : 128;
+    p.split = split_for(tiles(T, bm) * tiles(E, bn), H, bm == 256 ? 256 : 512);    // one or two to a compute unit
     p.parts = a.weight_type == MEGA_MOE_F32 ? 3 * E * H * 2 : 0;
     p.total = p.parts + (p.split.n > 1 ? p.split.n * T * E * 4 : 0);
     return p;
@@ -654,7 +670,17 @@ void launch_join(const float* parts, float* out, int64_t M, int64_t N, int64_t s
                        parts, out, M, N, stride, splits);
 }
 
-template <int PW, int BN>
+// The forward product's kinds: PW planes of w.
+template <int PW>
+struct Forward {
+    template <int BM, int BN, int STAGES, int STEP, int WM, int WN>
+    using Of = Kind<Lay::k_major, 1, Lay::k_major, PW, BM, BN, STAGES, false, STEP, WM, WN>;
+    using Few = Of<128, 32, PW == 3 ? 1 : 2, 64, 4, 1>;
+    using Some = Of<128, 64, PW == 3 ? 1 : 2, 64, 4, 1>;
+    using Many = std::conditional_t<PW == 3, Of<256, 128, 3, 32, 4, 2>, Of<128, 128, 2, 64, 2, 2>>;
+};
+
+template <int PW, typename K>
 void launch_logits(const mega_moe_router_logits_args& a, hipStream_t stream) {
     const Plan p = forward_plan(a);
     const int64_t T = a.num_tokens, H = a.hidden, E = a.num_experts;
@@ -668,10 +694,16 @@ void launch_logits(const mega_moe_router_logits_args& a, hipStream_t stream) {
     }
     float* parts = reinterpret_cast<float*>(at(a, p.parts));
     const Result out{T, E, p.split.n > 1 ? parts : a.logits, a.logits_stride, nullptr, nullptr, 0};
-    using K = Kind<Lay::k_major, 1, Lay::k_major, PW, 128, BN, PW == 3 ? 1 : 2, false>;
-    hipLaunchKernelGGL((moe_router_product<K>), dim3((unsigned)(tiles(T, 128) * tiles(E, BN) * p.split.n)), dim3(256), 0,
-                       stream, Product{A, W, out, p.split.k, p.split.n});
+    hipLaunchKernelGGL((moe_router_product<K>), dim3((unsigned)(tiles(T, K::BM) * tiles(E, K::BN) * p.split.n)),
+                       dim3(K::THREADS), 0, stream, Product{A, W, out, p.split.k, p.split.n});
     if (p.split.n > 1) launch_join(parts, a.logits, T, E, a.logits_stride, p.split.n, stream);
+}
+
+template <int PW>
+void launch_logits(const mega_moe_router_logits_args& a, hipStream_t stream) {
+    if (a.num_experts <= 32) launch_logits<PW, typename Forward<PW>::Few>(a, stream);
+    else if (a.num_experts <= 64) launch_logits<PW, typename Forward<PW>::Some>(a, stream);
+    else launch_logits<PW, typename Forward<PW>::Many>(a, stream);
 }
 
 }  // namespace
@@ -684,16 +716,8 @@ int64_t router_logits_workspace(const mega_moe_router_logits_args& a) {
 void launch_router_logits(const mega_moe_router_logits_args& a, hipStream_t stream) {
     const bool f = a.weight_type == MEGA_MOE_F32;
     if (a.num_tokens > SMALL_TOKENS) {
-        const int bn = columns(a.num_experts);
-        if (f) {
-            if (bn == 32) launch_logits<3, 32>(a, stream);
-            else if (bn == 64) launch_logits<3, 64>(a, stream);
-            else launch_logits<3, 128>(a, stream);
-        } else {
-            if (bn == 32) launch_logits<1, 32>(a, stream);
-            else if (bn == 64) launch_logits<1, 64>(a, stream);
-            else launch_logits<1, 128>(a, stream);
-        }
+        if (f) launch_logits<3>(a, stream);
+        else launch_logits<1>(a, stream);
         return;
     }
     const SmallTile s = small_tile(a);
