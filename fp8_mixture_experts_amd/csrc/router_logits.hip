@@ -103,8 +103,8 @@ moe_router_logits(mega_moe_router_logits_args a, int tile_t, int tile_e) {
 // split into planes in the workspace by moe_router_split beforehand: a tile's
 // values are used by many workgroups, which would each split them again.
 //
-// A workgroup computes BM x BN.  Steps of 64 or 32 k go from memory straight
-// into LDS (16 bytes a lane, no registers), STAGES - 1 of them ahead
+// A workgroup computes BM x BN.  Steps of 64 k go from memory straight into
+// LDS (16 bytes a lane, no registers), STAGES - 1 of them ahead
 // of the one that is multiplied.  An operand lies in memory, and in LDS, in
 // one of two ways:
 //   k_major    rows of k: a fragment's eight k are one 16-byte read
@@ -114,8 +114,8 @@ moe_router_logits(mega_moe_router_logits_args a, int tile_t, int tile_e) {
 //
 // LDS holds 16-byte chunks in the order in which they are loaded; where a
 // chunk comes from is permuted within its row, so that the reads of a fragment
-// spread over all banks: in a k_major row r chunk c lies at c ^ (r / 2) % 8 (of
-// 64 k; of 32 k at c ^ (r / 4) % 4); of a row_major row the pairs of chunks (16 columns, one turned read) are permuted
+// spread over all banks: in a k_major row r chunk c lies at c ^ (r / 2) % 8;
+// of a row_major row the pairs of chunks (16 columns, one turned read) are permuted
 // by the bits in which the eight rows of a read differ.
 // ---------------------------------------------------------------------------
 
@@ -134,6 +134,7 @@ typedef uint32_t u32x4a_t __attribute__((ext_vector_type(4), aligned(4)));
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 #define LDS_PTR __attribute__((address_space(3)))
 
+constexpr int STEP = 64;                       // k of a step
 constexpr uint32_t OUTSIDE = 0x7fffff00u;      // beyond every buffer's bytes
 
 // `bytes` bytes at `base`; both are the same for the whole wave.
@@ -152,7 +153,7 @@ __device__ __forceinline__ int pair_swizzle(int row) {
 }
 
 // One operand's planes of a step: R rows of m (or n) by STEP k.
-template <Lay L, int P, int R, int STEP, int THREADS>
+template <Lay L, int P, int R, int THREADS>
 struct Tile {
     static constexpr int CHUNKS = R * STEP / 8;          // of a plane
     static constexpr int PER_LANE = CHUNKS / THREADS;
@@ -162,7 +163,7 @@ struct Tile {
 
     __device__ __forceinline__ static int swizzle(int r) {
         if constexpr (L == Lay::row_major) return pair_swizzle<R>(r) << 1;
-        else return STEP == 64 ? r >> 1 & 7 : r >> 2 & 3;
+        else return r >> 1 & 7;
     }
 
     // Byte offset of this lane's chunk of load i of a plane, from the tile's
@@ -293,14 +294,13 @@ __device__ __forceinline__ void arrived() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-template <int STEP, typename F>
+template <typename F>
 __device__ __forceinline__ void over_kk(F&& f) {
+    static_assert(STEP == 64, "four instructions' k to a step");
     f(std::integral_constant<int, 0>{});
     f(std::integral_constant<int, 1>{});
-    if constexpr (STEP == 64) {
-        f(std::integral_constant<int, 2>{});
-        f(std::integral_constant<int, 3>{});
-    }
+    f(std::integral_constant<int, 2>{});
+    f(std::integral_constant<int, 3>{});
 }
 
 // Where a product goes: float32 rows (the result, or one split's part of it in
@@ -323,16 +323,16 @@ struct Product {
 };
 
 // The kind of a product, and what it needs of LDS (in chunks).
-template <Lay LA_, int PA_, Lay LB_, int PB_, int BM_, int BN_, int STAGES_, bool OUT_BF16_, int STEP_ = 64, int WM_ = 2,
+template <Lay LA_, int PA_, Lay LB_, int PB_, int BM_, int BN_, int STAGES_, bool OUT_BF16_, int WM_ = 2,
           int WN_ = 2>
 struct Kind {
     static constexpr Lay LA = LA_, LB = LB_;
-    static constexpr int PA = PA_, PB = PB_, BM = BM_, BN = BN_, STAGES = STAGES_, STEP = STEP_;
+    static constexpr int PA = PA_, PB = PB_, BM = BM_, BN = BN_, STAGES = STAGES_;
     static constexpr int WM = WM_, WN = WN_, THREADS = WM * WN * 64;     // waves over the tile
     static constexpr bool OUT_BF16 = OUT_BF16_;
     static constexpr int PITCH = BN + 4;         // BF16 results go out through LDS, as rows of floats
-    using TA = Tile<LA, PA, BM, STEP, THREADS>;
-    using TB = Tile<LB, PB, BN, STEP, THREADS>;
+    using TA = Tile<LA, PA, BM, THREADS>;
+    using TB = Tile<LB, PB, BN, THREADS>;
     static constexpr int STAGE = PA * TA::CHUNKS + PB * TB::CHUNKS;
     static constexpr int OUT = OUT_BF16 ? BM * PITCH / 4 : 0;
     static constexpr int LDS = STAGE * STAGES > OUT ? STAGE * STAGES : OUT;
@@ -344,7 +344,7 @@ __device__ __forceinline__ void product(u32x4_t* lds, const Product& x, unsigned
     constexpr Lay LA = K::LA, LB = K::LB;
     constexpr int PA = K::PA, PB = K::PB, BM = K::BM, BN = K::BN, STAGES = K::STAGES, STAGE = K::STAGE, PITCH = K::PITCH;
     constexpr bool OUT_BF16 = K::OUT_BF16;
-    constexpr int STEP = K::STEP, WM = K::WM, WN = K::WN, THREADS = K::THREADS;
+    constexpr int WM = K::WM, WN = K::WN, THREADS = K::THREADS;
     using TA = typename K::TA;
     using TB = typename K::TB;
     const Operand &A = x.a, &Bo = x.b;
@@ -402,7 +402,7 @@ __device__ __forceinline__ void product(u32x4_t* lds, const Product& x, unsigned
             at[1] = TB::turned_at(lb, wn);
             at[2] = TB::turned_at(lb, wn + 32);
         }
-        over_kk<STEP>([&](auto step) {
+        over_kk([&](auto step) {
             constexpr int kk = decltype(step)::value;
             bf16x8_t fa[PA][TM], fb[PB][TN];
             if constexpr (LA == Lay::k_major) {
@@ -634,13 +634,25 @@ struct Plan {
 
 int64_t padded(int64_t E) { return (E + 63) / 64 * 64; }
 
+int64_t forward_tiles(const mega_moe_router_logits_args& a) {
+    const int64_t E = a.num_experts;
+    return tiles(a.num_tokens, 128) * tiles(E, E <= 32 ? 32 : E <= 64 ? 64 : 128);
+}
+
+// Whether two workgroups share a compute unit: with float32 weights, where one
+// each would leave parts of K longer than 2048.  Measured at 8192 x 7168 x 256
+// 100 us in pairs and 112 alone, at 8192 x 2048 x 512 65 and 57; with BF16
+// weights, whose loads take more of the time than the products, 58 and 56.
+bool forward_pairs(const mega_moe_router_logits_args& a) {
+    if (a.num_experts <= 64 || a.weight_type != MEGA_MOE_F32) return false;
+    return a.hidden / split_for(forward_tiles(a), a.hidden, 256).n > 2048;
+}
+
 Plan forward_plan(const mega_moe_router_logits_args& a) {
     const int64_t T = a.num_tokens, E = a.num_experts, H = a.hidden;
     Plan p{};
     if (T <= SMALL_TOKENS) return p;
-    const bool f = a.weight_type == MEGA_MOE_F32;
-    const int bn = E <= 32 ? 32 : E <= 64 ? 64 : 128, bm = f && bn == 128 ? 256 : 128;
-    p.split = split_for(tiles(T, bm) * tiles(E, bn), H, bm == 256 ? 256 : 512);    // one or two to a compute unit
+    p.split = split_for(forward_tiles(a), H, E <= 64 || forward_pairs(a) ? 512 : 256);
     p.parts = a.weight_type == MEGA_MOE_F32 ? 3 * E * H * 2 : 0;
     p.total = p.parts + (p.split.n > 1 ? p.split.n * T * E * 4 : 0);
     return p;
@@ -673,11 +685,14 @@ void launch_join(const float* parts, float* out, int64_t M, int64_t N, int64_t s
 // The forward product's kinds: PW planes of w.
 template <int PW>
 struct Forward {
-    template <int BM, int BN, int STAGES, int STEP, int WM, int WN>
-    using Of = Kind<Lay::k_major, 1, Lay::k_major, PW, BM, BN, STAGES, false, STEP, WM, WN>;
-    using Few = Of<128, 32, PW == 3 ? 1 : 2, 64, 4, 1>;
-    using Some = Of<128, 64, PW == 3 ? 1 : 2, 64, 4, 1>;
-    using Many = std::conditional_t<PW == 3, Of<256, 128, 3, 32, 4, 2>, Of<128, 128, 2, 64, 2, 2>>;
+    template <int BN, int STAGES, int WM, int WN>
+    using Of = Kind<Lay::k_major, 1, Lay::k_major, PW, 128, BN, STAGES, false, WM, WN>;
+    using Few = Of<32, PW == 3 ? 1 : 2, 4, 1>;
+    using Some = Of<64, PW == 3 ? 1 : 2, 4, 1>;
+    // A workgroup to a compute unit, with steps in flight; and two of them that
+    // hide each other's loads.
+    using Many = Of<128, PW == 3 ? 2 : 4, 4, 2>;
+    using ManyPairs = Of<128, 1, 2, 2>;
 };
 
 template <int PW, typename K>
@@ -703,7 +718,8 @@ template <int PW>
 void launch_logits(const mega_moe_router_logits_args& a, hipStream_t stream) {
     if (a.num_experts <= 32) launch_logits<PW, typename Forward<PW>::Few>(a, stream);
     else if (a.num_experts <= 64) launch_logits<PW, typename Forward<PW>::Some>(a, stream);
-    else launch_logits<PW, typename Forward<PW>::Many>(a, stream);
+    else if (PW == 1 || !forward_pairs(a)) launch_logits<PW, typename Forward<PW>::Many>(a, stream);
+    else if constexpr (PW == 3) launch_logits<PW, typename Forward<PW>::ManyPairs>(a, stream);
 }
 
 }  // namespace
