@@ -490,7 +490,8 @@ int64_t mega_moe_router_logits_workspace_bytes(const mega_moe_router_logits_args
  * The router's selection: topk_idx and topk_weights as mega_moe_forward takes
  * them.  Experts are ordered by c = s + bias, computed in float64 (by the
  * logits themselves where there is no bias and one group: the same order);
- * equal ones by their index, the lowest first.  An expert whose logit or c is
+ * equal ones by their index, the lowest first (keys and group scores that differ
+ * by no more than float64's own rounding may come in either order).  An expert whose logit or c is
  * -inf or NaN is never taken.  With num_groups > 1 the experts, in num_groups equal
  * runs, are first narrowed to the topk_groups groups with the largest sums of
  * their group_top largest c (an expert never taken counts as -inf).  Slots are

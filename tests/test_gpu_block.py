@@ -348,7 +348,17 @@ def _check_topk(logits, k, score, bias=None, mask=None, groups=1, kept=1, top=1,
     U.near(w, want, want, 32 + logits.shape[1] // 64 + k, "topk_weights")
 
 
-@pytest.mark.parametrize("T,E,k,score,lt,bias,groups,kept,top,renormalize", TOPK)
+# batches above 2048 tokens give a token fewer lanes
+TOPK_LARGE = [
+    (2100, 100, 6, "softmax", F32, False, 1, 1, 1, True),
+    (2060, 256, 8, "sigmoid", F32, True, 8, 4, 2, True),
+    (2050, 96, 4, "softmax", BF16, True, 12, 5, 1, False),
+    (2049, 300, 31, "sigmoid", F32, True, 1, 1, 1, True),
+    (2052, 200, 30, "sigmoid", F32, True, 5, 2, 2, True),
+]
+
+
+@pytest.mark.parametrize("T,E,k,score,lt,bias,groups,kept,top,renormalize", TOPK + TOPK_LARGE)
 def test_selection_matches_the_reference(T, E, k, score, lt, bias, groups, kept, top, renormalize):
     r = _gen(T + 3 * E + k)
     logits = r(T, E, dtype=lt)
@@ -400,6 +410,60 @@ def test_selection_follows_near_ties_exactly():
     assert _topk(logits, 1, "sigmoid", bias)[0].tolist() == [[0]]
 
 
+@pytest.mark.parametrize("T,E", [(300, 64), (300, 256), (2100, 128), (200, 512)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups", [1, 4])
+def test_selection_orders_near_ties_in_float64(T, E, score, groups):
+    # every row: a few values, copied over the experts, some moved by one step of
+    # float32: groups and experts that float32 scores cannot tell apart
+    rng = np.random.default_rng(T + E + groups)
+    base = rng.standard_normal((T, 4)).astype(np.float32)
+    l = np.take_along_axis(base, rng.integers(0, 4, (T, E)), axis=1)
+    moved = rng.random((T, E)) < 0.3
+    l = np.where(moved, np.nextafter(l, np.where(rng.random((T, E)) < 0.5, np.inf, -np.inf).astype(np.float32)), l)
+    bias = np.where(rng.random(E) < 0.2, np.float32(2.0 ** -24), np.float32(0.0)).astype(np.float32)
+    k, kept, top = 7, 2, 2
+    logits, b = torch.from_numpy(l).cuda(), torch.from_numpy(bias).cuda()
+    idx, _ = _topk(logits, k, score, b, None, groups, kept, top)
+    want, _ = block.router_topk(l, k, score, bias, None, True, 2.5, groups, kept, top)
+    undecided = _beyond_float64(l, k, score, bias, groups, kept, top)
+    assert undecided.mean() < 0.2
+    same = np.all(idx.cpu().numpy() == want, axis=1)
+    assert np.all(same | undecided), np.argwhere(~(same | undecided))[:5].tolist()
+
+
+def _beyond_float64(l, k, score, bias, groups, kept, top):
+    """Rows whose order float64 cannot tell.  A key there is exp (one step), a
+    division and a sum: under four half steps of 1 (2^-53 each) from the true
+    one, and a group's score, the sum of two, under ten.  Two float64
+    computations of the same row may thus differ in the order of neighbours
+    nearer than twice that; 2^-48 is above it.  Equal logits with equal biases
+    are no such case: they give equal keys in both, and groups of equal pairs
+    equal scores.  Judged in 64-bit mantissas (2^-64)."""
+    x = l.astype(np.longdouble)
+    s = np.exp(x - x.max(axis=1, keepdims=True))
+    s = s / s.sum(axis=1, keepdims=True) if score == "softmax" else 1 / (1 + np.exp(-x))
+    out = np.zeros(len(l), bool)
+    size = l.shape[1] // groups
+    near = np.longdouble(2.0 ** -48)
+    for t in range(len(l)):
+        c = s[t] + bias.astype(np.longdouble)
+        what = [(l[t, e], bias[e]) for e in range(l.shape[1])]
+        live = list(range(l.shape[1]))
+        if groups > 1:
+            best = [sorted(range(g * size, (g + 1) * size), key=lambda e: -c[e])[:top] for g in range(groups)]
+            order = sorted(range(groups), key=lambda g: (-sum(c[e] for e in best[g]), g))
+            for a in order[:kept]:
+                for z in order[kept:]:
+                    if sorted(what[e] for e in best[a]) != sorted(what[e] for e in best[z]):
+                        out[t] |= sum(c[e] for e in best[a]) - sum(c[e] for e in best[z]) < near
+            live = [e for e in live if e // size in order[:kept]]
+        order = sorted(live, key=lambda e: (-c[e], e))[:k + 1]
+        for a, z in zip(order, order[1:]):
+            out[t] |= what[a] != what[z] and c[a] - c[z] < near
+    return out
+
+
 # ---- losses and gradients ------------------------------------------------------------------
 
 # tokens, experts, k, score, logits type, cuts (None: one sequence), masked tokens
@@ -414,6 +478,8 @@ SEQ = [
     (40, 1024, 4, "sigmoid", F32, [0, 40], True),
     (64, 8, 70, "softmax", F32, [0, 0, 0], False),
     (3000, 16, 2, "softmax", F32, None, False),
+    (2100, 200, 4, "softmax", F32, [3, 700, 2050], True),
+    (2100, 70, 6, "sigmoid", BF16, list(range(0, 2101, 21)), False),
 ]
 
 
@@ -526,3 +592,52 @@ def test_router_backward_of_a_repeated_expert_and_an_empty_row():
                                            np.ones(2), None, _np(o["counts"]), _np(o["tokens"]), k, 0.5, 0.25)
             U.near(d, g, mag, 128, f"{score} {renormalize}")
             assert not d[1].any()
+
+
+# ---- rows far apart: offsets beyond 32 bits -----------------------------------------------------
+
+def test_offsets_beyond_32_bits():
+    far = 1 << 31                        # elements from row to row: rows 0, 4 GiB and 8 GiB apart in BF16
+    r = _gen(31)
+    buf = torch.empty(2 * far + 4096, dtype=BF16, device="cuda")
+    T, H = 3, 256
+    h = buf.as_strided((T, H), (far, 1))
+    h.copy_(r(T, H))
+    w, n = r(H), torch.empty(T, H, dtype=BF16, device="cuda")
+    B.mega_moe_norm(B.make_args(B.mega_moe_norm_args, num_tokens=T, hidden=H, weight_type=B.MEGA_MOE_F32, pre_eps=1e-6,
+                                residual_scale=1.0, h=h, h_stride=far, r=h, r_stride=far, n=n, pre_weight=w),
+                    U.current_stream())
+    want = block.norm(U.f64(h), pre=U.f64(w), pre_eps=1e-6)
+    U.near(n, want["n"], want["n_mag"], NORM_ROUNDINGS, "n")
+    dh, dpre = buf.as_strided((T, H), (far, 1), 1024), torch.empty(H, device="cuda")
+    dn = r(T, H, dtype=BF16)
+    U.finish_norm_backward(B.make_args(
+        B.mega_moe_norm_backward_args, num_tokens=T, hidden=H, weight_type=B.MEGA_MOE_F32, pre_eps=1e-6, residual_scale=1.0,
+        r=h, r_stride=far, dn=dn, pre_weight=w, dh=dh, dh_stride=far, dpre_weight=dpre))
+    want = block.norm_backward(U.f64(h), dn=U.f64(dn), pre=U.f64(w), pre_eps=1e-6)
+    U.near(dh, want["dh"], want["dh_mag"], 2 * NORM_ROUNDINGS, "dh")
+    E, k = 40, 4
+    l = buf.as_strided((T, E), (far, 1), 2048)
+    l.copy_(r(T, E))
+    _check_topk(l, k, "softmax", stride=far)
+    idx, _ = block.router_topk(U.f64(l), k, "softmax")
+    o = _balance(l, torch.from_numpy(idx).cuda(), "softmax", None, None, stride=far)
+    want = block.balance_loss(U.f64(l), idx, "softmax", None, None, 0.5, 0.25)
+    U.near(o["loss"], want["loss"], want["loss_mag"], 128, "loss")
+    del buf, h, dh, l
+    # the router's product: rows 2^22 elements apart, beyond 2^32 at row 1024
+    T, H, E, far = 1030, 64, 8, 1 << 22
+    buf = torch.empty((T - 1) * far + H, dtype=BF16, device="cuda")
+    x, w, d = buf.as_strided((T, H), (far, 1)), r(E, H), r(T, E)
+    x.copy_(r(T, H))
+    logits, dw = torch.empty(T, E, device="cuda"), torch.empty(E, H, device="cuda")
+    a = B.make_args(B.mega_moe_router_logits_args, num_tokens=T, hidden=H, num_experts=E, weight_type=B.MEGA_MOE_F32, x=x,
+                    x_stride=far, w=w, logits=logits, dlogits=d, dw=dw)
+    B.set_args(a, **U.workspace(B.mega_moe_router_logits_workspace_bytes(a)))
+    B.mega_moe_router_logits(a, U.current_stream())
+    B.mega_moe_router_logits_backward(a, U.current_stream())
+    xs = U.f64(x)
+    want, mag = block.router_logits(xs, U.f64(w))
+    U.near(logits, want, mag, H + 16, "logits")
+    want = block.router_logits_backward(U.f64(d), xs, U.f64(w))
+    U.near(dw, want["dw"], want["dw_mag"], T + 16, "dw")
