@@ -35,17 +35,22 @@ __device__ __forceinline__ const u32x4_t* raw8(const void* p, size_t i) {
     else return reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(p) + i);
 }
 
-template <bool F32, int N>
-__device__ __forceinline__ void values8(const u32x4_t (&d)[N], float (&v)[8]) {
+template <bool F32>
+__device__ __forceinline__ void values8(const u32x4_t& d0, const u32x4_t& d1, float (&v)[8]) {
     if constexpr (F32) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            v[j] = __uint_as_float(d[0][j]);
-            v[4 + j] = __uint_as_float(d[N - 1][j]);
+            v[j] = __uint_as_float(d0[j]);
+            v[4 + j] = __uint_as_float(d1[j]);
         }
     } else {
-        unpack8(d[0], v);
+        unpack8(d0, v);
     }
+}
+
+template <bool F32, int N>
+__device__ __forceinline__ void values8(const u32x4_t (&d)[N], float (&v)[8]) {
+    values8<F32>(d[0], d[N - 1], v);
 }
 
 // Elements i .. i+7 (i a multiple of 8, p 16-byte aligned).
@@ -70,8 +75,21 @@ __device__ __forceinline__ void load8(const void* p, int type, size_t i, float (
     else load8<false>(p, i, v);
 }
 
-template <bool F32>
+__device__ __forceinline__ u32x4_t pack8(const float (&v)[8]) {
+    u32x4_t d;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) d[j] = bf16_pair(v[2 * j], v[2 * j + 1]);
+    return d;
+}
+
+// Elements i .. i+7 (i a multiple of 8, p 16-byte aligned).  STREAM: what is read
+// again only after a whole layer; it leaves the caches to what is read next.
+template <bool F32, bool STREAM = false>
 __device__ __forceinline__ void store8(void* p, size_t i, const float (&v)[8]) {
+    const auto put = [](u32x4_t* q, const u32x4_t& d) {
+        if constexpr (STREAM) __builtin_nontemporal_store(d, q);
+        else *q = d;
+    };
     if constexpr (F32) {
         u32x4_t a, b;
 #pragma unroll
@@ -80,19 +98,22 @@ __device__ __forceinline__ void store8(void* p, size_t i, const float (&v)[8]) {
             b[j] = __float_as_uint(v[4 + j]);
         }
         u32x4_t* q = reinterpret_cast<u32x4_t*>(static_cast<float*>(p) + i);
-        q[0] = a;
-        q[1] = b;
+        put(q, a);
+        put(q + 1, b);
     } else {
-        u32x4_t d;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) d[j] = bf16_pair(v[2 * j], v[2 * j + 1]);
-        *reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(p) + i) = d;
+        put(reinterpret_cast<u32x4_t*>(static_cast<uint16_t*>(p) + i), pack8(v));
     }
 }
 
-__device__ __forceinline__ void store8(void* p, int type, size_t i, const float (&v)[8]) {
-    if (type == MEGA_MOE_F32) store8<true>(p, i, v);
-    else store8<false>(p, i, v);
+template <bool F32>
+__device__ __forceinline__ void stream8(void* p, size_t i, const float (&v)[8]) {
+    store8<F32, true>(p, i, v);
+}
+
+// The same with the type as a uniform run-time value.
+__device__ __forceinline__ void stream8(void* p, int type, size_t i, const float (&v)[8]) {
+    if (type == MEGA_MOE_F32) stream8<true>(p, i, v);
+    else stream8<false>(p, i, v);
 }
 
 // Another lane's value by a data-parallel move: 1 and 2 are xor within a quad,
@@ -177,33 +198,14 @@ __device__ __forceinline__ double wave_max(double v) {
     return over_wave(v, [](double a, double b) { return fmax(a, b); });
 }
 
-// Sums of N values over the workgroup (up to 16 waves), the waves' sums added
-// in order.  `part` is an LDS array that no earlier sum of the same phase
-// uses; a barrier must lie between two uses of one.
-template <int N>
-__device__ __forceinline__ void block_sum(float (&v)[N], float (&part)[16][N]) {
-    const int wave = threadIdx.x >> 6, waves = (blockDim.x + 63) >> 6;
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
-    if (waves == 1) return;
-    if ((threadIdx.x & 63) == 0) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) part[wave][i] = v[i];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = part[0][i];
-    for (int w = 1; w < waves; ++w) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] += part[w][i];
-    }
-}
-
-// The same over groups of nt threads (whole waves), each for itself; every
-// group of the workgroup calls it.
+// Sums of N values over groups of nt threads (whole waves, up to 16), each for
+// itself; every group of the workgroup calls it.  The waves' sums meet in
+// `part`, an LDS array that no earlier sum of the same phase uses; a barrier
+// must lie between two uses of one.  Sixteen lanes then take a wave's sum each:
+// one read and four moves, not a chain of reads.
 template <int N>
 __device__ __forceinline__ void group_sum(float (&v)[N], float (&part)[16][N], int group, int nt) {
-    const int wave = threadIdx.x >> 6, waves = nt >> 6;
+    const int wave = threadIdx.x >> 6, waves = nt >> 6, lane = threadIdx.x & 15;
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
     if (waves == 1) return;
@@ -213,11 +215,13 @@ __device__ __forceinline__ void group_sum(float (&v)[N], float (&part)[16][N], i
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = part[group * waves][i];
-    for (int w = 1; w < waves; ++w) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] += part[group * waves + w][i];
-    }
+    for (int i = 0; i < N; ++i) v[i] = lanes_sum<16>(lane < waves ? part[group * waves + lane][i] : 0.0f);
+}
+
+// The same over the workgroup.
+template <int N>
+__device__ __forceinline__ void block_sum(float (&v)[N], float (&part)[16][N]) {
+    group_sum(v, part, 0, (int)blockDim.x);
 }
 
 }  // namespace mega_moe
