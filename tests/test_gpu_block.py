@@ -410,6 +410,26 @@ def test_selection_follows_near_ties_exactly():
     assert _topk(logits, 1, "sigmoid", bias)[0].tolist() == [[0]]
 
 
+# few and many slots (the keys of a lane in order or not), and group sizes of one
+# and several times 16, with scores that tie within a lane and across lanes
+@pytest.mark.parametrize("T,E,groups,ks", [(40, 64, 4, (1, 2, 3, 9)), (2100, 64, 1, (1, 9)), (2100, 256, 16, (4, 5, 11)),
+                                           (60, 240, 5, (1, 2, 3, 29)), (2060, 192, 4, (2, 8, 27)),
+                                           (50, 512, 8, (1, 4, 5, 40)), (30, 1024, 64, (8, 9, 61)),
+                                           (30, 960, 4, (2, 8, 13))])
+def test_selection_of_few_and_many_slots_among_ties(T, E, groups, ks):
+    r = _gen(T + E)
+    logits = torch.round(r(T, E) * 4) / 4            # about 30 values
+    logits[::7, : E // groups] = -float("inf")
+    bias = torch.round(r(E) * 2) / 2
+    for k in ks:
+        _check_topk(logits, k, "softmax")
+        _check_topk(logits, k, "sigmoid", bias)
+        if groups > 1:
+            need = -(-k * groups // E)                   # groups that hold k experts
+            _check_topk(logits, k, "sigmoid", bias, None, groups, max(need, 2), 2)
+            _check_topk(logits, k, "sigmoid", bias, None, groups, need, 1)
+
+
 @pytest.mark.parametrize("T,E", [(300, 64), (300, 256), (2100, 128), (200, 512)])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("groups", [1, 4])
