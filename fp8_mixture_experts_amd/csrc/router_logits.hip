@@ -28,7 +28,7 @@ __device__ __forceinline__ void split_bf16(const float (&v)[8], u32x4_t (&p)[P])
     }
 }
 
-// Small batches.  A tile of up to 16 tokens x 16 experts per workgroup; its 16
+// Small products.  A tile of up to 16 tokens x 16 experts per workgroup; its 16
 // waves take the K steps of 32 in turn, straight from memory, and their sums
 // meet in LDS.  What bounds it is how fast one compute unit takes in its rows
 // (about 40 GB/s, whatever the others do), so the tile is the one that leaves
@@ -590,8 +590,6 @@ moe_router_product_join(const float* ws, float* out, int64_t M, int64_t N, int64
 
 namespace {
 
-constexpr int64_t SMALL_TOKENS = 256;    // up to here the 16 x 16 tiles compute the logits
-
 struct Split {
     int n;               // parts of K
     int64_t k;           // K of a part, whole steps of 64
@@ -608,22 +606,34 @@ Split split_for(int64_t tiles, int64_t K, int64_t want) {
 
 int64_t tiles(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// The tile of a small batch: the fewest rows, by their bytes, for one compute
-// unit of 256, in as many turns as the tiles take.
+// The tile of a small product: the fewest bytes of rows for one compute unit of
+// 256, in as many turns as the tiles take.
 struct SmallTile {
     int t, e;
+    int64_t bytes;       // for a compute unit, per k
 };
 SmallTile small_tile(const mega_moe_router_logits_args& a) {
     const int w_bytes = a.weight_type == MEGA_MOE_F32 ? 4 : 2;
-    SmallTile best{16, 16};
-    int64_t least = INT64_MAX;
-    for (int t = 16; t >= 1; t /= 2)
-        for (int e = 16; e >= 1; e /= 2) {
-            const int64_t turns = tiles(tiles(a.num_tokens, t) * tiles(a.num_experts, e), 256);
-            const int64_t bytes = turns * (t * 2 + e * w_bytes);
-            if (bytes < least) least = bytes, best = SmallTile{t, e};
+    SmallTile best{16, 16, INT64_MAX};
+    for (int t = 4; t >= 0; --t)
+        for (int e = 4; e >= 0; --e) {
+            const int64_t n = (int64_t)((a.num_tokens - 1 >> t) + 1) * ((a.num_experts - 1 >> e) + 1);
+            const int64_t bytes = ((n - 1 >> 8) + 1) * ((2 << t) + (w_bytes << e));
+            if (bytes < best.bytes) best = SmallTile{1 << t, 1 << e, bytes};
         }
     return best;
+}
+
+// Whether the 16 x 16 tiles compute the logits: one launch at about 37 kB/us for
+// each compute unit, against two or three launches that read every row less
+// often.  They cross where a compute unit takes in 170 kB and 25 rows of w:
+// 16 x 16 and 128 x 128 tiles at 1024 x 640 x 128 5.5 and 10.8 us (82 kB), 8192 x
+// 640 x 31 9.9 and 9.3 (164 kB), 2048 x 7168 x 31 15.3 and 16.0 (459 kB), 512 x
+// 7168 x 512 54 and 19 (1.8 MB); with float32 weights 2048 x 1792 x 64 14.7 and
+// 18.3 (344 kB), 4096 x 1792 x 64 27 and 19 (688 kB).
+bool is_small(const mega_moe_router_logits_args& a, const SmallTile& s) {
+    const int w_bytes = a.weight_type == MEGA_MOE_F32 ? 4 : 2;
+    return s.bytes * a.hidden <= 170000 + 25 * w_bytes * a.hidden;
 }
 
 // The workspace: the planes of what is split, then the parts of a split K.
@@ -651,7 +661,7 @@ bool forward_pairs(const mega_moe_router_logits_args& a) {
 Plan forward_plan(const mega_moe_router_logits_args& a) {
     const int64_t T = a.num_tokens, E = a.num_experts, H = a.hidden;
     Plan p{};
-    if (T <= SMALL_TOKENS) return p;
+    if (is_small(a, small_tile(a))) return p;
     p.split = split_for(forward_tiles(a), H, E <= 64 || forward_pairs(a) ? 512 : 256);
     p.parts = a.weight_type == MEGA_MOE_F32 ? 3 * E * H * 2 : 0;
     p.total = p.parts + (p.split.n > 1 ? p.split.n * T * E * 4 : 0);
@@ -731,12 +741,12 @@ int64_t router_logits_workspace(const mega_moe_router_logits_args& a) {
 
 void launch_router_logits(const mega_moe_router_logits_args& a, hipStream_t stream) {
     const bool f = a.weight_type == MEGA_MOE_F32;
-    if (a.num_tokens > SMALL_TOKENS) {
+    const SmallTile s = small_tile(a);
+    if (!is_small(a, s)) {
         if (f) launch_logits<3>(a, stream);
         else launch_logits<1>(a, stream);
         return;
     }
-    const SmallTile s = small_tile(a);
     const dim3 grid((unsigned)(tiles(a.num_tokens, s.t) * tiles(a.num_experts, s.e)));
     if (f) hipLaunchKernelGGL((moe_router_logits<true>), grid, dim3(1024), 0, stream, a, s.t, s.e);
     else hipLaunchKernelGGL((moe_router_logits<false>), grid, dim3(1024), 0, stream, a, s.t, s.e);

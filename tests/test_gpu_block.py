@@ -238,7 +238,14 @@ def _logits_fields(T, H, E, wt, x, w, extra):
     return dict(num_tokens=T, hidden=H, num_experts=E, weight_type=U.TYPE[wt], x=x, w=w, x_stride=H + extra)
 
 
-@pytest.mark.parametrize("T,H,E,wt,extra", LOGITS)
+# products that go through tiles in LDS: few, some and many experts, one part of K
+# and several, workgroups in pairs, odd sizes
+LOGITS_LARGE = [(9001, 1032, 29, BF16, 8), (5003, 1160, 17, F32, 0), (5003, 904, 50, BF16, 0), (3300, 904, 61, F32, 16),
+                (2050, 520, 330, BF16, 0), (1030, 776, 260, F32, 8), (8200, 72, 330, BF16, 0), (257, 7168, 512, BF16, 0),
+                (8200, 4104, 130, F32, 8)]
+
+
+@pytest.mark.parametrize("T,H,E,wt,extra", LOGITS + LOGITS_LARGE)
 def test_router_logits_match_the_reference(T, H, E, wt, extra):
     x, w, _ = _logits_inputs(T, H, E, wt, extra)
     logits, buf = U.padded(T, E, F32, extra)
