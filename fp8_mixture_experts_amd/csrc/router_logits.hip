@@ -767,13 +767,22 @@ void launch_router_logits_backward(const mega_moe_router_logits_args& a, hipStre
                     Result{E, H, p.split.n > 1 ? parts : a.dw, H, nullptr, nullptr, 0}, p.split.k, p.split.n};
     const unsigned w_blocks = a.dw ? (unsigned)(tiles(E, 64) * tiles(H, 128) * p.split.n) : 0;
     const unsigned x_blocks = a.dx ? (unsigned)(tiles(T, 64) * tiles(H, 128)) : 0;
-    using KW = Kind<Lay::row_major, 3, Lay::row_major, 1, 64, 128, 1, false>;
-    using KX1 = Kind<Lay::k_major, 2, Lay::row_major, 1, 64, 128, 1, true>;
-    using KX2 = Kind<Lay::k_major, 2, Lay::row_major, 2, 64, 128, 1, true>;
-    if (f)
-        hipLaunchKernelGGL((moe_router_gradients<KW, KX2>), dim3(w_blocks + x_blocks), dim3(256), 0, stream, w, w_blocks, x);
-    else
-        hipLaunchKernelGGL((moe_router_gradients<KW, KX1>), dim3(w_blocks + x_blocks), dim3(256), 0, stream, w, w_blocks, x);
+    const auto go = [&](auto stages) {
+        constexpr int S = decltype(stages)::value;
+        using KW = Kind<Lay::row_major, 3, Lay::row_major, 1, 64, 128, S, false>;
+        using KX1 = Kind<Lay::k_major, 2, Lay::row_major, 1, 64, 128, S, true>;
+        using KX2 = Kind<Lay::k_major, 2, Lay::row_major, 2, 64, 128, S, true>;
+        const dim3 grid(w_blocks + x_blocks);
+        if (f) hipLaunchKernelGGL((moe_router_gradients<KW, KX2>), grid, dim3(256), 0, stream, w, w_blocks, x);
+        else hipLaunchKernelGGL((moe_router_gradients<KW, KX1>), grid, dim3(256), 0, stream, w, w_blocks, x);
+    };
+    // Up to two workgroups to a compute unit: each keeps a step's loads in flight
+    // while it multiplies.  More of them hide each other's loads, and with one
+    // step in LDS four fit.  One and two steps: 3383 x 640 x 216 24 and 21 us (425
+    // workgroups), 4096 x 2048 x 128 27 and 27 (1280), 4096 x 4096 x 64 29 and 33
+    // (2560), 2589 x 5760 x 72 with float32 weights 44 and 61 (2205).
+    if (w_blocks + x_blocks <= 512) go(std::integral_constant<int, 2>{});
+    else go(std::integral_constant<int, 1>{});
     if (a.dw && p.split.n > 1) launch_join(parts, a.dw, E, H, H, p.split.n, stream);
 }
 

@@ -261,7 +261,8 @@ def test_router_logits_match_the_reference(T, H, E, wt, extra):
         assert torch.all(buf[:, E:] == 7.0)
 
 
-@pytest.mark.parametrize("T,H,E,wt,extra", LOGITS)
+# gradients of more than two workgroups to a compute unit
+@pytest.mark.parametrize("T,H,E,wt,extra", LOGITS + [(8200, 1032, 66, F32, 8), (4100, 2056, 70, BF16, 0)])
 @pytest.mark.parametrize("add", [False, True])
 def test_router_logits_backward_matches_the_reference(T, H, E, wt, extra, add):
     x, w, r = _logits_inputs(T, H, E, wt, extra)
