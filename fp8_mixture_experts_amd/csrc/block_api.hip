@@ -91,10 +91,11 @@ struct Tensors {
     }
 };
 
-// A row stride as given (0: dense), or -1 if it cannot be used.
+// A row stride as given (0: dense), or -1 if it cannot be used: 2^21 rows of the
+// widest stride stay within 63 bits of bytes.
 int64_t stride_of(int64_t given, int64_t cols, int64_t unit) {
     if (given == 0) return cols;
-    return given >= cols && given % unit == 0 && given <= ((int64_t)1 << 40) ? given : -1;
+    return given >= cols && given % unit == 0 && given <= ((int64_t)1 << 38) ? given : -1;
 }
 
 // The current device can run the kernels and holds the stream and the first
@@ -232,7 +233,8 @@ int check_router(const Args& a) {
     if (const int rc = check_tokens(a.num_tokens)) return rc;
     if (a.num_experts < 1 || a.num_experts > MAX_EXPERTS)
         return fail(MEGA_MOE_ERR_INVALID_ARG, "num_experts must be in [1, %d], got %d", MAX_EXPERTS, a.num_experts);
-    if (a.num_topk < 1) return bad("num_topk must be >= 1");
+    if (a.num_topk < 1 || a.num_topk > MAX_EXPERTS)
+        return fail(MEGA_MOE_ERR_INVALID_ARG, "num_topk must be in [1, %d], got %d", MAX_EXPERTS, a.num_topk);
     if (!type_ok(a.logits_type)) return bad("logits_type is neither MEGA_MOE_BF16 nor MEGA_MOE_F32");
     if (a.score != MEGA_MOE_SCORE_SOFTMAX && a.score != MEGA_MOE_SCORE_SIGMOID) return bad("unknown score");
     return MEGA_MOE_OK;

@@ -363,8 +363,8 @@ int mega_moe_profile_end(mega_moe_handle* h, float* ms_out, int32_t capacity, in
  *     its _workspace_bytes function says, contents of no matter); calls that
  *     may overlap in time need one each.
  *   - num_tokens is at most 2^21 (2097152).
- *   - Row strides are in elements; 0 means dense rows.  Outputs must not
- *     overlap inputs or each other, except where it is said.
+ *   - Row strides are in elements, at most 2^38; 0 means dense rows.  Outputs
+ *     must not overlap inputs or each other, except where it is said.
  *   - Sums are in float32, in an order that depends only on the argument
  *     block: the same call gives the same bits.  Each output is rounded once.
  */
@@ -538,7 +538,7 @@ int mega_moe_router_topk(const mega_moe_router_topk_args* a, void* stream);
 typedef struct mega_moe_balance_loss_args {
     int32_t num_tokens;       /* T                                               */
     int32_t num_experts;      /* E in [1, 1024]                                  */
-    int32_t num_topk;         /* k >= 1                                          */
+    int32_t num_topk;         /* k in [1, 1024]                                  */
     int32_t logits_type;
     int32_t score;
     int32_t num_sequences;    /* B; 0 or 1 without cu_seqlens: all T tokens are one */

@@ -128,13 +128,14 @@ REFUSED = {
         dict(logits=None), dict(topk_idx=None), dict(topk_weights=None), dict(logits=M + 2), dict(bias=2 * M + 1),
         dict(topk_idx=3 * M + 2), dict(logits_stride=4), dict(topk_idx=M), dict(topk_weights=3 * M + 16)]),
     "mega_moe_balance_loss": (_balance, SIZES + [
-        dict(num_experts=0), dict(num_topk=0), dict(score=-1), dict(num_sequences=2), dict(cu_seqlens=8 * M),
+        dict(num_experts=0), dict(num_topk=0), dict(num_topk=1025), dict(num_topk=2 ** 31 - 1), dict(score=-1),
+        dict(logits_stride=2 ** 38 + 1), dict(num_sequences=2), dict(cu_seqlens=8 * M),
         dict(num_sequences=-1), dict(num_sequences=(1 << 21) + 1, cu_seqlens=8 * M), dict(balance_coeff=float("inf")),
         dict(z_coeff=float("nan")), dict(loss=None), dict(counts=None), dict(tokens=None), dict(logits=None),
         dict(topk_idx=None), dict(loss=3 * M + 2), dict(logits=M + 2), dict(workspace=None), dict(workspace_bytes=8),
         dict(workspace=7 * M + 8), dict(counts=2 * M), dict(probs=4 * M), dict(logits_stride=5)]),
     "mega_moe_router_backward": (_router_backward, SIZES + [
-        dict(num_experts=1025), dict(num_topk=0), dict(renormalize=-1), dict(weight_scale=float("inf")),
+        dict(num_experts=1025), dict(num_topk=0), dict(num_topk=2 ** 31 - 1), dict(renormalize=-1), dict(weight_scale=float("inf")),
         dict(dweights=None, dloss=None), dict(logits=None), dict(dlogits=None), dict(topk_idx=None), dict(counts=None),
         dict(tokens=None), dict(num_sequences=3), dict(cu_seqlens=8 * M), dict(dlogits=M), dict(dlogits=3 * M),
         dict(dlogits_stride=4), dict(dlogits=7 * M + 2)]),
