@@ -523,6 +523,8 @@ moe_router_topk(mega_moe_router_topk_args a) {
 // The gradient of a token's logits, its experts in 16, 32 or 64 lanes.  The
 // top-k weights reach the scores that were taken (one slot to a lane, added to
 // the row through LDS); softmax spreads minus their mean over all experts.
+// Bound by memory for large batches (32768 tokens of 256 experts 16 us, 4.2 TB/s),
+// by a token's chain of loads and sums for others: 8192 tokens 6.3 us.
 template <int LANES, int NI>
 __global__ void __launch_bounds__(256)
 moe_router_backward(mega_moe_router_backward_args a) {
@@ -653,10 +655,11 @@ using Int = std::integral_constant<int, N>;
 
 template <typename F>
 void by_experts(int E, int lanes, F&& go) {
-    if (E <= 64 && lanes <= 16) {
+    if (E <= 128 && lanes <= 16) {
         if (E <= 16) go(Int<16>{}, Int<1>{});
         else if (E <= 32) go(Int<16>{}, Int<2>{});
-        else go(Int<16>{}, Int<4>{});
+        else if (E <= 64) go(Int<16>{}, Int<4>{});
+        else go(Int<16>{}, Int<8>{});
     } else if (E <= 256 && lanes <= 32) {
         if (E <= 64) go(Int<32>{}, Int<2>{});
         else if (E <= 128) go(Int<32>{}, Int<4>{});
@@ -670,13 +673,14 @@ void by_experts(int E, int lanes, F&& go) {
     }
 }
 
-// Lanes per token (at least): 16 up to 64 experts; 32 up to 256 for a large
-// batch, else 64.  Fewer lanes do less work in all, a step over lanes serving
-// more tokens, but in a longer chain per wave: measured at 256 experts, 8192
-// tokens 7.4 us with 32 lanes and 10.1 with 64, 1024 tokens 4.9 and 4.6.
-// `slots` that each need a lane can ask for more.
+// Lanes per token (at least): fewer of them do less work in all, a step over lanes
+// serving more tokens, but in a longer chain per wave.  The selection (k = 8) with
+// 64, 32 and 16 lanes: 64 experts, 8192 tokens 7.3, 5.0 and 4.2 us; 128 experts,
+// 1024 tokens 4.2, 4.5 and 4.9, 4096 6.1, 5.0 and 5.1, 8192 9.2, 6.3 and 5.7; 256
+// experts, 1024 tokens 4.4, 5.0 and 5.7, 4096 6.2, 5.4 and 5.9, 8192 9.1, 6.9 and
+// 6.9.  `slots` that each need a lane can ask for more.
 int lanes_for(int E, int tokens, int slots) {
-    const int lanes = E <= 64 ? 16 : tokens > 2048 ? 32 : 64;
+    const int lanes = E <= 64 || (E <= 128 && tokens > 4096) ? 16 : tokens > 2048 ? 32 : 64;
     return slots > 32 ? 64 : slots > lanes ? 32 : lanes;
 }
 unsigned workgroups(int tokens, int lanes) { return (unsigned)(((int64_t)tokens * lanes + 255) / 256); }

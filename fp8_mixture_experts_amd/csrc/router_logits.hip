@@ -35,7 +35,7 @@ __device__ __forceinline__ void split_bf16(const float (&v)[8], u32x4_t (&p)[P])
 // the fewest bytes to each (small_tile below) and fills the rest of the matrix
 // instruction with zeros, and each wave has the loads of STEPS steps in flight
 // (H = 7168: its 14 steps in two rounds).  128 x 7168 x 32: 14 us with whole
-// tiles on 16 compute units, 6.5 us with 4 x 4 on 256.
+// tiles on 16 compute units, 7.1 us with 4 x 4 on 256.
 template <bool WF32>
 __global__ void __launch_bounds__(1024)
 moe_router_logits(mega_moe_router_logits_args a, int tile_t, int tile_e) {
@@ -505,6 +505,9 @@ __device__ __forceinline__ void product(u32x4_t* lds, const Product& x, unsigned
     }
 }
 
+// 8192 x 7168 x 256 with float32 weights: 83 us, 1.08 PFLOP/s of BF16 terms (a
+// large library product reaches 1.44), with 5.7 us before it to split w and 9 us
+// after it to add the parts of K.
 template <typename K>
 __global__ void __launch_bounds__(K::THREADS)
 moe_router_product(Product x) {
@@ -514,6 +517,9 @@ moe_router_product(Product x) {
 
 // Both gradients in one launch: workgroups of dw, which are few and long, and
 // then those of dx, which fill up what is left.
+// 4096 x 4096 x 64: 20 us (67 MB of x and dx: 13 us), and 6 us to split dlogits and
+// add the parts of dw.  Larger tiles (64 x 256, 128 x 128), which take in a third
+// less, were no faster (34 us in all against 29).
 template <typename KW, typename KX>
 __global__ void __launch_bounds__(256)
 moe_router_gradients(Product w, unsigned w_blocks, Product x) {

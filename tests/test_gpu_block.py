@@ -363,6 +363,8 @@ TOPK_LARGE = [
     (2050, 96, 4, "softmax", BF16, True, 12, 5, 1, False),
     (2049, 300, 31, "sigmoid", F32, True, 1, 1, 1, True),
     (2052, 200, 30, "sigmoid", F32, True, 5, 2, 2, True),
+    (4100, 128, 8, "softmax", F32, False, 1, 1, 1, True),
+    (4098, 112, 6, "sigmoid", BF16, True, 7, 3, 2, True),
 ]
 
 
@@ -508,6 +510,7 @@ SEQ = [
     (3000, 16, 2, "softmax", F32, None, False),
     (2100, 200, 4, "softmax", F32, [3, 700, 2050], True),
     (2100, 70, 6, "sigmoid", BF16, list(range(0, 2101, 21)), False),
+    (4100, 120, 5, "softmax", F32, [0, 9, 4000], True),
 ]
 
 
