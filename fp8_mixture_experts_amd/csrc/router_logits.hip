@@ -29,39 +29,49 @@ __device__ __forceinline__ void split_bf16(const float (&v)[8], u32x4_t (&p)[P])
 }
 
 // Small products.  A tile of up to 16 tokens x 16 experts per workgroup; its 16
-// waves take the K steps of 32 in turn, straight from memory, and their sums
-// meet in LDS.  What bounds it is how fast one compute unit takes in its rows
-// (about 40 GB/s, whatever the others do), so the tile is the one that leaves
-// the fewest bytes to each (small_tile below) and fills the rest of the matrix
-// instruction with zeros, and each wave has the loads of STEPS steps in flight
-// (H = 7168: its 14 steps in two rounds).  128 x 7168 x 32: 14 us with whole
-// tiles on 16 compute units, 7.1 us with 4 x 4 on 256.
+// waves take the K steps in turn, straight from memory, and their sums meet in
+// LDS.  What bounds it is how fast one compute unit takes in its rows (about 40
+// GB/s, whatever the others do), so the tile is the one that leaves the fewest
+// bytes to each (small_tile below).  What a smaller tile than 16 x 16 leaves of
+// the matrix instruction's rows and columns are other slices of k: rows and
+// columns of the same slice meet on its diagonal blocks, whose sums are added at
+// the end.  So every lane has something to load, and a wave the loads of STEPS
+// steps in flight.  128 x 7168 x 32: 14 us with whole tiles on 16 compute
+// units, 8.0 with 4 x 4 on 256 and the rest of the instruction zero, 6.1 so; one
+// token 5.4 and 4.2, with float32 weights 8.8 and 5.6.
 template <bool WF32>
 __global__ void __launch_bounds__(1024)
 moe_router_logits(mega_moe_router_logits_args a, int tile_t, int tile_e) {
-    constexpr int STEPS = 7;
+    // 512 x 4096 x 64: 8 steps 8.6 us, 7 8.9; with float32 weights 11.2 and
+    // 12.5, but 1 x 7168 x 32 5.8 and 5.4, and so at most other sizes
+    constexpr int STEPS = WF32 ? 7 : 8;
     __shared__ float part[16][16][17];
+    __shared__ float sums[16][17];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int r = lane & 15, kq = (lane >> 4) * 8;
     const int H = a.hidden, E = a.num_experts;
     const int e_tiles = (E + tile_e - 1) / tile_e;
     const int e0 = (int)(blockIdx.x % e_tiles) * tile_e;
     const int t0 = (int)(blockIdx.x / e_tiles) * tile_t;
+    // `wide` rows and columns of the tile, `slices` of k
+    const int wide = tile_t > tile_e ? tile_t : tile_e, slices = 16 / wide;
+    const int r = lane & 15 & (wide - 1), k_lane = (lane & 15) / wide * 32 + (lane >> 4) * 8;
     const bool has_t = r < tile_t && t0 + r < a.num_tokens, has_e = r < tile_e && e0 + r < E;
-    const uint16_t* x = a.x + (int64_t)(t0 + r) * a.x_stride;
-    const size_t w_row = (size_t)(e0 + r) * H;
+    const uint16_t* x = a.x + (int64_t)(t0 + r) * a.x_stride + k_lane;
+    const size_t w_row = (size_t)(e0 + r) * H + k_lane;
+    const int chunk = 32 * slices;               // k of a wave's step
+    const int left = H - k_lane;                 // k from this lane's first on
     f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int k0 = wave * 32; k0 < H; k0 += 512 * STEPS) {
+    for (int k0 = wave * chunk; k0 < H; k0 += 16 * chunk * STEPS) {
         u32x4_t xv[STEPS], wv[STEPS][WF32 ? 2 : 1];
 #pragma unroll
         for (int s = 0; s < STEPS; ++s) {
-            const int k = k0 + s * 512 + kq;
+            const int k = k0 + s * 16 * chunk;
             const u32x4_t none = {0u, 0u, 0u, 0u};
             xv[s] = none;
 #pragma unroll
             for (int i = 0; i < (WF32 ? 2 : 1); ++i) wv[s][i] = none;
-            if (has_t && k < H) xv[s] = *reinterpret_cast<const u32x4_t*>(x + k);
-            if (has_e && k < H) {
+            if (has_t && k < left) xv[s] = *reinterpret_cast<const u32x4_t*>(x + k);
+            if (has_e && k < left) {
 #pragma unroll
                 for (int i = 0; i < (WF32 ? 2 : 1); ++i) wv[s][i] = raw8<WF32>(a.w, w_row + k)[i];
             }
@@ -84,15 +94,21 @@ moe_router_logits(mega_moe_router_logits_args a, int tile_t, int tile_e) {
     }
     // lane l holds experts 4 (l / 16) .. + 3 of token l % 16
 #pragma unroll
-    for (int i = 0; i < 4; ++i) part[wave][r][(lane >> 4) * 4 + i] = acc[i];
+    for (int i = 0; i < 4; ++i) part[wave][lane & 15][(lane >> 4) * 4 + i] = acc[i];
     __syncthreads();
-    if (threadIdx.x >= 256) return;
-    const int to = threadIdx.x >> 4, eo = threadIdx.x & 15;
-    float s = 0.0f;
+    // the waves' sums, then the slices'
+    const int row = threadIdx.x >> 4, col = threadIdx.x & 15;
+    if (threadIdx.x < 256) {
+        float s = 0.0f;
 #pragma unroll
-    for (int w = 0; w < 16; ++w) s += part[w][to][eo];
-    if (to < tile_t && eo < tile_e && t0 + to < a.num_tokens && e0 + eo < E)
-        a.logits[(int64_t)(t0 + to) * a.logits_stride + e0 + eo] = s;
+        for (int w = 0; w < 16; ++w) s += part[w][row][col];
+        sums[row][col] = s;
+    }
+    __syncthreads();
+    if (row >= tile_t || col >= tile_e || t0 + row >= a.num_tokens || e0 + col >= E) return;
+    float s = 0.0f;
+    for (int i = 0; i < slices; ++i) s += sums[i * wide + row][i * wide + col];
+    a.logits[(int64_t)(t0 + row) * a.logits_stride + e0 + col] = s;
 }
 
 // ---------------------------------------------------------------------------
