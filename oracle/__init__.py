@@ -21,6 +21,9 @@ by the page "PR357 Green-Context Split MegaMoE code review" (cited as
   activation scales, the BF16 partial cast and the FP32 top-k combine; the
   two GEMMs also for MXFP4 weights.
 
+* ``block``   the operators around the layer, with their gradients: norms with
+  gate and residual, the router's product and selection, the balance loss.
+
 Every function is pinned by ``tests/test_oracle_*.py`` against something other
 than itself (exhaustive codec properties, a library cast, exact rational brute
 force, closed forms and metamorphic relations).  Parity unpinned: which of two
