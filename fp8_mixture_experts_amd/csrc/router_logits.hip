@@ -115,30 +115,32 @@ moe_router_logits(mega_moe_router_logits_args a, int tile_t, int tile_e) {
 // Tiles through LDS, for batches of tokens and for the gradients.
 // C[m, n] = sum over k of A[m, k] B[n, k] on 32 x 32 x 16 BF16 matrix
 // instructions, each operand as one to three BF16 planes whose products add
-// into the same accumulators, the small ones first.  float32 operands are
-// split into planes in the workspace by moe_router_split beforehand: a tile's
-// values are used by many workgroups, which would each split them again.
+// into the same accumulators, the small ones first.  The float32 operands of the
+// gradients are split into planes in the workspace by moe_router_split beforehand
+// (many workgroups use a value); a float32 w of the forward product is split where
+// its fragments are read, by the wave that has its columns.
 //
 // A workgroup computes BM x BN.  Steps of 64 k go from memory straight into
 // LDS (16 bytes a lane, no registers), STAGES - 1 of them ahead
 // of the one that is multiplied.  An operand lies in memory, and in LDS, in
-// one of two ways:
+// one of three ways:
 //   k_major    rows of k: a fragment's eight k are one 16-byte read
+//   k_float    the same in float32: two reads, then split
 //   row_major  k after k, each a row of m (or n): the LDS reads that turn
 //              4 x 16 values around give four k of a lane's row at a time
 // Lanes that point outside an operand read zeros.
 //
 // LDS holds 16-byte chunks in the order in which they are loaded; where a
 // chunk comes from is permuted within its row, so that the reads of a fragment
-// spread over all banks: in a k_major row r chunk c lies at c ^ (r / 2) % 8;
-// of a row_major row the pairs of chunks (16 columns, one turned read) are permuted
-// by the bits in which the eight rows of a read differ.
+// spread over all banks: in a k_major row r chunk c lies at c ^ (r / 2) % 8, in a
+// k_float row at c ^ r % 16; of a row_major row the pairs of chunks (16 columns, one
+// turned read) are permuted by the bits in which the eight rows of a read differ.
 // ---------------------------------------------------------------------------
 
-enum class Lay { k_major, row_major };
+enum class Lay { k_major, row_major, k_float };
 
 struct Operand {
-    const uint16_t* p;
+    const void* p;
     int64_t plane;         // elements from one plane to the next
     int64_t stride;        // elements from one row to the next, in memory
     int64_t rows, k;       // extents: of m or n, and of k (rows in memory: of m or n
@@ -171,14 +173,17 @@ __device__ __forceinline__ int pair_swizzle(int row) {
 // One operand's planes of a step: R rows of m (or n) by STEP k.
 template <Lay L, int P, int R, int THREADS>
 struct Tile {
-    static constexpr int CHUNKS = R * STEP / 8;          // of a plane
+    static constexpr int SIZE = L == Lay::k_float ? 4 : 2, PER = 16 / SIZE;  // bytes of an element, elements of a chunk
+    static constexpr int IN = L == Lay::k_float ? 1 : P;  // planes in memory and LDS
+    static constexpr int CHUNKS = R * STEP / PER;        // of a plane
     static constexpr int PER_LANE = CHUNKS / THREADS;
-    static constexpr int LOADS = P * PER_LANE;           // per lane and step
-    static constexpr int WIDTH = L == Lay::k_major ? STEP / 8 : R / 8;       // chunks of a row
+    static constexpr int LOADS = IN * PER_LANE;          // per lane and step
+    static constexpr int WIDTH = L == Lay::row_major ? R / 8 : STEP / PER;   // chunks of a row
     static_assert(CHUNKS % THREADS == 0, "whole loads");
 
     __device__ __forceinline__ static int swizzle(int r) {
         if constexpr (L == Lay::row_major) return pair_swizzle<R>(r) << 1;
+        else if constexpr (L == Lay::k_float) return r & 15;
         else return r >> 1 & 7;
     }
 
@@ -191,8 +196,8 @@ struct Tile {
         for (int i = 0; i < PER_LANE; ++i) {
             const int id = i * THREADS + (int)threadIdx.x, r = id / WIDTH;
             const int c = (id % WIDTH) ^ swizzle(r);
-            const bool in = L == Lay::k_major ? row0 + r < o.rows : row0 + c * 8 < o.rows;
-            at[i] = in ? (uint32_t)((r * o.stride + c * 8) * 2) : OUTSIDE;
+            const bool in = L == Lay::row_major ? row0 + c * 8 < o.rows : row0 + r < o.rows;
+            at[i] = in ? (uint32_t)((r * o.stride + c * PER) * SIZE) : OUTSIDE;
         }
     }
 
@@ -202,19 +207,20 @@ struct Tile {
         const int64_t left = (k_end < o.k ? k_end : o.k) - k0;
         const int wave = threadIdx.x >> 6;
 #pragma unroll
-        for (int p = 0; p < P; ++p) {
+        for (int p = 0; p < IN; ++p) {
             // rows past the last lie outside of the buffer; a k_major row's
             // chunks past its last k must be pointed there
-            const int64_t n = L == Lay::k_major ? o.rows - row0 : left < STEP ? left : STEP;
-            const int64_t width = L == Lay::k_major ? left : o.rows - row0;
-            const auto buf = buffer_of(o.p + p * o.plane + (L == Lay::k_major ? row0 * o.stride + k0 : k0 * o.stride + row0),
-                                       left > 0 ? (((n < R ? n : R) - 1) * o.stride + width) * 2 : 0);
+            const int64_t n = L != Lay::row_major ? o.rows - row0 : left < STEP ? left : STEP;
+            const int64_t width = L != Lay::row_major ? left : o.rows - row0;
+            const int64_t first = p * o.plane + (L != Lay::row_major ? row0 * o.stride + k0 : k0 * o.stride + row0);
+            const auto buf = buffer_of(static_cast<const char*>(o.p) + first * SIZE,
+                                       left > 0 ? (((n < R ? n : R) - 1) * o.stride + width) * SIZE : 0);
 #pragma unroll
             for (int i = 0; i < PER_LANE; ++i) {
                 uint32_t off = at[i];
-                if (L == Lay::k_major && left < STEP) {
+                if (L != Lay::row_major && left < STEP) {
                     const int id = i * THREADS + (int)threadIdx.x;
-                    if (((id % WIDTH) ^ swizzle(id / WIDTH)) * 8 >= left) off = OUTSIDE;
+                    if (((id % WIDTH) ^ swizzle(id / WIDTH)) * PER >= left) off = OUTSIDE;
                 }
                 u32x4_t* to = lds + p * CHUNKS + i * THREADS + __builtin_amdgcn_readfirstlane(wave) * 64;
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (LDS_PTR void*)to, 16, (int)off, 0, 0, 0);
@@ -227,6 +233,13 @@ struct Tile {
     __device__ __forceinline__ static bf16x8_t fragment(const u32x4_t* lds, int p, int r0, int kk) {
         const int lane = threadIdx.x & 63, r = r0 + (lane & 31), c = kk * 2 + (lane >> 5);
         return __builtin_bit_cast(bf16x8_t, lds[p * CHUNKS + r * WIDTH + (c ^ swizzle(r))]);
+    }
+    // The same of a k_float tile, split into its planes.
+    __device__ __forceinline__ static void fragment(const u32x4_t* lds, int r0, int kk, u32x4_t (&planes)[P]) {
+        const int lane = threadIdx.x & 63, r = r0 + (lane & 31), c = kk * 4 + (lane >> 5) * 2;
+        float v[8];
+        values8<true>(lds[r * WIDTH + (c ^ swizzle(r))], lds[r * WIDTH + ((c + 1) ^ swizzle(r))], v);
+        split_bf16<P>(v, planes);
     }
 
     // Of a row_major tile: where this lane's part of it starts, as an LDS byte
@@ -349,7 +362,7 @@ struct Kind {
     static constexpr int PITCH = BN + 4;         // BF16 results go out through LDS, as rows of floats
     using TA = Tile<LA, PA, BM, THREADS>;
     using TB = Tile<LB, PB, BN, THREADS>;
-    static constexpr int STAGE = PA * TA::CHUNKS + PB * TB::CHUNKS;
+    static constexpr int STAGE = TA::IN * TA::CHUNKS + TB::IN * TB::CHUNKS;
     static constexpr int OUT = OUT_BF16 ? BM * PITCH / 4 : 0;
     static constexpr int LDS = STAGE * STAGES > OUT ? STAGE * STAGES : OUT;
 };
@@ -391,7 +404,7 @@ __device__ __forceinline__ void product(u32x4_t* lds, const Product& x, unsigned
     tb.place(Bo, n0);
     const auto load = [&](int64_t k0, int stage) {
         ta.load(A, m0, k0, k_end, lds + stage * STAGE);
-        tb.load(Bo, n0, k0, k_end, lds + stage * STAGE + PA * TA::CHUNKS);
+        tb.load(Bo, n0, k0, k_end, lds + stage * STAGE + TA::IN * TA::CHUNKS);
     };
     constexpr int LOADS = TA::LOADS + TB::LOADS;
     // steps past the last load nothing but zeros, so that the count of loads in
@@ -410,7 +423,7 @@ __device__ __forceinline__ void product(u32x4_t* lds, const Product& x, unsigned
             load(k0 + (STAGES - 1) * STEP, stage == 0 ? STAGES - 1 : stage - 1);
         }
         const u32x4_t* la = lds + stage * STAGE;
-        const u32x4_t* lb = la + PA * TA::CHUNKS;
+        const u32x4_t* lb = la + TA::IN * TA::CHUNKS;
         uint32_t at[3] = {0, 0, 0};
         if constexpr (LA == Lay::row_major) at[0] = TA::turned_at(la, wm);
         if constexpr (LB == Lay::row_major) {
@@ -432,6 +445,14 @@ __device__ __forceinline__ void product(u32x4_t* lds, const Product& x, unsigned
                 for (int p = 0; p < PB; ++p)
 #pragma unroll
                     for (int j = 0; j < TN; ++j) fb[p][j] = TB::fragment(lb, p, wn + j * 32, kk);
+            } else if constexpr (LB == Lay::k_float) {
+#pragma unroll
+                for (int j = 0; j < TN; ++j) {
+                    u32x4_t planes[PB];
+                    TB::fragment(lb, wn + j * 32, kk, planes);
+#pragma unroll
+                    for (int p = 0; p < PB; ++p) fb[p][j] = __builtin_bit_cast(bf16x8_t, planes[p]);
+                }
             } else if constexpr (LA == Lay::row_major) {
                 turned<kk * TA::NEXT_KK, TA::NEXT_HALF, TA::NEXT_PLANE, kk * TB::NEXT_KK, TB::NEXT_HALF>(at[0], fa, at[1],
                                                                                                          at[2], fb);
@@ -521,9 +542,8 @@ __device__ __forceinline__ void product(u32x4_t* lds, const Product& x, unsigned
     }
 }
 
-// 8192 x 7168 x 256 with float32 weights: 83 us, 1.08 PFLOP/s of BF16 terms (a
-// large library product reaches 1.44), with 5.7 us before it to split w and 9 us
-// after it to add the parts of K.
+// 8192 x 7168 x 256 with float32 weights: 90 us, 1.0 PFLOP/s of BF16 terms (a
+// large library product reaches 1.44), with 9 us after it to add the parts of K.
 template <typename K>
 __global__ void __launch_bounds__(K::THREADS)
 moe_router_product(Product x) {
@@ -647,15 +667,14 @@ SmallTile small_tile(const mega_moe_router_logits_args& a) {
 }
 
 // Whether the 16 x 16 tiles compute the logits: one launch at about 37 kB/us for
-// each compute unit, against two or three launches that read every row less
-// often.  They cross where a compute unit takes in 170 kB and 25 rows of w:
-// 16 x 16 and 128 x 128 tiles at 1024 x 640 x 128 5.5 and 10.8 us (82 kB), 8192 x
+// each compute unit, against one or two launches that read every row less often.
+// They cross where a compute unit takes in about 200 kB and 25 rows of BF16:
+// 16 x 16 and 128-row tiles at 1024 x 640 x 128 5.5 and 10.8 us (82 kB), 8192 x
 // 640 x 31 9.9 and 9.3 (164 kB), 2048 x 7168 x 31 15.3 and 16.0 (459 kB), 512 x
-// 7168 x 512 54 and 19 (1.8 MB); with float32 weights 2048 x 1792 x 64 14.7 and
-// 18.3 (344 kB), 4096 x 1792 x 64 27 and 19 (688 kB).
+// 7168 x 512 54 and 19 (1.8 MB); with float32 weights 512 x 4096 x 128 15.6 and
+// 17.9 (393 kB), 1024 x 1792 x 256 28 and 19.5 (688 kB).
 bool is_small(const mega_moe_router_logits_args& a, const SmallTile& s) {
-    const int w_bytes = a.weight_type == MEGA_MOE_F32 ? 4 : 2;
-    return s.bytes * a.hidden <= 170000 + 25 * w_bytes * a.hidden;
+    return s.bytes * a.hidden <= 200000 + 50 * a.hidden;
 }
 
 // The workspace: the planes of what is split, then the parts of a split K.
@@ -673,7 +692,7 @@ int64_t forward_tiles(const mega_moe_router_logits_args& a) {
 
 // Whether two workgroups share a compute unit: with float32 weights, where one
 // each would leave parts of K longer than 2048.  Measured at 8192 x 7168 x 256
-// 100 us in pairs and 112 alone, at 8192 x 2048 x 512 65 and 57; with BF16
+// 102 us in pairs and 115 alone, at 8192 x 2048 x 512 66 and 63; with BF16
 // weights, whose loads take more of the time than the products, 58 and 56.
 bool forward_pairs(const mega_moe_router_logits_args& a) {
     if (a.num_experts <= 64 || a.weight_type != MEGA_MOE_F32) return false;
@@ -684,9 +703,10 @@ Plan forward_plan(const mega_moe_router_logits_args& a) {
     const int64_t T = a.num_tokens, E = a.num_experts, H = a.hidden;
     Plan p{};
     if (is_small(a, small_tile(a))) return p;
-    p.split = split_for(forward_tiles(a), H, E <= 64 || forward_pairs(a) ? 512 : 256);
-    p.parts = a.weight_type == MEGA_MOE_F32 ? 3 * E * H * 2 : 0;
-    p.total = p.parts + (p.split.n > 1 ? p.split.n * T * E * 4 : 0);
+    // two workgroups to a compute unit, or one
+    const bool two = E <= 32 ? a.weight_type == MEGA_MOE_BF16 : E <= 64 || forward_pairs(a);
+    p.split = split_for(forward_tiles(a), H, two ? 512 : 256);
+    p.total = p.split.n > 1 ? p.split.n * T * E * 4 : 0;
     return p;
 }
 
@@ -714,44 +734,48 @@ void launch_join(const float* parts, float* out, int64_t M, int64_t N, int64_t s
                        parts, out, M, N, stride, splits);
 }
 
-// The forward product's kinds: PW planes of w.
-template <int PW>
-struct Forward {
+// The forward product's kinds.  A float32 w is split where its fragments are
+// read, so the fewer waves share columns, the less is split: with a wave's 32
+// columns its own (1 x 4 waves) 8192 x 7168 x 256 takes 102 us and 512 x 7168 x
+// 256 22, with planes of w in the workspace 112 and 27, and with 4 x 2 waves that
+// split 155 and 26.
+struct Bf16Forward {
     template <int BN, int STAGES, int WM, int WN>
-    using Of = Kind<Lay::k_major, 1, Lay::k_major, PW, 128, BN, STAGES, false, WM, WN>;
-    using Few = Of<32, PW == 3 ? 1 : 2, 4, 1>;
-    using Some = Of<64, PW == 3 ? 1 : 2, 4, 1>;
-    // A workgroup to a compute unit, with steps in flight; and two of them that
+    using Of = Kind<Lay::k_major, 1, Lay::k_major, 1, 128, BN, STAGES, false, WM, WN>;
+    using Few = Of<32, 2, 4, 1>;
+    using Some = Of<64, 2, 4, 1>;
+    using Many = Of<128, 4, 4, 2>;
+    using ManyPairs = Many;
+};
+struct F32Forward {
+    template <int BN, int STAGES, int WM, int WN>
+    using Of = Kind<Lay::k_major, 1, Lay::k_float, 3, 128, BN, STAGES, false, WM, WN>;
+    using Few = Of<32, 4, 4, 1>;
+    using Some = Of<64, 2, 2, 2>;
+    // A workgroup to a compute unit, with a step in flight; and two of them that
     // hide each other's loads.
-    using Many = Of<128, PW == 3 ? 2 : 4, 4, 2>;
-    using ManyPairs = Of<128, 1, 2, 2>;
+    using Many = Of<128, 2, 1, 4>;
+    using ManyPairs = Of<128, 1, 1, 4>;
 };
 
-template <int PW, typename K>
-void launch_logits(const mega_moe_router_logits_args& a, hipStream_t stream) {
+template <typename K>
+void launch_product(const mega_moe_router_logits_args& a, hipStream_t stream) {
     const Plan p = forward_plan(a);
     const int64_t T = a.num_tokens, H = a.hidden, E = a.num_experts;
-    const Operand A{a.x, 0, a.x_stride, T, H};
-    Operand W{static_cast<const uint16_t*>(a.w), 0, H, E, H};
-    if (PW == 3) {
-        launch_split(Planes{static_cast<const float*>(a.w), H, E, H, reinterpret_cast<uint16_t*>(at(a, p.w_planes)), H, 3},
-                     Planes{}, stream);
-        W.p = reinterpret_cast<uint16_t*>(at(a, p.w_planes));
-        W.plane = E * H;
-    }
     float* parts = reinterpret_cast<float*>(at(a, p.parts));
     const Result out{T, E, p.split.n > 1 ? parts : a.logits, a.logits_stride, nullptr, nullptr, 0};
+    const Product x{Operand{a.x, 0, a.x_stride, T, H}, Operand{a.w, 0, H, E, H}, out, p.split.k, p.split.n};
     hipLaunchKernelGGL((moe_router_product<K>), dim3((unsigned)(tiles(T, K::BM) * tiles(E, K::BN) * p.split.n)),
-                       dim3(K::THREADS), 0, stream, Product{A, W, out, p.split.k, p.split.n});
+                       dim3(K::THREADS), 0, stream, x);
     if (p.split.n > 1) launch_join(parts, a.logits, T, E, a.logits_stride, p.split.n, stream);
 }
 
-template <int PW>
-void launch_logits(const mega_moe_router_logits_args& a, hipStream_t stream) {
-    if (a.num_experts <= 32) launch_logits<PW, typename Forward<PW>::Few>(a, stream);
-    else if (a.num_experts <= 64) launch_logits<PW, typename Forward<PW>::Some>(a, stream);
-    else if (PW == 1 || !forward_pairs(a)) launch_logits<PW, typename Forward<PW>::Many>(a, stream);
-    else if constexpr (PW == 3) launch_logits<PW, typename Forward<PW>::ManyPairs>(a, stream);
+template <typename F>
+void launch_forward(const mega_moe_router_logits_args& a, hipStream_t stream) {
+    if (a.num_experts <= 32) launch_product<typename F::Few>(a, stream);
+    else if (a.num_experts <= 64) launch_product<typename F::Some>(a, stream);
+    else if (forward_pairs(a)) launch_product<typename F::ManyPairs>(a, stream);
+    else launch_product<typename F::Many>(a, stream);
 }
 
 }  // namespace
@@ -765,8 +789,8 @@ void launch_router_logits(const mega_moe_router_logits_args& a, hipStream_t stre
     const bool f = a.weight_type == MEGA_MOE_F32;
     const SmallTile s = small_tile(a);
     if (!is_small(a, s)) {
-        if (f) launch_logits<3>(a, stream);
-        else launch_logits<1>(a, stream);
+        if (f) launch_forward<F32Forward>(a, stream);
+        else launch_forward<Bf16Forward>(a, stream);
         return;
     }
     const dim3 grid((unsigned)(tiles(a.num_tokens, s.t) * tiles(a.num_experts, s.e)));
