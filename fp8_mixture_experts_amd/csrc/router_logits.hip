@@ -42,9 +42,10 @@ __device__ __forceinline__ void split_bf16(const float (&v)[8], u32x4_t (&p)[P])
 template <bool WF32>
 __global__ void __launch_bounds__(1024)
 moe_router_logits(mega_moe_router_logits_args a, int tile_t, int tile_e) {
-    // 512 x 4096 x 64: 8 steps 8.6 us, 7 8.9; with float32 weights 11.2 and
-    // 12.5, but 1 x 7168 x 32 5.8 and 5.4, and so at most other sizes
-    constexpr int STEPS = WF32 ? 7 : 8;
+    // Few enough that two workgroups share a compute unit (64 registers): with 8
+    // steps, and 7 with float32 weights, 1024 x 640 x 151 takes 8.4 and 14.7 us, so
+    // 6.9 and 8.7, and 1 x 7168 x 32 as long.
+    constexpr int STEPS = WF32 ? 2 : 4;
     __shared__ float part[16][16][17];
     __shared__ float sums[16][17];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -666,15 +667,16 @@ SmallTile small_tile(const mega_moe_router_logits_args& a) {
     return best;
 }
 
-// Whether the 16 x 16 tiles compute the logits: one launch at about 37 kB/us for
+// Whether the 16 x 16 tiles compute the logits: one launch at about 40 kB/us for
 // each compute unit, against one or two launches that read every row less often.
-// They cross where a compute unit takes in about 200 kB and 25 rows of BF16:
-// 16 x 16 and 128-row tiles at 1024 x 640 x 128 5.5 and 10.8 us (82 kB), 8192 x
-// 640 x 31 9.9 and 9.3 (164 kB), 2048 x 7168 x 31 15.3 and 16.0 (459 kB), 512 x
-// 7168 x 512 54 and 19 (1.8 MB); with float32 weights 512 x 4096 x 128 15.6 and
-// 17.9 (393 kB), 1024 x 1792 x 256 28 and 19.5 (688 kB).
+// They cross where a compute unit takes in about 300 kB and 20 rows of BF16:
+// 16 x 16 and 128-row tiles at 1024 x 640 x 128 5.0 and 10.7 us (82 kB), 8192 x
+// 640 x 31 8.5 and 9.5 (164 kB), 2048 x 7168 x 31 15.3 and 15.8 (459 kB), 4096 x
+// 4096 x 31 17.2 and 16.5 (524 kB), 512 x 7168 x 512 51 and 19 (1.8 MB); with
+// float32 weights 512 x 4096 x 128 14 and 18 (393 kB), 1024 x 1792 x 256 22 and 20
+// (688 kB).
 bool is_small(const mega_moe_router_logits_args& a, const SmallTile& s) {
-    return s.bytes * a.hidden <= 200000 + 50 * a.hidden;
+    return s.bytes * a.hidden <= 300000 + 40 * a.hidden;
 }
 
 // The workspace: the planes of what is split, then the parts of a split K.

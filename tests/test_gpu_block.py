@@ -242,7 +242,8 @@ def _logits_fields(T, H, E, wt, x, w, extra):
 # and several, workgroups in pairs, odd sizes
 LOGITS_LARGE = [(9001, 1032, 29, BF16, 8), (5003, 1160, 17, F32, 0), (5003, 904, 50, BF16, 0), (3300, 904, 61, F32, 16),
                 (2050, 520, 330, BF16, 0), (1030, 776, 260, F32, 8), (8200, 72, 330, BF16, 0), (257, 7168, 512, BF16, 0),
-                (8200, 4104, 130, F32, 8)]
+                (8200, 4104, 130, F32, 8), (9001, 1160, 29, BF16, 8), (5003, 1480, 17, F32, 0),
+                (5003, 1096, 50, BF16, 0), (13000, 72, 330, BF16, 0)]
 
 
 @pytest.mark.parametrize("T,H,E,wt,extra", LOGITS + LOGITS_LARGE)
