@@ -126,6 +126,31 @@ def test_norm_alone_in_place_and_with_few_outputs():
     assert (q == torch.from_numpy(codecs.e4m3_encode_rne(want["q"])).cuda()).float().mean() >= 0.999
 
 
+# several rows to a group of threads, each loaded while the one before it is stored
+@pytest.mark.parametrize("T,H,stream", [(5000, 640, BF16), (2100, 1032, F32), (777, 7168, BF16)])
+def test_norm_and_gradients_in_place_equal_those_apart(T, H, stream):
+    r = _gen(T + H)
+    h, y, dn, w, gate = r(T, H, dtype=stream), r(T, H, dtype=BF16), r(T, H, dtype=BF16), r(H), r(T, dtype=BF16)
+    base = dict(num_tokens=T, hidden=H, stream_type=U.TYPE[stream], weight_type=B.MEGA_MOE_F32, pre_eps=1e-6,
+                post_eps=1e-6, residual_scale=0.5, y=y, gate=gate, gate_kind=U.KIND["token"], gate_type=B.MEGA_MOE_BF16,
+                post_weight=w, pre_weight=w)
+    out = []
+    for place in (False, True):
+        src = h.clone()
+        to, n = src if place else torch.empty_like(h), torch.empty(T, H, dtype=BF16, device="cuda")
+        B.mega_moe_norm(B.make_args(B.mega_moe_norm_args, h=src, r=to, n=n, **base), U.current_stream())
+        dr = h.clone()
+        dh, dy, dgate, dw = dr if place else torch.empty_like(h), torch.empty_like(y), r(T), r(H)
+        a = B.make_args(B.mega_moe_norm_backward_args, r=to, dr=dr, dn=dn, dh=dh, dy=dy, dgate=dgate, dpost_weight=dw,
+                        **base)
+        B.set_args(a, **U.workspace(B.mega_moe_norm_workspace_bytes(a)))
+        B.mega_moe_norm_backward(a, U.current_stream())
+        out.append((to, n, dh, dy, dgate, dw))
+    torch.cuda.synchronize()
+    for apart, inside in zip(*out):
+        assert torch.equal(apart, inside)
+
+
 def test_norm_of_zero_tiny_and_not_finite_rows():
     T, H = 6, 256
     h = torch.zeros(T, H, device="cuda")
