@@ -116,33 +116,32 @@ moe_router_logits(mega_moe_router_logits_args a, int tile_t, int tile_e) {
 // Tiles through LDS, for batches of tokens and for the gradients.
 // C[m, n] = sum over k of A[m, k] B[n, k] on 32 x 32 x 16 BF16 matrix
 // instructions, each operand as one to three BF16 planes whose products add
-// into the same accumulators, the small ones first.  The float32 operands of the
-// gradients are split into planes in the workspace by moe_router_split beforehand
-// (many workgroups use a value); a float32 w of the forward product is split where
-// its fragments are read, by the wave that has its columns.
+// into the same accumulators, the small ones first.  A float32 operand is split
+// into its planes where its fragments are read.
 //
 // A workgroup computes BM x BN.  Steps of 64 k go from memory straight into
 // LDS (16 bytes a lane, no registers), STAGES - 1 of them ahead
 // of the one that is multiplied.  An operand lies in memory, and in LDS, in
-// one of three ways:
+// one of four ways:
 //   k_major    rows of k: a fragment's eight k are one 16-byte read
-//   k_float    the same in float32: two reads, then split
+//   k_float    the same in float32: two reads
 //   row_major  k after k, each a row of m (or n): the LDS reads that turn
 //              4 x 16 values around give four k of a lane's row at a time
+//   row_float  the same in float32: eight reads of one value
 // Lanes that point outside an operand read zeros.
 //
 // LDS holds 16-byte chunks in the order in which they are loaded; where a
 // chunk comes from is permuted within its row, so that the reads of a fragment
 // spread over all banks: in a k_major row r chunk c lies at c ^ (r / 2) % 8, in a
-// k_float row at c ^ r % 16; of a row_major row the pairs of chunks (16 columns, one
-// turned read) are permuted by the bits in which the eight rows of a read differ.
+// k_float row at c ^ r % 16, in a row_float row at c ^ (r & 8); of a row_major row the
+// pairs of chunks (16 columns, one turned read) are permuted by the bits in which the
+// eight rows of a read differ.
 // ---------------------------------------------------------------------------
 
-enum class Lay { k_major, row_major, k_float };
+enum class Lay { k_major, row_major, k_float, row_float };
 
 struct Operand {
     const void* p;
-    int64_t plane;         // elements from one plane to the next
     int64_t stride;        // elements from one row to the next, in memory
     int64_t rows, k;       // extents: of m or n, and of k (rows in memory: of m or n
                            // for k_major, of k for row_major)
@@ -150,7 +149,6 @@ struct Operand {
 
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4a_t __attribute__((ext_vector_type(4), aligned(4)));
-typedef short s16x4_t __attribute__((ext_vector_type(4)));
 #define LDS_PTR __attribute__((address_space(3)))
 
 constexpr int STEP = 64;                       // k of a step
@@ -174,17 +172,18 @@ __device__ __forceinline__ int pair_swizzle(int row) {
 // One operand's planes of a step: R rows of m (or n) by STEP k.
 template <Lay L, int P, int R, int THREADS>
 struct Tile {
-    static constexpr int SIZE = L == Lay::k_float ? 4 : 2, PER = 16 / SIZE;  // bytes of an element, elements of a chunk
-    static constexpr int IN = L == Lay::k_float ? 1 : P;  // planes in memory and LDS
-    static constexpr int CHUNKS = R * STEP / PER;        // of a plane
-    static constexpr int PER_LANE = CHUNKS / THREADS;
-    static constexpr int LOADS = IN * PER_LANE;          // per lane and step
-    static constexpr int WIDTH = L == Lay::row_major ? R / 8 : STEP / PER;   // chunks of a row
+    static constexpr bool ROWS_OF_K = L == Lay::k_major || L == Lay::k_float;
+    static constexpr bool FLOAT = L == Lay::k_float || L == Lay::row_float;
+    static constexpr int SIZE = FLOAT ? 4 : 2, PER = 16 / SIZE;      // bytes of an element, elements of a chunk
+    static constexpr int CHUNKS = R * STEP / PER;
+    static constexpr int PER_LANE = CHUNKS / THREADS;    // loads per lane and step
+    static constexpr int WIDTH = (ROWS_OF_K ? STEP : R) / PER;       // chunks of a row
     static_assert(CHUNKS % THREADS == 0, "whole loads");
 
     __device__ __forceinline__ static int swizzle(int r) {
         if constexpr (L == Lay::row_major) return pair_swizzle<R>(r) << 1;
         else if constexpr (L == Lay::k_float) return r & 15;
+        else if constexpr (L == Lay::row_float) return r & 8;
         else return r >> 1 & 7;
     }
 
@@ -197,7 +196,7 @@ struct Tile {
         for (int i = 0; i < PER_LANE; ++i) {
             const int id = i * THREADS + (int)threadIdx.x, r = id / WIDTH;
             const int c = (id % WIDTH) ^ swizzle(r);
-            const bool in = L == Lay::row_major ? row0 + c * 8 < o.rows : row0 + r < o.rows;
+            const bool in = ROWS_OF_K ? row0 + r < o.rows : row0 + c * PER < o.rows;
             at[i] = in ? (uint32_t)((r * o.stride + c * PER) * SIZE) : OUTSIDE;
         }
     }
@@ -207,40 +206,48 @@ struct Tile {
     __device__ __forceinline__ void load(const Operand& o, int64_t row0, int64_t k0, int64_t k_end, u32x4_t* lds) const {
         const int64_t left = (k_end < o.k ? k_end : o.k) - k0;
         const int wave = threadIdx.x >> 6;
+        // rows past the last lie outside of the buffer; chunks past the last k of
+        // a row of k must be pointed there
+        const int64_t n = ROWS_OF_K ? o.rows - row0 : left < STEP ? left : STEP;
+        const int64_t width = ROWS_OF_K ? left : o.rows - row0;
+        const int64_t first = ROWS_OF_K ? row0 * o.stride + k0 : k0 * o.stride + row0;
+        const auto buf = buffer_of(static_cast<const char*>(o.p) + first * SIZE,
+                                   left > 0 ? (((n < R ? n : R) - 1) * o.stride + width) * SIZE : 0);
 #pragma unroll
-        for (int p = 0; p < IN; ++p) {
-            // rows past the last lie outside of the buffer; a k_major row's
-            // chunks past its last k must be pointed there
-            const int64_t n = L != Lay::row_major ? o.rows - row0 : left < STEP ? left : STEP;
-            const int64_t width = L != Lay::row_major ? left : o.rows - row0;
-            const int64_t first = p * o.plane + (L != Lay::row_major ? row0 * o.stride + k0 : k0 * o.stride + row0);
-            const auto buf = buffer_of(static_cast<const char*>(o.p) + first * SIZE,
-                                       left > 0 ? (((n < R ? n : R) - 1) * o.stride + width) * SIZE : 0);
-#pragma unroll
-            for (int i = 0; i < PER_LANE; ++i) {
-                uint32_t off = at[i];
-                if (L != Lay::row_major && left < STEP) {
-                    const int id = i * THREADS + (int)threadIdx.x;
-                    if (((id % WIDTH) ^ swizzle(id / WIDTH)) * PER >= left) off = OUTSIDE;
-                }
-                u32x4_t* to = lds + p * CHUNKS + i * THREADS + __builtin_amdgcn_readfirstlane(wave) * 64;
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (LDS_PTR void*)to, 16, (int)off, 0, 0, 0);
+        for (int i = 0; i < PER_LANE; ++i) {
+            uint32_t off = at[i];
+            if (ROWS_OF_K && left < STEP) {
+                const int id = i * THREADS + (int)threadIdx.x;
+                if (((id % WIDTH) ^ swizzle(id / WIDTH)) * PER >= left) off = OUTSIDE;
             }
+            u32x4_t* to = lds + i * THREADS + __builtin_amdgcn_readfirstlane(wave) * 64;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(buf, (LDS_PTR void*)to, 16, (int)off, 0, 0, 0);
         }
     }
 
-    // The fragment of rows r0 .. r0 + 31 and k 16 kk .. + 15 of a plane of a
-    // k_major tile: lane l holds row r0 + l % 32, k 8 (l / 32) .. + 7 of them.
-    __device__ __forceinline__ static bf16x8_t fragment(const u32x4_t* lds, int p, int r0, int kk) {
+    // The fragment of rows r0 .. r0 + 31 and k 16 kk .. + 15 of a k_major tile:
+    // lane l holds row r0 + l % 32, k 8 (l / 32) .. + 7 of them.
+    __device__ __forceinline__ static bf16x8_t fragment(const u32x4_t* lds, int r0, int kk) {
         const int lane = threadIdx.x & 63, r = r0 + (lane & 31), c = kk * 2 + (lane >> 5);
-        return __builtin_bit_cast(bf16x8_t, lds[p * CHUNKS + r * WIDTH + (c ^ swizzle(r))]);
+        return __builtin_bit_cast(bf16x8_t, lds[r * WIDTH + (c ^ swizzle(r))]);
     }
-    // The same of a k_float tile, split into its planes.
-    __device__ __forceinline__ static void fragment(const u32x4_t* lds, int r0, int kk, u32x4_t (&planes)[P]) {
-        const int lane = threadIdx.x & 63, r = r0 + (lane & 31), c = kk * 4 + (lane >> 5) * 2;
+    // The same of a float tile, split into its planes.
+    __device__ __forceinline__ static void fragment(const u32x4_t* lds, int r0, int kk, bf16x8_t (&planes)[P]) {
+        const int lane = threadIdx.x & 63, r = r0 + (lane & 31);
         float v[8];
-        values8<true>(lds[r * WIDTH + (c ^ swizzle(r))], lds[r * WIDTH + ((c + 1) ^ swizzle(r))], v);
-        split_bf16<P>(v, planes);
+        if constexpr (L == Lay::k_float) {
+            const int c = kk * 4 + (lane >> 5) * 2;
+            values8<true>(lds[r * WIDTH + (c ^ swizzle(r))], lds[r * WIDTH + ((c + 1) ^ swizzle(r))], v);
+        } else {
+            const int k = kk * 16 + (lane >> 5) * 8;     // eight k with the same swizzle
+            const float* q = reinterpret_cast<const float*>(lds + k * WIDTH + (r / 4 ^ swizzle(k))) + r % 4;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = q[i * WIDTH * 4];
+        }
+        u32x4_t p[P];
+        split_bf16<P>(v, p);
+#pragma unroll
+        for (int i = 0; i < P; ++i) planes[i] = __builtin_bit_cast(bf16x8_t, p[i]);
     }
 
     // Of a row_major tile: where this lane's part of it starts, as an LDS byte
@@ -253,13 +260,12 @@ struct Tile {
         const u32x4_t* chunk = lds + row * WIDTH + (col / 8 ^ swizzle(row));
         return (uint32_t)(uintptr_t)(LDS_PTR const void*)chunk + (col >> 2 & 1) * 8;
     }
-    // Bytes on from there: to the next 16 k, the other four k, the next plane.
-    static constexpr int NEXT_KK = 16 * WIDTH * 16, NEXT_HALF = 4 * WIDTH * 16, NEXT_PLANE = CHUNKS * 16;
+    // Bytes on from there: to the next 16 k, and the other four k.
+    static constexpr int NEXT_KK = 16 * WIDTH * 16, NEXT_HALF = 4 * WIDTH * 16;
 };
 
 // The turned reads of one kk, with the wait for them: the compiler would wait
-// for the loads into LDS in flight before each.  N0 planes from at0, N1 from
-// at1 and from at2 (one tile's two fragments).
+// for the loads into LDS in flight before each.
 typedef uint64_t Half;
 __device__ __forceinline__ bf16x8_t halves(Half a, Half b) {
     struct Two { Half v[2]; };
@@ -268,7 +274,7 @@ __device__ __forceinline__ bf16x8_t halves(Half a, Half b) {
 
 #define TURN(dst, at, off) "ds_read_b64_tr_b16 %" dst ", %" at " offset:%" off "\n\t"
 
-// Fragments f1[j] of tile columns at1, at2: P = 1.
+// The two fragments at at1 and at2.
 template <int OFF, int HALF>
 __device__ __forceinline__ void turned(uint32_t at1, uint32_t at2, bf16x8_t (&f)[1][2]) {
     Half a, b, c, d;
@@ -279,42 +285,6 @@ __device__ __forceinline__ void turned(uint32_t at1, uint32_t at2, bf16x8_t (&f)
                  : "memory");
     f[0][0] = halves(a, b);
     f[0][1] = halves(c, d);
-}
-
-// The same with two planes.
-template <int OFF, int HALF, int PLANE>
-__device__ __forceinline__ void turned(uint32_t at1, uint32_t at2, bf16x8_t (&f)[2][2]) {
-    Half a, b, c, d, e, g, h, i;
-    asm volatile(TURN("0", "8", "10") TURN("1", "8", "11") TURN("2", "9", "10") TURN("3", "9", "11")
-                 TURN("4", "8", "12") TURN("5", "8", "13") TURN("6", "9", "12") TURN("7", "9", "13")
-                 "s_waitcnt lgkmcnt(0)"
-                 : "=&v"(a), "=&v"(b), "=&v"(c), "=&v"(d), "=&v"(e), "=&v"(g), "=&v"(h), "=&v"(i)
-                 : "v"(at1), "v"(at2), "n"(OFF), "n"(OFF + HALF), "n"(OFF + PLANE), "n"(OFF + PLANE + HALF)
-                 : "memory");
-    f[0][0] = halves(a, b);
-    f[0][1] = halves(c, d);
-    f[1][0] = halves(e, g);
-    f[1][1] = halves(h, i);
-}
-
-// Three planes of one fragment of A, and one of two fragments of B.
-template <int AOFF, int AHALF, int APLANE, int BOFF, int BHALF>
-__device__ __forceinline__ void turned(uint32_t at0, bf16x8_t (&fa)[3][1], uint32_t at1, uint32_t at2, bf16x8_t (&fb)[1][2]) {
-    Half a, b, c, d, e, g, h, i, j, k;
-    asm volatile(TURN("0", "10", "13") TURN("1", "10", "14") TURN("2", "10", "15") TURN("3", "10", "16")
-                 TURN("4", "10", "17") TURN("5", "10", "18") TURN("6", "11", "19") TURN("7", "11", "20")
-                 TURN("8", "12", "19") TURN("9", "12", "20")
-                 "s_waitcnt lgkmcnt(0)"
-                 : "=&v"(a), "=&v"(b), "=&v"(c), "=&v"(d), "=&v"(e), "=&v"(g), "=&v"(h), "=&v"(i), "=&v"(j), "=&v"(k)
-                 : "v"(at0), "v"(at1), "v"(at2), "n"(AOFF), "n"(AOFF + AHALF), "n"(AOFF + APLANE),
-                   "n"(AOFF + APLANE + AHALF), "n"(AOFF + 2 * APLANE), "n"(AOFF + 2 * APLANE + AHALF), "n"(BOFF),
-                   "n"(BOFF + BHALF)
-                 : "memory");
-    fa[0][0] = halves(a, b);
-    fa[1][0] = halves(c, d);
-    fa[2][0] = halves(e, g);
-    fb[0][0] = halves(h, i);
-    fb[0][1] = halves(j, k);
 }
 
 // Waits until this wave has at most N loads in flight, then for the others.
@@ -363,7 +333,7 @@ struct Kind {
     static constexpr int PITCH = BN + 4;         // BF16 results go out through LDS, as rows of floats
     using TA = Tile<LA, PA, BM, THREADS>;
     using TB = Tile<LB, PB, BN, THREADS>;
-    static constexpr int STAGE = TA::IN * TA::CHUNKS + TB::IN * TB::CHUNKS;
+    static constexpr int STAGE = TA::CHUNKS + TB::CHUNKS;
     static constexpr int OUT = OUT_BF16 ? BM * PITCH / 4 : 0;
     static constexpr int LDS = STAGE * STAGES > OUT ? STAGE * STAGES : OUT;
 };
@@ -405,9 +375,9 @@ __device__ __forceinline__ void product(u32x4_t* lds, const Product& x, unsigned
     tb.place(Bo, n0);
     const auto load = [&](int64_t k0, int stage) {
         ta.load(A, m0, k0, k_end, lds + stage * STAGE);
-        tb.load(Bo, n0, k0, k_end, lds + stage * STAGE + TA::IN * TA::CHUNKS);
+        tb.load(Bo, n0, k0, k_end, lds + stage * STAGE + TA::CHUNKS);
     };
-    constexpr int LOADS = TA::LOADS + TB::LOADS;
+    constexpr int LOADS = TA::PER_LANE + TB::PER_LANE;
     // steps past the last load nothing but zeros, so that the count of loads in
     // flight is the same in every round
 #pragma unroll
@@ -424,43 +394,36 @@ __device__ __forceinline__ void product(u32x4_t* lds, const Product& x, unsigned
             load(k0 + (STAGES - 1) * STEP, stage == 0 ? STAGES - 1 : stage - 1);
         }
         const u32x4_t* la = lds + stage * STAGE;
-        const u32x4_t* lb = la + TA::IN * TA::CHUNKS;
-        uint32_t at[3] = {0, 0, 0};
-        if constexpr (LA == Lay::row_major) at[0] = TA::turned_at(la, wm);
+        const u32x4_t* lb = la + TA::CHUNKS;
+        uint32_t at[2] = {0, 0};
+        static_assert(LA != Lay::row_major, "only B is turned");
         if constexpr (LB == Lay::row_major) {
-            static_assert(TN == 2, "two fragments to a turned read");
-            at[1] = TB::turned_at(lb, wn);
-            at[2] = TB::turned_at(lb, wn + 32);
+            static_assert(TN == 2 && PB == 1, "two fragments to a turned read");
+            at[0] = TB::turned_at(lb, wn);
+            at[1] = TB::turned_at(lb, wn + 32);
         }
         over_kk([&](auto step) {
             constexpr int kk = decltype(step)::value;
             bf16x8_t fa[PA][TM], fb[PB][TN];
-            if constexpr (LA == Lay::k_major) {
 #pragma unroll
-                for (int p = 0; p < PA; ++p)
+            for (int i = 0; i < TM; ++i) {
+                bf16x8_t planes[PA];
+                if constexpr (TA::FLOAT) TA::fragment(la, wm + i * 32, kk, planes);
+                else planes[0] = TA::fragment(la, wm + i * 32, kk);
 #pragma unroll
-                    for (int i = 0; i < TM; ++i) fa[p][i] = TA::fragment(la, p, wm + i * 32, kk);
+                for (int p = 0; p < PA; ++p) fa[p][i] = planes[p];
             }
-            if constexpr (LB == Lay::k_major) {
-#pragma unroll
-                for (int p = 0; p < PB; ++p)
-#pragma unroll
-                    for (int j = 0; j < TN; ++j) fb[p][j] = TB::fragment(lb, p, wn + j * 32, kk);
-            } else if constexpr (LB == Lay::k_float) {
+            if constexpr (LB == Lay::row_major) {
+                turned<kk * TB::NEXT_KK, TB::NEXT_HALF>(at[0], at[1], fb);
+            } else {
 #pragma unroll
                 for (int j = 0; j < TN; ++j) {
-                    u32x4_t planes[PB];
-                    TB::fragment(lb, wn + j * 32, kk, planes);
+                    bf16x8_t planes[PB];
+                    if constexpr (TB::FLOAT) TB::fragment(lb, wn + j * 32, kk, planes);
+                    else planes[0] = TB::fragment(lb, wn + j * 32, kk);
 #pragma unroll
-                    for (int p = 0; p < PB; ++p) fb[p][j] = __builtin_bit_cast(bf16x8_t, planes[p]);
+                    for (int p = 0; p < PB; ++p) fb[p][j] = planes[p];
                 }
-            } else if constexpr (LA == Lay::row_major) {
-                turned<kk * TA::NEXT_KK, TA::NEXT_HALF, TA::NEXT_PLANE, kk * TB::NEXT_KK, TB::NEXT_HALF>(at[0], fa, at[1],
-                                                                                                         at[2], fb);
-            } else if constexpr (PB == 1) {
-                turned<kk * TB::NEXT_KK, TB::NEXT_HALF>(at[1], at[2], fb);
-            } else {
-                turned<kk * TB::NEXT_KK, TB::NEXT_HALF, TB::NEXT_PLANE>(at[1], at[2], fb);
             }
             // the planes' products, the smallest first; beyond the last plane's
             // weight they are dropped
@@ -554,9 +517,11 @@ moe_router_product(Product x) {
 
 // Both gradients in one launch: workgroups of dw, which are few and long, and
 // then those of dx, which fill up what is left.
-// 4096 x 4096 x 64: 20 us (67 MB of x and dx: 13 us), and 6 us to split dlogits and
-// add the parts of dw.  Larger tiles (64 x 256, 128 x 128), which take in a third
-// less, were no faster (34 us in all against 29).
+// 4096 x 4096 x 64: 21 us (67 MB of x and dx: 13 us), and 4 us to add the parts of
+// dw.  Larger tiles (64 x 256 for dw, for dx 64 x 256 or 128 x 128), which take in
+// a quarter less, were slower (31 to 33 us in all against 26).  With dlogits and w
+// split into planes beforehand, by a launch of their own, 28 us and 15.5 us against
+// 13.3 at 1024 x 2048 x 128, but 188 against 200 at 8192 x 7168 x 256.
 template <typename KW, typename KX>
 __global__ void __launch_bounds__(256)
 moe_router_gradients(Product w, unsigned w_blocks, Product x) {
@@ -565,40 +530,19 @@ moe_router_gradients(Product w, unsigned w_blocks, Product x) {
     else product<KX>(lds, x, blockIdx.x - w_blocks);
 }
 
-// float32 rows as P BF16 planes, [P][rows][width]; columns behind the last are 0.
-struct Planes {
-    const float* from;
-    int64_t stride, rows, cols;
-    uint16_t* to;
-    int64_t width;         // a multiple of 8
-    int planes;            // 2 or 3
-};
-
-__device__ __forceinline__ void split_row_part(const Planes& s, int64_t unit) {
-    const int64_t units = s.width / 8, r = unit / units, c = (unit - r * units) * 8;
-    const float* q = s.from + r * s.stride + c;
-    float v[8];
-    if (c + 8 <= s.cols) {
-        const u32x4a_t a = *reinterpret_cast<const u32x4a_t*>(q), b = *reinterpret_cast<const u32x4a_t*>(q + 4);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(a[i]), v[4 + i] = __uint_as_float(b[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = c + i < s.cols ? q[i] : 0.0f;
-    }
-    u32x4_t p[3];
-    split_bf16<3>(v, p);
-#pragma unroll
-    for (int i = 0; i < 3; ++i)
-        if (i < s.planes) *reinterpret_cast<u32x4_t*>(s.to + ((int64_t)i * s.rows + r) * s.width + c) = p[i];
-}
-
+// Rows of `cols` floats as rows of `width`, a multiple of 4; columns behind the
+// last are 0.
 __global__ void __launch_bounds__(256)
-moe_router_split(Planes s0, Planes s1) {
-    const int64_t n0 = s0.rows * (s0.width / 8), n = n0 + s1.rows * (s1.width / 8);
+moe_router_pad(const float* from, int64_t stride, int64_t rows, int cols, float* to, int width) {
+    const int64_t units = width / 4, n = rows * units;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-        if (i < n0) split_row_part(s0, i);
-        else split_row_part(s1, i - n0);
+        const int64_t r = i / units;
+        const int c = (int)(i - r * units) * 4;
+        const float* q = from + r * stride + c;
+        u32x4_t v;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = c + j < cols ? __float_as_uint(q[j]) : 0u;
+        *reinterpret_cast<u32x4_t*>(to + r * width + c) = v;
     }
 }
 
@@ -632,6 +576,8 @@ moe_router_product_join(const float* ws, float* out, int64_t M, int64_t N, int64
 }
 
 namespace {
+
+constexpr int64_t MAX_TILE_STRIDE = 1 << 22;     // of floats: 128 rows within 32-bit byte offsets
 
 struct Split {
     int n;               // parts of K
@@ -679,13 +625,13 @@ bool is_small(const mega_moe_router_logits_args& a, const SmallTile& s) {
     return s.bytes * a.hidden <= 300000 + 40 * a.hidden;
 }
 
-// The workspace: the planes of what is split, then the parts of a split K.
+// The workspace: dlogits with whole chunks, then the parts of a split K.
 struct Plan {
     Split split;
-    int64_t w_planes, d_planes, parts, total;   // byte offsets, and bytes in all
+    int64_t parts, total;   // byte offset, and bytes in all
 };
 
-int64_t padded(int64_t E) { return (E + 63) / 64 * 64; }
+int64_t padded(int64_t E) { return (E + 3) / 4 * 4; }
 
 int64_t forward_tiles(const mega_moe_router_logits_args& a) {
     const int64_t E = a.num_experts;
@@ -716,19 +662,12 @@ Plan backward_plan(const mega_moe_router_logits_args& a) {
     const int64_t T = a.num_tokens, E = a.num_experts, H = a.hidden;
     Plan p{};
     p.split = split_for(tiles(E, 64) * tiles(H, 128), T, 256);     // few: they are joined again
-    p.d_planes = a.weight_type == MEGA_MOE_F32 ? 2 * E * H * 2 : 0;
-    p.parts = p.d_planes + 3 * T * padded(E) * 2;
+    p.parts = T * padded(E) * 4;
     p.total = p.parts + (p.split.n > 1 ? p.split.n * E * H * 4 : 0);
     return p;
 }
 
 uint8_t* at(const mega_moe_router_logits_args& a, int64_t offset) { return static_cast<uint8_t*>(a.workspace) + offset; }
-
-void launch_split(const Planes& s0, const Planes& s1, hipStream_t stream) {
-    const int64_t blocks = tiles(s0.rows * (s0.width / 8) + s1.rows * (s1.width / 8), 256);
-    if (blocks > 0)
-        hipLaunchKernelGGL(moe_router_split, dim3((unsigned)(blocks > 65536 ? 65536 : blocks)), dim3(256), 0, stream, s0, s1);
-}
 
 void launch_join(const float* parts, float* out, int64_t M, int64_t N, int64_t stride, int splits, hipStream_t stream) {
     const int64_t blocks = tiles(M * N, 1024);
@@ -766,7 +705,7 @@ void launch_product(const mega_moe_router_logits_args& a, hipStream_t stream) {
     const int64_t T = a.num_tokens, H = a.hidden, E = a.num_experts;
     float* parts = reinterpret_cast<float*>(at(a, p.parts));
     const Result out{T, E, p.split.n > 1 ? parts : a.logits, a.logits_stride, nullptr, nullptr, 0};
-    const Product x{Operand{a.x, 0, a.x_stride, T, H}, Operand{a.w, 0, H, E, H}, out, p.split.k, p.split.n};
+    const Product x{Operand{a.x, a.x_stride, T, H}, Operand{a.w, H, E, H}, out, p.split.k, p.split.n};
     hipLaunchKernelGGL((moe_router_product<K>), dim3((unsigned)(tiles(T, K::BM) * tiles(E, K::BN) * p.split.n)),
                        dim3(K::THREADS), 0, stream, x);
     if (p.split.n > 1) launch_join(parts, a.logits, T, E, a.logits_stride, p.split.n, stream);
@@ -804,31 +743,39 @@ void launch_router_logits_backward(const mega_moe_router_logits_args& a, hipStre
     const int64_t T = a.num_tokens, H = a.hidden, E = a.num_experts, Ep = padded(E);
     const Plan p = backward_plan(a);
     const bool f = a.weight_type == MEGA_MOE_F32;
-    uint16_t* dp = reinterpret_cast<uint16_t*>(at(a, p.d_planes));
-    uint16_t* wp = reinterpret_cast<uint16_t*>(at(a, p.w_planes));
-    launch_split(Planes{a.dlogits, a.dlogits_stride, T, E, dp, Ep, a.dw ? 3 : 2},
-                 a.dx && f ? Planes{static_cast<const float*>(a.w), H, E, H, wp, H, 2} : Planes{}, stream);
-    const Product x{Operand{dp, T * Ep, Ep, T, Ep}, Operand{f ? wp : static_cast<const uint16_t*>(a.w), E * H, H, H, E},
-                    Result{T, H, nullptr, a.dx_stride, a.dx, a.dx_add, a.dx_add_stride}, Ep, 1};
+    // dlogits as it is where its rows are whole aligned chunks, and a tile of it
+    // within 32-bit offsets
+    const float* d = a.dlogits;
+    int64_t d_stride = a.dlogits_stride;
+    if (T > 0 && (E % 4 || d_stride % 4 || (uintptr_t)d % 16 || d_stride > MAX_TILE_STRIDE)) {
+        float* to = reinterpret_cast<float*>(at(a, 0));
+        const int64_t blocks = tiles(T * Ep / 4, 256);
+        hipLaunchKernelGGL(moe_router_pad, dim3((unsigned)(blocks > 65536 ? 65536 : blocks)), dim3(256), 0, stream, d,
+                           d_stride, T, (int)E, to, (int)Ep);
+        d = to;
+        d_stride = Ep;
+    }
+    const Product x{Operand{d, d_stride, T, Ep}, Operand{a.w, H, H, E},
+                    Result{T, H, nullptr, a.dx_stride, a.dx, a.dx_add, a.dx_add_stride}, (Ep + 63) / 64 * 64, 1};
     float* parts = reinterpret_cast<float*>(at(a, p.parts));
-    const Product w{Operand{dp, T * Ep, Ep, Ep, T}, Operand{a.x, 0, a.x_stride, H, T},
+    const Product w{Operand{d, d_stride, Ep, T}, Operand{a.x, a.x_stride, H, T},
                     Result{E, H, p.split.n > 1 ? parts : a.dw, H, nullptr, nullptr, 0}, p.split.k, p.split.n};
     const unsigned w_blocks = a.dw ? (unsigned)(tiles(E, 64) * tiles(H, 128) * p.split.n) : 0;
     const unsigned x_blocks = a.dx ? (unsigned)(tiles(T, 64) * tiles(H, 128)) : 0;
     const auto go = [&](auto stages) {
         constexpr int S = decltype(stages)::value;
-        using KW = Kind<Lay::row_major, 3, Lay::row_major, 1, 64, 128, S, false>;
-        using KX1 = Kind<Lay::k_major, 2, Lay::row_major, 1, 64, 128, S, true>;
-        using KX2 = Kind<Lay::k_major, 2, Lay::row_major, 2, 64, 128, S, true>;
+        using KW = Kind<Lay::row_float, 3, Lay::row_major, 1, 64, 128, S, false>;
+        using KX1 = Kind<Lay::k_float, 2, Lay::row_major, 1, 64, 128, S, true>;
+        using KX2 = Kind<Lay::k_float, 2, Lay::row_float, 2, 64, 128, S, true>;
         const dim3 grid(w_blocks + x_blocks);
         if (f) hipLaunchKernelGGL((moe_router_gradients<KW, KX2>), grid, dim3(256), 0, stream, w, w_blocks, x);
         else hipLaunchKernelGGL((moe_router_gradients<KW, KX1>), grid, dim3(256), 0, stream, w, w_blocks, x);
     };
     // Up to two workgroups to a compute unit: each keeps a step's loads in flight
     // while it multiplies.  More of them hide each other's loads, and with one
-    // step in LDS four fit.  One and two steps: 3383 x 640 x 216 24 and 21 us (425
-    // workgroups), 4096 x 2048 x 128 27 and 27 (1280), 4096 x 4096 x 64 29 and 33
-    // (2560), 2589 x 5760 x 72 with float32 weights 44 and 61 (2205).
+    // step in LDS four fit.  One and two steps: 3383 x 640 x 216 22 and 19 us (425
+    // workgroups), 4096 x 2048 x 128 25 and 26 (1280), 4096 x 4096 x 64 27 and 32
+    // (2304), 2589 x 5760 x 72 with float32 weights 47 and 69 (2205).
     if (w_blocks + x_blocks <= 512) go(std::integral_constant<int, 2>{});
     else go(std::integral_constant<int, 1>{});
     if (a.dw && p.split.n > 1) launch_join(parts, a.dw, E, H, H, p.split.n, stream);

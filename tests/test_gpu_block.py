@@ -311,6 +311,30 @@ def test_router_logits_backward_matches_the_reference(T, H, E, wt, extra, add):
         assert torch.all(dx_buf[:, H:] == 7.0)
 
 
+@pytest.mark.parametrize("T,H,E,wt", [(300, 264, 20, BF16), (70, 1032, 68, F32), (2100, 520, 64, BF16)])
+def test_router_logits_backward_of_views_equals_that_of_copies(T, H, E, wt):
+    # rows of dlogits that start between 16-byte words, and rows of a wider array
+    # with NaN around them
+    x, w, r = _logits_inputs(T, H, E, wt, 0)
+    d = r(T, E, scale=0.01)
+    out = []
+    for lead, tail in ((0, 0), (1, 3), (4, 4), (2, 1)):
+        wide = torch.full((T, lead + E + tail), float("nan"), device="cuda")
+        wide[:, lead:lead + E] = d
+        dx, dw = torch.empty(T, H, dtype=BF16, device="cuda"), torch.empty(E, H, device="cuda")
+        a = B.make_args(B.mega_moe_router_logits_args, dlogits=wide[:, lead:], dlogits_stride=lead + E + tail, dx=dx,
+                        dw=dw, **_logits_fields(T, H, E, wt, x, w, 0))
+        B.set_args(a, **U.workspace(B.mega_moe_router_logits_workspace_bytes(a)))
+        B.mega_moe_router_logits_backward(a, U.current_stream())
+        out.append((dx, dw))
+    torch.cuda.synchronize()
+    want = block.router_logits_backward(U.f64(d), U.f64(x), U.f64(w))
+    U.near(out[0][0], want["dx"], want["dx_mag"], 2 * 2 ** 8 + E + 16, "dx")
+    U.near(out[0][1], want["dw"], want["dw_mag"], T + 16, "dw")
+    for dx, dw in out[1:]:
+        assert torch.equal(dx, out[0][0]) and torch.equal(dw, out[0][1])
+
+
 def test_router_logits_backward_of_parts_and_no_tokens():
     T, H, E = 20, 64, 6
     x, w, r = _logits_inputs(T, H, E, F32, 0)
