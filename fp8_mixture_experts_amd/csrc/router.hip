@@ -15,8 +15,9 @@ constexpr int NO_EXPERT = 0x7fffffff;
 // the largest key and the lowest index that has it, by moves between lanes.  For
 // more than a few rounds the lanes sort their keys first.  What bounds it is that
 // chain of vector instructions: a token's logits are read once and are small.
-// 8192 tokens of 256 experts, k = 8: the logits' order 6.7 us; sigmoid with a
-// bias 8.6, in 8 groups too 11 (the 8.5 MB that it has to move: 1.7 us).
+// 8192 tokens of 256 experts, k = 8: the logits' order 6.6 us; sigmoid with a
+// bias 8.5, in 8 groups too 11 to 12.5, as near ones turn up (the 8.5 MB that it
+// has to move: 1.7 us).
 //
 // Without bias and groups the keys are the logits, which order the experts as
 // the scores do.  Otherwise the order is that of score + bias in float64, but
@@ -195,15 +196,15 @@ __device__ __forceinline__ void top2_of_16(float (&first)[N], float (&second)[N]
     top2_step<1, left(8), false>(first, second);
 }
 
-// A lane's keys in order, the largest first and equal ones by index, by merging
-// neighbours R apart.
-template <int N>
+// A lane's keys in order, the largest first and, with BY_INDEX, equal ones by
+// index, by merging neighbours R apart.
+template <int N, bool BY_INDEX>
 struct Sorted {
     float key[N];
     int at[N];
     template <int A, int B>
     __device__ __forceinline__ void order() {
-        const bool swap = key[B] > key[A] || (key[B] == key[A] && at[B] < at[A]);
+        const bool swap = key[B] > key[A] || (BY_INDEX && key[B] == key[A] && at[B] < at[A]);
         const float k = swap ? key[B] : key[A];
         const int i = swap ? at[B] : at[A];
         key[B] = swap ? key[A] : key[B];
@@ -381,9 +382,15 @@ moe_router_topk(mega_moe_router_topk_args a) {
                 }
             }
             const uint32_t mul = ((1u << 20) + size - 1) / size;     // e / size for e * size < 2^20
+            if (G <= 32) {
 #pragma unroll
-            for (int i = 0; i < NI; ++i)
-                if (!(kept >> ((uint32_t)(i * LANES + lane) * mul >> 20 & 63) & 1)) key[i] = -INFINITY;
+                for (int i = 0; i < NI; ++i)
+                    if (!__builtin_amdgcn_ubfe((uint32_t)kept, (uint32_t)(i * LANES + lane) * mul >> 20, 1)) key[i] = -INFINITY;
+            } else {
+#pragma unroll
+                for (int i = 0; i < NI; ++i)
+                    if (!(kept >> ((uint32_t)(i * LANES + lane) * mul >> 20 & 63) & 1)) key[i] = -INFINITY;
+            }
         }
     }
     // The rounds; slot j belongs to lane j % LANES.  With scores one candidate
@@ -404,7 +411,8 @@ moe_router_topk(mega_moe_router_topk_args a) {
     // from NI / 2 rounds on.  8192 tokens, 256 experts: one round 4.4 us without
     // and 5.2 with, eight 7.3 and 6.7; 32768 of 1024: one 30 and 43, eight 67 and 63.
     if (rounds > NI / 2) {
-        Sorted<NI> mem;
+        // equal scores are ordered with the near ones below
+        Sorted<NI, !SCORED> mem;
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
             mem.key[i] = key[i];
@@ -448,6 +456,8 @@ moe_router_topk(mega_moe_router_topk_args a) {
         return a.logits_type == MEGA_MOE_F32 ? static_cast<const float*>(a.logits)[at_row + e]
                                              : bf16_value(static_cast<const uint16_t*>(a.logits)[at_row + e]);
     };
+    // the logits of the candidates: for their weights, and to tell near ones apart
+    float x = one_each && mine >= 0 ? logit(mine) : 0.0f;
     if constexpr (SCORED) {
         // which candidates are too close to the next one to be told apart
         const float next = __shfl_down(c, 1, LANES);
@@ -460,7 +470,7 @@ moe_router_topk(mega_moe_router_topk_args a) {
             // candidates by their float64 keys; those without an expert last
             const bool cand = lane <= k && mine >= 0;
             double d = -INFINITY;
-            if (cand) d = 1.0 / (1.0 + exp(-(double)logit(mine))) + (a.bias ? (double)a.bias[mine] : 0.0);
+            if (cand) d = 1.0 / (1.0 + exp(-(double)x)) + (a.bias ? (double)a.bias[mine] : 0.0);
             const int order = cand ? mine : NO_EXPERT - LANES + lane;
             int rank = 0;
             for (int i = 0; i <= k; ++i) {
@@ -470,7 +480,9 @@ moe_router_topk(mega_moe_router_topk_args a) {
             }
             // lanes behind the candidates stay where they are
             if (lane > k) rank = lane;
-            mine = __builtin_amdgcn_ds_permute((int)(((threadIdx.x & 63) - lane + rank) * 4), mine);
+            const int to = (int)(((threadIdx.x & 63) - lane + rank) * 4);
+            mine = __builtin_amdgcn_ds_permute(to, mine);
+            x = __int_as_float(__builtin_amdgcn_ds_permute(to, __float_as_int(x)));
         }
         if (one_each && in && lane < k) idx_out[lane] = mine;
         if (!one_each && in && !live)
@@ -487,7 +499,10 @@ moe_router_topk(mega_moe_router_topk_args a) {
                                                     a.topk_idx + (size_t)(t0 + r) * k);
             }
             __threadfence_block();
-            if (live && one_each && lane < k) mine = idx_out[lane];
+            if (live && one_each && lane < k) {
+                mine = idx_out[lane];
+                x = mine >= 0 ? logit(mine) : 0.0f;
+            }
         }
     } else {
         if (one_each && in && lane < k) idx_out[lane] = mine;
@@ -495,17 +510,17 @@ moe_router_topk(mega_moe_router_topk_args a) {
     // the weights of the slots, from their own logits
     if (!in) return;
     float* w_out = a.topk_weights + (size_t)t * k;
-    const auto score_of = [&](int e) {
+    const auto score_of = [&](int e, float l) {
         if (e < 0) return 0.0f;
-        const float x = logit(e);
-        return softmax ? expf(x - top) * inv : sigmoid(x);
+        return softmax ? expf(l - top) * inv : sigmoid(l);
     };
     float w = 0.0f, total = 0.0f;
     if (one_each) {
-        if (lane < k) total = w = score_of(mine);
+        if (lane < k) total = w = score_of(mine, x);
     } else {
         for (int j = lane; j < k; j += LANES) {
-            w = score_of(idx_out[j]);
+            const int e = idx_out[j];
+            w = score_of(e, e >= 0 ? logit(e) : 0.0f);
             w_out[j] = w;
             total += w;
         }
@@ -523,8 +538,8 @@ moe_router_topk(mega_moe_router_topk_args a) {
 // The gradient of a token's logits, its experts in 16, 32 or 64 lanes.  The
 // top-k weights reach the scores that were taken (one slot to a lane, added to
 // the row through LDS); softmax spreads minus their mean over all experts.
-// Bound by memory for large batches (32768 tokens of 256 experts 16 us, 4.2 TB/s),
-// by a token's chain of loads and sums for others: 8192 tokens 6.3 us.
+// Bound by memory for large batches (32768 tokens of 256 experts 15.4 us, 4.5
+// TB/s), by a token's chain of loads and sums for others: 8192 tokens 6.2 us.
 template <int LANES, int NI>
 __global__ void __launch_bounds__(256)
 moe_router_backward(mega_moe_router_backward_args a) {

@@ -9,17 +9,24 @@ namespace mega_moe {
 template <int NI, int LANES = 64>
 __device__ __forceinline__ void load_row(const void* logits, int type, size_t row, int E, float (&l)[NI]) {
     const int lane = threadIdx.x & (LANES - 1);
+    const auto load = [&](auto index) {
+        if (type == MEGA_MOE_F32) {
+            const float* p = static_cast<const float*>(logits) + row;
+#pragma unroll
+            for (int i = 0; i < NI; ++i) l[i] = p[index(i)];
+        } else {
+            const uint16_t* p = static_cast<const uint16_t*>(logits) + row;
+#pragma unroll
+            for (int i = 0; i < NI; ++i) l[i] = bf16_value(p[index(i)]);
+        }
+    };
+    if (E == NI * LANES) {
+        load([&](int i) { return i * LANES + lane; });
+        return;
+    }
     // lanes behind the last expert read it once more and drop it: no branches
     // between the loads
-    if (type == MEGA_MOE_F32) {
-        const float* p = static_cast<const float*>(logits) + row;
-#pragma unroll
-        for (int i = 0; i < NI; ++i) l[i] = p[min(i * LANES + lane, E - 1)];
-    } else {
-        const uint16_t* p = static_cast<const uint16_t*>(logits) + row;
-#pragma unroll
-        for (int i = 0; i < NI; ++i) l[i] = bf16_value(p[min(i * LANES + lane, E - 1)]);
-    }
+    load([&](int i) { return min(i * LANES + lane, E - 1); });
 #pragma unroll
     for (int i = 0; i < NI; ++i) l[i] = i * LANES + lane < E ? l[i] : -INFINITY;
 }
