@@ -10,8 +10,10 @@
 // workgroup; the workgroup that ends last adds up the losses.
 //
 // The logits are read once (8 MB at 8192 x 256: 2 us); what bounds it is the
-// chain of a token's loads, exponentials and sums, and the two launches: 8.8 and
-// 5.6 us there, with 13 sequences; 3.8 and 2.5 us at 576 x 32.
+// chain of a token's loads, exponentials and sums, and the two launches: 8.5 and
+// 5.5 us there, with 13 sequences; 3.5 and 2.6 us at 576 x 32.  p is computed once
+// for all the sequences that a chunk meets: computed for each of them in turn,
+// 32768 x 256 with 64 sequences took 35 us, so 27.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -66,9 +68,7 @@ __device__ __forceinline__ void sequence_span(const mega_moe_balance_loss_args& 
 }
 
 // A token's experts lie in LANES lanes; the groups of lanes take the tokens in
-// turn, each lane keeping the sums of its experts.  The whole
-// chunk is loaded before the sequences are looked up, so that the two chains
-// of loads run side by side.
+// turn, each lane keeping the sums of its experts.
 constexpr int part_threads(int lanes) { return lanes == 32 ? 1024 : 512; }
 
 template <int LANES, int NI>
@@ -83,6 +83,14 @@ moe_balance_part(mega_moe_balance_loss_args a, BalanceWs ws, int B) {
     const int E = a.num_experts, k = a.num_topk;
     const int c0 = blockIdx.x * CHUNK, c1 = min(c0 + CHUNK, a.num_tokens);
     if (blockIdx.x == 0 && tid == 0) *ws.done = 0;
+    // the ends of up to 64 sequences, in every wave's lanes: asked for first, so
+    // that the look-up below waits for nothing that the logits do not wait for
+    const bool in_lanes = a.cu_seqlens && B <= 64;
+    int ends = 0x7fffffff, start = 0;
+    if (in_lanes) {
+        start = a.cu_seqlens[0];
+        if ((tid & 63) < B) ends = a.cu_seqlens[(tid & 63) + 1];
+    }
     constexpr int ROWS = CHUNK / GROUPS;         // tokens per group
     const bool sigmoids = a.score == MEGA_MOE_SCORE_SIGMOID;
     float l[ROWS][NI];
@@ -100,17 +108,49 @@ moe_balance_part(mega_moe_balance_loss_args a, BalanceWs ws, int B) {
             for (int i = 0; i < NI; ++i) l[r][i] = 0.0f;
         }
     }
+    // the logits become p, once for all the sequences that the chunk meets
+    float zr[ROWS];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+        float ex[NI], top, sum = 0.0f;
+        zr[r] = 0.0f;
+        if (!sigmoids || a.z_coeff != 0.0f) {
+            row_exp<LANES>(l[r], ex, top, sum);
+            const float lse = row_lse(top, sum);
+            zr[r] = lse * lse;
+        }
+        if (sigmoids) {
+            sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                ex[i] = sigmoid(l[r][i]);
+                sum += ex[i];
+            }
+            sum = lanes_sum<LANES>(sum);
+        }
+        const float inv = sum > 0.0f ? 1.0f / sum : sum;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) l[r][i] = ex[i] * inv;
+    }
     int p = c0;
     while (p < c1) {
-        const int b = sequence_of<64>(a.cu_seqlens, B, p);
+        int b, lo, hi;
+        if (in_lanes) {
+            // as many sequences end at p or before
+            const int n = __builtin_popcountll(__builtin_amdgcn_ballot_w64(ends <= p));
+            b = p < start || n >= B ? -1 : n;
+            hi = __builtin_amdgcn_readlane(ends, b < 0 ? 0 : b);
+        } else {
+            b = sequence_of<64>(a.cu_seqlens, B, p);
+            if (b >= 0) sequence_span(a, b, lo, hi);
+            else start = a.cu_seqlens[0];
+        }
         if (b < 0) {
             // before the first sequence, or behind the last
-            if (p >= a.cu_seqlens[0]) break;
-            p = a.cu_seqlens[0];
+            if (p >= start) break;
+            p = start;
             continue;
         }
-        int lo, hi;
-        sequence_span(a, b, lo, hi);
         if (hi <= p) break;                      // cu_seqlens decreases
         const int end = min(hi, c1);
         for (int e = tid; e < LANES * NI; e += THREADS) count[e] = 0;
@@ -124,24 +164,9 @@ moe_balance_part(mega_moe_balance_loss_args a, BalanceWs ws, int B) {
             const int t = c0 + r * GROUPS + group;
             if (!live[r] || t < p || t >= end) continue;
             ++n;
-            float ex[NI], top, sum = 0.0f;
-            if (!sigmoids || a.z_coeff != 0.0f) {
-                row_exp<LANES>(l[r], ex, top, sum);
-                const float lse = row_lse(top, sum);
-                z += lse * lse;
-            }
-            if (sigmoids) {
-                sum = 0.0f;
+            z += zr[r];
 #pragma unroll
-                for (int i = 0; i < NI; ++i) {
-                    ex[i] = sigmoid(l[r][i]);
-                    sum += ex[i];
-                }
-                sum = lanes_sum<LANES>(sum);
-            }
-            const float inv = sum > 0.0f ? 1.0f / sum : sum;
-#pragma unroll
-            for (int i = 0; i < NI; ++i) acc[i] += ex[i] * inv;
+            for (int i = 0; i < NI; ++i) acc[i] += l[r][i];
             if (slot[r] >= 0 && slot[r] < E) atomicAdd(&count[slot[r]], 1);
             for (int j = lane + LANES; j < k; j += LANES) {
                 const int e = a.topk_idx[(size_t)t * k + j];
