@@ -362,8 +362,8 @@ int row_threads(int H) { return (H / 8 + 63) / 64 * 64; }
 // Rows at a time in a workgroup of up to 1024 threads.
 int row_groups(int H) { return 1024 / row_threads(H); }
 
-// Workgroups of the norm: one to a compute unit, each with a row or more in
-// flight.  Two to a unit measured 115 us against 110 (8192 rows of 7168, gate by
+// Workgroups of the norm for many rows: one to a compute unit, each with a row or
+// more in flight.  Two to a unit measured 115 us against 110 (8192 rows of 7168, gate by
 // channel, E4M3 output) and 98 against 95 (no block output).
 constexpr int NORM_BLOCKS = 256;
 }  // namespace
@@ -372,10 +372,19 @@ void launch_norm(const mega_moe_norm_args& a, hipStream_t stream) {
     const int nt = row_threads(a.hidden);
     // no more rows to a workgroup than leave every compute unit some
     const int most = (a.num_tokens + NORM_BLOCKS - 1) / NORM_BLOCKS;
-    const int groups = most < row_groups(a.hidden) ? most : row_groups(a.hidden);
+    int groups = most < row_groups(a.hidden) ? most : row_groups(a.hidden);
+    int limit = NORM_BLOCKS;
+    // Where all rows are on their way at once, three or more to a compute unit (24
+    // waves), each has a workgroup of its own: 700 x 4096 8.2 us against 9.3, 3000 x
+    // 1024 8.2 against 9.4; at two to a unit it is slower, 400 x 5120 7.2 against 6.8.
+    const int together = 24 / (nt / 64);
+    if (together >= 3 && a.num_tokens <= NORM_BLOCKS * together) {
+        groups = 1;
+        limit = a.num_tokens;
+    }
     const int blocks = (a.num_tokens + groups - 1) / groups;
     const auto go = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, dim3((unsigned)(blocks < NORM_BLOCKS ? blocks : NORM_BLOCKS)),
+        hipLaunchKernelGGL(kernel, dim3((unsigned)(blocks < limit ? blocks : limit)),
                            dim3((unsigned)(nt * groups)), 0, stream, a, nt);
     };
     const bool f = a.stream_type == MEGA_MOE_F32, full = a.gate_kind == MEGA_MOE_GATE_FULL;

@@ -37,6 +37,10 @@ NORM = [
     (2, 8192, F32, F32, "full", BF16, True, 0),
     (1030, 384, BF16, F32, "channel", F32, True, 0),
     (577, 4096, F32, F32, "token", F32, False, 0),
+    # several rounds of rows, the last of them not full
+    (6300, 136, BF16, BF16, "channel", F32, True, 0),
+    (2100, 1000, F32, F32, "full", BF16, True, 8),
+    (6200, 256, BF16, F32, "token", BF16, False, 0),
 ]
 
 
