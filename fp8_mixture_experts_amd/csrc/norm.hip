@@ -122,10 +122,18 @@ moe_norm(mega_moe_norm_args a, int nt) {
         const float sf = amax / 448.0f;
         // tiny blocks are scaled up first, so that the reciprocal is finite
         const float up = sf < 0x1p-100f ? 0x1p100f : 1.0f;
-        const float inv = amax == 0.0f ? 0.0f : 1.0f / ((amax * up) / 448.0f);
+        float d = (amax * up) / 448.0f;
+        const float inv = amax == 0.0f ? 0.0f : 1.0f / d;
+        if (inv == 0.0f) d = 0.0f;               // a scale of 0 or infinity: codes of 0
+        // The quotient n / d: the product with the reciprocal is off by up to a step and
+        // a half, and next to a tie takes another code; one step of Newton's iteration
+        // (the exact remainder, times the reciprocal) rounds it as a division does.
         float v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = n[i] * up * inv;
+        for (int i = 0; i < 8; ++i) {
+            const float x = n[i] * up, q = x * inv;
+            v[i] = fmaf(-fmaf(q, d, -x), inv, q);
+        }
         int lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
         lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], lo, true);
         int hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[4], v[5], 0, false);

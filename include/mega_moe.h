@@ -385,8 +385,10 @@ int mega_moe_profile_end(mega_moe_handle* h, float* ms_out, int32_t capacity, in
  *   n = r * rsqrt(mean(r^2) + pre_eps) * pre_weight
  *   q_sf = max |n| over 128 columns / 448, q = e4m3(n / q_sf)
  * n is taken of r before r is rounded to its type, and q of n before n is
- * rounded.  Where a block's maximum is 0, q_sf and q are 0 (as in the layer's
- * own re-quantisation); a block with a NaN has q_sf and q NaN.
+ * rounded; the quotient is rounded as float32 divides (where q_sf is subnormal,
+ * that by the scale before it is rounded).  Where a block's maximum is 0, q_sf
+ * and q are 0 (as in the layer's own re-quantisation); a block with a NaN has
+ * q_sf and q NaN.
  */
 typedef struct mega_moe_norm_args {
     int32_t num_tokens;       /* T; 0 is a no-op                                 */

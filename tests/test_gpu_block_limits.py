@@ -1,0 +1,76 @@
+"""GPU tests of the operators around the layer where rounding or float32's range
+decides."""
+
+import numpy as np
+import pytest
+import torch
+
+from fp8_mixture_experts_amd import binding as B
+from oracle import codecs
+from tests import block_util as U
+from tests.test_gpu_block import _np
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+# ---- codes of the norm ---------------------------------------------------------------
+
+def _next_to_ties(blocks, seed):
+    """Blocks of 128 float32 values next to ties of E4M3, where the product with
+    the reciprocal of amax / 448 rounds to another code than the quotient.  Also
+    their scales, the quotients' codes and how many of the products' differ."""
+    rng = np.random.default_rng(seed)
+    grid = codecs.e4m3_decode(np.arange(127, dtype=np.uint8)).astype(np.float64)
+    ties = (grid[1:] + grid[:-1]) / 2
+    out, scales, differ = [], [], 0
+    for _ in range(blocks):
+        amax = np.float32(rng.uniform(1.0, 2.0) * 2.0 ** rng.integers(-3, 4))
+        sf = amax / np.float32(448.0)
+        near = (ties * np.float64(sf)).astype(np.float32)
+        cand = np.concatenate([near] + [(near.view(np.int32) + d).view(np.float32) for d in (-3, -2, -1, 1, 2, 3)])
+        cand = cand[cand < amax]
+        other = (codecs.e4m3_encode_rne((cand * (np.float32(1.0) / sf)).astype(np.float64))
+                 != codecs.e4m3_encode_rne((cand / sf).astype(np.float64)))
+        pick = np.concatenate([cand[other], rng.permutation(cand[~other])])[:127]
+        differ += min(int(other.sum()), 127)
+        b = np.concatenate([[amax], pick]).astype(np.float32) * rng.choice([-1.0, 1.0], 128).astype(np.float32)
+        out.append(b)
+        scales.append(sf)
+    v, s = np.stack(out), np.array(scales, np.float32)
+    return v.reshape(-1), s, codecs.e4m3_encode_rne((v / s[:, None]).astype(np.float64)).reshape(-1), differ
+
+
+@pytest.mark.parametrize("H", [128, 1024, 8192])
+def test_codes_are_those_of_the_quotient(H):
+    # ones as the stream and no epsilon: the pre-norm is 1 and n the weight itself
+    w, sf, want, differ = _next_to_ties(H // 128, H)
+    assert differ >= H // 128
+    T = 3
+    h = torch.ones(T, H, dtype=BF16, device="cuda")
+    q, q_sf = torch.empty(T, H, dtype=torch.uint8, device="cuda"), torch.empty(T, H // 128, device="cuda")
+    B.mega_moe_norm(B.make_args(B.mega_moe_norm_args, num_tokens=T, hidden=H, stream_type=B.MEGA_MOE_BF16,
+                                weight_type=B.MEGA_MOE_F32, residual_scale=1.0, h=h, q=q, q_sf=q_sf,
+                                pre_weight=torch.from_numpy(w).cuda()), U.current_stream())
+    for t in range(T):
+        assert np.array_equal(_np(q_sf)[t], sf)
+        assert np.array_equal(_np(q)[t], want), int((_np(q)[t] != want).sum())
+
+
+def test_codes_keep_the_sign_of_zero_and_blocks_of_an_infinite_scale():
+    H = 384
+    w = np.ones(H, np.float32)
+    w[:128:2] = -0.0                              # zeros of both signs beside ones
+    w[1:128:4] = 0.0
+    w[128:256] = -0.0                             # a block of zeros
+    w[256] = np.inf                               # n / inf is 0, inf / inf is not a number
+    h = torch.ones(1, H, dtype=BF16, device="cuda")
+    q, q_sf = torch.empty(1, H, dtype=torch.uint8, device="cuda"), torch.empty(1, H // 128, device="cuda")
+    B.mega_moe_norm(B.make_args(B.mega_moe_norm_args, num_tokens=1, hidden=H, stream_type=B.MEGA_MOE_BF16,
+                                weight_type=B.MEGA_MOE_F32, residual_scale=1.0, h=h, q=q, q_sf=q_sf,
+                                pre_weight=torch.from_numpy(w).cuda()), U.current_stream())
+    got, v = _np(q)[0], U.codes(q)[0]
+    assert np.array_equal(got[:128] == 0x80, np.signbit(w[:128])) and np.all(v[3:128:4] == 448.0)
+    assert not v[128:256].any() and _np(q_sf)[0, 1] == 0.0
+    assert np.isnan(v[256]) and not v[257:].any() and np.isinf(_np(q_sf)[0, 2])
