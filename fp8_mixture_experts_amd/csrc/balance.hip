@@ -127,6 +127,7 @@ moe_balance_part(mega_moe_balance_loss_args a, BalanceWs ws, int B) {
                 sum += ex[i];
             }
             sum = lanes_sum<LANES>(sum);
+            if (sum < SMALL_SUM) row_exp<LANES>(l[r], ex, top, sum);
         }
         const float inv = sum > 0.0f ? 1.0f / sum : sum;
 #pragma unroll

@@ -53,6 +53,12 @@ __device__ __forceinline__ void row_exp(const float (&l)[NI], float (&ex)[NI], f
 // any expert adds nothing to a loss.
 __device__ __forceinline__ float row_lse(float top, float sum) { return sum == 0.0f ? 0.0f : logf(sum) + top; }
 
+// Sums of scores below this are too small for their quotients: the reciprocals get
+// near float32's largest value, and the scores subnormal or 0.  It means that every
+// logit in the sum is below -55, where 1 + exp(logit) is 1 in float32: sigmoids are
+// there in the proportions of exp(logit - largest logit), whose sum is 1 or more.
+constexpr float SMALL_SUM = 0x1p-80f;
+
 // The hardware reciprocal is within one step of the quotient, and its argument
 // is at least 1.
 __device__ __forceinline__ float sigmoid(float x) { return __builtin_amdgcn_rcpf(1.0f + expf(-x)); }

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from fp8_mixture_experts_amd import binding as B
-from oracle import codecs
+from oracle import block, codecs
 from tests import block_util as U
 from tests.test_gpu_block import _np
 
@@ -74,3 +74,55 @@ def test_codes_keep_the_sign_of_zero_and_blocks_of_an_infinite_scale():
     assert np.array_equal(got[:128] == 0x80, np.signbit(w[:128])) and np.all(v[3:128:4] == 448.0)
     assert not v[128:256].any() and _np(q_sf)[0, 1] == 0.0
     assert np.isnan(v[256]) and not v[257:].any() and np.isinf(_np(q_sf)[0, 2])
+
+
+# ---- scores near the smallest floats ---------------------------------------------------
+
+# where a row's logits lie: ordinary, on both sides of where sums of sigmoids get
+# too small for their reciprocals, and where every sigmoid is below the smallest float
+BASES = np.array([0.0, -30.0, -54.0, -56.0, -70.0, -87.0, -88.5, -91.0, -95.0, -100.0, -104.0, -120.0, -300.0], np.float32)
+
+
+def _low_rows(T, E, k, seed, bf16=False):
+    """Logits around BASES in turn, and k different experts of every token."""
+    rng = np.random.default_rng(seed)
+    l = (rng.standard_normal((T, E)) + BASES[np.arange(T) % len(BASES), None]).astype(np.float32)
+    idx = np.argsort(rng.random((T, E)), axis=1)[:, :k].astype(np.int32)
+    l = torch.from_numpy(l).cuda()
+    return (l.to(BF16) if bf16 else l), idx
+
+
+def _losses(logits, idx, score, cu, z_coeff):
+    T, E = logits.shape
+    n = 1 if cu is None else len(cu) - 1
+    o = dict(loss=torch.full((2,), 7.0, device="cuda"), counts=torch.empty(n, E, dtype=torch.int32, device="cuda"),
+             tokens=torch.empty(n + 2, dtype=torch.int32, device="cuda"), probs=torch.full((n, E), 7.0, device="cuda"))
+    a = B.make_args(B.mega_moe_balance_loss_args, num_tokens=T, num_experts=E, num_topk=idx.shape[1],
+                    logits_type=U.TYPE[logits.dtype], score=U.SCORE[score], num_sequences=0 if cu is None else n,
+                    balance_coeff=0.5, z_coeff=z_coeff, logits=logits, topk_idx=torch.from_numpy(idx).cuda(),
+                    cu_seqlens=None if cu is None else torch.tensor(cu, dtype=torch.int32).cuda(), **o)
+    B.set_args(a, **U.workspace(B.mega_moe_balance_loss_workspace_bytes(a)))
+    B.mega_moe_balance_loss(a, U.current_stream())
+    torch.cuda.synchronize()
+    return o
+
+
+LOW = [(13, 4, 1, False), (26, 16, 2, False), (65, 30, 3, True), (100, 64, 4, False), (60, 100, 6, False), (130, 256, 8, False),
+       (39, 500, 4, True), (27, 1000, 8, False)]
+
+
+@pytest.mark.parametrize("T,E,k,bf16", LOW)
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("z", [0.0, 0.25])
+def test_balance_loss_of_low_logits(T, E, k, bf16, score, z):
+    logits, idx = _low_rows(T, E, k, T + E, bf16)
+    for cu in (None, list(range(T + 1))):            # all tokens together, and each for itself
+        o = _losses(logits, idx, score, cu, z)
+        want = block.balance_loss(U.f64(logits), idx, score, cu, None, 0.5, z)
+        assert np.array_equal(_np(o["counts"]), want["counts"])
+        # p: 32 roundings and E / 64 + 6 adds; then at most T adds of positive terms,
+        # E of them in the loss, and one per sequence
+        adds = 32 + E // 64 + T
+        U.near(o["probs"], want["probs"], want["probs"], adds, "probs")
+        U.near(o["loss"], want["loss"], want["loss_mag"], adds + E + T, "loss")
+    assert np.allclose(_np(o["probs"]).sum(axis=1), 1.0, atol=1e-5)      # every token is one sequence's all
