@@ -647,6 +647,17 @@ moe_router_backward(mega_moe_router_backward_args a) {
                 c += s[i] * f[i];
             }
             den = softmax ? 1.0f : lanes_sum<LANES>(den);
+            if (den < SMALL_SUM) {
+                // the slopes' share in den too: 1 - s is 1
+                if (!z) row_exp<LANES>(l, ex, top, sum);
+                den = sum;
+                c = 0.0f;
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    slope[i] = ex[i];
+                    c += ex[i] * f[i];
+                }
+            }
             const float id = den > 0.0f ? 1.0f / den : den;
             c = lanes_sum<LANES>(c) * id;
             const float lse = z ? a.dloss[1] * a.z_coeff * 2.0f / (float)max(n, 1) * row_lse(top, sum) * inv : 0.0f;

@@ -8,7 +8,7 @@ import torch
 from fp8_mixture_experts_amd import binding as B
 from oracle import block, codecs
 from tests import block_util as U
-from tests.test_gpu_block import _np
+from tests.test_gpu_block import _gen, _np
 
 pytestmark = pytest.mark.gpu
 
@@ -126,3 +126,34 @@ def test_balance_loss_of_low_logits(T, E, k, bf16, score, z):
         U.near(o["probs"], want["probs"], want["probs"], adds, "probs")
         U.near(o["loss"], want["loss"], want["loss_mag"], adds + E + T, "loss")
     assert np.allclose(_np(o["probs"]).sum(axis=1), 1.0, atol=1e-5)      # every token is one sequence's all
+
+
+def _gradient(logits, idx, score, dw=None, renormalize=True, scale=1.5, losses=None, z=0.0):
+    """dlogits and the reference's, of the weights' gradient, the losses' or both."""
+    T, E = logits.shape
+    k = idx.shape[1]
+    d = torch.full((T, E), 7.0, device="cuda")
+    f = dict(num_tokens=T, num_experts=E, num_topk=k, logits_type=U.TYPE[logits.dtype], score=U.SCORE[score], logits=logits,
+             dlogits=d)
+    want = {}
+    if dw is not None:
+        f.update(topk_idx=torch.from_numpy(idx).cuda(), dweights=dw, renormalize=int(renormalize), weight_scale=scale)
+        want.update(idx=idx, dweights=U.f64(dw), renormalize=renormalize, scale=scale)
+    if losses is not None:
+        ref = block.balance_loss(U.f64(logits), idx, score, None, None, 0.5, z)
+        f.update(dloss=losses, counts=torch.from_numpy(ref["counts"].astype(np.int32)).cuda(),
+                 tokens=torch.from_numpy(ref["tokens"].astype(np.int32)).cuda(), balance_coeff=0.5, z_coeff=z)
+        want.update(dloss=U.f64(losses), counts=ref["counts"], tokens=ref["tokens"], k=k, balance_coeff=0.5, z_coeff=z)
+    B.mega_moe_router_backward(B.make_args(B.mega_moe_router_backward_args, **f), U.current_stream())
+    torch.cuda.synchronize()
+    return (d, *block.router_backward(U.f64(logits), score, **want))
+
+
+@pytest.mark.parametrize("T,E,k,bf16", LOW)
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("z", [0.0, 0.25])
+def test_gradient_of_the_losses_of_low_logits(T, E, k, bf16, score, z):
+    logits, idx = _low_rows(T, E, k, T + E + 1, bf16)
+    d, want, mag = _gradient(logits, idx, score, losses=_gen(T)(2), z=z)
+    # scores: 32 roundings and E / 64 + 6 adds; the sums over experts the same again
+    U.near(d, want, mag, 2 * (48 + E // 64), "dlogits")
