@@ -510,28 +510,56 @@ moe_router_topk(mega_moe_router_topk_args a) {
     // the weights of the slots, from their own logits
     if (!in) return;
     float* w_out = a.topk_weights + (size_t)t * k;
+    // the score, or its proportion to that of the logit `most`
+    bool small = false;
+    float most = -INFINITY;
     const auto score_of = [&](int e, float l) {
         if (e < 0) return 0.0f;
-        return softmax ? expf(l - top) * inv : sigmoid(l);
+        if (small) return expf(l - most);
+        if (softmax) return expf(l - top) * inv;
+        // 1 + exp(l) is 1, and what the reciprocal would flush to 0 a subnormal
+        return l < -64.0f ? expf(l) : sigmoid(l);
     };
     float w = 0.0f, total = 0.0f;
-    if (one_each) {
-        if (lane < k) total = w = score_of(mine, x);
-    } else {
-        for (int j = lane; j < k; j += LANES) {
-            const int e = idx_out[j];
-            w = score_of(e, e >= 0 ? logit(e) : 0.0f);
-            w_out[j] = w;
-            total += w;
+    const auto slots = [&](auto&& f) {
+        if (one_each) {
+            if (lane < k) f(lane, mine, x);
+        } else {
+            for (int j = lane; j < k; j += LANES) {
+                const int e = idx_out[j];
+                f(j, e, e >= 0 ? logit(e) : 0.0f);
+            }
         }
-    }
-    total = lanes_sum<LANES>(total);
+    };
+    const auto score_slots = [&] {
+        total = 0.0f;
+        slots([&](int j, int e, float l) {
+            w = score_of(e, l);
+            if (!one_each) w_out[j] = w;
+            total += w;
+        });
+        total = lanes_sum<LANES>(total);
+    };
+    score_slots();
     float scale = a.weight_scale;
-    if (a.renormalize) scale = total == 0.0f ? 0.0f : scale / total;
+    if (a.renormalize) {
+        if (total < SMALL_SUM) {
+            // Only their proportions are asked for.  Where no score is above 2^-80 they
+            // are those of exp(logit), of a softmax always.
+            slots([&](int, int e, float l) { most = e >= 0 ? fmaxf(most, l) : most; });
+            most = lanes_max<LANES>(most);
+            small = most > -INFINITY;
+            if (small) score_slots();
+        }
+        scale = total == 0.0f ? 0.0f : scale / total;
+    }
+    // a quotient beyond float32, though the weights are not
+    const bool apart = isinf(scale);
+    const auto scaled = [&](float w) { return apart ? w / total * a.weight_scale : w * scale; };
     if (one_each) {
-        if (lane < k) w_out[lane] = w * scale;
+        if (lane < k) w_out[lane] = scaled(w);
     } else {
-        for (int j = lane; j < k; j += LANES) w_out[j] *= scale;
+        for (int j = lane; j < k; j += LANES) w_out[j] = scaled(w_out[j]);
     }
 }
 

@@ -8,7 +8,7 @@ import torch
 from fp8_mixture_experts_amd import binding as B
 from oracle import block, codecs
 from tests import block_util as U
-from tests.test_gpu_block import _gen, _np
+from tests.test_gpu_block import _gen, _np, _topk
 
 pytestmark = pytest.mark.gpu
 
@@ -157,3 +157,71 @@ def test_gradient_of_the_losses_of_low_logits(T, E, k, bf16, score, z):
     d, want, mag = _gradient(logits, idx, score, losses=_gen(T)(2), z=z)
     # scores: 32 roundings and E / 64 + 6 adds; the sums over experts the same again
     U.near(d, want, mag, 2 * (48 + E // 64), "dlogits")
+
+
+# ---- quotients of small scores ------------------------------------------------------------
+
+def _below_the_top(T, E, k, seed):
+    """Rows of which one expert has nearly all of the softmax, and k others: their
+    scores are next to or below the smallest float."""
+    rng = np.random.default_rng(seed)
+    l = (rng.standard_normal((T, E)) - rng.choice([20.0, 60.0, 87.0, 95.0, 100.0], (T, 1))).astype(np.float32)
+    l[:, 0] = 0.0
+    idx = np.argsort(rng.random((T, E - 1)), axis=1)[:, :k].astype(np.int32) + 1
+    return torch.from_numpy(l).cuda(), idx
+
+
+SLOTS = [(26, 4, 1), (39, 8, 2), (52, 40, 5), (65, 64, 8), (40, 256, 8), (2100, 100, 6), (30, 100, 70), (26, 600, 100)]
+
+
+@pytest.mark.parametrize("T,E,k", SLOTS)
+@pytest.mark.parametrize("renormalize", [True, False])
+def test_weights_of_small_scores(T, E, k, renormalize):
+    # sigmoids of low logits; the order is that of the logits, and of scores with a
+    # bias that moves only the first expert
+    first = torch.zeros(E, device="cuda")
+    first[0] = -10.0
+    low, _ = _low_rows(T, E, k, T + 2)
+    top, _ = _below_the_top(T, E, k, T + 3)
+    for logits, score, bias in ((low, "sigmoid", None), (low, "sigmoid", first), (top, "softmax", first),
+                                (top, "softmax", None)):
+        if bias is not None and k == E:
+            continue
+        # slots beyond what float32 can tell are not asked for: the indices are
+        # checked elsewhere, the weights are those of the indices given
+        idx, w = _topk(logits, k, score, bias, renormalize=renormalize)
+        at = _np(idx)
+        assert at.min() >= 0 and all(len(set(r)) == k for r in at.tolist())
+        s = np.take_along_axis(block.scores(U.f64(logits), score), at.astype(np.int64), axis=1)
+        want = 2.5 * s / (s.sum(axis=1, keepdims=True) if renormalize else 1.0)
+        # exp and the division carry a few roundings, and the difference to the
+        # row's largest logit half a step of up to 128
+        U.near(w, want, want, 32 + 128 + E // 64 + k, f"{score} {bias is not None}")
+
+
+# logits, score, bias: every expert that is taken has a score below the smallest normal float
+ONLY = [([0.0, -95.0], "softmax", [-10.0, 0.0]), ([-95.0, -110.0], "sigmoid", None), ([-88.0, -120.0], "sigmoid", [0.0, -1.0]),
+        ([0.0, -100.0, -103.0], "softmax", [-10.0, 0.0, -1.0])]
+
+
+@pytest.mark.parametrize("logits,score,bias", ONLY)
+def test_weight_of_the_only_slot_is_the_scale(logits, score, bias):
+    idx, w = _topk(torch.tensor([logits], device="cuda"), 1, score, None if bias is None else torch.tensor(bias, device="cuda"))
+    assert w.tolist() == [[2.5]], (idx.tolist(), w.tolist())
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_large_weight_scale_over_a_small_sum(score):
+    # scale / sum is beyond float32 in some rows, the weights in none
+    T, E, k = 9, 32, 3
+    r = _gen(5)
+    l = r(T, E) - 6.0
+    l[:, 0] = 3.0
+    bias = torch.zeros(E, device="cuda")
+    bias[0] = -10.0
+    scale = 1e37
+    idx, w = _topk(l, k, score, bias, scale=scale)
+    s = np.take_along_axis(block.scores(U.f64(l), score), _np(idx).astype(np.int64), axis=1)
+    want = float(np.float32(scale)) * s / s.sum(axis=1, keepdims=True)
+    assert float(np.float32(scale)) / s.sum(axis=1).min() > 3.5e38
+    U.near(w, want, want, 64, "weights")
