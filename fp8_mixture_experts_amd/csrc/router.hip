@@ -590,10 +590,26 @@ moe_router_backward(mega_moe_router_backward_args a) {
         load_row<NI, LANES>(a.logits, a.logits_type, at_row, E, l);
         if (softmax || z) row_exp<LANES>(l, ex, top, sum);
         const float inv = sum > 0.0f ? 1.0f / sum : sum;
+        // The losses see the sigmoids' proportions alone: of a row without a logit above
+        // LOW_LOGIT those of exp(logit - largest), whose sum has a reciprocal.
+        float most = -INFINITY;
+        if (!softmax && b >= 0) {
+            most = top;
+            if (!z) {
+                most = l[0];
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            if (softmax) s[i] = slope[i] = ex[i] * inv;
-            else sigmoid_slope(l[i], s[i], slope[i]);
+                for (int i = 1; i < NI; ++i) most = fmaxf(most, l[i]);
+                most = lanes_max<LANES>(most);
+            }
+        }
+        const bool low = most < LOW_LOGIT && most > -INFINITY;
+        const float shift = low ? most : 0.0f, one = low ? 0.0f : 1.0f;
+        if (softmax || b >= 0) {                 // the weights' gradient alone has no use for other sigmoids
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                if (softmax) s[i] = slope[i] = ex[i] * inv;
+                else sigmoid_slope(l[i], s[i], slope[i], shift, one);
+            }
         }
         if (a.dweights) {
             const int32_t* idx = a.topk_idx + (size_t)t * k;
@@ -675,17 +691,6 @@ moe_router_backward(mega_moe_router_backward_args a) {
                 c += s[i] * f[i];
             }
             den = softmax ? 1.0f : lanes_sum<LANES>(den);
-            if (den < SMALL_SUM) {
-                // the slopes' share in den too: 1 - s is 1
-                if (!z) row_exp<LANES>(l, ex, top, sum);
-                den = sum;
-                c = 0.0f;
-#pragma unroll
-                for (int i = 0; i < NI; ++i) {
-                    slope[i] = ex[i];
-                    c += ex[i] * f[i];
-                }
-            }
             const float id = den > 0.0f ? 1.0f / den : den;
             c = lanes_sum<LANES>(c) * id;
             const float lse = z ? a.dloss[1] * a.z_coeff * 2.0f / (float)max(n, 1) * row_lse(top, sum) * inv : 0.0f;

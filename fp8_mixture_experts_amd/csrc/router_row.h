@@ -63,10 +63,14 @@ constexpr float SMALL_SUM = 0x1p-80f;
 // is at least 1.
 __device__ __forceinline__ float sigmoid(float x) { return __builtin_amdgcn_rcpf(1.0f + expf(-x)); }
 
+// Below it 1 + exp(x) is 1 in float32.
+constexpr float LOW_LOGIT = -60.0f;
+
 // sigmoid(x) and its derivative, from exp(-|x|): s (1 - s) would cancel where s
-// is near 1.
-__device__ __forceinline__ void sigmoid_slope(float x, float& s, float& slope) {
-    const float e = expf(-fabsf(x)), d = __builtin_amdgcn_rcpf(1.0f + e);
+// is near 1.  With a `shift` below LOW_LOGIT that x does not pass, and `one` 0,
+// both are exp(x - shift): the sigmoid and its derivative over the sigmoid of shift.
+__device__ __forceinline__ void sigmoid_slope(float x, float& s, float& slope, float shift = 0.0f, float one = 1.0f) {
+    const float e = expf(-fabsf(x - shift)), d = __builtin_amdgcn_rcpf(fmaf(e, one, 1.0f));
     s = x >= 0.0f ? d : e * d;
     slope = e * d * d;
 }
