@@ -617,6 +617,7 @@ moe_router_backward(mega_moe_router_backward_args a) {
             float* row = s_row[threadIdx.x / LANES];
             // rounds of LANES slots: first their scores' sum and its product
             // with dw, then the slots' parts of the gradient
+            float ref = softmax ? top : 0.0f, fac = softmax ? inv : 1.0f, most_taken = -INFINITY;
             const auto slot = [&](int j, int& e, float& g, float& sj, float& slj) {
                 e = j < k ? idx[j] : -1;
                 g = sj = slj = 0.0f;
@@ -628,25 +629,38 @@ moe_router_backward(mega_moe_router_backward_args a) {
                 const float x = a.logits_type == MEGA_MOE_F32
                                     ? static_cast<const float*>(a.logits)[at_row + e]
                                     : bf16_value(static_cast<const uint16_t*>(a.logits)[at_row + e]);
-                if (softmax) sj = slj = expf(x - top) * inv;
-                else sigmoid_slope(x, sj, slj);
+                most_taken = fmaxf(most_taken, x);
+                if (softmax) sj = slj = expf(x - ref) * fac;
+                else sigmoid_slope(x, sj, slj, ref, fac);
             };
             int e;
-            float g, sj, slj, total = 0.0f, dot = 0.0f;
-            for (int j0 = 0; j0 < k; j0 += LANES) {
-                slot(j0 + lane, e, g, sj, slj);
-                total += sj;
-                dot += g * sj;
-            }
-            total = lanes_sum<LANES>(total);
-            dot = lanes_sum<LANES>(dot);
+            float g, sj, slj, total, dot;
             const bool renorm = a.renormalize != 0;
-            const float scale = renorm ? (total == 0.0f ? 0.0f : a.weight_scale / total) : a.weight_scale;
-            const float mean = renorm && total != 0.0f ? dot / total : 0.0f;
+            for (bool again = renorm;;) {
+                total = dot = 0.0f;
+                for (int j0 = 0; j0 < k; j0 += LANES) {
+                    slot(j0 + lane, e, g, sj, slj);
+                    total += sj;
+                    dot += g * sj;
+                }
+                total = lanes_sum<LANES>(total);
+                dot = lanes_sum<LANES>(dot);
+                if (!again || !(total < SMALL_SUM)) break;
+                // Once more, relative to the largest of them: only the proportions count,
+                // and those of the sigmoids' slopes are the same, since 1 - s is 1.
+                ref = lanes_max<LANES>(most_taken);
+                if (ref == -INFINITY) break;
+                fac = softmax ? 1.0f : 0.0f;
+                again = false;
+            }
+            // the factor of a slot's slope, and weight_scale apart: their product may be
+            // beyond float32 where the gradients are not
+            const float part = !renorm ? 1.0f : total == 0.0f ? 0.0f : 1.0f / total;
+            const float mean = renorm ? dot * part : 0.0f;
             float c = 0.0f;
             for (int j0 = 0; j0 < k; j0 += LANES) {
                 if (k > LANES) slot(j0 + lane, e, g, sj, slj);
-                const float v = e >= 0 ? scale * (g - mean) * slj : 0.0f;
+                const float v = e >= 0 ? a.weight_scale * ((g - mean) * (slj * part)) : 0.0f;
                 c += v;
                 // an expert taken twice: found by who wrote last
                 if (e >= 0) row[e] = __int_as_float(lane);

@@ -225,3 +225,36 @@ def test_large_weight_scale_over_a_small_sum(score):
     want = float(np.float32(scale)) * s / s.sum(axis=1, keepdims=True)
     assert float(np.float32(scale)) / s.sum(axis=1).min() > 3.5e38
     U.near(w, want, want, 64, "weights")
+
+
+@pytest.mark.parametrize("T,E,k", SLOTS)
+@pytest.mark.parametrize("renormalize", [True, False])
+def test_gradient_of_the_weights_of_small_scores(T, E, k, renormalize):
+    r = _gen(T + E)
+    for (logits, idx), score in ((_low_rows(T, E, k, T + 4), "sigmoid"), (_below_the_top(T, E, min(k, E - 1), T + 5), "softmax"),
+                                 (_low_rows(T, E, k, T + 6), "softmax")):
+        dw = r(T, idx.shape[1])
+        d, want, mag = _gradient(logits, idx, score, dw, renormalize)
+        # as for the weights, twice, and the sums over slots
+        U.near(d, want, mag, 2 * (48 + 128 + E // 64) + 2 * k, score)
+
+
+@pytest.mark.parametrize("logits,score,bias", ONLY)
+def test_gradient_of_the_only_weight_is_zero(logits, score, bias):
+    l = torch.tensor([logits], device="cuda")
+    idx, _ = _topk(l, 1, score, None if bias is None else torch.tensor(bias, device="cuda"))
+    d, want, _ = _gradient(l, _np(idx), score, dw=torch.full((1, 1), 3.0, device="cuda"))
+    assert not want.any() and np.all(np.abs(_np(d)) <= 2.0 ** -20), d.tolist()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_gradient_of_a_large_weight_scale_over_a_small_sum(score):
+    T, E, k = 9, 32, 3
+    r = _gen(6)
+    l = r(T, E) - 6.0
+    l[:, 0] = 3.0
+    idx = (np.arange(T * k).reshape(T, k) % (E - 1) + 1).astype(np.int32)
+    scale = float(np.float32(1e37))
+    assert scale / np.take_along_axis(block.scores(U.f64(l), score), idx.astype(np.int64), axis=1).sum(axis=1).min() > 3.5e38
+    d, want, mag = _gradient(l, idx, score, r(T, k), True, scale)
+    U.near(d, want, mag, 128, "dlogits")
