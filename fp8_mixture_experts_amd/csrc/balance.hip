@@ -25,7 +25,7 @@
 namespace mega_moe {
 
 constexpr int CHUNK = 32;             // tokens per chunk
-constexpr int SLICE = 32;             // experts per workgroup of the second launch
+constexpr int SLICE = BALANCE_SLICE;
 
 struct BalanceWs {
     float* p;             // [records][E]
@@ -348,7 +348,7 @@ void launch_balance_loss(const mega_moe_balance_loss_args& a, hipStream_t stream
     else if (E <= 256) part(integral_constant<int, 32>{}, integral_constant<int, 8>{});
     else if (E <= 512) part(integral_constant<int, 64>{}, integral_constant<int, 8>{});
     else part(integral_constant<int, 64>{}, integral_constant<int, 16>{});
-    const dim3 finish((unsigned)(B * ((E + SLICE - 1) / SLICE)));
+    const dim3 finish((unsigned)balance_finish_groups(B, E));
     if (chunks / B >= 16) hipLaunchKernelGGL((moe_balance_finish<32>), finish, dim3(1024), 0, stream, a, w, B);
     else hipLaunchKernelGGL((moe_balance_finish<8>), finish, dim3(256), 0, stream, a, w, B);
 }

@@ -251,8 +251,13 @@ int check_sequences(const Args& a) {
 
 int check_balance_sizes(const mega_moe_balance_loss_args* a) {
     if (!a) return bad("the argument block is NULL");
-    const int rc = check_router(*a);
-    return rc ? rc : check_sequences(*a);
+    if (const int rc = check_router(*a)) return rc;
+    if (const int rc = check_sequences(*a)) return rc;
+    const int64_t groups = balance_finish_groups(a->num_sequences, a->num_experts);
+    if (groups > BALANCE_MAX_GROUPS)
+        return fail(MEGA_MOE_ERR_UNSUPPORTED, "built for num_sequences * ceil(num_experts / 32) <= %lld, got %lld",
+                    (long long)BALANCE_MAX_GROUPS, (long long)groups);
+    return MEGA_MOE_OK;
 }
 
 bool words_aligned(std::initializer_list<const void*> list) {

@@ -543,7 +543,8 @@ typedef struct mega_moe_balance_loss_args {
     int32_t num_topk;         /* k in [1, 1024]                                  */
     int32_t logits_type;
     int32_t score;
-    int32_t num_sequences;    /* B; 0 or 1 without cu_seqlens: all T tokens are one */
+    int32_t num_sequences;    /* B; 0 or 1 without cu_seqlens: all T tokens are one;
+                                 B * ceil(E / 32) below 2^24                     */
     float balance_coeff, z_coeff;   /* finite                                    */
     const void* logits;       /* [T, E]                                          */
     const int32_t* topk_idx;  /* [T, k]                                          */

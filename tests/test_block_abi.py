@@ -198,3 +198,21 @@ def test_workspace_bytes_need_no_gpu_and_refuse_bad_sizes():
     assert B.mega_moe_router_logits_workspace_bytes(_logits(num_experts=0)) == -1
     assert B.mega_moe_balance_loss_workspace_bytes(_balance()) > 0
     assert B.mega_moe_balance_loss_workspace_bytes(_balance(num_topk=0)) == -1
+
+
+@pytest.mark.parametrize("experts,most", [(32, 1 << 21), (224, 1 << 21), (225, (1 << 21) - 1), (256, (1 << 21) - 1), (1024, (1 << 19) - 1)])
+def test_more_sequences_than_a_launch_has_workgroups_for_are_unsupported(experts, most):
+    # the second launch has a workgroup of 256 threads for 32 experts of a sequence,
+    # and a launch fewer than 2^32 threads
+    G = 1 << 36          # stand-in addresses further apart than the arrays are long
+
+    def call(n):
+        return _balance(num_experts=experts, num_sequences=n, logits=G, topk_idx=2 * G, loss=3 * G, counts=4 * G, tokens=5 * G,
+                        probs=6 * G, cu_seqlens=7 * G, workspace=8 * G, workspace_bytes=1 << 40)
+
+    assert B.mega_moe_balance_loss_workspace_bytes(call(most)) > 0
+    if most < 1 << 21:
+        assert B.mega_moe_balance_loss_workspace_bytes(call(most + 1)) == -1
+        with pytest.raises(B.MegaMoEError) as ei:
+            B.mega_moe_balance_loss(call(most + 1), None)
+        assert ei.value.code == B.MEGA_MOE_ERR_UNSUPPORTED and "num_sequences" in B.mega_moe_last_error()
