@@ -131,6 +131,8 @@ int check_device(const void* tensor, void* stream) {
         (void)hipGetLastError();
         return bad("a tensor is not in memory that the device knows");
     }
+    // the runtime has an answer for ordinary host memory too
+    if (at.type == hipMemoryTypeUnregistered) return bad("the tensors are in host memory that the device does not know");
     if (at.type == hipMemoryTypeDevice && at.device != dev)
         return fail(MEGA_MOE_ERR_INVALID_ARG, "the tensors are on device %d, the current device is %d", at.device, dev);
     return MEGA_MOE_OK;

@@ -258,3 +258,40 @@ def test_gradient_of_a_large_weight_scale_over_a_small_sum(score):
     assert scale / np.take_along_axis(block.scores(U.f64(l), score), idx.astype(np.int64), axis=1).sum(axis=1).min() > 3.5e38
     d, want, mag = _gradient(l, idx, score, r(T, k), True, scale)
     U.near(d, want, mag, 128, "dlogits")
+
+
+# ---- tensors the device does not know ------------------------------------------------------------
+
+def test_a_first_tensor_in_host_memory_is_refused():
+    T, H, E, k = 4, 256, 8, 2
+    here = dict(device="cuda")
+    rows, wide = torch.zeros(T, H, dtype=BF16, **here), torch.zeros(T, E, **here)
+    w, out, idx = torch.ones(H, **here), torch.full((T, H), 7.0, dtype=BF16, **here), torch.zeros(T, k, dtype=torch.int32, **here)
+    ws = U.workspace(1 << 20)
+    calls = [
+        (B.mega_moe_norm, B.mega_moe_norm_args, "h", rows, dict(num_tokens=T, hidden=H, weight_type=1, residual_scale=1.0,
+                                                               pre_weight=w, n=out)),
+        (B.mega_moe_norm_backward, B.mega_moe_norm_backward_args, "dr", rows, dict(num_tokens=T, hidden=H, residual_scale=1.0, dh=out)),
+        (B.mega_moe_router_logits, B.mega_moe_router_logits_args, "x", rows, dict(num_tokens=T, hidden=H, num_experts=E, logits=wide,
+                                                                                 w=torch.zeros(E, H, dtype=BF16, **here), **ws)),
+        (B.mega_moe_router_logits_backward, B.mega_moe_router_logits_args, "dlogits", wide,
+         dict(num_tokens=T, hidden=H, num_experts=E, w=torch.zeros(E, H, dtype=BF16, **here), dx=out, **ws)),
+        (B.mega_moe_router_topk, B.mega_moe_router_topk_args, "logits", wide,
+         dict(num_tokens=T, num_experts=E, num_topk=k, logits_type=1, topk_idx=idx, topk_weights=torch.zeros(T, k, **here))),
+        (B.mega_moe_balance_loss, B.mega_moe_balance_loss_args, "loss", torch.zeros(2, **here),
+         dict(num_tokens=T, num_experts=E, num_topk=k, logits_type=1, logits=wide, topk_idx=idx,
+              counts=torch.zeros(E, dtype=torch.int32, **here), tokens=torch.zeros(3, dtype=torch.int32, **here), **ws)),
+        (B.mega_moe_router_backward, B.mega_moe_router_backward_args, "logits", wide,
+         dict(num_tokens=T, num_experts=E, num_topk=k, logits_type=1, topk_idx=idx, dweights=torch.zeros(T, k, **here),
+              dlogits=torch.zeros(T, E, **here))),
+    ]
+    for call, cls, first, good, others in calls:
+        a = B.make_args(cls, **{first: good}, **others)
+        assert call(a, U.current_stream()) == 0, call.__name__
+        # aligned as a device's tensor is, in ordinary memory: the refusal is the host's
+        host = torch.zeros(good.numel() * good.element_size() + 64, dtype=torch.uint8)
+        B.set_args(a, **{first: host.data_ptr() + -host.data_ptr() % 64})
+        with pytest.raises(B.MegaMoEError) as ei:
+            call(a, U.current_stream())
+        assert ei.value.code == B.MEGA_MOE_ERR_INVALID_ARG and "host memory" in B.mega_moe_last_error()
+    torch.cuda.synchronize()
