@@ -295,3 +295,62 @@ def test_a_first_tensor_in_host_memory_is_refused():
             call(a, U.current_stream())
         assert ei.value.code == B.MEGA_MOE_ERR_INVALID_ARG and "host memory" in B.mega_moe_last_error()
     torch.cuda.synchronize()
+
+
+# ---- float32 operands of the router's products ------------------------------------------------
+
+def _full(r, *shape):
+    """Floats whose 24 bits of mantissa are all in use."""
+    v = r(*shape)
+    return torch.where(v.abs() < 1e-3, torch.full_like(v, 0.7), v)
+
+
+def _two_terms(v):
+    """What is left of a float32 in two BF16 terms."""
+    first = v.to(BF16).float()
+    return first + (v - first).to(BF16).float()
+
+
+# through each of the kernels: 16 x 16 tiles; few, some, many experts, workgroups in
+# pairs, K in parts and not
+@pytest.mark.parametrize("T,H,E", [(3, 40, 5), (64, 512, 64), (129, 2048, 257), (5003, 1160, 17), (3300, 904, 61),
+                                   (1030, 776, 260), (8200, 4104, 130), (515, 1152, 300), (2050, 520, 330)])
+def test_logits_of_float32_weights_lose_no_bit(T, H, E):
+    # a one in every row of x: the logits are columns of w
+    r = _gen(T + H)
+    w = _full(r, E, H)
+    at = torch.randint(0, H, (T,), device="cuda", generator=torch.Generator(device="cuda").manual_seed(H))
+    x = torch.zeros(T, H, dtype=BF16, device="cuda")
+    x[torch.arange(T, device="cuda"), at] = 1.0
+    logits = torch.full((T, E), 7.0, device="cuda")
+    a = B.make_args(B.mega_moe_router_logits_args, num_tokens=T, hidden=H, num_experts=E, weight_type=B.MEGA_MOE_F32, x=x, w=w,
+                    logits=logits)
+    B.set_args(a, **U.workspace(B.mega_moe_router_logits_workspace_bytes(a)))
+    B.mega_moe_router_logits(a, U.current_stream())
+    want = w[:, at].t()
+    assert (_two_terms(want) != want).float().mean() > 0.5       # two terms would not do
+    assert torch.equal(logits, want), int((logits != want).sum())
+
+
+# one step of 64 k in LDS and two, parts of T and not, rows of dlogits padded and not
+BACKWARD = [(3, 40, 5), (64, 512, 64), (129, 2048, 257), (515, 1152, 300), (2050, 640, 72), (8200, 1032, 66), (4100, 2056, 70),
+            (1100, 256, 8)]
+
+
+@pytest.mark.parametrize("T,H,E", BACKWARD)
+@pytest.mark.parametrize("wt", [BF16, F32])
+def test_dw_loses_no_bit(T, H, E, wt):
+    # a one in every column of x: the columns of dw are rows of dlogits
+    r = _gen(T + E)
+    d = _full(r, T, E)
+    at = torch.randint(0, T, (H,), device="cuda", generator=torch.Generator(device="cuda").manual_seed(T))
+    x = torch.zeros(T, H, dtype=BF16, device="cuda")
+    x[at, torch.arange(H, device="cuda")] = 1.0
+    w, dx, dw = r(E, H, dtype=wt), torch.empty(T, H, dtype=BF16, device="cuda"), torch.full((E, H), 7.0, device="cuda")
+    a = B.make_args(B.mega_moe_router_logits_args, num_tokens=T, hidden=H, num_experts=E, weight_type=U.TYPE[wt], x=x, w=w,
+                    dlogits=d, dx=dx, dw=dw)
+    B.set_args(a, **U.workspace(B.mega_moe_router_logits_workspace_bytes(a)))
+    B.mega_moe_router_logits_backward(a, U.current_stream())
+    want = d[at].t()
+    assert (_two_terms(want) != want).float().mean() > 0.5
+    assert torch.equal(dw, want), int((dw != want).sum())
