@@ -719,6 +719,48 @@ void launch_forward(const mega_moe_router_logits_args& a, hipStream_t stream) {
     else launch_product<typename F::Many>(a, stream);
 }
 
+// The gradients' kinds, with steps in LDS as they are launched.
+struct Bf16Gradients {
+    template <int S>
+    using W = Kind<Lay::row_float, 3, Lay::row_major, 1, 64, 128, S, false>;
+    template <int S>
+    using X = Kind<Lay::k_float, 2, Lay::row_major, 1, 64, 128, S, true>;
+};
+struct F32Gradients {
+    template <int S>
+    using W = Bf16Gradients::W<S>;
+    template <int S>
+    using X = Kind<Lay::k_float, 2, Lay::row_float, 2, 64, 128, S, true>;
+};
+
+// Workgroups that a compute unit's 160 kB of LDS hold.
+template <typename KW, typename KX>
+constexpr unsigned to_a_unit() {
+    return 163840u / ((KW::LDS > KX::LDS ? KW::LDS : KX::LDS) * 16u);
+}
+
+// One step in LDS or two.  Two, with which a workgroup keeps a step's loads in flight
+// while it multiplies, where each has a place on the 256 compute units at once: two to
+// a unit with BF16 weights (64 kB), one with float32 weights (96 kB).  More of them
+// hide each other's loads, and with one step four and three to a unit fit.  One and
+// two steps, us (workgroups), BF16 weights: 3383 x 640 x 216 22 and 19 (425), 4096 x
+// 2048 x 128 25 and 26 (1280), 4096 x 4096 x 64 27 and 32 (2304); float32: 3383 x 640
+// x 216 21 and 26 (425), 768 x 3584 x 96 17 and 19 (448), 256 x 7168 x 256 13 and 17
+// (448).  Up to 64 experts dx has no second step to wait for, and two are better with
+// float32 weights too: 640 x 4096 x 64 14.7 and 13.3 (384), 512 x 5120 x 32 12.4 and
+// 11.9 (400).
+template <typename G>
+void launch_gradients(const Product& w, unsigned w_blocks, const Product& x, unsigned x_blocks, hipStream_t stream) {
+    const auto go = [&](auto stages) {
+        constexpr int S = decltype(stages)::value;
+        hipLaunchKernelGGL((moe_router_gradients<typename G::template W<S>, typename G::template X<S>>),
+                           dim3(w_blocks + x_blocks), dim3(256), 0, stream, w, w_blocks, x);
+    };
+    constexpr unsigned PLACES = 256 * to_a_unit<typename G::template W<2>, typename G::template X<2>>();
+    if (w_blocks + x_blocks <= (x.a.k > STEP ? PLACES : 512)) go(std::integral_constant<int, 2>{});
+    else go(std::integral_constant<int, 1>{});
+}
+
 }  // namespace
 
 int64_t router_logits_workspace(const mega_moe_router_logits_args& a) {
@@ -762,22 +804,8 @@ void launch_router_logits_backward(const mega_moe_router_logits_args& a, hipStre
                     Result{E, H, p.split.n > 1 ? parts : a.dw, H, nullptr, nullptr, 0}, p.split.k, p.split.n};
     const unsigned w_blocks = a.dw ? (unsigned)(tiles(E, 64) * tiles(H, 128) * p.split.n) : 0;
     const unsigned x_blocks = a.dx ? (unsigned)(tiles(T, 64) * tiles(H, 128)) : 0;
-    const auto go = [&](auto stages) {
-        constexpr int S = decltype(stages)::value;
-        using KW = Kind<Lay::row_float, 3, Lay::row_major, 1, 64, 128, S, false>;
-        using KX1 = Kind<Lay::k_float, 2, Lay::row_major, 1, 64, 128, S, true>;
-        using KX2 = Kind<Lay::k_float, 2, Lay::row_float, 2, 64, 128, S, true>;
-        const dim3 grid(w_blocks + x_blocks);
-        if (f) hipLaunchKernelGGL((moe_router_gradients<KW, KX2>), grid, dim3(256), 0, stream, w, w_blocks, x);
-        else hipLaunchKernelGGL((moe_router_gradients<KW, KX1>), grid, dim3(256), 0, stream, w, w_blocks, x);
-    };
-    // Up to two workgroups to a compute unit: each keeps a step's loads in flight
-    // while it multiplies.  More of them hide each other's loads, and with one
-    // step in LDS four fit.  One and two steps: 3383 x 640 x 216 22 and 19 us (425
-    // workgroups), 4096 x 2048 x 128 25 and 26 (1280), 4096 x 4096 x 64 27 and 32
-    // (2304), 2589 x 5760 x 72 with float32 weights 47 and 69 (2205).
-    if (w_blocks + x_blocks <= 512) go(std::integral_constant<int, 2>{});
-    else go(std::integral_constant<int, 1>{});
+    if (f) launch_gradients<F32Gradients>(w, w_blocks, x, x_blocks, stream);
+    else launch_gradients<Bf16Gradients>(w, w_blocks, x, x_blocks, stream);
     if (a.dw && p.split.n > 1) launch_join(parts, a.dw, E, H, H, p.split.n, stream);
 }
 
