@@ -12,7 +12,7 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
 // Eight floats as the sum of P BF16 vectors: each term is what is left, rounded
-// to nearest.  Two leave 2^-18 of the value, three nothing (24 bits).  Finite
+// to nearest.  Two leave 2^-17 of the value, three nothing (24 bits).  Finite
 // values below BF16's largest; an infinity becomes NaN.
 template <int P>
 __device__ __forceinline__ void split_bf16(const float (&v)[8], u32x4_t (&p)[P]) {
@@ -115,7 +115,7 @@ moe_router_logits(mega_moe_router_logits_args a, int tile_t, int tile_e) {
 // ---------------------------------------------------------------------------
 // Tiles through LDS, for batches of tokens and for the gradients.
 // C[m, n] = sum over k of A[m, k] B[n, k] on 32 x 32 x 16 BF16 matrix
-// instructions, each operand as one to three BF16 planes whose products add
+// instructions, each operand as one BF16 plane or three whose products add
 // into the same accumulators, the small ones first.  A float32 operand is split
 // into its planes where its fragments are read.
 //
@@ -719,7 +719,13 @@ void launch_forward(const mega_moe_router_logits_args& a, hipStream_t stream) {
     else launch_product<typename F::Many>(a, stream);
 }
 
-// The gradients' kinds, with steps in LDS as they are launched.
+// The gradients' kinds, with steps in LDS as they are launched.  In dx, which is rounded
+// to BF16, two terms of dlogits do for BF16 weights: the 2^-17 that they leave shows
+// only where the sum over the experts is some 256 times smaller than its terms, and
+// rows of w of 8 bits hardly differ by so little (4096 x 4096 x 64 25 us, 26 with three
+// terms; 8192 x 7168 x 256 181 and 198).  Float32 rows may: with what is 256 times their differences in common, and
+// dlogits that add up to 0, as a softmax's do, two terms of both are half a step
+// of BF16 (4096 x 4096 x 64: 30 us, so 33; 8192 x 7168 x 256 237 and 300).
 struct Bf16Gradients {
     template <int S>
     using W = Kind<Lay::row_float, 3, Lay::row_major, 1, 64, 128, S, false>;
@@ -730,7 +736,7 @@ struct F32Gradients {
     template <int S>
     using W = Bf16Gradients::W<S>;
     template <int S>
-    using X = Kind<Lay::k_float, 2, Lay::row_float, 2, 64, 128, S, true>;
+    using X = Kind<Lay::k_float, 3, Lay::row_float, 3, 64, 128, S, true>;
 };
 
 // Workgroups that a compute unit's 160 kB of LDS hold.
@@ -743,12 +749,11 @@ constexpr unsigned to_a_unit() {
 // while it multiplies, where each has a place on the 256 compute units at once: two to
 // a unit with BF16 weights (64 kB), one with float32 weights (96 kB).  More of them
 // hide each other's loads, and with one step four and three to a unit fit.  One and
-// two steps, us (workgroups), BF16 weights: 3383 x 640 x 216 22 and 19 (425), 4096 x
-// 2048 x 128 25 and 26 (1280), 4096 x 4096 x 64 27 and 32 (2304); float32: 3383 x 640
-// x 216 21 and 26 (425), 768 x 3584 x 96 17 and 19 (448), 256 x 7168 x 256 13 and 17
-// (448).  Up to 64 experts dx has no second step to wait for, and two are better with
-// float32 weights too: 640 x 4096 x 64 14.7 and 13.3 (384), 512 x 5120 x 32 12.4 and
-// 11.9 (400).
+// two steps, us (workgroups), BF16 weights: 3383 x 640 x 216 21 and 19 (425), 768 x 3584
+// x 96 17 and 15 (448), 4096 x 2048 x 128 24 and 25 (1280), 4096 x 4096 x 64 25 and
+// 29 (2304), but 4096 x 896 x 64 17.7 and 16.9 (560); float32: 64 x 7168 x 256 13.2 and 15.8 (280), 3383 x 640 x 216 24 and 29
+// (425), 768 x 3584 x 96 17 and 20 (448), 4096 x 4096 x 64 33 and 53 (2304), but 640 x
+// 4096 x 64 14.6 and 13.8 (384) and 256 x 2048 x 128 8.6 and 8.3 (96).
 template <typename G>
 void launch_gradients(const Product& w, unsigned w_blocks, const Product& x, unsigned x_blocks, hipStream_t stream) {
     const auto go = [&](auto stages) {
@@ -757,7 +762,7 @@ void launch_gradients(const Product& w, unsigned w_blocks, const Product& x, uns
                            dim3(w_blocks + x_blocks), dim3(256), 0, stream, w, w_blocks, x);
     };
     constexpr unsigned PLACES = 256 * to_a_unit<typename G::template W<2>, typename G::template X<2>>();
-    if (w_blocks + x_blocks <= (x.a.k > STEP ? PLACES : 512)) go(std::integral_constant<int, 2>{});
+    if (w_blocks + x_blocks <= PLACES) go(std::integral_constant<int, 2>{});
     else go(std::integral_constant<int, 1>{});
 }
 

@@ -456,8 +456,9 @@ int64_t mega_moe_norm_workspace_bytes(const mega_moe_norm_backward_args* a);
  * The router's product and its gradients: logits = x . w^T, in float32, and
  *   dx = dlogits . w (+ dx_add),   dw = dlogits^T . x.
  * The products run on the BF16 matrix cores.  A float32 operand is split into
- * BF16 terms: three where the result is float32 (the split is exact), two
- * where it is rounded to BF16 (dx).  x, dlogits and w must be finite and below
+ * three BF16 terms, whose sum is exact (of two such operands' products what is
+ * below 2^-24 of each is left out); in dx with BF16 weights dlogits into two,
+ * which leave less than 2^-16 of it.  x, dlogits and w must be finite and below
  * BF16's largest value (an infinity may come out as NaN).
  */
 typedef struct mega_moe_router_logits_args {

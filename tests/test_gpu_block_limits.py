@@ -354,3 +354,36 @@ def test_dw_loses_no_bit(T, H, E, wt):
     want = d[at].t()
     assert (_two_terms(want) != want).float().mean() > 0.5
     assert torch.equal(dw, want), int((dw != want).sum())
+
+
+def _next_to_bf16_ties(r, *shape):
+    """Floats one step of float32 above or below the middle of two BF16 values."""
+    v = r(*shape).view(torch.int32) & ~0xffff
+    return (v + 0x8000 + torch.where(r(*shape) > 0, 1, -1).to(torch.int32)).view(F32)
+
+
+@pytest.mark.parametrize("T,H,E", BACKWARD)
+@pytest.mark.parametrize("which", ["dlogits", "w"])
+def test_dx_of_float32_weights_is_rounded_once(T, H, E, which):
+    # dx is one product of a one with a float next to a tie of BF16
+    r = _gen(T + E + H)
+    d, w = torch.zeros(T, E, device="cuda"), torch.zeros(E, H, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(E)
+    if which == "w":
+        at = torch.randint(0, E, (T,), device="cuda", generator=g)
+        d[torch.arange(T, device="cuda"), at] = 1.0
+        w = _next_to_bf16_ties(r, E, H)
+        exact = w[at]
+    else:
+        at = torch.randint(0, E, (H,), device="cuda", generator=g)
+        w[at, torch.arange(H, device="cuda")] = 1.0
+        d = _next_to_bf16_ties(r, T, E)
+        exact = d[:, at]
+    dx = torch.empty(T, H, dtype=BF16, device="cuda")
+    a = B.make_args(B.mega_moe_router_logits_args, num_tokens=T, hidden=H, num_experts=E, weight_type=B.MEGA_MOE_F32, w=w,
+                    dlogits=d, dx=dx)
+    B.set_args(a, **U.workspace(B.mega_moe_router_logits_workspace_bytes(a)))
+    B.mega_moe_router_logits_backward(a, U.current_stream())
+    want = exact.to(BF16)
+    assert (_two_terms(exact).to(BF16) != want).float().mean() > 0.2     # two terms would not do
+    assert torch.equal(dx, want), int((dx != want).sum())
