@@ -10,10 +10,10 @@
 // workgroup; the workgroup that ends last adds up the losses.
 //
 // The logits are read once (8 MB at 8192 x 256: 2 us); what bounds it is the
-// chain of a token's loads, exponentials and sums, and the two launches: 8.5 and
-// 5.5 us there, with 13 sequences; 3.5 and 2.6 us at 576 x 32.  p is computed once
+// chain of a token's loads, exponentials and sums, and the two launches: 8.6 and
+// 5.6 us there, with 13 sequences; 3.5 and 2.6 us at 576 x 32.  p is computed once
 // for all the sequences that a chunk meets: computed for each of them in turn,
-// 32768 x 256 with 64 sequences took 35 us, so 27.
+// 32768 x 256 with 64 sequences took a third longer than so (17.4 and 12.5 us).
 #include <hip/hip_runtime.h>
 
 #include <type_traits>

@@ -14,14 +14,15 @@ namespace mega_moe {
 //
 // Memory bound: every tensor is read or written once.  The next row's loads
 // stay in flight over the two row sums; two rows at a time for a group took as
-// long (110 us) with half as many registers again.  The weights are read once per
+// long with half as many registers again.  The weights are read once per
 // workgroup: read again for each row they were 40% more bytes to the compute
 // units than the rows.  r is read again after the whole layer and streamed past
 // the caches, n and q are read next and are not: with the readers behind it, and
 // 256 MiB between r and its reader, 249 us, against 253 with nothing streamed and
 // 259 with n streamed too.  8192 rows of 7168 in BF16 with y, a gate by channel
-// and all three outputs: 108 us, 4.9 TB/s (a copy of 1 GiB: 5.1 TB/s); 577 rows
-// of 4096 in float32: 7.7 us.
+// and all three outputs: 96 to 98 us, 5.5 TB/s (a copy of 1 GiB: 5.1 TB/s; part of
+// the 530 MB stays in the last-level cache); the codes' exact quotients are 1 us of
+// it. 577 rows of 4096 in float32: 7.5 to 7.9 us.
 template <bool SF32, bool FULL>
 __global__ void __launch_bounds__(1024)
 moe_norm(mega_moe_norm_args a, int nt) {
@@ -153,9 +154,12 @@ moe_norm(mega_moe_norm_args a, int nt) {
 // Memory bound: the next row's loads stay in flight over the two row sums (the
 // barriers would leave the memory idle otherwise), and the weights lie in LDS.
 // dh waits for the whole layer's gradients before it is read and is streamed past
-// the caches, dy is read next and is not (full gate, BF16: 48 us against 53).
-// 4096 rows of 4096, all gradients, with the sums over the rows: BF16 and a gate
-// by channel 41 us, 4.9 TB/s; float32 and a full gate in BF16 85 us, 5.1 TB/s.
+// the caches, dy is read next and is not: with a reader of dy behind it 58 us
+// against 60 (BF16, a gate by channel), a full gate as long, float32 with one 91
+// against 89.  4096 rows of 4096, all gradients: BF16 and a gate by channel 41 to 42
+// us, 4.8 TB/s (201 MB), a full gate in BF16 50 to 53, 5.1 TB/s (268 MB); float32 58
+// to 59, 5.1 TB/s (302 MB), with a full gate in BF16 70 to 72, 5.1 TB/s (369 MB), and
+// 36 bytes of scratch a lane.  The sums over the rows take 4 to 5 us more.
 template <bool SF32, bool FULL>
 __global__ void __launch_bounds__(1024)
 moe_norm_backward(mega_moe_norm_backward_args a, float* ws, int nt) {
@@ -371,8 +375,8 @@ int row_threads(int H) { return (H / 8 + 63) / 64 * 64; }
 int row_groups(int H) { return 1024 / row_threads(H); }
 
 // Workgroups of the norm for many rows: one to a compute unit, each with a row or
-// more in flight.  Two to a unit measured 115 us against 110 (8192 rows of 7168, gate by
-// channel, E4M3 output) and 98 against 95 (no block output).
+// more in flight.  Two to a unit measured 101 us against 96 (8192 rows of 7168, gate by
+// channel, E4M3 output) and 85 against 82 (no gate, no codes).
 constexpr int NORM_BLOCKS = 256;
 }  // namespace
 

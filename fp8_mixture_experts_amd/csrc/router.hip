@@ -15,20 +15,23 @@ constexpr int NO_EXPERT = 0x7fffffff;
 // the largest key and the lowest index that has it, by moves between lanes.  For
 // more than a few rounds the lanes sort their keys first.  What bounds it is that
 // chain of vector instructions: a token's logits are read once and are small.
-// 8192 tokens of 256 experts, k = 8: the logits' order 6.6 us; sigmoid with a
-// bias 8.5, in 8 groups too 11 to 12.5, as near ones turn up (the 8.5 MB that it
-// has to move: 1.7 us).
+// 8192 tokens of 256 experts, k = 8: the logits' order 7.6 us a call; sigmoid with a
+// bias 8.2, in 8 groups too 10.8 (the 8.5 MB that it has to move: 1.7 us).  How many
+// near ones turn up goes by the data (below): softmax in 8 groups 14 us from float32
+// logits and 23 from BF16 ones, sigmoid with a bias in 8 groups 11 from either.
 //
 // Without bias and groups the keys are the logits, which order the experts as
 // the scores do.  Otherwise the order is that of score + bias in float64, but
 // it is found in float32 first, with one round more than there are slots: a
 // float32 score is off by less than `close` (below), so where any two
 // neighbours of the order lie further apart than both their errors, the order
-// is the float64 one.  Nearer ones (in one token of some hundreds) are ordered
-// again by their float64 keys, one candidate to a lane; where that is not
-// enough (softmax, whose float64 sum takes every expert; three near ones at the
-// last slot; more slots than lanes) the token goes through exact_topk, which
-// computes all of it in float64.  Groups with near scores, likewise, are
+// is the float64 one.  Nearer ones (in one token of some hundreds with float32
+// logits; BF16 ones are often equal: without a bias, over 8 groups, a third of the
+// tokens have two such among their first nine of 256 experts) are ordered again by
+// their float64 keys, one candidate to a lane; where that is not enough (softmax, whose
+// float64 sum takes every expert; three near ones at the last slot; more slots than
+// lanes) the token goes through exact_topk, a whole wave to one token after another,
+// which computes all of it in float64.  Groups with near scores, likewise, are
 // ordered by exact_groups.
 // ---------------------------------------------------------------------------
 
@@ -566,8 +569,9 @@ moe_router_topk(mega_moe_router_topk_args a) {
 // The gradient of a token's logits, its experts in 16, 32 or 64 lanes.  The
 // top-k weights reach the scores that were taken (one slot to a lane, added to
 // the row through LDS); softmax spreads minus their mean over all experts.
-// Bound by memory for large batches (32768 tokens of 256 experts 15.4 us, 4.5
-// TB/s), by a token's chain of loads and sums for others: 8192 tokens 6.2 us.
+// Bound by memory for large batches (32768 tokens of 256 experts from the weights
+// 15.8 us, 4.4 TB/s, for sigmoids 14.0, 5.0 TB/s; with the losses 20 and 23), by a
+// token's chain of loads and sums for others: 8192 tokens 6.3, 5.1, 7.4 and 8.7 us.
 template <int LANES, int NI>
 __global__ void __launch_bounds__(256)
 moe_router_backward(mega_moe_router_backward_args a) {

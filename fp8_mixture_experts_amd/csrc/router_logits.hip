@@ -506,8 +506,10 @@ __device__ __forceinline__ void product(u32x4_t* lds, const Product& x, unsigned
     }
 }
 
-// 8192 x 7168 x 256 with float32 weights: 90 us, 1.0 PFLOP/s of BF16 terms (a
-// large library product reaches 1.44), with 9 us after it to add the parts of K.
+// 8192 x 7168 x 256 with float32 weights: 90 to 97 us, 1.0 PFLOP/s of BF16 terms (a
+// large library product reaches 1.44), with 9 us after it to add the parts of K;
+// with BF16 weights 47 and 7 us (129 MB: 25 us), of which a compute unit takes in
+// 1.8 MB at some 40 kB/us.
 template <typename K>
 __global__ void __launch_bounds__(K::THREADS)
 moe_router_product(Product x) {
@@ -517,11 +519,11 @@ moe_router_product(Product x) {
 
 // Both gradients in one launch: workgroups of dw, which are few and long, and
 // then those of dx, which fill up what is left.
-// 4096 x 4096 x 64: 21 us (67 MB of x and dx: 13 us), and 4 us to add the parts of
-// dw.  Larger tiles (64 x 256 for dw, for dx 64 x 256 or 128 x 128), which take in
+// 4096 x 4096 x 64: 21 to 26 us (67 MB of x and dx: 13 us), and 4 us to add the parts
+// of dw.  Larger tiles (64 x 256 for dw, for dx 64 x 256 or 128 x 128), which take in
 // a quarter less, were slower (31 to 33 us in all against 26).  With dlogits and w
-// split into planes beforehand, by a launch of their own, 28 us and 15.5 us against
-// 13.3 at 1024 x 2048 x 128, but 188 against 200 at 8192 x 7168 x 256.
+// split into planes beforehand, by a launch of their own, 28 us, and 15.5 us against
+// 13.3 at 1024 x 2048 x 128.
 template <typename KW, typename KX>
 __global__ void __launch_bounds__(256)
 moe_router_gradients(Product w, unsigned w_blocks, Product x) {
@@ -619,7 +621,7 @@ SmallTile small_tile(const mega_moe_router_logits_args& a) {
 // 16 x 16 and 128-row tiles at 1024 x 640 x 128 5.0 and 10.7 us (82 kB), 8192 x
 // 640 x 31 8.5 and 9.5 (164 kB), 2048 x 7168 x 31 15.3 and 15.8 (459 kB), 4096 x
 // 4096 x 31 17.2 and 16.5 (524 kB), 512 x 7168 x 512 51 and 19 (1.8 MB); with
-// float32 weights 512 x 4096 x 128 14 and 18 (393 kB), 1024 x 1792 x 256 22 and 20
+// float32 weights 512 x 4096 x 128 14 and 18 (393 kB), 1024 x 1792 x 256 22 and 19
 // (688 kB).
 bool is_small(const mega_moe_router_logits_args& a, const SmallTile& s) {
     return s.bytes * a.hidden <= 300000 + 40 * a.hidden;
@@ -639,9 +641,14 @@ int64_t forward_tiles(const mega_moe_router_logits_args& a) {
 }
 
 // Whether two workgroups share a compute unit: with float32 weights, where one
-// each would leave parts of K longer than 2048.  Measured at 8192 x 7168 x 256
-// 102 us in pairs and 115 alone, at 8192 x 2048 x 512 66 and 63; with BF16
-// weights, whose loads take more of the time than the products, 58 and 56.
+// each would leave parts of K longer than 2048.  In pairs and alone, us (part of K):
+// 8192 x 7168 x 256 105 and 116, 16384 x 7168 x 128 107 and 117, 2048 x 7168 x 1024
+// 95 and 100 (3584), 8192 x 5120 x 384 108 and 148 (2560), 32768 x 7168 x 72 179 and
+// 194 (7168), but 16384 x 2560 x 256 82 and 76 (2560); 8192 x 2048 x 512 66 and 59, 8192
+// x 4096 x 256 66 and 66 (2048), 4096 x 7168 x 256 59 and 57 (1792), 8192 x 4096 x 128
+// 43 and 39 (1024), but where the tiles leave a last round half empty 8192 x 1024 x
+// 1024 55 and 65 (1024) and 2000 x 6144 x 300 41 and 49 (768).  With BF16 weights, whose
+// loads take more of the time than the products, 8192 x 7168 x 256 takes 58 and 56.
 bool forward_pairs(const mega_moe_router_logits_args& a) {
     if (a.num_experts <= 64 || a.weight_type != MEGA_MOE_F32) return false;
     return a.hidden / split_for(forward_tiles(a), a.hidden, 256).n > 2048;
@@ -719,13 +726,14 @@ void launch_forward(const mega_moe_router_logits_args& a, hipStream_t stream) {
     else launch_product<typename F::Many>(a, stream);
 }
 
-// The gradients' kinds, with steps in LDS as they are launched.  In dx, which is rounded
-// to BF16, two terms of dlogits do for BF16 weights: the 2^-17 that they leave shows
-// only where the sum over the experts is some 256 times smaller than its terms, and
-// rows of w of 8 bits hardly differ by so little (4096 x 4096 x 64 25 us, 26 with three
-// terms; 8192 x 7168 x 256 181 and 198).  Float32 rows may: with what is 256 times their differences in common, and
-// dlogits that add up to 0, as a softmax's do, two terms of both are half a step
-// of BF16 (4096 x 4096 x 64: 30 us, so 33; 8192 x 7168 x 256 237 and 300).
+// The gradients' kinds, with steps in LDS as they are launched.  In dx, which is
+// rounded to BF16, two terms of dlogits do for BF16 weights: the 2^-17 that they leave
+// shows only where the sum over the experts is some 256 times smaller than its terms,
+// and rows of w of 8 bits hardly differ by so little (4096 x 4096 x 64 25 us, 26 with
+// three terms; 8192 x 7168 x 256 181 and 198).  Float32 rows may: with what is 256 times
+// their differences in common, and dlogits that add up to 0, as a softmax's do, two
+// terms of both are half a step of BF16 (4096 x 4096 x 64 30 us and, with three, 33;
+// 8192 x 7168 x 256 237 and 300).
 struct Bf16Gradients {
     template <int S>
     using W = Kind<Lay::row_float, 3, Lay::row_major, 1, 64, 128, S, false>;
@@ -749,11 +757,12 @@ constexpr unsigned to_a_unit() {
 // while it multiplies, where each has a place on the 256 compute units at once: two to
 // a unit with BF16 weights (64 kB), one with float32 weights (96 kB).  More of them
 // hide each other's loads, and with one step four and three to a unit fit.  One and
-// two steps, us (workgroups), BF16 weights: 3383 x 640 x 216 21 and 19 (425), 768 x 3584
-// x 96 17 and 15 (448), 4096 x 2048 x 128 24 and 25 (1280), 4096 x 4096 x 64 25 and
-// 29 (2304), but 4096 x 896 x 64 17.7 and 16.9 (560); float32: 64 x 7168 x 256 13.2 and 15.8 (280), 3383 x 640 x 216 24 and 29
-// (425), 768 x 3584 x 96 17 and 20 (448), 4096 x 4096 x 64 33 and 53 (2304), but 640 x
-// 4096 x 64 14.6 and 13.8 (384) and 256 x 2048 x 128 8.6 and 8.3 (96).
+// two steps, us (workgroups), BF16 weights: 3383 x 640 x 216 21 and 19 (425), 768 x
+// 3584 x 96 17 and 15 (448), 4096 x 2048 x 128 24 and 25 (1280), 4096 x 4096 x 64 25
+// and 29 (2304), but 4096 x 896 x 64 17.7 and 16.9 (560); float32: 64 x 7168 x 256 13.2
+// and 15.8 (280), 3383 x 640 x 216 24 and 29 (425), 768 x 3584 x 96 17 and 20 (448),
+// 4096 x 4096 x 64 33 and 53 (2304), but 640 x 4096 x 64 14.6 and 13.8 (384) and 256 x
+// 2048 x 128 8.6 and 8.3 (96).
 template <typename G>
 void launch_gradients(const Product& w, unsigned w_blocks, const Product& x, unsigned x_blocks, hipStream_t stream) {
     const auto go = [&](auto stages) {

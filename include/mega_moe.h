@@ -355,7 +355,8 @@ int mega_moe_profile_end(mega_moe_handle* h, float* ms_out, int32_t capacity, in
  *   - Each call takes one argument block, which the call reads and does not
  *     keep.  Clear it first: a field that is 0 or NULL is off or the default.
  *   - The current HIP device must be the one of the stream and the tensors; a
- *     call whose stream or first tensor belongs to another device is refused.
+ *     call whose stream or first tensor belongs to another device, or whose
+ *     first tensor is in ordinary host memory, is refused.
  *   - Calls are asynchronous on `stream`, allocate nothing, issue no memory
  *     sets and keep nothing between calls, so they may run on several streams
  *     at once and be captured in a HIP graph.  A call that needs a workspace
