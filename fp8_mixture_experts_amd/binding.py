@@ -46,6 +46,15 @@ MEGA_MOE_GATE_CHANNEL = 2
 MEGA_MOE_GATE_FULL = 3
 MEGA_MOE_SCORE_SOFTMAX = 0
 MEGA_MOE_SCORE_SIGMOID = 1
+MEGA_MOE_SCALE_BLOCK = 0
+MEGA_MOE_SCALE_ROW = 1
+MEGA_MOE_ACT_NONE = 0
+MEGA_MOE_ACT_SWIGLU = 1
+MEGA_MOE_ROTARY_HALF = 0
+MEGA_MOE_ROTARY_INTERLEAVED = 1
+MEGA_MOE_ROTARY_PLAIN = 0
+MEGA_MOE_ROTARY_LINEAR = 1
+MEGA_MOE_ROTARY_BY_PARTS = 2
 
 
 class mega_moe_config(ctypes.Structure):
@@ -76,7 +85,7 @@ class mega_moe_views(ctypes.Structure):
 # ---- argument blocks of the operators around the layer -----------------------
 
 _TYPES = {"i32": ctypes.c_int32, "i64": ctypes.c_int64, "f32": ctypes.c_float,
-          "ptr": ctypes.c_void_p}
+          "f64": ctypes.c_double, "ptr": ctypes.c_void_p}
 
 
 def _fields(*runs):
@@ -130,6 +139,48 @@ class mega_moe_router_backward_args(_Args):
                        ("ptr", "logits topk_idx token_mask dweights dloss cu_seqlens counts tokens "
                                "dlogits"),
                        ("i64", "logits_stride dlogits_stride"))
+
+
+class mega_moe_product_args(_Args):
+    _fields_ = _fields(("i32", "m n k b_scale out_type reserved"),
+                       ("ptr", "a a_sf b b_sf add out workspace"),
+                       ("i64", "workspace_bytes a_stride b_stride a_sf_stride b_sf_stride "
+                               "add_stride out_stride"))
+
+class mega_moe_quantize_args(_Args):
+    _fields_ = _fields(("i32", "num_tokens columns x_type activation scale"),
+                       ("f32", "activation_clamp"),
+                       ("ptr", "x up h q q_sf qt qt_sf"),
+                       ("i64", "x_stride up_stride h_stride"))
+
+class mega_moe_swiglu_backward_args(_Args):
+    _fields_ = _fields(("i32", "num_tokens columns x_type"),
+                       ("f32", "activation_clamp"),
+                       ("ptr", "x up dh dx dup q q_sf qt qt_sf"),
+                       ("i64", "x_stride up_stride dh_stride dx_stride dup_stride"))
+
+class mega_moe_rotary_args(_Args):
+    _fields_ = _fields(("i32", "num_tokens q_heads k_heads head_dim rotary_dim rotary_start layout "
+                               "type weight_type first_position"),
+                       ("f32", "eps scale"),
+                       ("ptr", "q k q_weight k_weight positions inv_freq q_out k_out"),
+                       ("i64", "q_stride k_stride q_out_stride k_out_stride q_head_stride "
+                               "k_head_stride q_out_head_stride k_out_head_stride"))
+
+class mega_moe_rotary_backward_args(_Args):
+    _fields_ = _fields(("i32", "num_tokens q_heads k_heads head_dim rotary_dim rotary_start layout "
+                               "type weight_type first_position"),
+                       ("f32", "eps scale"),
+                       ("ptr", "q k q_weight k_weight positions inv_freq dq_out dk_out dq dk "
+                               "dq_weight dk_weight workspace"),
+                       ("i64", "workspace_bytes q_stride k_stride dq_out_stride dk_out_stride "
+                               "dq_stride dk_stride q_head_stride k_head_stride dq_out_head_stride "
+                               "dk_out_head_stride dq_head_stride dk_head_stride"))
+
+class mega_moe_rotary_frequencies_args(_Args):
+    _fields_ = _fields(("i32", "rotary_dim scaling"),
+                       ("f64", "base factor original_length fast_turns slow_turns"),
+                       ("ptr", "inv_freq scale"))
 
 
 def make_args(cls, **fields):
@@ -208,14 +259,23 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                       ("router_logits_backward", mega_moe_router_logits_args),
                       ("router_topk", mega_moe_router_topk_args),
                       ("balance_loss", mega_moe_balance_loss_args),
-                      ("router_backward", mega_moe_router_backward_args)):
+                      ("router_backward", mega_moe_router_backward_args),
+                      ("product", mega_moe_product_args),
+                      ("quantize", mega_moe_quantize_args),
+                      ("swiglu_backward", mega_moe_swiglu_backward_args),
+                      ("rotary", mega_moe_rotary_args),
+                      ("rotary_backward", mega_moe_rotary_backward_args)):
         f = getattr(lib, "mega_moe_" + name)
         f.argtypes, f.restype = [ctypes.POINTER(cls), vp], ctypes.c_int
     for name, cls in (("norm", mega_moe_norm_backward_args),
                       ("router_logits", mega_moe_router_logits_args),
-                      ("balance_loss", mega_moe_balance_loss_args)):
+                      ("balance_loss", mega_moe_balance_loss_args),
+                      ("product", mega_moe_product_args),
+                      ("rotary", mega_moe_rotary_backward_args)):
         f = getattr(lib, f"mega_moe_{name}_workspace_bytes")
         f.argtypes, f.restype = [ctypes.POINTER(cls)], i64
+    lib.mega_moe_rotary_frequencies.argtypes = [ctypes.POINTER(mega_moe_rotary_frequencies_args)]
+    lib.mega_moe_rotary_frequencies.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -391,6 +451,39 @@ def mega_moe_balance_loss_workspace_bytes(args: mega_moe_balance_loss_args) -> i
 
 def mega_moe_router_backward(args: mega_moe_router_backward_args, stream) -> int:
     return _check(load().mega_moe_router_backward(args, stream))
+
+
+def mega_moe_product(args: mega_moe_product_args, stream) -> int:
+    return _check(load().mega_moe_product(args, stream))
+
+
+def mega_moe_product_workspace_bytes(args: mega_moe_product_args) -> int:
+    return load().mega_moe_product_workspace_bytes(args)
+
+
+def mega_moe_quantize(args: mega_moe_quantize_args, stream) -> int:
+    return _check(load().mega_moe_quantize(args, stream))
+
+
+def mega_moe_swiglu_backward(args: mega_moe_swiglu_backward_args, stream) -> int:
+    return _check(load().mega_moe_swiglu_backward(args, stream))
+
+
+def mega_moe_rotary(args: mega_moe_rotary_args, stream) -> int:
+    return _check(load().mega_moe_rotary(args, stream))
+
+
+def mega_moe_rotary_backward(args: mega_moe_rotary_backward_args, stream) -> int:
+    return _check(load().mega_moe_rotary_backward(args, stream))
+
+
+def mega_moe_rotary_workspace_bytes(args: mega_moe_rotary_backward_args) -> int:
+    return load().mega_moe_rotary_workspace_bytes(args)
+
+
+def mega_moe_rotary_frequencies(args: mega_moe_rotary_frequencies_args) -> int:
+    """inv_freq and scale are in host memory (CPU tensors, or their addresses)."""
+    return _check(load().mega_moe_rotary_frequencies(args))
 
 
 # ---- convenience wrapper (still marshalling only) ---------------------------

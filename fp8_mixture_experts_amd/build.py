@@ -21,7 +21,8 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
 SOURCES = ["dispatch.hip", "expert_ffn.hip", "combine.hip", "transform.hip", "api.hip",
-           "norm.hip", "router_logits.hip", "router.hip", "balance.hip", "block_api.hip"]
+           "norm.hip", "router_logits.hip", "router.hip", "balance.hip", "block_api.hip",
+           "product.hip", "quantize.hip", "rotary.hip", "dense_api.hip"]
 
 COMMON = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-I", INCLUDE, "-I", CSRC,
           "-Wall", "-Wno-unused-result"]

@@ -592,6 +592,209 @@ typedef struct mega_moe_router_backward_args {
 } mega_moe_router_backward_args;
 int mega_moe_router_backward(const mega_moe_router_backward_args* a, void* stream);
 
+/*
+ * The dense path next to the layer: the products that a block takes of the
+ * same E4M3 rows (attention's projections, a shared expert beside the routed
+ * ones, blocks without experts), what makes their operands, and the norm and
+ * rotation of the heads that they give.  The conventions are those of the
+ * operators above; rows of E4M3 codes start on 16 bytes.
+ *
+ * A training step takes its products from the same operators: with the codes
+ * and scales of dout by rows and by columns (mega_moe_quantize, or
+ * mega_moe_swiglu_backward), of x by columns and of w by blocks both ways,
+ *   out = x . w^T,   dx = dout . (w^T)^T,   dw = dout^T . (x^T)^T.
+ */
+#define MEGA_MOE_SCALE_BLOCK 0  /* one scale for 128 x 128 codes                */
+#define MEGA_MOE_SCALE_ROW 1    /* one scale for 128 codes of a row             */
+
+/*
+ * out = a . b^T + add, of E4M3 codes with float scales:
+ *   out[i, j] = add[i, j] + sum over blocks s of 128 columns of
+ *               a_sf[i, s] * b_sf[j or j / 128, s] * sum over c in s of a[i, c] * b[j, c]
+ * Both sums are in float32, the product of the two scales is rounded to float32.
+ * With a BF16 output the inner sums are those of the FP8 matrix instruction,
+ * which cuts what lies about 2^-16 below its largest products (1.3e-5 of a
+ * random sum, BF16's own rounding being 1.7e-3); with a float32 output all products are
+ * exact and the sums are float32's.  k may be 0: out = add, or 0.
+ */
+typedef struct mega_moe_product_args {
+    int32_t m;                /* rows of a and out, up to 2^21; 0 is a no-op     */
+    int32_t n;                /* rows of b: a multiple of 8 up to 2^21; 0 is a no-op */
+    int32_t k;                /* columns of a and b: a multiple of 128 up to 2^21 */
+    int32_t b_scale;          /* MEGA_MOE_SCALE_*: the scales of b               */
+    int32_t out_type;         /* type of out and add                             */
+    int32_t reserved;         /* 0                                               */
+    const uint8_t* a;         /* [m, k] E4M3                                     */
+    const float* a_sf;        /* [m, k/128]                                      */
+    const uint8_t* b;         /* [n, k] E4M3                                     */
+    const float* b_sf;        /* [ceil(n/128), k/128], or [n, k/128] by rows     */
+    const void* add;          /* [m, n], or NULL; may be out itself (same stride) */
+    void* out;                /* [m, n]                                          */
+    void* workspace;          /* may be NULL where the bytes needed are 0        */
+    int64_t workspace_bytes;
+    int64_t a_stride, b_stride;          /* >= k, of 16, up to 2^22              */
+    int64_t a_sf_stride, b_sf_stride;    /* >= k/128, up to 2^22                 */
+    int64_t add_stride, out_stride;      /* >= n, of 8                           */
+} mega_moe_product_args;
+int mega_moe_product(const mega_moe_product_args* a, void* stream);
+
+/* Workspace bytes that the call needs (-1 if invalid): from m, n, k, b_scale and
+ * out_type.  Host-only. */
+int64_t mega_moe_product_workspace_bytes(const mega_moe_product_args* a);
+
+#define MEGA_MOE_ACT_NONE 0     /* h = x                                        */
+#define MEGA_MOE_ACT_SWIGLU 1   /* h = silu(x) * up                             */
+
+/*
+ * The operands of the products: h = x, or silu(x) * up in float32, as E4M3
+ * codes with scales, as the norm makes them (sf = max |h| of the block / 448,
+ * code = e4m3(h / sf), the quotient rounded as float32 divides; a block whose
+ * maximum is 0 has scale and codes 0, one with a NaN has both NaN).  q are h's rows; qt those of its transpose, with the tokens
+ * behind num_tokens, up to a multiple of 128, as codes 0 (they take no part in
+ * scales).  With SCALE_ROW every row of q, and of qt, has a scale for 128 of
+ * its codes; with SCALE_BLOCK (weights, "tokens" being their rows) q and qt
+ * share one for 128 x 128.  Where activation_clamp is not 0, x and up are
+ * first clamped to [-clamp, clamp] as the layer's.
+ */
+typedef struct mega_moe_quantize_args {
+    int32_t num_tokens;       /* T; 0 is a no-op                                 */
+    int32_t columns;          /* C, a multiple of 128 up to 2^17                 */
+    int32_t x_type;           /* type of x and up                                */
+    int32_t activation;       /* MEGA_MOE_ACT_*                                  */
+    int32_t scale;            /* MEGA_MOE_SCALE_*                                */
+    float activation_clamp;   /* >= 0; 0: none                                   */
+    const void* x;            /* [T, C]                                          */
+    const void* up;           /* [T, C] with SWIGLU, else NULL                   */
+    uint16_t* h;              /* [T, C] BF16, or NULL                            */
+    uint8_t* q;               /* [T, C] E4M3, dense, or NULL (with q_sf)         */
+    float* q_sf;              /* [T, C/128]; by blocks [Tp/128, C/128]           */
+    uint8_t* qt;              /* [C, Tp] E4M3, dense, Tp = T rounded up to 128, or
+                                 NULL (with qt_sf)                               */
+    float* qt_sf;             /* [C, Tp/128]; by blocks [C/128, Tp/128]          */
+    int64_t x_stride, up_stride, h_stride;           /* >= C, of 8               */
+} mega_moe_quantize_args;
+int mega_moe_quantize(const mega_moe_quantize_args* a, void* stream);
+
+/*
+ * The gradients of h = silu(x) * up, of x and up clamped as in
+ * mega_moe_quantize, with s = 1 / (1 + exp(-x)):
+ *   dx = dh * up * s * (1 + x * (1 - s)),   dup = dh * x * s
+ * and 0 where a value lies beyond its clamp.  They come in x's type, as the
+ * rows [dx, dup] of 2C columns in E4M3, and as those of their transpose; codes
+ * and scales (SCALE_ROW) as in mega_moe_quantize, of the unrounded gradients.
+ */
+typedef struct mega_moe_swiglu_backward_args {
+    int32_t num_tokens, columns, x_type;
+    float activation_clamp;
+    const void* x;            /* [T, C] x_type                                   */
+    const void* up;           /* [T, C]                                          */
+    const void* dh;           /* [T, C]                                          */
+    void* dx;                 /* [T, C], or NULL                                 */
+    void* dup;                /* [T, C], or NULL                                 */
+    uint8_t* q;               /* [T, 2C] E4M3, dense, or NULL (with q_sf)        */
+    float* q_sf;              /* [T, 2C/128]                                     */
+    uint8_t* qt;              /* [2C, Tp] E4M3, dense, or NULL (with qt_sf)      */
+    float* qt_sf;             /* [2C, Tp/128]                                    */
+    int64_t x_stride, up_stride, dh_stride, dx_stride, dup_stride;   /* >= C, of 8 */
+} mega_moe_swiglu_backward_args;
+int mega_moe_swiglu_backward(const mega_moe_swiglu_backward_args* a, void* stream);
+
+#define MEGA_MOE_ROTARY_HALF 0         /* column i turns with column i + R/2    */
+#define MEGA_MOE_ROTARY_INTERLEAVED 1  /* column 2i turns with column 2i + 1    */
+
+/*
+ * The norms of the heads of q and k, and their rotation by position.  Per
+ * token t and head, in float32:
+ *   n = x * rsqrt(mean(x^2) + eps) * weight      (n = x without the weight)
+ * and of the columns [rotary_start, rotary_start + R) of n every pair (a, b),
+ * i in [0, R/2), becomes
+ *   scale * (a cos - b sin),  scale * (b cos + a sin),
+ *   angle = positions[t] * inv_freq[i],
+ * the angle taken in float64 and reduced before it is rounded.  The other columns are n.
+ */
+typedef struct mega_moe_rotary_args {
+    int32_t num_tokens;       /* T; 0 is a no-op                                 */
+    int32_t q_heads, k_heads; /* in [0, 1024], not both 0                        */
+    int32_t head_dim;         /* D, a multiple of 8 up to 512                    */
+    int32_t rotary_dim;       /* R, a multiple of 16 up to D; 0: norms alone     */
+    int32_t rotary_start;     /* a multiple of 8, up to D - R                    */
+    int32_t layout;           /* MEGA_MOE_ROTARY_*                               */
+    int32_t type;             /* type of q, k and the outputs                    */
+    int32_t weight_type;
+    int32_t first_position;   /* >= 0; token t's without positions is first + t  */
+    float eps;                /* >= 0                                            */
+    float scale;              /* of the rotated part; 0: 1                       */
+    const void* q;            /* [T, q_heads, D] (NULL without heads)            */
+    const void* k;            /* [T, k_heads, D]                                 */
+    const void* q_weight;     /* [D], or NULL: no norm of q                      */
+    const void* k_weight;     /* [D], or NULL: no norm of k                      */
+    const int32_t* positions; /* [T], or NULL                                    */
+    const float* inv_freq;    /* [R/2] (mega_moe_rotary_frequencies)             */
+    void* q_out;              /* [T, q_heads, D]; may be q itself (same strides) */
+    void* k_out;              /* [T, k_heads, D]; may be k itself                */
+    int64_t q_stride, k_stride, q_out_stride, k_out_stride;  /* of a token, of 8; 0: dense */
+    int64_t q_head_stride, k_head_stride, q_out_head_stride, k_out_head_stride;
+                              /* of a head: >= D, of 8, up to 2^20; 0: D         */
+} mega_moe_rotary_args;
+int mega_moe_rotary(const mega_moe_rotary_args* a, void* stream);
+
+/*
+ * The gradients of mega_moe_rotary, whose q and k these are: of q and k, and
+ * of the weights, summed over tokens and heads (set to 0 with num_tokens 0).
+ * q and k are only read where there is a weight.
+ */
+typedef struct mega_moe_rotary_backward_args {
+    int32_t num_tokens, q_heads, k_heads, head_dim, rotary_dim, rotary_start, layout, type,
+        weight_type, first_position;
+    float eps, scale;
+    const void* q;            /* as in mega_moe_rotary; NULL without its weight  */
+    const void* k;
+    const void* q_weight;
+    const void* k_weight;
+    const int32_t* positions;
+    const float* inv_freq;
+    const void* dq_out;       /* [T, q_heads, D]                                 */
+    const void* dk_out;       /* [T, k_heads, D]                                 */
+    void* dq;                 /* [T, q_heads, D]; may be dq_out itself (same strides) */
+    void* dk;                 /* [T, k_heads, D]; may be dk_out itself           */
+    float* dq_weight;         /* [D], or NULL                                    */
+    float* dk_weight;         /* [D], or NULL                                    */
+    void* workspace;          /* may be NULL where the bytes needed are 0        */
+    int64_t workspace_bytes;
+    int64_t q_stride, k_stride, dq_out_stride, dk_out_stride, dq_stride, dk_stride;
+    int64_t q_head_stride, k_head_stride, dq_out_head_stride, dk_out_head_stride,
+        dq_head_stride, dk_head_stride;
+} mega_moe_rotary_backward_args;
+int mega_moe_rotary_backward(const mega_moe_rotary_backward_args* a, void* stream);
+
+/* Workspace bytes of a mega_moe_rotary_backward call (-1 if invalid): from the
+ * sizes and which of the weights' gradients are not NULL.  Host-only. */
+int64_t mega_moe_rotary_workspace_bytes(const mega_moe_rotary_backward_args* a);
+
+#define MEGA_MOE_ROTARY_PLAIN 0     /* inv_freq[i] = base^(-2i/R)               */
+#define MEGA_MOE_ROTARY_LINEAR 1    /* the same divided by factor               */
+#define MEGA_MOE_ROTARY_BY_PARTS 2  /* divided where a turn is long             */
+
+/*
+ * The frequencies of mega_moe_rotary, written to host memory (the caller
+ * copies them to the device), and the scale that goes with them.  BY_PARTS:
+ * a frequency that makes more than fast_turns turns over original_length
+ * positions stays, one that makes fewer than slow_turns is divided by factor,
+ * and between them (by index, over the whole indices around both bounds) the
+ * two are mixed linearly; scale = 0.1 ln(factor) + 1 (else 1).
+ */
+typedef struct mega_moe_rotary_frequencies_args {
+    int32_t rotary_dim;       /* R, a positive multiple of 16                    */
+    int32_t scaling;          /* MEGA_MOE_ROTARY_PLAIN, _LINEAR or _BY_PARTS     */
+    double base;              /* > 1                                             */
+    double factor;            /* >= 1 (0 with PLAIN)                             */
+    double original_length;   /* > 0 with BY_PARTS                               */
+    double fast_turns, slow_turns;   /* fast > slow > 0 with BY_PARTS            */
+    float* inv_freq;          /* [R/2] in host memory                            */
+    float* scale;             /* [1] in host memory, or NULL                     */
+} mega_moe_rotary_frequencies_args;
+int mega_moe_rotary_frequencies(const mega_moe_rotary_frequencies_args* a);
+
 #ifdef __cplusplus
 }
 #endif
