@@ -11,7 +11,7 @@ namespace {
 
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
-typedef float f32x16_t __attribute__((ext_vector_type(16)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 
@@ -54,21 +54,15 @@ __device__ __forceinline__ void load4_lds(__amdgpu_buffer_rsrc_t r, uint8_t* lds
 // operand meet distinct banks.
 __device__ __forceinline__ int turn(int row) { return (row & 7) ^ ((row >> 3) & 1); }
 
-// The operand of 32 rows (slice s) for half h of a step: lane r + 32 g has row
-// r, chunks 4 h + g and 4 h + 2 + g (alike for a and b).  Every read of a stage is one
-// of integers: of other types the compiler would wait for all loads into LDS first.
-__device__ __forceinline__ i32x8_t operand(const uint8_t* rows, int s, int h) {
-    const int r = threadIdx.x & 31, g = (threadIdx.x >> 5) & 1;
-    const uint8_t* row = rows + (32 * s + r) * BK;
-    const i32x4_t lo = *reinterpret_cast<const i32x4_t*>(row + 16 * ((4 * h + g) ^ turn(r)));
-    const i32x4_t hi = *reinterpret_cast<const i32x4_t*>(row + 16 * ((4 * h + 2 + g) ^ turn(r)));
+// The operand of 16 rows (slice s) of a step: lane r + 16 g has row r, chunks g and
+// g + 4 (alike for a and b).  Every read of a stage is one of integers: of other types the
+// compiler would wait for all loads into LDS first.
+__device__ __forceinline__ i32x8_t operand(const uint8_t* rows, int s) {
+    const int r = threadIdx.x & 15, g = (threadIdx.x >> 4) & 3;
+    const uint8_t* row = rows + (16 * s + r) * BK;
+    const i32x4_t lo = *reinterpret_cast<const i32x4_t*>(row + 16 * (g ^ turn(r)));
+    const i32x4_t hi = *reinterpret_cast<const i32x4_t*>(row + 16 * ((g + 4) ^ turn(r)));
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-}
-
-// A quarter (16 bytes a lane: 32 columns) of the same, for the F16 products.
-__device__ __forceinline__ i32x4_t quarter(const uint8_t* rows, int s, int p) {
-    const int r = threadIdx.x & 31, g = (threadIdx.x >> 5) & 1;
-    return *reinterpret_cast<const i32x4_t*>(rows + (32 * s + r) * BK + 16 * ((2 * p + g) ^ turn(r)));
 }
 
 // Eight codes as F16: exact.
@@ -80,32 +74,64 @@ __device__ __forceinline__ f16x8_t half_values(int lo, int hi) {
     return f16x8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-__device__ __forceinline__ f32x16_t product_f8(const i32x8_t& a, const i32x8_t& b, const f32x16_t& c) {
-    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, 0, 0, 0);   // scales 0: none
-}
+// An operand as the matrix instructions take it, and its products with another's:
+// 16 x 16 x 128, in one instruction or in four that follow each other.
+template <bool EXACT>
+struct Ready {
+    static constexpr int N = 1;
+    i32x8_t v;
+    Ready() = default;
+    __device__ __forceinline__ explicit Ready(const i32x8_t& raw) : v(raw) {}
+    __device__ __forceinline__ f32x4_t times(const Ready& o, int, const f32x4_t& c) const {
+        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(v, o.v, c, 0, 0, 0, 0, 0, 0);   // scales 0: none
+    }
+};
 
-// Tiles.  BM x BN results, by WM x WN waves, S steps in LDS.
-template <int BM_, int BN_, int WM_, int WN_, int S_>
+template <>
+struct Ready<true> {
+    static constexpr int N = 4;
+    f16x8_t v[4];
+    Ready() = default;
+    __device__ __forceinline__ explicit Ready(const i32x8_t& raw) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] = half_values(raw[2 * q], raw[2 * q + 1]);
+    }
+    __device__ __forceinline__ f32x4_t times(const Ready& o, int q, const f32x4_t& c) const {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(v[q], o.v[q], c, 0, 0, 0);
+    }
+};
+
+// Tiles.  BM x BN results, by WK groups of WM x WN waves: a group has every WK-th
+// step, and the groups' sums meet at the end.  S rounds (a step of every group) in LDS.
+template <int BM_, int BN_, int WM_, int WN_, int WK_, int S_>
 struct Tile {
-    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, S = S_;
-    static constexpr int NW = WM * WN, NT = 64 * NW;
+    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, WK = WK_, S = S_;
+    static constexpr int NW = WM * WN, NT = 64 * NW * WK;  // NW: of a group
     static constexpr int TM = BM / WM, TN = BN / WN;       // a wave's
-    static constexpr int SM = TM / 32, SN = TN / 32;
+    static constexpr int SM = TM / 16, SN = TN / 16;
     static constexpr int A_LOADS = BM / 8 / NW, B_LOADS = BN / 8 / NW;     // of 1 KB
     static constexpr int A_SF = BM / NW, B_SF = BN / NW;   // scales that a wave loads, a lane each
-    static constexpr int OFF_B = BM * BK, OFF_SFA = OFF_B + BN * BK, OFF_SFB = OFF_SFA + BM * 4;
+    static constexpr int OFF_B = BM * BK, OFF_SFA = OFF_B + BN * BK, OFF_SFB = OFF_SFA + NW * 256;
     template <bool ROWS>
-    static constexpr int stage() { return OFF_SFB + (ROWS ? BN * 4 : 0); }
+    static constexpr int stage() { return OFF_SFB + (ROWS ? NW * 256 : 0); } // of a group
+    // A wave's scales lie in 256 bytes of LDS, the lanes behind A_SF (B_SF) repeating the
+    // last: masking them off would end the block of code that the compiler schedules as one.
+    static constexpr int at_sfa(int row) { return row / A_SF * 256 + row % A_SF * 4; }
+    static constexpr int at_sfb(int row) { return row / B_SF * 256 + row % B_SF * 4; }
     template <bool ROWS>
     static constexpr int loads() { return A_LOADS + B_LOADS + 1 + (ROWS ? 1 : 0); }
     // results leave through LDS, PW columns of a wave at a time
     static constexpr int PW = TN < 64 ? TN : 64, PITCH = PW + 4;
     template <bool ROWS>
     static constexpr int lds() {
-        const int a = S * stage<ROWS>(), b = NW * TM * PITCH * 4;
+        const int a = S * WK * stage<ROWS>(), b = WK * NW * TM * PITCH * 4;
         return a > b ? a : b;
     }
     static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && A_SF <= 64 && B_SF <= 64, "loads");
+    static_assert((8 * NW) % 16 == 0, "turn() is the same for a wave's rows");
+    static_assert(TM % A_SF == 0 && TN % B_SF == 0 && A_SF % 16 == 0 && B_SF % 16 == 0, "scales of a wave's rows");
+    static_assert(TN == 128 || 128 % TN == 0, "one block of scales to a wave");
+    static_assert(lds<true>() <= 160 * 1024, "LDS");
 };
 
 // What workgroup `id` of `total` computes: the runs of ids that go to one of the
@@ -119,13 +145,18 @@ __device__ __forceinline__ int in_order(int id, int total) {
 
 // One tile, or one of `splits` parts of its steps.  b's rows are the matrix
 // instruction's first operand, a's the second, so that a lane has one row of
-// the result (32 of a slice) and register v column 8 (v / 4) + 4 (lane / 32) + v % 4: the
-// scale of a's row is one value for a lane.
+// a result (16 of a slice) and register v column 4 (lane / 16) + v: the scale of
+// a's row is one value for a lane.
+//
+// A round's barrier lies before its last column of blocks, whose operands are in
+// registers by then: behind it the round's place in LDS is free for new loads,
+// and the next round's operands are read while the matrix unit has that column.
 template <typename T, bool EXACT, bool ROWS>
 __global__ void __launch_bounds__(T::NT) moe_product(ProductArgs p) {
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-    constexpr int STAGE = T::template stage<ROWS>(), LOADS = T::template loads<ROWS>(), S = T::S;
-    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    constexpr int STAGE = T::template stage<ROWS>(), LOADS = T::template loads<ROWS>(), S = T::S, ROUND = STAGE * T::WK;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int group = wave / T::NW, w = wave % T::NW;
     const int wm = w / T::WN, wn = w % T::WN;
     const int tiles_m = (p.m + T::BM - 1) / T::BM, tiles_n = (p.n + T::BN - 1) / T::BN;
     int at = in_order(blockIdx.x, gridDim.x);
@@ -137,155 +168,186 @@ __global__ void __launch_bounds__(T::NT) moe_product(ProductArgs p) {
     const int64_t m0 = (int64_t)(band * 8 + at % rows_of_band) * T::BM, n0 = (int64_t)(at / rows_of_band) * T::BN;
     const int step0 = (int)((int64_t)p.steps * split / p.splits);
     const int steps = (int)((int64_t)p.steps * (split + 1) / p.splits) - step0;
+    const int rounds = (steps + T::WK - 1) / T::WK;
 
     const int rows_a = (int)min((int64_t)T::BM, p.m - m0), rows_b = (int)min((int64_t)T::BN, p.n - n0);
-    const __amdgpu_buffer_rsrc_t ra = buffer(p.a + m0 * p.a_stride + (int64_t)step0 * BK,
-                                             (uint32_t)((rows_a - 1) * p.a_stride + (int64_t)steps * BK));
-    const __amdgpu_buffer_rsrc_t rb = buffer(p.b + n0 * p.b_stride + (int64_t)step0 * BK,
-                                             (uint32_t)((rows_b - 1) * p.b_stride + (int64_t)steps * BK));
-    const __amdgpu_buffer_rsrc_t rsa = buffer(p.a_sf + m0 * p.a_sf_stride + step0,
-                                              (uint32_t)((rows_a - 1) * p.a_sf_stride + steps) * 4);
-    const __amdgpu_buffer_rsrc_t rsb = buffer(ROWS ? p.b_sf + n0 * p.b_sf_stride + step0 : nullptr,
-                                              ROWS ? (uint32_t)((rows_b - 1) * p.b_sf_stride + steps) * 4 : 0u);
+    const uint8_t* const a0 = p.a + m0 * p.a_stride + (int64_t)step0 * BK;
+    const uint8_t* const b0 = p.b + n0 * p.b_stride + (int64_t)step0 * BK;
+    const float* const a_sf0 = p.a_sf + m0 * p.a_sf_stride + step0;
+    const float* const b_sf0 = ROWS ? p.b_sf + n0 * p.b_sf_stride + step0 : nullptr;
+    const uint32_t bytes_a = (uint32_t)((rows_a - 1) * p.a_stride + (int64_t)steps * BK);
+    const uint32_t bytes_b = (uint32_t)((rows_b - 1) * p.b_stride + (int64_t)steps * BK);
+    const uint32_t bytes_sfa = (uint32_t)((rows_a - 1) * p.a_sf_stride + steps) * 4;
+    const uint32_t bytes_sfb = (uint32_t)((rows_b - 1) * p.b_sf_stride + steps) * 4;
     // a wave's rows of a step: 8 (NW j + w) + lane / 8, and the chunk that belongs to lane % 8;
     // rows behind the last lie beyond the buffer by this offset alone
     const int r8 = 8 * w + (lane >> 3);
     const int voff_a = r8 * (int)p.a_stride + 16 * ((lane & 7) ^ turn(r8));
     const int voff_b = r8 * (int)p.b_stride + 16 * ((lane & 7) ^ turn(r8));
-    static_assert((8 * T::NW) % 16 == 0 || T::NW == 1, "turn() is the same for a wave's rows");
     const int jump_a = 8 * T::NW * (int)p.a_stride, jump_b = 8 * T::NW * (int)p.b_stride;
     const int voff_sfa = (w * T::A_SF + min(lane, T::A_SF - 1)) * (int)p.a_sf_stride * 4;
     const int voff_sfb = (w * T::B_SF + min(lane, T::B_SF - 1)) * (int)p.b_sf_stride * 4;
 
-    // The same number of instructions for every step, past the last one too.
-    const auto issue = [&](int i) {
-        uint8_t* stage = lds + (i % S) * STAGE;
-        const bool real = i < steps;
-        const int k = real ? i : 0;
-        if (real || lane == 0) {
+    // The loads of the group's step of a round; past the last step the same number of
+    // instructions, on buffers of no bytes: LDS gets zeros.
+    const auto issue = [&](int place, int round) {
+        uint8_t* stage = lds + place + group * STAGE;
+        const int step = round * T::WK + group;
+        const uint32_t real = step < steps ? ~0u : 0u;
+        const __amdgpu_buffer_rsrc_t ra = buffer(a0, bytes_a & real), rb = buffer(b0, bytes_b & real);
 #pragma unroll
-            for (int j = 0; j < T::A_LOADS; ++j)
-                load16_lds(ra, stage + (T::NW * j + w) * 1024, voff_a + j * jump_a, k * BK);
+        for (int j = 0; j < T::A_LOADS; ++j) load16_lds(ra, stage + (T::NW * j + w) * 1024, voff_a + j * jump_a, step * BK);
 #pragma unroll
-            for (int j = 0; j < T::B_LOADS; ++j)
-                load16_lds(rb, stage + T::OFF_B + (T::NW * j + w) * 1024, voff_b + j * jump_b, k * BK);
-        }
-        if (lane < T::A_SF && (real || lane == 0)) load4_lds(rsa, stage + T::OFF_SFA + w * T::A_SF * 4, voff_sfa, k * 4);
-        if constexpr (ROWS) {
-            if (lane < T::B_SF && (real || lane == 0)) load4_lds(rsb, stage + T::OFF_SFB + w * T::B_SF * 4, voff_sfb, k * 4);
-        }
+        for (int j = 0; j < T::B_LOADS; ++j)
+            load16_lds(rb, stage + T::OFF_B + (T::NW * j + w) * 1024, voff_b + j * jump_b, step * BK);
+        load4_lds(buffer(a_sf0, bytes_sfa & real), stage + T::OFF_SFA + w * 256, voff_sfa, step * 4);
+        if constexpr (ROWS) load4_lds(buffer(b_sf0, bytes_sfb & real), stage + T::OFF_SFB + w * 256, voff_sfb, step * 4);
     };
 
     // b's block of scales: one for the wave (tiles start and end with blocks, or within one)
     const int64_t last_block = (p.n - 1) / 128;
-    const float* b_sf = ROWS ? nullptr : p.b_sf + min((n0 + wn * T::TN) / 128, last_block) * p.b_sf_stride + step0;
-    static_assert(T::TN == 128 || 128 % T::TN == 0, "one block of scales to a wave");
+    // read through the scalar cache: a vector load's wait would be one for the stages in flight too
+    typedef const __attribute__((address_space(4))) float* constants_t;
+    const constants_t b_sf = (constants_t)(ROWS ? nullptr : p.b_sf + min((n0 + wn * T::TN) / 128, last_block) * p.b_sf_stride + step0);
 
-    f32x16_t acc[T::SN][T::SM];
+    f32x4_t acc[T::SN][T::SM];
 #pragma unroll
     for (int j = 0; j < T::SN; ++j)
 #pragma unroll
-        for (int i = 0; i < T::SM; ++i) acc[j][i] = f32x16_t{};
+        for (int i = 0; i < T::SM; ++i) acc[j][i] = f32x4_t{};
 
-    const auto add_step = [&](const uint8_t* stage, int step, const f32x16_t& d, int j, int i, float sa) {
-        if constexpr (ROWS) {
-            const uint8_t* sfb = stage + T::OFF_SFB + (wn * T::TN + 32 * j + ((lane >> 5) & 1) * 4) * 4;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const i32x4_t s = *reinterpret_cast<const i32x4_t*>(sfb + q * 32);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[j][i][4 * q + e] = fmaf(d[4 * q + e], sa * __int_as_float(s[e]), acc[j][i][4 * q + e]);
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) acc[j][i][e] = fmaf(d[e], sa, acc[j][i][e]);
-        }
+    // where the wave's rows of a stage are: a's, b's and the scales of both
+    const int at_x = group * STAGE + wm * T::TM * BK, at_y = group * STAGE + T::OFF_B + wn * T::TN * BK;
+    const int at_sa = group * STAGE + T::OFF_SFA + wm * T::at_sfa(T::TM) + (lane & 15) * 4;
+    const int at_sb = group * STAGE + T::OFF_SFB + wn * T::at_sfb(T::TN) + (lane >> 4) * 16;
+    // (loaded past the end too: a branch around it would end the block of code)
+    const auto block_scale = [&](int step) {
+        if constexpr (ROWS) return 1.0f;
+        const float s = b_sf[min(step, steps - 1)];
+        return step < steps ? s : 0.0f;
+    };
+    const auto row_scale = [&](int place, int i) {
+        return __int_as_float(*reinterpret_cast<const int*>(lds + place + at_sa + T::at_sfa(16 * i)));
+    };
+    const auto column_scales = [&](int place, int j) {
+        return *reinterpret_cast<const i32x4_t*>(lds + place + at_sb + T::at_sfb(16 * j));
+    };
+    // this wave's loads of the next round are there and its reads of this one done, then every wave's
+    const auto meet = [&]() {
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((S - 2) * LOADS) : "memory");
     };
 
     if (steps > 0) {
 #pragma unroll
-        for (int i = 0; i < S - 1; ++i) issue(i);
-        for (int step = 0; step < steps; ++step) {
-            // this wave's loads of the step are there, then every wave's
-            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((S - 2) * LOADS) : "memory");
-            issue(step + S - 1);
-            const uint8_t* stage = lds + (step % S) * STAGE;
-            const uint8_t* rows_x = stage + wm * T::TM * BK;
-            const uint8_t* rows_w = stage + T::OFF_B + wn * T::TN * BK;
-            const float sb = ROWS ? 1.0f : b_sf[step];
-            float sa[T::SM];
+        for (int i = 0; i < S; ++i) issue(i * ROUND, i);
+        asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((S - 1) * LOADS) : "memory");
+        int place = 0, step = group;
+        float sa[T::SM], sb = block_scale(step);
+        i32x8_t x_raw[T::SM], y_raw = operand(lds + at_y, 0);
 #pragma unroll
-            for (int i = 0; i < T::SM; ++i)
-                sa[i] = sb * __int_as_float(*reinterpret_cast<const int*>(stage + T::OFF_SFA + (wm * T::TM + 32 * i + (lane & 31)) * 4));
-            if constexpr (EXACT) {
-                f32x16_t d[T::SN][T::SM];
+        for (int i = 0; i < T::SM; ++i) {
+            x_raw[i] = operand(lds + at_x, i);
+            sa[i] = row_scale(0, i);
+        }
+        for (int round = 0; round < rounds; ++round, step += T::WK) {
+            const int next = place + ROUND == S * ROUND ? 0 : place + ROUND;
+            // while the matrix unit has the next blocks, those before them are added: EXACT by whole
+            // columns of blocks, whose chains of four go on side by side, else three blocks later
+            constexpr int BEHIND = EXACT ? T::SM : 3, RING = EXACT ? 2 * T::SM : 4, BLOCKS = T::SN * T::SM;
+            f32x4_t d[RING];
+            float s[T::SM];
+            i32x4_t cs[2];
+            const auto add_block = [&](int n) {
+                const int j = n / T::SM, i = n % T::SM;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    i32x4_t x[T::SM], y[T::SN];
+                for (int e = 0; e < 4; ++e)
+                    acc[j][i][e] = fmaf(d[n % RING][e], ROWS ? s[i] * __int_as_float(cs[j & 1][e]) : s[i], acc[j][i][e]);
+            };
 #pragma unroll
-                    for (int i = 0; i < T::SM; ++i) x[i] = quarter(rows_x, i, q);
+            for (int i = 0; i < T::SM; ++i) s[i] = sa[i] * sb;
+            Ready<EXACT> x[T::SM];
 #pragma unroll
-                    for (int j = 0; j < T::SN; ++j) y[j] = quarter(rows_w, j, q);
+            for (int i = 0; i < T::SM; ++i) x[i] = Ready<EXACT>(x_raw[i]);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        f16x8_t xh[T::SM];
-#pragma unroll
-                        for (int i = 0; i < T::SM; ++i) xh[i] = half_values(x[i][2 * h], x[i][2 * h + 1]);
-#pragma unroll
-                        for (int j = 0; j < T::SN; ++j) {
-                            const f16x8_t yh = half_values(y[j][2 * h], y[j][2 * h + 1]);
-#pragma unroll
-                            for (int i = 0; i < T::SM; ++i)
-                                d[j][i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(yh, xh[i], q + h == 0 ? f32x16_t{} : d[j][i], 0, 0, 0);
-                        }
-                    }
+            for (int j = 0; j < T::SN; ++j) {
+                const Ready<EXACT> y(y_raw);
+                if constexpr (ROWS) cs[j & 1] = column_scales(place, j);
+                if (j + 1 < T::SN) {
+                    y_raw = operand(lds + place + at_y, j + 1);
+                } else {
+                    meet();
+                    issue(place, round + S);
+                    sb = block_scale(step + T::WK);
+                    y_raw = operand(lds + next + at_y, 0);
                 }
+                const auto read_next = [&](int i) {
+                    x_raw[i] = operand(lds + next + at_x, i);
+                    sa[i] = row_scale(next, i);
+                };
+                if constexpr (EXACT) {
 #pragma unroll
-                for (int j = 0; j < T::SN; ++j)
+                    for (int q = 0; q < Ready<EXACT>::N; ++q)
 #pragma unroll
-                    for (int i = 0; i < T::SM; ++i) add_step(stage, step, d[j][i], j, i, sa[i]);
-            } else {
-                i32x8_t x[T::SM][2];
-#pragma unroll
-                for (int i = 0; i < T::SM; ++i) x[i][0] = operand(rows_x, i, 0), x[i][1] = operand(rows_x, i, 1);
-#pragma unroll
-                for (int j = 0; j < T::SN; ++j) {
-                    const i32x8_t y0 = operand(rows_w, j, 0), y1 = operand(rows_w, j, 1);
+                        for (int i = 0; i < T::SM; ++i) {
+                            f32x4_t& o = d[(j * T::SM + i) % RING];
+                            o = y.times(x[i], q, q == 0 ? f32x4_t{} : o);
+                        }
+                    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                     for (int i = 0; i < T::SM; ++i) {
-                        f32x16_t d = product_f8(y0, x[i][0], f32x16_t{});
-                        d = product_f8(y1, x[i][1], d);
-                        add_step(stage, step, d, j, i, sa[i]);
+                        if (j + 1 == T::SN) read_next(i);
+                        if (j > 0) add_block((j - 1) * T::SM + i);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < T::SM; ++i) {
+                        const int n = j * T::SM + i;
+                        d[n % RING] = y.times(x[i], 0, f32x4_t{});
+                        __builtin_amdgcn_sched_barrier(0);
+                        if (j + 1 == T::SN) read_next(i);
+                        if (n >= BEHIND) add_block(n - BEHIND);
+                        __builtin_amdgcn_sched_barrier(0);
                     }
                 }
             }
+#pragma unroll
+            for (int n = BLOCKS > BEHIND ? BLOCKS - BEHIND : 0; n < BLOCKS; ++n) add_block(n);
+            place = next;
         }
     }
     // the loads past the end are done, and every wave has read its last stage
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     __syncthreads();
-    float* mine = reinterpret_cast<float*>(lds) + w * T::TM * T::PITCH;
+    // a group's wave has TM x PW sums at a time in LDS; the groups' are added in order
+    float* tile = reinterpret_cast<float*>(lds);
+    constexpr int OF_WAVE = T::TM * T::PITCH;
 #pragma unroll
     for (int piece = 0; piece < T::TN / T::PW; ++piece) {
 #pragma unroll
-        for (int j = 0; j < T::PW / 32; ++j)
+        for (int j = 0; j < T::PW / 16; ++j)
 #pragma unroll
             for (int i = 0; i < T::SM; ++i)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const f32x16_t& d = acc[piece * (T::PW / 32) + j][i];
-                    *reinterpret_cast<float4*>(mine + (32 * i + (lane & 31)) * T::PITCH + 32 * j + 8 * q + 4 * ((lane >> 5) & 1)) =
-                        float4{d[4 * q], d[4 * q + 1], d[4 * q + 2], d[4 * q + 3]};
-                }
-        __builtin_amdgcn_wave_barrier();                 // the wave's own LDS operations stay in order
+                *reinterpret_cast<f32x4_t*>(tile + wave * OF_WAVE + (16 * i + (lane & 15)) * T::PITCH + 16 * j + 4 * (lane >> 4)) =
+                    acc[piece * (T::PW / 16) + j][i];
+        if constexpr (T::WK == 1) __builtin_amdgcn_wave_barrier();   // the wave's own LDS operations stay in order
+        else __syncthreads();
         constexpr int ACROSS = T::PW / 8;                // lanes of a row
-#pragma unroll
-        for (int i = 0; i < T::TM * ACROSS / 64; ++i) {
-            const int r = (i * 64 + lane) / ACROSS, c = (lane % ACROSS) * 8;
+        static_assert(T::TM * ACROSS % (64 * T::WK) == 0, "rows of a wave");
+#pragma unroll 2
+        for (int i = 0; i < T::TM * ACROSS / 64 / T::WK; ++i) {
+            const int r = ((i * T::WK + group) * 64 + lane) / ACROSS, c = (lane % ACROSS) * 8;
             const int64_t row = m0 + wm * T::TM + r, col = n0 + wn * T::TN + piece * T::PW + c;
             if (row >= p.m || col >= p.n) continue;
             float v[8];
-            load8<true>(mine, (size_t)r * T::PITCH + c, v);
+            load8<true>(tile + w * OF_WAVE, (size_t)r * T::PITCH + c, v);
+#pragma unroll
+            for (int g = 1; g < T::WK; ++g) {
+                float o[8];
+                load8<true>(tile + (g * T::NW + w) * OF_WAVE, (size_t)r * T::PITCH + c, o);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] += o[e];
+            }
             if (p.splits > 1) {
                 store8<true>(p.parts, ((size_t)split * p.m + row) * p.n + col, v);
                 continue;
@@ -298,7 +360,107 @@ __global__ void __launch_bounds__(T::NT) moe_product(ProductArgs p) {
             }
             store8<EXACT>(p.out, row * p.out_stride + col, v);
         }
-        __builtin_amdgcn_wave_barrier();
+        if constexpr (T::WK == 1) __builtin_amdgcn_wave_barrier();
+        else __syncthreads();
+    }
+}
+
+// Few rows of a (up to 16 MT): a workgroup has 16 rows of b over all of k, its
+// eight waves every eighth step each, from memory into registers, and their sums
+// meet in LDS.  b is read once and by no other workgroup, so it streams past the
+// caches; a comes from the caches.
+template <int MT, bool EXACT, bool ROWS>
+__global__ void __launch_bounds__(512) moe_product_few(ProductArgs p) {
+    constexpr int W = 8, U = MT == 1 ? 4 : 2, PITCH = 20;
+    __shared__ __attribute__((aligned(16))) float sums[W][16 * MT][PITCH];
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r = lane & 15, g = lane >> 4;
+    const int64_t n0 = (int64_t)blockIdx.x * 16;
+    const int rows_b = (int)min((int64_t)16, p.n - n0);
+    const __amdgpu_buffer_rsrc_t ra = buffer(p.a, (uint32_t)((p.m - 1) * p.a_stride + (int64_t)p.steps * BK));
+    const __amdgpu_buffer_rsrc_t rb = buffer(p.b + n0 * p.b_stride, (uint32_t)((rows_b - 1) * p.b_stride + (int64_t)p.steps * BK));
+    const __amdgpu_buffer_rsrc_t rsa = buffer(p.a_sf, (uint32_t)((p.m - 1) * p.a_sf_stride + p.steps) * 4);
+    const __amdgpu_buffer_rsrc_t rsb = buffer(ROWS ? p.b_sf + n0 * p.b_sf_stride : p.b_sf + n0 / 128 * p.b_sf_stride,
+                                              (uint32_t)((ROWS ? (rows_b - 1) * p.b_sf_stride : 0) + p.steps) * 4);
+    // a lane has chunks g and g + 4 of a row's 128 bytes, alike for a and b
+    const int voff_a = r * (int)p.a_stride + g * 16, voff_b = r * (int)p.b_stride + g * 16;
+    const int voff_sa = r * (int)p.a_sf_stride * 4, voff_sb = ROWS ? r * (int)p.b_sf_stride * 4 : 0;
+    struct Step {
+        u32x4_t b[2], a[MT][2];
+        uint32_t sa[MT], sb;
+    };
+    const auto fetch = [&](Step& s, int step) {
+        const int off = step * BK;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) s.b[h] = __builtin_amdgcn_raw_buffer_load_b128(rb, voff_b + 64 * h, off, 2);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                s.a[i][h] = __builtin_amdgcn_raw_buffer_load_b128(ra, voff_a + 16 * i * (int)p.a_stride + 64 * h, off, 0);
+            s.sa[i] = __builtin_amdgcn_raw_buffer_load_b32(rsa, voff_sa + 64 * i * (int)p.a_sf_stride, step * 4, 0);
+        }
+        s.sb = __builtin_amdgcn_raw_buffer_load_b32(rsb, voff_sb, step * 4, 0);
+    };
+    f32x4_t acc[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) acc[i] = f32x4_t{};
+    const auto add_step = [&](const Step& s) {
+        float sb[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sb[e] = ROWS ? __shfl(__uint_as_float(s.sb), 4 * g + e) : __uint_as_float(s.sb);
+        const Ready<EXACT> y(__builtin_bit_cast(i32x8_t, __builtin_shufflevector(s.b[0], s.b[1], 0, 1, 2, 3, 4, 5, 6, 7)));
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            const Ready<EXACT> x(__builtin_bit_cast(i32x8_t, __builtin_shufflevector(s.a[i][0], s.a[i][1], 0, 1, 2, 3, 4, 5, 6, 7)));
+            f32x4_t d = f32x4_t{};
+#pragma unroll
+            for (int q = 0; q < Ready<EXACT>::N; ++q) d = y.times(x, q, d);
+            const float sa = __uint_as_float(s.sa[i]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][e] = fmaf(d[e], sa * sb[e], acc[i][e]);
+        }
+    };
+    // U steps in flight behind the U that are added
+    Step now[U], next[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (w + W * u < p.steps) fetch(now[u], w + W * u);
+    for (int step = w; step < p.steps; step += W * U) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (step + W * (U + u) < p.steps) fetch(next[u], step + W * (U + u));
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (step + W * u < p.steps) add_step(now[u]);
+#pragma unroll
+        for (int u = 0; u < U; ++u) now[u] = next[u];
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i) *reinterpret_cast<f32x4_t*>(&sums[w][16 * i + r][4 * g]) = acc[i];
+    __syncthreads();
+    // a thread has two columns of a row
+    const int row = threadIdx.x >> 3, c = (threadIdx.x & 7) * 2;
+    const int64_t col = n0 + c;
+    if (row >= 16 * MT || row >= p.m || col >= p.n) return;
+    float v[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        v[0] += sums[i][row][c];
+        v[1] += sums[i][row][c + 1];
+    }
+    if constexpr (EXACT) {
+        if (p.add) {
+            const float2 o = *reinterpret_cast<const float2*>(static_cast<const float*>(p.add) + row * p.add_stride + col);
+            v[0] += o.x, v[1] += o.y;
+        }
+        *reinterpret_cast<float2*>(static_cast<float*>(p.out) + row * p.out_stride + col) = float2{v[0], v[1]};
+    } else {
+        if (p.add) {
+            const uint32_t o = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p.add) + row * p.add_stride + col);
+            v[0] += __uint_as_float(o << 16), v[1] += __uint_as_float(o & 0xffff0000u);
+        }
+        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + row * p.out_stride + col) = bf16_pair(v[0], v[1]);
     }
 }
 
@@ -329,11 +491,11 @@ __global__ void __launch_bounds__(256) moe_product_join(ProductArgs p) {
 
 namespace {
 
-using Wide = Tile<256, 256, 4, 2, 2>;
-using Mid = Tile<128, 128, 2, 2, 2>;
-using Low = Tile<64, 128, 1, 4, 3>;
+using Wide = Tile<256, 256, 4, 2, 1, 2>;
+using Mid = Tile<128, 128, 2, 2, 1, 2>;
+using Low = Tile<64, 64, 2, 2, 1, 4>;
 
-enum Kind { WIDE, MID, LOW };
+enum Kind { WIDE, MID, LOW, FEW, FEW2, FEW4 };
 
 struct Plan {
     Kind kind;
@@ -346,7 +508,8 @@ Plan plan(int m, int n, int k, bool f32) {
     const int steps = k / BK;
     Plan p;
     int64_t tiles;
-    if (m <= 64) p.kind = LOW, tiles = tiles_of(m, n, 64, 128);
+    if (m <= 32) return Plan{m <= 16 ? FEW : FEW2, 1};
+    if (m <= 64) p.kind = LOW, tiles = tiles_of(m, n, 64, 64);
     else if (!f32 && tiles_of(m, n, 256, 256) >= 256) p.kind = WIDE, tiles = tiles_of(m, n, 256, 256);
     else p.kind = MID, tiles = tiles_of(m, n, 128, 128);
     p.splits = 1;
@@ -365,9 +528,17 @@ void go(const ProductArgs& p, hipStream_t stream) {
                        (unsigned)T::template lds<ROWS>(), stream, p);
 }
 
+template <int MT, bool EXACT, bool ROWS>
+void go_few(const ProductArgs& p, hipStream_t stream) {
+    hipLaunchKernelGGL((moe_product_few<MT, EXACT, ROWS>), dim3((unsigned)((p.n + 15) / 16)), dim3(512), 0, stream, p);
+}
+
 template <bool EXACT, bool ROWS>
 void go(Kind kind, const ProductArgs& p, hipStream_t stream) {
-    if (kind == LOW) go<Low, EXACT, ROWS>(p, stream);
+    if (kind == FEW) go_few<1, EXACT, ROWS>(p, stream);
+    else if (kind == FEW2) go_few<2, EXACT, ROWS>(p, stream);
+    else if (kind == FEW4) go_few<4, EXACT, ROWS>(p, stream);
+    else if (kind == LOW) go<Low, EXACT, ROWS>(p, stream);
     else if (kind == MID) go<Mid, EXACT, ROWS>(p, stream);
     else if constexpr (!EXACT) go<Wide, EXACT, ROWS>(p, stream);
 }
