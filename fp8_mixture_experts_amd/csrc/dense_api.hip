@@ -100,7 +100,7 @@ extern "C" {
 
 int64_t mega_moe_product_workspace_bytes(const mega_moe_product_args* a) {
     if (check_product_sizes(a)) return -1;
-    return product_workspace(a->m, a->n, a->k, a->b_scale, a->out_type);
+    return a->m == 0 || a->n == 0 ? 0 : product_workspace(product_plan(a->m, a->n, a->k, a->out_type), a->m, a->n);
 }
 
 int mega_moe_product(const mega_moe_product_args* args, void* stream) {
@@ -125,7 +125,8 @@ int mega_moe_product(const mega_moe_product_args* args, void* stream) {
     if (a.a_stride > MAX_X_STRIDE || a.b_stride > MAX_X_STRIDE || a.a_sf_stride > MAX_SF_STRIDE || a.b_sf_stride > MAX_SF_STRIDE)
         return fail(MEGA_MOE_ERR_UNSUPPORTED, "built for strides of codes <= %lld and of scales <= %lld",
                     (long long)MAX_X_STRIDE, (long long)MAX_SF_STRIDE);
-    const int64_t need = product_workspace(a.m, a.n, a.k, a.b_scale, a.out_type), size = type_bytes(a.out_type);
+    const ProductPlan plan = product_plan(a.m, a.n, a.k, a.out_type);
+    const int64_t need = product_workspace(plan, a.m, a.n), size = type_bytes(a.out_type);
     if ((rc = check_workspace(a.workspace, a.workspace_bytes, need))) return rc;
     Tensors ts;
     if (k > 0) {
@@ -138,7 +139,7 @@ int mega_moe_product(const mega_moe_product_args* args, void* stream) {
     ts.add("out", a.out, m, n, a.out_stride, size, true);
     ts.add("workspace", a.workspace, 1, need, need, 1, true);
     if ((rc = ts.check("out", "add")) || (rc = check_device(k > 0 ? (const void*)a.a : a.out, stream))) return rc;
-    launch_product(a, (hipStream_t)stream);
+    launch_product(a, plan, (hipStream_t)stream);
     return launched();
 }
 

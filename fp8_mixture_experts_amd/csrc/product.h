@@ -7,9 +7,15 @@
 
 namespace mega_moe {
 
-// Bytes of partial sums that a call puts into its workspace.
-int64_t product_workspace(int m, int n, int k, int b_scale, int out_type);
+// The kernel and tile of a call, and the parts that its steps are split into.
+struct ProductPlan {
+    int kind, splits;
+};
+ProductPlan product_plan(int m, int n, int k, int out_type);
 
-void launch_product(const mega_moe_product_args& a, hipStream_t stream);
+// Bytes of partial sums that a call puts into its workspace.
+int64_t product_workspace(const ProductPlan& plan, int m, int n);
+
+void launch_product(const mega_moe_product_args& a, const ProductPlan& plan, hipStream_t stream);
 
 }  // namespace mega_moe

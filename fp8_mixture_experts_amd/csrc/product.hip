@@ -333,10 +333,11 @@ __global__ void __launch_bounds__(T::NT) moe_product(ProductArgs p) {
         if constexpr (T::WK == 1) __builtin_amdgcn_wave_barrier();   // the wave's own LDS operations stay in order
         else __syncthreads();
         constexpr int ACROSS = T::PW / 8;                // lanes of a row
-        static_assert(T::TM * ACROSS % (64 * T::WK) == 0, "rows of a wave");
+        constexpr int ITEMS = T::TM * ACROSS, AT_ONCE = 64 * T::WK;
 #pragma unroll 2
-        for (int i = 0; i < T::TM * ACROSS / 64 / T::WK; ++i) {
+        for (int i = 0; i < (ITEMS + AT_ONCE - 1) / AT_ONCE; ++i) {
             const int r = ((i * T::WK + group) * 64 + lane) / ACROSS, c = (lane % ACROSS) * 8;
+            if (ITEMS % AT_ONCE && r >= T::TM) continue;
             const int64_t row = m0 + wm * T::TM + r, col = n0 + wn * T::TN + piece * T::PW + c;
             if (row >= p.m || col >= p.n) continue;
             float v[8];
@@ -365,14 +366,13 @@ __global__ void __launch_bounds__(T::NT) moe_product(ProductArgs p) {
     }
 }
 
-// Few rows of a (up to 16 MT): a workgroup has 16 rows of b over all of k, its
-// eight waves every eighth step each, from memory into registers, and their sums
+// Up to 16 rows of a: a workgroup has 16 rows of b over all of k, its eight waves every eighth step each, from memory into registers, and their sums
 // meet in LDS.  b is read once and by no other workgroup, so it streams past the
 // caches; a comes from the caches.
-template <int MT, bool EXACT, bool ROWS>
+template <bool EXACT, bool ROWS>
 __global__ void __launch_bounds__(512) moe_product_few(ProductArgs p) {
-    constexpr int W = 8, U = MT == 1 ? 4 : 2, PITCH = 20;
-    __shared__ __attribute__((aligned(16))) float sums[W][16 * MT][PITCH];
+    constexpr int W = 8, U = 4, PITCH = 20;
+    __shared__ __attribute__((aligned(16))) float sums[W][16][PITCH];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, g = lane >> 4;
     const int64_t n0 = (int64_t)blockIdx.x * 16;
@@ -386,39 +386,30 @@ __global__ void __launch_bounds__(512) moe_product_few(ProductArgs p) {
     const int voff_a = r * (int)p.a_stride + g * 16, voff_b = r * (int)p.b_stride + g * 16;
     const int voff_sa = r * (int)p.a_sf_stride * 4, voff_sb = ROWS ? r * (int)p.b_sf_stride * 4 : 0;
     struct Step {
-        u32x4_t b[2], a[MT][2];
-        uint32_t sa[MT], sb;
+        u32x4_t b[2], a[2];
+        uint32_t sa, sb;
     };
     const auto fetch = [&](Step& s, int step) {
-        const int off = step * BK;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) s.b[h] = __builtin_amdgcn_raw_buffer_load_b128(rb, voff_b + 64 * h, off, 2);
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                s.a[i][h] = __builtin_amdgcn_raw_buffer_load_b128(ra, voff_a + 16 * i * (int)p.a_stride + 64 * h, off, 0);
-            s.sa[i] = __builtin_amdgcn_raw_buffer_load_b32(rsa, voff_sa + 64 * i * (int)p.a_sf_stride, step * 4, 0);
+        for (int h = 0; h < 2; ++h) {
+            s.b[h] = __builtin_amdgcn_raw_buffer_load_b128(rb, voff_b + 64 * h, step * BK, 2);
+            s.a[h] = __builtin_amdgcn_raw_buffer_load_b128(ra, voff_a + 64 * h, step * BK, 0);
         }
+        s.sa = __builtin_amdgcn_raw_buffer_load_b32(rsa, voff_sa, step * 4, 0);
         s.sb = __builtin_amdgcn_raw_buffer_load_b32(rsb, voff_sb, step * 4, 0);
     };
-    f32x4_t acc[MT];
-#pragma unroll
-    for (int i = 0; i < MT; ++i) acc[i] = f32x4_t{};
+    f32x4_t acc = f32x4_t{};
     const auto add_step = [&](const Step& s) {
-        float sb[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sb[e] = ROWS ? __shfl(__uint_as_float(s.sb), 4 * g + e) : __uint_as_float(s.sb);
         const Ready<EXACT> y(__builtin_bit_cast(i32x8_t, __builtin_shufflevector(s.b[0], s.b[1], 0, 1, 2, 3, 4, 5, 6, 7)));
+        const Ready<EXACT> x(__builtin_bit_cast(i32x8_t, __builtin_shufflevector(s.a[0], s.a[1], 0, 1, 2, 3, 4, 5, 6, 7)));
+        f32x4_t d = f32x4_t{};
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            const Ready<EXACT> x(__builtin_bit_cast(i32x8_t, __builtin_shufflevector(s.a[i][0], s.a[i][1], 0, 1, 2, 3, 4, 5, 6, 7)));
-            f32x4_t d = f32x4_t{};
+        for (int q = 0; q < Ready<EXACT>::N; ++q) d = y.times(x, q, d);
+        const float sa = __uint_as_float(s.sa);
 #pragma unroll
-            for (int q = 0; q < Ready<EXACT>::N; ++q) d = y.times(x, q, d);
-            const float sa = __uint_as_float(s.sa[i]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[i][e] = fmaf(d[e], sa * sb[e], acc[i][e]);
+        for (int e = 0; e < 4; ++e) {
+            const float sb = ROWS ? __shfl(__uint_as_float(s.sb), 4 * g + e) : __uint_as_float(s.sb);
+            acc[e] = fmaf(d[e], sa * sb, acc[e]);
         }
     };
     // U steps in flight behind the U that are added
@@ -436,13 +427,12 @@ __global__ void __launch_bounds__(512) moe_product_few(ProductArgs p) {
 #pragma unroll
         for (int u = 0; u < U; ++u) now[u] = next[u];
     }
-#pragma unroll
-    for (int i = 0; i < MT; ++i) *reinterpret_cast<f32x4_t*>(&sums[w][16 * i + r][4 * g]) = acc[i];
+    *reinterpret_cast<f32x4_t*>(&sums[w][r][4 * g]) = acc;
     __syncthreads();
     // a thread has two columns of a row
     const int row = threadIdx.x >> 3, c = (threadIdx.x & 7) * 2;
     const int64_t col = n0 + c;
-    if (row >= 16 * MT || row >= p.m || col >= p.n) return;
+    if (row >= p.m || col >= p.n) return;
     float v[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < W; ++i) {
@@ -493,33 +483,35 @@ namespace {
 
 using Wide = Tile<256, 256, 4, 2, 1, 2>;
 using Mid = Tile<128, 128, 2, 2, 1, 2>;
-using Low = Tile<64, 64, 2, 2, 1, 4>;
-
-enum Kind { WIDE, MID, LOW, FEW, FEW2, FEW4 };
-
-struct Plan {
-    Kind kind;
-    int splits;
-};
+using Pair = Tile<64, 64, 2, 2, 1, 3>;       // two workgroups to a compute unit
+using Deep = Tile<64, 64, 2, 2, 2, 3>;       // one, of two groups of waves
+using Low = Tile<32, 32, 2, 1, 4, 3>;
 
 int64_t tiles_of(int m, int n, int bm, int bn) { return (int64_t)((m + bm - 1) / bm) * ((n + bn - 1) / bn); }
 
-Plan plan(int m, int n, int k, bool f32) {
-    const int steps = k / BK;
-    Plan p;
-    int64_t tiles;
-    if (m <= 32) return Plan{m <= 16 ? FEW : FEW2, 1};
-    if (m <= 64) p.kind = LOW, tiles = tiles_of(m, n, 64, 64);
-    else if (!f32 && tiles_of(m, n, 256, 256) >= 256) p.kind = WIDE, tiles = tiles_of(m, n, 256, 256);
-    else p.kind = MID, tiles = tiles_of(m, n, 128, 128);
-    p.splits = 1;
-    if (p.kind != WIDE && tiles < 256 && steps > 1) {
-        p.splits = (int)((512 + tiles - 1) / tiles);
-        if (p.splits > 16) p.splits = 16;
-        if (p.splits > steps) p.splits = steps;
-    }
-    return p;
-}
+// What a kind takes, in us, with f tiles on the busiest of 256 compute units and s steps:
+//   call + f * tile + f * s * step + s * fill,
+// and what splitting it adds. Fitted (non-negative least squares of relative errors) to 64 shapes of m in
+// [1, 8192], k in [128, 8192], n in [64, 16384]: the least of them is on average within 2% of
+// the fastest of all measured, 14% at worst. Beside these, 32 x 64, 128 x 64, 256 x 128 and
+// 128 x 256 were measured; without them the choice is 1% worse.
+struct Cost {
+    float call, tile, step, fill;
+};
+constexpr Cost COST_FP8[] = {{2.9f, 0.84f, 0.086f, 0.0f},   // few rows (16 columns to a workgroup)
+                             {2.0f, 2.4f, 0.103f, 0.0f},    // Low
+                             {1.3f, 2.9f, 0.219f, 0.0f},    // Deep
+                             {3.4f, 0.37f, 0.209f, 0.058f}, // Pair
+                             {3.2f, 1.1f, 0.541f, 0.062f},  // Mid
+                             {0.0f, 5.7f, 1.45f, 0.0f}};    // Wide
+constexpr Cost COST_EXACT[] = {{2.9f, 0.84f, 0.086f, 0.0f},
+                               {1.9f, 2.7f, 0.136f, 0.0f},
+                               {1.3f, 3.4f, 0.381f, 0.0f},
+                               {2.6f, 1.3f, 0.347f, 0.123f},
+                               {0.8f, 4.4f, 0.98f, 0.201f}};
+constexpr float JOIN = 4.4f, JOIN_ELEMENT = 1.37e-6f;       // a second launch, and its sums
+enum Kind { FEW, LOW, DEEP, PAIR, MID, WIDE };
+constexpr int ROWS_OF[] = {16, 32, 64, 64, 128, 256}, COLUMNS_OF[] = {16, 32, 64, 64, 128, 256};
 
 template <typename T, bool EXACT, bool ROWS>
 void go(const ProductArgs& p, hipStream_t stream) {
@@ -528,37 +520,54 @@ void go(const ProductArgs& p, hipStream_t stream) {
                        (unsigned)T::template lds<ROWS>(), stream, p);
 }
 
-template <int MT, bool EXACT, bool ROWS>
-void go_few(const ProductArgs& p, hipStream_t stream) {
-    hipLaunchKernelGGL((moe_product_few<MT, EXACT, ROWS>), dim3((unsigned)((p.n + 15) / 16)), dim3(512), 0, stream, p);
-}
-
 template <bool EXACT, bool ROWS>
-void go(Kind kind, const ProductArgs& p, hipStream_t stream) {
-    if (kind == FEW) go_few<1, EXACT, ROWS>(p, stream);
-    else if (kind == FEW2) go_few<2, EXACT, ROWS>(p, stream);
-    else if (kind == FEW4) go_few<4, EXACT, ROWS>(p, stream);
-    else if (kind == LOW) go<Low, EXACT, ROWS>(p, stream);
-    else if (kind == MID) go<Mid, EXACT, ROWS>(p, stream);
-    else if constexpr (!EXACT) go<Wide, EXACT, ROWS>(p, stream);
+void go(int kind, const ProductArgs& p, hipStream_t stream) {
+    switch (kind) {
+        case FEW:
+            hipLaunchKernelGGL((moe_product_few<EXACT, ROWS>), dim3((unsigned)((p.n + 15) / 16)), dim3(512), 0, stream, p);
+            break;
+        case LOW: go<Low, EXACT, ROWS>(p, stream); break;
+        case DEEP: go<Deep, EXACT, ROWS>(p, stream); break;
+        case PAIR: go<Pair, EXACT, ROWS>(p, stream); break;
+        case MID: go<Mid, EXACT, ROWS>(p, stream); break;
+        default:
+            if constexpr (!EXACT) go<Wide, EXACT, ROWS>(p, stream);
+    }
 }
 
 }  // namespace
 
-int64_t product_workspace(int m, int n, int k, int b_scale, int out_type) {
-    if (m == 0 || n == 0) return 0;
-    const Plan q = plan(m, n, k, out_type == MEGA_MOE_F32);
-    return q.splits > 1 ? (int64_t)q.splits * m * n * 4 : 0;
+ProductPlan product_plan(int m, int n, int k, int out_type) {
+    const bool f32 = out_type == MEGA_MOE_F32;
+    const Cost* cost = f32 ? COST_EXACT : COST_FP8;
+    const int steps = k / BK;
+    ProductPlan best = {m <= 16 ? FEW : LOW, 1};
+    float least = INFINITY;
+    for (int kind = m <= 16 ? FEW : LOW; kind <= (f32 ? MID : WIDE); ++kind) {
+        const int64_t tiles = tiles_of(m, n, ROWS_OF[kind], COLUMNS_OF[kind]);
+        // parts of the steps only where a compute unit would have no tile without them
+        for (int splits = 1; splits == 1 || (kind != FEW && splits <= steps && tiles * splits <= 512 && splits <= 64); splits *= 2) {
+            const float f = (float)((tiles * splits + 255) / 256), s = (float)((steps + splits - 1) / splits);
+            float us = cost[kind].call + f * (cost[kind].tile + s * cost[kind].step) + s * cost[kind].fill;
+            if (splits > 1) us += JOIN + JOIN_ELEMENT * splits * (float)m * n;
+            if (us < least) {
+                least = us;
+                best = {kind, splits};
+            }
+        }
+    }
+    return best;
 }
 
-void launch_product(const mega_moe_product_args& g, hipStream_t stream) {
+int64_t product_workspace(const ProductPlan& plan, int m, int n) { return plan.splits > 1 ? (int64_t)plan.splits * m * n * 4 : 0; }
+
+void launch_product(const mega_moe_product_args& g, const ProductPlan& plan, hipStream_t stream) {
     const bool f32 = g.out_type == MEGA_MOE_F32, rows = g.b_scale == MEGA_MOE_SCALE_ROW;
-    const Plan q = plan(g.m, g.n, g.k, f32);
     const ProductArgs p = {g.a, g.b, g.a_sf, g.b_sf, g.add, g.out, static_cast<float*>(g.workspace), g.a_stride, g.b_stride,
-                           g.a_sf_stride, g.b_sf_stride, g.add_stride, g.out_stride, g.m, g.n, g.k / BK, q.splits};
-    if (f32) rows ? go<true, true>(q.kind, p, stream) : go<true, false>(q.kind, p, stream);
-    else rows ? go<false, true>(q.kind, p, stream) : go<false, false>(q.kind, p, stream);
-    if (q.splits > 1) {
+                           g.a_sf_stride, g.b_sf_stride, g.add_stride, g.out_stride, g.m, g.n, g.k / BK, plan.splits};
+    if (f32) rows ? go<true, true>(plan.kind, p, stream) : go<true, false>(plan.kind, p, stream);
+    else rows ? go<false, true>(plan.kind, p, stream) : go<false, false>(plan.kind, p, stream);
+    if (plan.splits > 1) {
         const int64_t n = ((int64_t)g.m * (g.n / 8) + 255) / 256;
         const dim3 grid((unsigned)(n < 65536 ? n : 65536));
         if (f32) hipLaunchKernelGGL(moe_product_join<true>, grid, dim3(256), 0, stream, p);

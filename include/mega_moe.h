@@ -638,8 +638,8 @@ typedef struct mega_moe_product_args {
 } mega_moe_product_args;
 int mega_moe_product(const mega_moe_product_args* a, void* stream);
 
-/* Workspace bytes that the call needs (-1 if invalid): from m, n, k, b_scale and
- * out_type.  Host-only. */
+/* Workspace bytes that the call needs (-1 if invalid): from m, n, k and out_type.
+ * Host-only. */
 int64_t mega_moe_product_workspace_bytes(const mega_moe_product_args* a);
 
 #define MEGA_MOE_ACT_NONE 0     /* h = x                                        */
