@@ -33,7 +33,8 @@ struct QuantArgs {
 // largest magnitude as float32 bits (a NaN is the largest).
 struct Scale {
     float sf, up, d, inv;
-    __device__ explicit Scale(uint32_t m) {
+    Scale() = default;
+    __device__ __forceinline__ explicit Scale(uint32_t m) {
         const float amax = __uint_as_float(m);
         sf = amax / 448.0f;
         // tiny blocks are scaled up first, so that the reciprocal is finite
@@ -41,6 +42,17 @@ struct Scale {
         d = (amax * up) / 448.0f;
         inv = amax == 0.0f ? 0.0f : 1.0f / d;
         if (inv == 0.0f) d = 0.0f;               // a scale of 0 or infinity: codes of 0
+    }
+    // That of lane R of the lane's four.
+    template <int R>
+    __device__ __forceinline__ Scale of_quad() const {
+        const auto move = [](float v) {
+            return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x55 * R, 0xf, 0xf, true));
+        };
+        Scale o;
+        o.sf = 0.0f;
+        o.up = move(up), o.d = move(d), o.inv = move(inv);
+        return o;
     }
     // v / sf, rounded as a division rounds it: the product with the reciprocal
     // and one step of Newton's iteration.
@@ -57,55 +69,62 @@ struct Scale {
 __device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return a > b ? a : b; }
 
-// Of the smaller exponential, so that a low gate keeps its share down to the subnormals.
+// s = 1 / (1 + exp(-g)), of the smaller exponential, so that a low gate keeps its share
+// down to the subnormals.  exp(-|g|) is the square of 2^(-|g| log2(e) / 2), whose
+// argument's rounding error (and log2(e)'s) is put back to first order: the square root is a normal number
+// wherever the square is not 0. 1 + e is in [1, 2], where the hardware's reciprocal and one
+// step of Newton's iteration leave an error below a step.
 __device__ __forceinline__ float sigmoid(float g) {
-    const float e = expf(-fabsf(g));
-    return (g < 0.0f ? e : 1.0f) / (1.0f + e);
+    constexpr float HALF_LOG2E = 0.72134751081466675f, REST = 9.6298151675e-9f, TWO_LN2 = 1.3862943611198906f;
+    const float a = -fminf(fabsf(g), 256.0f), x = a * HALF_LOG2E;
+    const float off = fmaf(a, REST, fmaf(a, HALF_LOG2E, -x)), h = __builtin_amdgcn_exp2f(x), hh = h * h;
+    const float e = fmaf(hh, off * TWO_LN2, hh), t = 1.0f + e, r = __builtin_amdgcn_rcpf(t);
+    return (g < 0.0f ? e : 1.0f) * fmaf(fmaf(-t, r, 1.0f), r, r);
 }
 
 // The layer's clamp: fminf and fmaxf would turn a NaN into a bound.
 __device__ __forceinline__ float clamped(float v, float c) { return v > c ? c : v < -c ? -c : v; }
 
-// The eight values of output `which` from the raw inputs.
-template <int KIND>
-__device__ __forceinline__ void values(int which, float (&x)[8], const float (&up)[8], const float (&dh)[8], float clamp) {
-    if constexpr (KIND == PLAIN) return;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float g = clamped(x[i], clamp), u = clamped(up[i], clamp);
-        const float s = sigmoid(g);
-        if constexpr (KIND == SWIGLU) {
-            x[i] = g * s * u;
-        } else {
-            if (which == 0) x[i] = fabsf(x[i]) > clamp ? 0.0f : dh[i] * u * (s * (1.0f + g * (1.0f - s)));
-            else x[i] = fabsf(up[i]) > clamp ? 0.0f : dh[i] * (g * s);
-        }
-    }
-}
-
-// Eight columns of one row as they lie in memory.
+// Eight columns of one row as they lie in memory, and what is made of them.
 template <int KIND, bool F32>
 struct Raw {
-    static constexpr int N = F32 ? 2 : 1;
+    static constexpr int N = F32 ? 2 : 1, OUTS = KIND == GRAD ? 2 : 1;
     u32x4_t x[N], up[N], dh[N];
-    __device__ __forceinline__ void load(const QuantArgs& a, int64_t t, int col) {
+    // (zeros where the row is none)
+    __device__ __forceinline__ void load(const QuantArgs& a, int64_t t, int col, bool live) {
+        const u32x4_t none = {0u, 0u, 0u, 0u};
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            x[i] = raw8<F32>(a.x, t * a.x_stride + col)[i];
-            if constexpr (KIND != PLAIN) up[i] = raw8<F32>(a.up, t * a.up_stride + col)[i];
-            if constexpr (KIND == GRAD) dh[i] = raw8<F32>(a.dh, t * a.dh_stride + col)[i];
+            x[i] = live ? raw8<F32>(a.x, t * a.x_stride + col)[i] : none;
+            if constexpr (KIND != PLAIN) up[i] = live ? raw8<F32>(a.up, t * a.up_stride + col)[i] : none;
+            if constexpr (KIND == GRAD) dh[i] = live ? raw8<F32>(a.dh, t * a.dh_stride + col)[i] : none;
         }
     }
-    __device__ __forceinline__ void zero() {
-#pragma unroll
-        for (int i = 0; i < N; ++i) x[i] = up[i] = dh[i] = u32x4_t{0u, 0u, 0u, 0u};
+    // (the clamp is uniform, and mostly there is none)
+    __device__ __forceinline__ void get(float clamp, float (&v)[OUTS][8]) const {
+        if (KIND == PLAIN || clamp == INFINITY) make<false>(clamp, v);
+        else make<true>(clamp, v);
     }
-    __device__ __forceinline__ void get(int which, float clamp, float (&v)[8]) const {
-        float u[8] = {}, d[8] = {};
-        values8<F32>(x, v);
+    template <bool CLAMP>
+    __device__ __forceinline__ void make(float clamp, float (&v)[OUTS][8]) const {
+        float g[8], u[8] = {}, d[8] = {};
+        values8<F32>(x, g);
         if constexpr (KIND != PLAIN) values8<F32>(up, u);
         if constexpr (KIND == GRAD) values8<F32>(dh, d);
-        values<KIND>(which, v, u, d, clamp);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if constexpr (KIND == PLAIN) {
+                v[0][i] = g[i];
+            } else {
+                const float gc = CLAMP ? clamped(g[i], clamp) : g[i], uc = CLAMP ? clamped(u[i], clamp) : u[i], s = sigmoid(gc);
+                if constexpr (KIND == SWIGLU) {
+                    v[0][i] = gc * s * uc;
+                } else {
+                    v[0][i] = CLAMP && fabsf(g[i]) > clamp ? 0.0f : d[i] * uc * (s * (1.0f + gc * (1.0f - s)));
+                    v[OUTS - 1][i] = CLAMP && fabsf(u[i]) > clamp ? 0.0f : d[i] * (gc * s);
+                }
+            }
+        }
     }
 };
 
@@ -128,11 +147,12 @@ __global__ void __launch_bounds__(256) moe_quantize_rows(QuantArgs a) {
         const int64_t t = i / blocks;
         const int b = (int)(i - t * blocks), col = b * 128 + lane * 8;
         Raw<KIND, F32> raw;
-        raw.load(a, t, col);
+        raw.load(a, t, col, true);
+        float made[OUTS][8];
+        raw.get(a.clamp, made);
 #pragma unroll
         for (int which = 0; which < OUTS; ++which) {
-            float v[8];
-            raw.get(which, a.clamp, v);
+            const float (&v)[8] = made[which];
             store_out<KIND, F32>(a, which, t, col, v);
             if (!a.q) continue;
             uint32_t m = 0;
@@ -149,59 +169,86 @@ __global__ void __launch_bounds__(256) moe_quantize_rows(QuantArgs a) {
 }
 
 // Codes by columns, by blocks, and by rows beside them: a workgroup has a tile
-// of 128 rows x 128 columns, a thread eight columns of four rows that follow
+// of 128 rows x 128 columns, a thread eight columns of R rows that follow
 // each other.  A column's largest value is that of the thread's rows, of the
-// wave's four groups of rows and, through LDS, of the eight waves.  The codes by
-// columns turn in LDS: a thread has four neighbours of each, and a row of 128
-// leaves as whole lines.
-template <int KIND, bool F32, bool BLOCK>
-__global__ void __launch_bounds__(512) moe_quantize_tile(QuantArgs a) {
-    constexpr int OUTS = KIND == GRAD ? 2 : 1;
-    __shared__ uint32_t top[8][128];
-    __shared__ uint32_t turned[128 * 32];                // [column][4 rows], words swizzled
+// wave's four groups of rows and, through LDS, of the eight waves; its scale is worked
+// out by one thread, a row's by one of the row's lanes (three divisions each, of
+// which a thread would have 36).  The codes by columns turn in LDS: a thread has four
+// neighbours of each, and a row of 128 leaves as whole lines.
+template <int KIND, bool F32, bool BLOCK, int R>
+__global__ void __launch_bounds__(2048 / R) moe_quantize_tile(QuantArgs a) {
+    constexpr int OUTS = KIND == GRAD ? 2 : 1, WAVES = 32 / R;
+    constexpr bool AHEAD = R == 2 && !F32;               // the next tile's loads in flight behind this one's codes
+    __shared__ uint32_t top[WAVES][128];
+    __shared__ float col_up[128], col_d[128], col_inv[128];
+    __shared__ __attribute__((aligned(16))) uint8_t turned[128 * 128];   // [column][row], chunks of 16 swizzled
     const int lane = threadIdx.x & 15, group = threadIdx.x >> 4, wave = threadIdx.x >> 6;
     const int blocks = a.C / 128, row_blocks = (a.T + 127) / 128;
     const int64_t tiles = (int64_t)blocks * row_blocks;
+    typedef Raw<KIND, F32> Rows[R];
+    const auto fetch = [&](Rows& raw, int64_t tile) {
+        const int64_t rb = tile / blocks, t = rb * 128 + group * R;
+        const int col = (int)(tile - rb * blocks) * 128 + lane * 8;
+#pragma unroll
+        for (int r = 0; r < R; ++r) raw[r].load(a, t + r, col, t + r < a.T);
+    };
+    Rows ahead;
+    if constexpr (AHEAD) {
+        if (blockIdx.x < tiles) fetch(ahead, blockIdx.x);
+    }
     for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
         const int rb = (int)(tile / blocks), b = (int)(tile - (int64_t)rb * blocks);
         const int col = b * 128 + lane * 8;
-        const int64_t t0 = (int64_t)rb * 128 + group * 4;
-        Raw<KIND, F32> raw[4];
+        const int64_t t0 = (int64_t)rb * 128 + group * R;
+        Rows here;
+        if constexpr (!AHEAD) fetch(here, tile);
+        float made[OUTS][R][8];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            if (t0 + r < a.T) raw[r].load(a, t0 + r, col);
-            else raw[r].zero();
+        for (int r = 0; r < R; ++r) {
+            float v[OUTS][8];
+            if constexpr (AHEAD) ahead[r].get(a.clamp, v);
+            else here[r].get(a.clamp, v);
+#pragma unroll
+            for (int which = 0; which < OUTS; ++which) {
+                // rows behind the last are 0 whatever is made of zeros
+                if (t0 + r < a.T) store_out<KIND, F32>(a, which, t0 + r, col, v[which]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) made[which][r][e] = v[which][e];
+            }
+        }
+        if constexpr (AHEAD) {
+            if (tile + gridDim.x < tiles) fetch(ahead, tile + gridDim.x);
         }
 #pragma unroll
         for (int which = 0; which < OUTS; ++which) {
-            float v[4][8];
-            uint32_t m[4] = {};                          // by rows
+            const float (&v)[R][8] = made[which];
+            const int64_t row0 = (int64_t)which * a.C + b * 128;         // of qt
+            uint32_t m[R] = {};                          // by rows
             uint32_t mc[8] = {};                         // by columns
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                raw[r].get(which, a.clamp, v[r]);
-                // rows behind the last are 0 whatever is made of zeros
-                if (t0 + r < a.T) store_out<KIND, F32>(a, which, t0 + r, col, v[r]);
+            for (int r = 0; r < R; ++r)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const uint32_t x = magnitude(v[r][e]);
                     m[r] = larger(m[r], x);
                     mc[e] = larger(mc[e], x);
                 }
-            }
+            Scale of_block;
             if constexpr (BLOCK) {
-                uint32_t all = larger(larger(m[0], m[1]), larger(m[2], m[3]));
+                uint32_t all = m[0];
+#pragma unroll
+                for (int r = 1; r < R; ++r) all = larger(all, m[r]);
                 all = over_lanes<64>(all, larger);
                 if ((threadIdx.x & 63) == 0) top[wave][0] = all;
                 __syncthreads();
 #pragma unroll
-                for (int w = 0; w < 8; ++w) all = larger(all, top[w][0]);
-                m[0] = all;
-            } else {
-                if (a.q) {
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) m[r] = over_lanes<16>(m[r], larger);
+                for (int w = 0; w < WAVES; ++w) all = larger(all, top[w][0]);
+                of_block = Scale(all);
+                if (threadIdx.x == 0) {
+                    if (a.q) a.q_sf[(int64_t)rb * blocks + b] = of_block.sf;
+                    if (a.qt) a.qt_sf[(int64_t)b * row_blocks + rb] = of_block.sf;
                 }
+            } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     auto p = __builtin_amdgcn_permlane16_swap(mc[e], mc[e], false, false);
@@ -211,45 +258,56 @@ __global__ void __launch_bounds__(512) moe_quantize_tile(QuantArgs a) {
                 }
                 if ((threadIdx.x & 63) < 16) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) top[wave][lane * 8 + e] = mc[e];
+                    for (int e = 0; e < 8; e += 4)
+                        *reinterpret_cast<u32x4_t*>(&top[wave][lane * 8 + e]) = u32x4_t{mc[e], mc[e + 1], mc[e + 2], mc[e + 3]};
                 }
                 __syncthreads();
+                if (threadIdx.x < 128) {
+                    uint32_t x = top[0][threadIdx.x];
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-#pragma unroll
-                    for (int w = 0; w < 8; ++w) mc[e] = larger(mc[e], top[w][lane * 8 + e]);
+                    for (int w = 1; w < WAVES; ++w) x = larger(x, top[w][threadIdx.x]);
+                    const Scale s(x);
+                    a.qt_sf[(row0 + threadIdx.x) * row_blocks + rb] = s.sf;
+                    col_up[threadIdx.x] = s.up, col_d[threadIdx.x] = s.d, col_inv[threadIdx.x] = s.inv;
+                }
             }
             if (a.q) {
+                Scale mine = of_block;
+                if constexpr (!BLOCK) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const Scale s(m[BLOCK ? 0 : r]);
-                    if (t0 + r >= a.T) continue;
-                    const int64_t row = (t0 + r) * OUTS + which;
-                    *reinterpret_cast<uint2*>(a.q + row * a.C + col) =
-                        uint2{s.codes(v[r][0], v[r][1], v[r][2], v[r][3]), s.codes(v[r][4], v[r][5], v[r][6], v[r][7])};
-                    if (!BLOCK && lane == 0) a.q_sf[row * blocks + b] = s.sf;
-                    if (BLOCK && threadIdx.x == 0 && r == 0) a.q_sf[(int64_t)rb * blocks + b] = s.sf;
+                    for (int r = 0; r < R; ++r) m[r] = over_lanes<16>(m[r], larger);
+                    uint32_t own = lane & 1 ? m[1] : m[0];
+                    if constexpr (R == 4) own = lane & 2 ? (lane & 1 ? m[3] : m[2]) : own;
+                    mine = Scale(own);
+                    if (lane < R && t0 + lane < a.T) a.q_sf[((t0 + lane) * OUTS + which) * blocks + b] = mine.sf;
+                }
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const Scale s = r == 0 ? mine.of_quad<0>() : r == 1 ? mine.of_quad<1>() : r == 2 ? mine.of_quad<2>() : mine.of_quad<3>();
+                    const uint2 d = {s.codes(v[r][0], v[r][1], v[r][2], v[r][3]), s.codes(v[r][4], v[r][5], v[r][6], v[r][7])};
+                    if (t0 + r < a.T) *reinterpret_cast<uint2*>(a.q + ((t0 + r) * OUTS + which) * a.C + col) = d;
                 }
             }
             if (a.qt) {
-                const int64_t row0 = (int64_t)which * a.C + b * 128;     // of qt
+                if (!BLOCK) __syncthreads();
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const Scale s(BLOCK ? m[0] : mc[e]);
-                    // the eight threads' words of four that a row's 16 bytes are spread over the banks
-                    turned[(lane * 8 + e) * 32 + (group ^ ((lane & 7) * 4))] = s.codes(v[0][e], v[1][e], v[2][e], v[3][e]);
-                    if (!BLOCK && group == 0) a.qt_sf[(row0 + lane * 8 + e) * row_blocks + rb] = s.sf;
-                    if (BLOCK && threadIdx.x == 0 && e == 0) a.qt_sf[(int64_t)b * row_blocks + rb] = s.sf;
+                    Scale s = of_block;
+                    if (!BLOCK) s.up = col_up[lane * 8 + e], s.d = col_d[lane * 8 + e], s.inv = col_inv[lane * 8 + e];
+                    // the 16 bytes of a row lie at chunk ^ (column / 8 % 8)
+                    uint8_t* to = turned + (lane * 8 + e) * 128 + ((group * R) ^ ((lane & 7) * 16));
+                    if constexpr (R == 4) *reinterpret_cast<uint32_t*>(to) = s.codes(v[0][e], v[1][e], v[2][e], v[R - 1][e]);
+                    else *reinterpret_cast<uint16_t*>(to) = (uint16_t)s.codes(v[0][e], v[1][e], 0.0f, 0.0f);
                 }
                 __syncthreads();
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int c = (threadIdx.x >> 3) + 64 * i, w = (threadIdx.x & 7) * 4;
-                    const u32x4_t d = *reinterpret_cast<const u32x4_t*>(&turned[c * 32 + (w ^ (((c >> 3) & 7) * 4))]);
-                    *reinterpret_cast<u32x4_t*>(a.qt + (row0 + c) * ((int64_t)row_blocks * 128) + (int64_t)rb * 128 + w * 4) = d;
+                for (int i = 0; i < R / 2; ++i) {
+                    const int c = (threadIdx.x >> 3) + 256 / R * i, w = (threadIdx.x & 7) * 16;
+                    const u32x4_t d = *reinterpret_cast<const u32x4_t*>(turned + c * 128 + (w ^ (((c >> 3) & 7) * 16)));
+                    *reinterpret_cast<u32x4_t*>(a.qt + (row0 + c) * ((int64_t)row_blocks * 128) + (int64_t)rb * 128 + w) = d;
                 }
             }
-            __syncthreads();                             // top and turned are written again
+            if (BLOCK) __syncthreads();                  // top is written again (else two barriers lie between)
         }
     }
 }
@@ -263,11 +321,15 @@ template <int KIND, bool F32>
 void launch(const QuantArgs& a, bool block, hipStream_t stream) {
     if (a.qt || (block && a.q)) {
         const int64_t tiles = (int64_t)(a.C / 128) * ((a.T + 127) / 128);
+        // The gradients' values, of two outputs, leave a compute unit one workgroup: of 16 waves, which
+        // goes on to further tiles with their loads in flight (float32's do not fit beside the values).
+        constexpr int R = KIND == GRAD ? 2 : 4;
+        const int64_t most = R == 2 && !F32 ? 256 : MAX_GRID;
         const auto go = [&](auto kernel) {
-            hipLaunchKernelGGL(kernel, dim3((unsigned)(tiles < MAX_GRID ? tiles : MAX_GRID)), dim3(512), 0, stream, a);
+            hipLaunchKernelGGL(kernel, dim3((unsigned)(tiles < most ? tiles : most)), dim3(2048 / R), 0, stream, a);
         };
-        if (KIND != GRAD && block) go(moe_quantize_tile<KIND, F32, KIND != GRAD>);
-        else go(moe_quantize_tile<KIND, F32, false>);
+        if (KIND != GRAD && block) go(moe_quantize_tile<KIND, F32, KIND != GRAD, R>);
+        else go(moe_quantize_tile<KIND, F32, false, R>);
     } else {
         const int64_t n = ((int64_t)a.T * (a.C / 128) + 15) / 16;
         hipLaunchKernelGGL((moe_quantize_rows<KIND, F32>), dim3((unsigned)(n < MAX_GRID ? n : MAX_GRID)), dim3(256), 0, stream, a);
