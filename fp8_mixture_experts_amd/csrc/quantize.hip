@@ -29,44 +29,48 @@ struct QuantArgs {
     float clamp;                // infinite: none
 };
 
-// A block's scale and what its values are multiplied and divided by, from the
-// largest magnitude as float32 bits (a NaN is the largest).
+// A block's scale, and what its values are multiplied by, from the largest magnitude
+// as float32 bits (a NaN is the largest).
 struct Scale {
-    float sf, up, d, inv;
+    float sf, up, hi, lo;        // sf = 1 / ((hi + lo) up), to 2^-46
     Scale() = default;
     __device__ __forceinline__ explicit Scale(uint32_t m) {
         const float amax = __uint_as_float(m);
         sf = amax / 448.0f;
         // tiny blocks are scaled up first, so that the reciprocal is finite
         up = sf < 0x1p-100f ? 0x1p100f : 1.0f;
-        d = (amax * up) / 448.0f;
-        inv = amax == 0.0f ? 0.0f : 1.0f / d;
-        if (inv == 0.0f) d = 0.0f;               // a scale of 0 or infinity: codes of 0
+        const float d = (amax * up) / 448.0f;
+        hi = amax == 0.0f ? 0.0f : 1.0f / d;
+        // a scale of 0 or infinity: codes of 0
+        lo = hi == 0.0f ? 0.0f : fmaf(-d, hi, 1.0f) * hi;
     }
-    // That of lane R of the lane's four.
-    template <int R>
+    // That of lane L of the lane's four.
+    template <int L>
     __device__ __forceinline__ Scale of_quad() const {
         const auto move = [](float v) {
-            return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x55 * R, 0xf, 0xf, true));
+            return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), 0x55 * L, 0xf, 0xf, true));
         };
         Scale o;
         o.sf = 0.0f;
-        o.up = move(up), o.d = move(d), o.inv = move(inv);
+        o.up = move(up), o.hi = move(hi), o.lo = move(lo);
         return o;
     }
-    // v / sf, rounded as a division rounds it: the product with the reciprocal
-    // and one step of Newton's iteration.
+    // v / sf: one rounding of a sum that is off by 2^-46, so that it is the quotient's own
+    // but within that of the middle between two floats; no tie between codes lies there.
+    template <bool TINY>
     __device__ __forceinline__ float quotient(float v) const {
-        const float x = v * up, q = x * inv;
-        return fmaf(-fmaf(q, d, -x), inv, q);
+        if constexpr (TINY) v *= up;
+        return fmaf(v, hi, v * lo);
     }
+    template <bool TINY>
     __device__ __forceinline__ uint32_t codes(float a, float b, float c, float e) const {
-        const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(quotient(a), quotient(b), 0, false);
-        return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(quotient(c), quotient(e), lo, true);
+        const int p = __builtin_amdgcn_cvt_pk_fp8_f32(quotient<TINY>(a), quotient<TINY>(b), 0, false);
+        return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(quotient<TINY>(c), quotient<TINY>(e), p, true);
     }
 };
 
-__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+// The larger magnitude; of a NaN and another, the NaN.
+__device__ __forceinline__ float larger(float a, float b) { return __builtin_elementwise_maximum(fabsf(a), fabsf(b)); }
 __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return a > b ? a : b; }
 
 // s = 1 / (1 + exp(-g)), of the smaller exponential, so that a low gate keeps its share
@@ -155,14 +159,13 @@ __global__ void __launch_bounds__(256) moe_quantize_rows(QuantArgs a) {
             const float (&v)[8] = made[which];
             store_out<KIND, F32>(a, which, t, col, v);
             if (!a.q) continue;
-            uint32_t m = 0;
+            float m = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) m = larger(m, magnitude(v[e]));
-            m = over_lanes<16>(m, larger);
-            const Scale s(m);
+            for (int e = 0; e < 8; ++e) m = larger(m, v[e]);
+            const Scale s(over_lanes<16>(__float_as_uint(m), [](uint32_t x, uint32_t y) { return larger(x, y); }));
             const int64_t row = t * OUTS + which;        // [T, OUTS * C] codes
             *reinterpret_cast<uint2*>(a.q + row * a.C + col) =
-                uint2{s.codes(v[0], v[1], v[2], v[3]), s.codes(v[4], v[5], v[6], v[7])};
+                uint2{s.codes<true>(v[0], v[1], v[2], v[3]), s.codes<true>(v[4], v[5], v[6], v[7])};
             if (lane == 0) a.q_sf[row * blocks + b] = s.sf;
         }
     }
@@ -180,7 +183,8 @@ __global__ void __launch_bounds__(2048 / R) moe_quantize_tile(QuantArgs a) {
     constexpr int OUTS = KIND == GRAD ? 2 : 1, WAVES = 32 / R;
     constexpr bool AHEAD = R == 2 && !F32;               // the next tile's loads in flight behind this one's codes
     __shared__ uint32_t top[WAVES][128];
-    __shared__ float col_up[128], col_d[128], col_inv[128];
+    __shared__ __attribute__((aligned(16))) float col_up[128], col_hi[128], col_lo[128];
+    __shared__ int col_tiny[2];
     __shared__ __attribute__((aligned(16))) uint8_t turned[128 * 128];   // [column][row], chunks of 16 swizzled
     const int lane = threadIdx.x & 15, group = threadIdx.x >> 4, wave = threadIdx.x >> 6;
     const int blocks = a.C / 128, row_blocks = (a.T + 127) / 128;
@@ -223,22 +227,20 @@ __global__ void __launch_bounds__(2048 / R) moe_quantize_tile(QuantArgs a) {
         for (int which = 0; which < OUTS; ++which) {
             const float (&v)[R][8] = made[which];
             const int64_t row0 = (int64_t)which * a.C + b * 128;         // of qt
-            uint32_t m[R] = {};                          // by rows
-            uint32_t mc[8] = {};                         // by columns
+            const auto max_bits = [](uint32_t x, uint32_t y) { return larger(x, y); };
+            float m[R], mc[8];                           // by rows, and by columns
 #pragma unroll
-            for (int r = 0; r < R; ++r)
+            for (int r = 0; r < R; ++r) {
+                m[r] = larger(v[r][0], v[r][1]);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const uint32_t x = magnitude(v[r][e]);
-                    m[r] = larger(m[r], x);
-                    mc[e] = larger(mc[e], x);
-                }
+                for (int e = 2; e < 8; e += 2) m[r] = larger(larger(v[r][e], v[r][e + 1]), m[r]);
+            }
             Scale of_block;
             if constexpr (BLOCK) {
-                uint32_t all = m[0];
+                float most = m[0];
 #pragma unroll
-                for (int r = 1; r < R; ++r) all = larger(all, m[r]);
-                all = over_lanes<64>(all, larger);
+                for (int r = 1; r < R; ++r) most = larger(most, m[r]);
+                uint32_t all = over_lanes<64>(__float_as_uint(most), max_bits);
                 if ((threadIdx.x & 63) == 0) top[wave][0] = all;
                 __syncthreads();
 #pragma unroll
@@ -249,17 +251,22 @@ __global__ void __launch_bounds__(2048 / R) moe_quantize_tile(QuantArgs a) {
                     if (a.qt) a.qt_sf[(int64_t)b * row_blocks + rb] = of_block.sf;
                 }
             } else {
+                uint32_t bits[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    auto p = __builtin_amdgcn_permlane16_swap(mc[e], mc[e], false, false);
-                    mc[e] = larger(p[0], p[1]);
-                    p = __builtin_amdgcn_permlane32_swap(mc[e], mc[e], false, false);
-                    mc[e] = larger(p[0], p[1]);
+                    mc[e] = larger(v[0][e], v[1][e]);
+#pragma unroll
+                    for (int r = 2; r < R; r += 2) mc[e] = larger(larger(v[r][e], v[r + 1][e]), mc[e]);
+                    bits[e] = __float_as_uint(mc[e]);
+                    auto p = __builtin_amdgcn_permlane16_swap(bits[e], bits[e], false, false);
+                    bits[e] = larger(p[0], p[1]);
+                    p = __builtin_amdgcn_permlane32_swap(bits[e], bits[e], false, false);
+                    bits[e] = larger(p[0], p[1]);
                 }
                 if ((threadIdx.x & 63) < 16) {
 #pragma unroll
                     for (int e = 0; e < 8; e += 4)
-                        *reinterpret_cast<u32x4_t*>(&top[wave][lane * 8 + e]) = u32x4_t{mc[e], mc[e + 1], mc[e + 2], mc[e + 3]};
+                        *reinterpret_cast<u32x4_t*>(&top[wave][lane * 8 + e]) = u32x4_t{bits[e], bits[e + 1], bits[e + 2], bits[e + 3]};
                 }
                 __syncthreads();
                 if (threadIdx.x < 128) {
@@ -268,37 +275,53 @@ __global__ void __launch_bounds__(2048 / R) moe_quantize_tile(QuantArgs a) {
                     for (int w = 1; w < WAVES; ++w) x = larger(x, top[w][threadIdx.x]);
                     const Scale s(x);
                     a.qt_sf[(row0 + threadIdx.x) * row_blocks + rb] = s.sf;
-                    col_up[threadIdx.x] = s.up, col_d[threadIdx.x] = s.d, col_inv[threadIdx.x] = s.inv;
+                    col_up[threadIdx.x] = s.up, col_hi[threadIdx.x] = s.hi, col_lo[threadIdx.x] = s.lo;
+                    const bool tiny = __any(s.up != 1.0f);
+                    if ((threadIdx.x & 63) == 0) col_tiny[wave] = tiny;
                 }
             }
             if (a.q) {
                 Scale mine = of_block;
                 if constexpr (!BLOCK) {
+                    uint32_t bits[R];
 #pragma unroll
-                    for (int r = 0; r < R; ++r) m[r] = over_lanes<16>(m[r], larger);
-                    uint32_t own = lane & 1 ? m[1] : m[0];
-                    if constexpr (R == 4) own = lane & 2 ? (lane & 1 ? m[3] : m[2]) : own;
+                    for (int r = 0; r < R; ++r) bits[r] = over_lanes<16>(__float_as_uint(m[r]), max_bits);
+                    uint32_t own = lane & 1 ? bits[1] : bits[0];
+                    if constexpr (R == 4) own = lane & 2 ? (lane & 1 ? bits[3] : bits[2]) : own;
                     mine = Scale(own);
                     if (lane < R && t0 + lane < a.T) a.q_sf[((t0 + lane) * OUTS + which) * blocks + b] = mine.sf;
                 }
+                const auto row_codes = [&](auto tiny) {
+                    constexpr bool TINY = decltype(tiny)::value;
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    const Scale s = r == 0 ? mine.of_quad<0>() : r == 1 ? mine.of_quad<1>() : r == 2 ? mine.of_quad<2>() : mine.of_quad<3>();
-                    const uint2 d = {s.codes(v[r][0], v[r][1], v[r][2], v[r][3]), s.codes(v[r][4], v[r][5], v[r][6], v[r][7])};
-                    if (t0 + r < a.T) *reinterpret_cast<uint2*>(a.q + ((t0 + r) * OUTS + which) * a.C + col) = d;
-                }
+                    for (int r = 0; r < R; ++r) {
+                        const Scale s = r == 0 ? mine.of_quad<0>() : r == 1 ? mine.of_quad<1>() : r == 2 ? mine.of_quad<2>() : mine.of_quad<3>();
+                        const uint2 d = {s.codes<TINY>(v[r][0], v[r][1], v[r][2], v[r][3]), s.codes<TINY>(v[r][4], v[r][5], v[r][6], v[r][7])};
+                        if (t0 + r < a.T) *reinterpret_cast<uint2*>(a.q + ((t0 + r) * OUTS + which) * a.C + col) = d;
+                    }
+                };
+                if (__any(mine.up != 1.0f)) row_codes(std::true_type());
+                else row_codes(std::false_type());
             }
             if (a.qt) {
                 if (!BLOCK) __syncthreads();
+                const auto column_codes = [&](auto tiny) {
+                    constexpr bool TINY = decltype(tiny)::value;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    Scale s = of_block;
-                    if (!BLOCK) s.up = col_up[lane * 8 + e], s.d = col_d[lane * 8 + e], s.inv = col_inv[lane * 8 + e];
-                    // the 16 bytes of a row lie at chunk ^ (column / 8 % 8)
-                    uint8_t* to = turned + (lane * 8 + e) * 128 + ((group * R) ^ ((lane & 7) * 16));
-                    if constexpr (R == 4) *reinterpret_cast<uint32_t*>(to) = s.codes(v[0][e], v[1][e], v[2][e], v[R - 1][e]);
-                    else *reinterpret_cast<uint16_t*>(to) = (uint16_t)s.codes(v[0][e], v[1][e], 0.0f, 0.0f);
-                }
+                    for (int e = 0; e < 8; ++e) {
+                        Scale s = of_block;
+                        if constexpr (!BLOCK) {
+                            s.hi = col_hi[lane * 8 + e], s.lo = col_lo[lane * 8 + e];
+                            if constexpr (TINY) s.up = col_up[lane * 8 + e];
+                        }
+                        // the 16 bytes of a row lie at chunk ^ (column / 8 % 8)
+                        uint8_t* to = turned + (lane * 8 + e) * 128 + ((group * R) ^ ((lane & 7) * 16));
+                        if constexpr (R == 4) *reinterpret_cast<uint32_t*>(to) = s.codes<TINY>(v[0][e], v[1][e], v[2][e], v[R - 1][e]);
+                        else *reinterpret_cast<uint16_t*>(to) = (uint16_t)__builtin_amdgcn_cvt_pk_fp8_f32(s.quotient<TINY>(v[0][e]), s.quotient<TINY>(v[1][e]), 0, false);
+                    }
+                };
+                if (BLOCK ? of_block.up != 1.0f : (col_tiny[0] | col_tiny[1]) != 0) column_codes(std::true_type());
+                else column_codes(std::false_type());
                 __syncthreads();
 #pragma unroll
                 for (int i = 0; i < R / 2; ++i) {

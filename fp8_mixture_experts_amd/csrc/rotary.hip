@@ -9,7 +9,9 @@ namespace mega_moe {
 
 namespace {
 
-constexpr int THREADS = 256;
+constexpr int THREADS = 256;             // of the forward kernel
+constexpr int BACK_THREADS = 1024;       // of the backward kernel: few workgroups leave few sums
+constexpr int BACK_BLOCKS = 256;         // one to a compute unit
 constexpr double INV_2PI = 0.15915494309189533577;
 
 // cos and sin of position * inv_freq, times scale.  The angle in turns is taken
@@ -68,16 +70,48 @@ struct Heads {
     }
 };
 
-template <typename Args>
+template <int NT, typename Args>
 __device__ __forceinline__ void fill_turns(const Args& a, float2* cs, int64_t t0, int tokens) {
     const int half = a.rotary_dim / 2;
     const float scale = a.scale == 0.0f ? 1.0f : a.scale;
-    for (int i = threadIdx.x; i < tokens * half; i += THREADS) {
+    for (int i = threadIdx.x; i < tokens * half; i += NT) {
         const int t = i / half;
         const int p = a.positions ? a.positions[t0 + t] : a.first_position + (int)(t0 + t);
         cs[i] = turn(p, a.inv_freq[i - t * half], scale);
     }
 }
+
+// One head of one token: a group's item, and the one `by` items on.
+struct Item {
+    int t, head, heads, by_t, by_head;
+    __device__ Item(int first, int by, int heads_) : heads(heads_) {
+        t = first / heads, head = first - t * heads;
+        by_t = by / heads, by_head = by - by_t * heads;
+    }
+    __device__ __forceinline__ void next() {
+        t += by_t, head += by_head;
+        if (head >= heads) head -= heads, ++t;
+    }
+};
+
+// A tensor of heads.
+struct Rows {
+    const void* p;
+    int64_t token, head;
+    __device__ __forceinline__ int64_t at(int64_t t, int h, int col) const { return t * token + h * head + col; }
+};
+
+// Eight columns as they lie in memory.
+template <bool F32>
+struct Raw {
+    static constexpr int N = F32 ? 2 : 1;
+    u32x4_t d[N];
+    __device__ __forceinline__ void load(bool live, const Rows& rows, int64_t t, int head, int col) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) d[n] = live ? raw8<F32>(rows.p, rows.at(t, head, col))[n] : u32x4_t{0u, 0u, 0u, 0u};
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const { values8<F32>(d, v); }
+};
 
 // LANES lanes hold a head of up to 8 LANES columns.
 int lanes_of(int D) { return D <= 64 ? 8 : D <= 128 ? 16 : D <= 256 ? 32 : 64; }
@@ -85,125 +119,127 @@ int lanes_of(int D) { return D <= 64 ? 8 : D <= 128 ? 16 : D <= 256 ? 32 : 64; }
 }  // namespace
 
 // A workgroup takes `tokens` tokens and, of their heads, every gridDim.y-th
-// round of 256 / LANES; q's heads come first, then k's.
+// round of 256 / LANES: q's, then k's.  Eight workgroups to a compute unit keep the
+// memory busy: with the next round's loads in flight in each, whose registers
+// leave room for seven, 49 us against 38 (8192 tokens of 32 + 8 heads of 128).
 template <bool F32, int LANES>
 __global__ void __launch_bounds__(THREADS) moe_rotary(mega_moe_rotary_args a, int tokens) {
     extern __shared__ float2 turns[];
     constexpr int G = THREADS / LANES;
     const int64_t t0 = (int64_t)blockIdx.x * tokens;
-    const int n = (int)min((int64_t)tokens, a.num_tokens - t0);
-    const int heads = a.q_heads + a.k_heads;
+    const int n = (int)min((int64_t)tokens, a.num_tokens - t0), by = gridDim.y * G;
     const Heads<LANES, mega_moe_rotary_args> h(a, turns);
-    float wq[8] = {}, wk[8] = {};
-    if (h.in && a.q_weight) load8(a.q_weight, a.weight_type, h.col, wq);
-    if (h.in && a.k_weight) load8(a.k_weight, a.weight_type, h.col, wk);
-    fill_turns(a, turns, t0, n);
+    fill_turns<THREADS>(a, turns, t0, n);
     __syncthreads();
     const float inv_d = 1.0f / (float)a.head_dim;
-    for (int first = blockIdx.y * G; first < n * heads; first += gridDim.y * G) {
-        const int item = first + threadIdx.x / LANES;
-        const int t = item / heads, head = item - t * heads;
-        const bool q = head < a.q_heads, live = item < n * heads && h.in;
-        const int hh = q ? head : head - a.q_heads;
-        float v[8] = {};
-        if (live) {
-            if (q) load8<F32>(a.q, (t0 + t) * a.q_stride + hh * a.q_head_stride + h.col, v);
-            else load8<F32>(a.k, (t0 + t) * a.k_stride + hh * a.k_head_stride + h.col, v);
-        }
-        float s = 0.0f;
+    const auto run = [&](int heads, const Rows& in, const Rows& out, const void* weight) {
+        if (heads == 0) return;
+        float w[8] = {};
+        if (h.in && weight) load8(weight, a.weight_type, h.col, w);
+        Item at(blockIdx.y * G + threadIdx.x / LANES, by, heads);
+        for (int first = blockIdx.y * G; first < n * heads; first += by, at.next()) {
+            const bool live = at.t < n && h.in;
+            Raw<F32> raw;
+            raw.load(live, in, t0 + at.t, at.head, h.col);
+            float v[8], s = 0.0f;
+            raw.get(v);
+            if (weight) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s += v[i] * v[i];
-        s = lanes_sum<LANES>(s);
-        if (q ? a.q_weight != nullptr : a.k_weight != nullptr) {
-            const float rs = rsqrtf(s * inv_d + a.eps);
+                for (int i = 0; i < 8; ++i) s += v[i] * v[i];
+                const float rs = rsqrtf(lanes_sum<LANES>(s) * inv_d + a.eps);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = v[i] * rs * (q ? wq[i] : wk[i]);
+                for (int i = 0; i < 8; ++i) v[i] = v[i] * rs * w[i];
+            }
+            h.template rotate<false>(at.t < n ? at.t : 0, v);
+            if (live) store8<F32>(const_cast<void*>(out.p), out.at(t0 + at.t, at.head, h.col), v);
         }
-        h.template rotate<false>(item < n * heads ? t : 0, v);
-        if (live) {
-            if (q) store8<F32>(a.q_out, (t0 + t) * a.q_out_stride + hh * a.q_out_head_stride + h.col, v);
-            else store8<F32>(a.k_out, (t0 + t) * a.k_out_stride + hh * a.k_out_head_stride + h.col, v);
-        }
-    }
+    };
+    run(a.q_heads, Rows{a.q, a.q_stride, a.q_head_stride}, Rows{a.q_out, a.q_out_stride, a.q_out_head_stride}, a.q_weight);
+    run(a.k_heads, Rows{a.k, a.k_stride, a.k_head_stride}, Rows{a.k_out, a.k_out_stride, a.k_out_head_stride}, a.k_weight);
 }
 
-// Gradients: a workgroup goes from one run of tokens to the next and keeps its
-// sums over tokens and heads, those of q and of k, in registers; at the end its
-// groups meet in LDS and its sums go to the workspace, [grid][sums][D].
+// Gradients: a workgroup goes from one run of tokens to the next (of their heads it
+// takes every gridDim.y-th round).  Its sums over tokens and heads lie in LDS, a place
+// for each thread, and in registers during a run; at the end the groups' meet
+// in order and the workgroup's go to the workspace, [grid][sums][D].  The next round's loads
+// are in flight over the two sums of a head.
 template <bool F32, int LANES>
-__global__ void __launch_bounds__(THREADS) moe_rotary_backward(mega_moe_rotary_backward_args a, float* ws, int tokens) {
+__global__ void __launch_bounds__(BACK_THREADS) moe_rotary_backward(mega_moe_rotary_backward_args a, float* ws, int tokens) {
     extern __shared__ float2 turns[];
-    constexpr int G = THREADS / LANES;
-    const int heads = a.q_heads + a.k_heads;
+    constexpr int G = BACK_THREADS / LANES;
+    __shared__ __attribute__((aligned(16))) float part[2][BACK_THREADS][8];
+    const int by = gridDim.y * G;
     const Heads<LANES, mega_moe_rotary_backward_args> h(a, turns);
-    float wq[8] = {}, wk[8] = {}, sq[8] = {}, sk[8] = {};
-    if (h.in && a.q_weight) load8(a.q_weight, a.weight_type, h.col, wq);
-    if (h.in && a.k_weight) load8(a.k_weight, a.weight_type, h.col, wk);
     const float inv_d = 1.0f / (float)a.head_dim;
+    {
+        const float zero[8] = {};
+        store8<true>(part[0][threadIdx.x], 0, zero);
+        store8<true>(part[1][threadIdx.x], 0, zero);
+    }
     for (int64_t t0 = (int64_t)blockIdx.x * tokens; t0 < a.num_tokens; t0 += (int64_t)gridDim.x * tokens) {
         const int n = (int)min((int64_t)tokens, a.num_tokens - t0);
-        fill_turns(a, turns, t0, n);
+        fill_turns<BACK_THREADS>(a, turns, t0, n);
         __syncthreads();
-        for (int first = 0; first < n * heads; first += G) {
-            const int item = first + threadIdx.x / LANES;
-            const int t = item / heads, head = item - t * heads;
-            const bool q = head < a.q_heads, live = item < n * heads && h.in;
-            const bool normed = q ? a.q_weight != nullptr : a.k_weight != nullptr;
-            const int hh = q ? head : head - a.q_heads;
-            float u[8] = {}, x[8] = {};
-            if (live) {
-                if (q) load8<F32>(a.dq_out, (t0 + t) * a.dq_out_stride + hh * a.dq_out_head_stride + h.col, u);
-                else load8<F32>(a.dk_out, (t0 + t) * a.dk_out_stride + hh * a.dk_out_head_stride + h.col, u);
-                if (normed) {
-                    if (q) load8<F32>(a.q, (t0 + t) * a.q_stride + hh * a.q_head_stride + h.col, x);
-                    else load8<F32>(a.k, (t0 + t) * a.k_stride + hh * a.k_head_stride + h.col, x);
-                }
-            }
-            h.template rotate<true>(item < n * heads ? t : 0, u);
-            float s = 0.0f, p = 0.0f;
+#pragma unroll 1
+        for (int side = 0; side < 2; ++side) {
+            const bool q = side == 0;
+            const int heads = q ? a.q_heads : a.k_heads;
+            if (heads == 0) continue;
+            const Rows in = q ? Rows{a.q, a.q_stride, a.q_head_stride} : Rows{a.k, a.k_stride, a.k_head_stride};
+            const Rows dout = q ? Rows{a.dq_out, a.dq_out_stride, a.dq_out_head_stride} : Rows{a.dk_out, a.dk_out_stride, a.dk_out_head_stride};
+            const Rows dx = q ? Rows{a.dq, a.dq_stride, a.dq_head_stride} : Rows{a.dk, a.dk_stride, a.dk_head_stride};
+            const void* weight = q ? a.q_weight : a.k_weight;
+            float w[8] = {}, sum[8];
+            if (h.in && weight) load8(weight, a.weight_type, h.col, w);
+            load8<true>(part[side][threadIdx.x], 0, sum);
+            Item at(blockIdx.y * G + threadIdx.x / LANES, by, heads);
+            Raw<F32> raw_u, raw_x;
+            const auto fetch = [&]() {
+                const bool live = at.t < n && h.in;
+                raw_u.load(live, dout, t0 + at.t, at.head, h.col);
+                raw_x.load(live && weight, in, t0 + at.t, at.head, h.col);
+            };
+            fetch();
+            for (int first = blockIdx.y * G; first < n * heads; first += by) {
+                const int t = at.t, head = at.head;
+                const bool live = t < n && h.in;
+                float u[8], x[8];
+                raw_u.get(u);
+                raw_x.get(x);
+                at.next();
+                if (first + by < n * heads) fetch();
+                h.template rotate<true>(t < n ? t : 0, u);
+                if (weight) {
+                    float s = 0.0f, p = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                s += x[i] * x[i];
-                p += u[i] * (q ? wq[i] : wk[i]) * x[i];
-            }
-            s = lanes_sum<LANES>(s);
-            p = lanes_sum<LANES>(p);
-            if (normed) {
-                const float rs = rsqrtf(s * inv_d + a.eps);
-                const float mean = p * rs * inv_d;           // of u * weight * xh
+                    for (int i = 0; i < 8; ++i) {
+                        s += x[i] * x[i];
+                        p += u[i] * w[i] * x[i];
+                    }
+                    const float rs = rsqrtf(lanes_sum<LANES>(s) * inv_d + a.eps);
+                    const float mean = lanes_sum<LANES>(p) * rs * inv_d;     // of u * weight * xh
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float xh = x[i] * rs, g = u[i] * xh;
-                    // a lane or a group that is out has u = 0, but xh may be infinite
-                    if (live && q) sq[i] += g;
-                    if (live && !q) sk[i] += g;
-                    u[i] = rs * (u[i] * (q ? wq[i] : wk[i]) - xh * mean);
+                    for (int i = 0; i < 8; ++i) {
+                        const float xh = x[i] * rs;
+                        // a lane or a group that is out has u = 0, but xh may be infinite
+                        if (live) sum[i] += u[i] * xh;
+                        u[i] = rs * (u[i] * w[i] - xh * mean);
+                    }
                 }
+                if (live) store8<F32>(const_cast<void*>(dx.p), dx.at(t0 + t, head, h.col), u);
             }
-            if (live) {
-                if (q) store8<F32>(a.dq, (t0 + t) * a.dq_stride + hh * a.dq_head_stride + h.col, u);
-                else store8<F32>(a.dk, (t0 + t) * a.dk_stride + hh * a.dk_head_stride + h.col, u);
-            }
+            store8<true>(part[side][threadIdx.x], 0, sum);
         }
         __syncthreads();
     }
-    // the groups' sums meet in LDS, in order
-    __shared__ float part[G][LANES * 8];
-    int k = 0;
-    const auto put = [&](const float (&s)[8]) {
-        store8<true>(&part[threadIdx.x / LANES][0], (size_t)(threadIdx.x & (LANES - 1)) * 8, s);
-        __syncthreads();
-        for (int c = threadIdx.x; c < a.head_dim; c += THREADS) {
-            float o = 0.0f;
-#pragma unroll
-            for (int g = 0; g < G; ++g) o += part[g][c];
-            ws[((size_t)blockIdx.x * rotary_sums(a) + k) * a.head_dim + c] = o;
-        }
-        __syncthreads();
-        ++k;
-    };
-    if (a.dq_weight) put(sq);
-    if (a.dk_weight) put(sk);
+    __syncthreads();
+    for (int i = threadIdx.x; i < rotary_sums(a) * a.head_dim; i += BACK_THREADS) {
+        const int k = i / a.head_dim, c = i - k * a.head_dim, side = a.dq_weight ? k : 1;
+        float o = 0.0f;
+#pragma unroll 16
+        for (int g = 0; g < G; ++g) o += part[side][g * LANES + c / 8][c & 7];
+        ws[(size_t)(blockIdx.y * gridDim.x + blockIdx.x) * rotary_sums(a) * a.head_dim + i] = o;
+    }
 }
 
 // Adds the workgroups' sums: a workgroup has 16 of the sums' columns, its 64
@@ -215,7 +251,7 @@ moe_rotary_reduce(const float* ws, float* out0, float* out1, int D, int sums, in
     const int col = blockIdx.x * 16 + lane;              // of sums * D
     float s = 0.0f;
     if (col < sums * D) {
-#pragma unroll 4
+#pragma unroll 16
         for (int i = group; i < rows; i += 64) s += ws[(size_t)i * sums * D + col];
     }
     part[group][lane] = s;
@@ -250,15 +286,29 @@ void by_lanes(const Args& a, F go) {
     }
 }
 
-constexpr int BACKWARD_BLOCKS = 1024;
+// The runs of tokens of the backward kernel: as long as leave every compute unit one,
+// with their turns in 32 KB of LDS.
+int back_tokens(const mega_moe_rotary_backward_args& a) {
+    const int most = a.rotary_dim > 0 ? 8192 / a.rotary_dim : 64;
+    const int n = (a.num_tokens + BACK_BLOCKS - 1) / BACK_BLOCKS;
+    return n < 1 ? 1 : n < most ? n : most;
+}
+
+// Its grid; few tokens: their heads over several workgroups.
+dim3 back_grid(const mega_moe_rotary_backward_args& a) {
+    const int tokens = back_tokens(a), need = (a.num_tokens + tokens - 1) / tokens;
+    const int blocks = need < BACK_BLOCKS ? need : BACK_BLOCKS, G = BACK_THREADS / lanes_of(a.head_dim);
+    const int rounds = (tokens * (a.q_heads + a.k_heads) + G - 1) / G, split = blocks > 0 ? BACK_BLOCKS / blocks : 1;
+    return dim3((unsigned)blocks, (unsigned)(split < rounds ? split : rounds));
+}
 
 }  // namespace
 
 void launch_rotary(const mega_moe_rotary_args& a, hipStream_t stream) {
-    const int tokens = tokens_of(a.num_tokens, a.rotary_dim), G = THREADS / lanes_of(a.head_dim);
+    const int tokens = tokens_of(a.num_tokens, a.rotary_dim);
     const int blocks = (a.num_tokens + tokens - 1) / tokens;
     // few tokens: their heads over several workgroups
-    const int rounds = (tokens * (a.q_heads + a.k_heads) + G - 1) / G;
+    const int G = THREADS / lanes_of(a.head_dim), rounds = (tokens * (a.q_heads + a.k_heads) + G - 1) / G;
     int split = (1024 + blocks - 1) / blocks;
     if (split > rounds) split = rounds;
     const unsigned lds = (unsigned)(tokens * a.rotary_dim * 4);
@@ -273,20 +323,19 @@ void launch_rotary(const mega_moe_rotary_args& a, hipStream_t stream) {
 }
 
 int rotary_backward_blocks(const mega_moe_rotary_backward_args& a) {
-    const int tokens = tokens_of(a.num_tokens, a.rotary_dim);
-    const int need = (a.num_tokens + tokens - 1) / tokens;
-    return need < BACKWARD_BLOCKS ? need : BACKWARD_BLOCKS;
+    const dim3 g = back_grid(a);
+    return (int)(g.x * g.y);
 }
 
 void launch_rotary_backward(const mega_moe_rotary_backward_args& a, hipStream_t stream) {
-    const int tokens = tokens_of(a.num_tokens, a.rotary_dim), blocks = rotary_backward_blocks(a);
+    const int tokens = back_tokens(a), blocks = rotary_backward_blocks(a);
     const unsigned lds = (unsigned)(tokens * a.rotary_dim * 4);
     float* ws = static_cast<float*>(a.workspace);
     if (blocks > 0) {
         const auto go = [&](auto f32) {
             by_lanes<decltype(f32)::value>(a, [&](auto lanes) {
-                hipLaunchKernelGGL((moe_rotary_backward<decltype(f32)::value, decltype(lanes)::value>), dim3((unsigned)blocks),
-                                   dim3(THREADS), lds, stream, a, ws, tokens);
+                hipLaunchKernelGGL((moe_rotary_backward<decltype(f32)::value, decltype(lanes)::value>), back_grid(a),
+                                   dim3(BACK_THREADS), lds, stream, a, ws, tokens);
             });
         };
         if (a.type == MEGA_MOE_F32) go(std::true_type());
