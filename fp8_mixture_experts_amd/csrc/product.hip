@@ -50,9 +50,14 @@ __device__ __forceinline__ void load4_lds(__amdgpu_buffer_rsrc_t r, uint8_t* lds
 }
 
 // A stage's rows are 128 bytes; their 16-byte chunk c lies at c ^ turn(row), so
-// that a load instruction covers eight whole rows and the 32 rows of a matrix
-// operand meet distinct banks.
-__device__ __forceinline__ int turn(int row) { return (row & 7) ^ ((row >> 3) & 1); }
+// that a load instruction covers eight whole rows and an operand's reads meet
+// distinct banks. A wave's 16-byte reads are served 16 lanes at a time, lanes 0-3, 12-15,
+// 20-27 and then 4-11, 16-19, 28-31 of each half: rows 0-3 and 12-15 of one chunk go with
+// rows 4-11 of the next, so that these have the upper four places of their chunk and those the lower
+// four. (With row ^ row / 8 % 2 half of the reads' cycles were conflicts.)
+__device__ __forceinline__ int turn(int row) {
+    return (((row >> 2) ^ (row >> 3)) & 1) << 2 | ((row >> 3) & 1) << 1 | ((row >> 1) & 1);
+}
 
 // The operand of 16 rows (slice s) of a step: lane r + 16 g has row r, chunks g and
 // g + 4 (alike for a and b).  Every read of a stage is one of integers: of other types the
@@ -148,9 +153,9 @@ __device__ __forceinline__ int in_order(int id, int total) {
 // a result (16 of a slice) and register v column 4 (lane / 16) + v: the scale of
 // a's row is one value for a lane.
 //
-// A round's barrier lies before its last column of blocks, whose operands are in
+// A round's barrier lies before its last two columns of blocks, whose operands are in
 // registers by then: behind it the round's place in LDS is free for new loads,
-// and the next round's operands are read while the matrix unit has that column.
+// and the next round's operands are read while the matrix unit has those columns.
 template <typename T, bool EXACT, bool ROWS>
 __global__ void __launch_bounds__(T::NT) moe_product(ProductArgs p) {
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
@@ -188,20 +193,22 @@ __global__ void __launch_bounds__(T::NT) moe_product(ProductArgs p) {
     const int voff_sfa = (w * T::A_SF + min(lane, T::A_SF - 1)) * (int)p.a_sf_stride * 4;
     const int voff_sfb = (w * T::B_SF + min(lane, T::B_SF - 1)) * (int)p.b_sf_stride * 4;
 
-    // The loads of the group's step of a round; past the last step the same number of
+    // Load `part` (of LOADS) of the group's step of a round; past the last step the same
     // instructions, on buffers of no bytes: LDS gets zeros.
-    const auto issue = [&](int place, int round) {
+    const auto issue = [&](int place, int round, int part) {
         uint8_t* stage = lds + place + group * STAGE;
         const int step = round * T::WK + group;
         const uint32_t real = step < steps ? ~0u : 0u;
-        const __amdgpu_buffer_rsrc_t ra = buffer(a0, bytes_a & real), rb = buffer(b0, bytes_b & real);
-#pragma unroll
-        for (int j = 0; j < T::A_LOADS; ++j) load16_lds(ra, stage + (T::NW * j + w) * 1024, voff_a + j * jump_a, step * BK);
-#pragma unroll
-        for (int j = 0; j < T::B_LOADS; ++j)
-            load16_lds(rb, stage + T::OFF_B + (T::NW * j + w) * 1024, voff_b + j * jump_b, step * BK);
-        load4_lds(buffer(a_sf0, bytes_sfa & real), stage + T::OFF_SFA + w * 256, voff_sfa, step * 4);
-        if constexpr (ROWS) load4_lds(buffer(b_sf0, bytes_sfb & real), stage + T::OFF_SFB + w * 256, voff_sfb, step * 4);
+        if (part < T::A_LOADS) {
+            load16_lds(buffer(a0, bytes_a & real), stage + (T::NW * part + w) * 1024, voff_a + part * jump_a, step * BK);
+        } else if (part < T::A_LOADS + T::B_LOADS) {
+            const int j = part - T::A_LOADS;
+            load16_lds(buffer(b0, bytes_b & real), stage + T::OFF_B + (T::NW * j + w) * 1024, voff_b + j * jump_b, step * BK);
+        } else if (part == T::A_LOADS + T::B_LOADS) {
+            load4_lds(buffer(a_sf0, bytes_sfa & real), stage + T::OFF_SFA + w * 256, voff_sfa, step * 4);
+        } else if constexpr (ROWS) {
+            load4_lds(buffer(b_sf0, bytes_sfb & real), stage + T::OFF_SFB + w * 256, voff_sfb, step * 4);
+        }
     };
 
     // b's block of scales: one for the wave (tiles start and end with blocks, or within one)
@@ -239,16 +246,21 @@ __global__ void __launch_bounds__(T::NT) moe_product(ProductArgs p) {
 
     if (steps > 0) {
 #pragma unroll
-        for (int i = 0; i < S; ++i) issue(i * ROUND, i);
+        for (int i = 0; i < S; ++i)
+#pragma unroll
+            for (int part = 0; part < LOADS; ++part) issue(i * ROUND, i, part);
         asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((S - 1) * LOADS) : "memory");
         int place = 0, step = group;
         float sa[T::SM], sb = block_scale(step);
-        i32x8_t x_raw[T::SM], y_raw = operand(lds + at_y, 0);
+        i32x8_t x_raw[T::SM], y_raw[2] = {operand(lds + at_y, 0), operand(lds + at_y, 1)};
+        i32x4_t cs_next[2] = {};
+        if constexpr (ROWS) cs_next[0] = column_scales(0, 0), cs_next[1] = column_scales(0, 1);
 #pragma unroll
         for (int i = 0; i < T::SM; ++i) {
             x_raw[i] = operand(lds + at_x, i);
             sa[i] = row_scale(0, i);
         }
+        static_assert(T::SN >= 2, "two columns are read ahead");
         for (int round = 0; round < rounds; ++round, step += T::WK) {
             const int next = place + ROUND == S * ROUND ? 0 : place + ROUND;
             // while the matrix unit has the next blocks, those before them are added: EXACT by whole
@@ -256,34 +268,41 @@ __global__ void __launch_bounds__(T::NT) moe_product(ProductArgs p) {
             constexpr int BEHIND = EXACT ? T::SM : 3, RING = EXACT ? 2 * T::SM : 4, BLOCKS = T::SN * T::SM;
             f32x4_t d[RING];
             float s[T::SM];
-            i32x4_t cs[2];
+            i32x4_t cs[T::SN + 2];
+            cs[0] = cs_next[0], cs[1] = cs_next[1];
             const auto add_block = [&](int n) {
                 const int j = n / T::SM, i = n % T::SM;
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    acc[j][i][e] = fmaf(d[n % RING][e], ROWS ? s[i] * __int_as_float(cs[j & 1][e]) : s[i], acc[j][i][e]);
+                    acc[j][i][e] = fmaf(d[n % RING][e], ROWS ? s[i] * __int_as_float(cs[j][e]) : s[i], acc[j][i][e]);
             };
 #pragma unroll
             for (int i = 0; i < T::SM; ++i) s[i] = sa[i] * sb;
+            sb = block_scale(step + T::WK);
             Ready<EXACT> x[T::SM];
 #pragma unroll
             for (int i = 0; i < T::SM; ++i) x[i] = Ready<EXACT>(x_raw[i]);
 #pragma unroll
             for (int j = 0; j < T::SN; ++j) {
-                const Ready<EXACT> y(y_raw);
-                if constexpr (ROWS) cs[j & 1] = column_scales(place, j);
-                if (j + 1 < T::SN) {
-                    y_raw = operand(lds + place + at_y, j + 1);
-                } else {
-                    meet();
-                    issue(place, round + S);
-                    sb = block_scale(step + T::WK);
-                    y_raw = operand(lds + next + at_y, 0);
-                }
+                const Ready<EXACT> y(y_raw[0]);
+                // the round's last reads were those of two columns ahead
+                if (j == T::SN - 2) meet();
+                const int from = j + 2 < T::SN ? place : next, ahead = (j + 2) % T::SN;
+                y_raw[0] = y_raw[1];
+                y_raw[1] = operand(lds + from + at_y, ahead);
+                if constexpr (ROWS) cs[j + 2] = column_scales(from, ahead);
+                // The new loads one by one between the last columns' instructions: one after the other they
+                // would hold up every wave for as long as the loads take.
+                constexpr int SLOTS = 2 * T::SM * Ready<EXACT>::N, PER = (LOADS + SLOTS - 1) / SLOTS;
+                const auto load_some = [&](int slot) {
+#pragma unroll
+                    for (int part = slot * PER; part < (slot + 1) * PER && part < LOADS; ++part) issue(place, round + S, part);
+                };
                 const auto read_next = [&](int i) {
                     x_raw[i] = operand(lds + next + at_x, i);
                     sa[i] = row_scale(next, i);
                 };
+                const int last = j - (T::SN - 2);                // 0 and 1: the columns behind the barrier
                 if constexpr (EXACT) {
 #pragma unroll
                     for (int q = 0; q < Ready<EXACT>::N; ++q)
@@ -291,6 +310,11 @@ __global__ void __launch_bounds__(T::NT) moe_product(ProductArgs p) {
                         for (int i = 0; i < T::SM; ++i) {
                             f32x4_t& o = d[(j * T::SM + i) % RING];
                             o = y.times(x[i], q, q == 0 ? f32x4_t{} : o);
+                            if (last >= 0) {
+                                __builtin_amdgcn_sched_barrier(0);
+                                load_some((last * Ready<EXACT>::N + q) * T::SM + i);
+                                __builtin_amdgcn_sched_barrier(0);
+                            }
                         }
                     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -305,6 +329,7 @@ __global__ void __launch_bounds__(T::NT) moe_product(ProductArgs p) {
                         const int n = j * T::SM + i;
                         d[n % RING] = y.times(x[i], 0, f32x4_t{});
                         __builtin_amdgcn_sched_barrier(0);
+                        if (last >= 0) load_some(last * T::SM + i);
                         if (j + 1 == T::SN) read_next(i);
                         if (n >= BEHIND) add_block(n - BEHIND);
                         __builtin_amdgcn_sched_barrier(0);
@@ -313,6 +338,7 @@ __global__ void __launch_bounds__(T::NT) moe_product(ProductArgs p) {
             }
 #pragma unroll
             for (int n = BLOCKS > BEHIND ? BLOCKS - BEHIND : 0; n < BLOCKS; ++n) add_block(n);
+            cs_next[0] = cs[T::SN], cs_next[1] = cs[T::SN + 1];
             place = next;
         }
     }
