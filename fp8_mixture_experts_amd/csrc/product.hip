@@ -125,6 +125,8 @@ struct Tile {
     static constexpr int at_sfb(int row) { return row / B_SF * 256 + row % B_SF * 4; }
     template <bool ROWS>
     static constexpr int loads() { return A_LOADS + B_LOADS + 1 + (ROWS ? 1 : 0); }
+    // two rounds of the widest tile fill LDS; each wave's first columns of b are the even blocks of loads
+    static constexpr bool EARLY = SN >= 8 && S == 2 && TN / 2 == 8 * NW;
     // results leave through LDS, PW columns of a wave at a time
     static constexpr int PW = TN < 64 ? TN : 64, PITCH = PW + 4;
     template <bool ROWS>
@@ -239,16 +241,30 @@ __global__ void __launch_bounds__(T::NT) moe_product(ProductArgs p) {
     const auto column_scales = [&](int place, int j) {
         return *reinterpret_cast<const i32x4_t*>(lds + place + at_sb + T::at_sfb(16 * j));
     };
+    // With wide tiles, whose two rounds fill LDS, what of a round's place is read first takes new loads half a
+    // round earlier: a's rows and scales, and the rows of b's first columns (loads 0, 2, .. of b).
+    constexpr bool EARLY = T::EARLY;
+    constexpr int FIRST = EARLY ? T::A_LOADS + T::B_LOADS / 2 + 1 : 0;
+    const auto order = [&](int n) {                      // of the loads
+        if (!EARLY) return n;
+        if (n < T::A_LOADS) return n;
+        if (n < FIRST - 1) return T::A_LOADS + 2 * (n - T::A_LOADS);
+        if (n == FIRST - 1) return T::A_LOADS + T::B_LOADS;
+        if (n < T::A_LOADS + T::B_LOADS + 1) return T::A_LOADS + 2 * (n - FIRST) + 1;
+        return n;
+    };
     // this wave's loads of the next round are there and its reads of this one done, then every wave's
     const auto meet = [&]() {
-        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((S - 2) * LOADS) : "memory");
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((S - 2) * LOADS + FIRST) : "memory");
     };
+    // the reads of a's rows and of b's first columns are done
+    const auto meet_early = [&]() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
 
     if (steps > 0) {
 #pragma unroll
         for (int i = 0; i < S; ++i)
 #pragma unroll
-            for (int part = 0; part < LOADS; ++part) issue(i * ROUND, i, part);
+            for (int n = 0; n < LOADS; ++n) issue(i * ROUND, i, order(n));
         asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((S - 1) * LOADS) : "memory");
         int place = 0, step = group;
         float sa[T::SM], sb = block_scale(step);
@@ -286,6 +302,7 @@ __global__ void __launch_bounds__(T::NT) moe_product(ProductArgs p) {
             for (int j = 0; j < T::SN; ++j) {
                 const Ready<EXACT> y(y_raw[0]);
                 // the round's last reads were those of two columns ahead
+                if (EARLY && j == 2) meet_early();
                 if (j == T::SN - 2) meet();
                 const int from = j + 2 < T::SN ? place : next, ahead = (j + 2) % T::SN;
                 y_raw[0] = y_raw[1];
@@ -293,16 +310,20 @@ __global__ void __launch_bounds__(T::NT) moe_product(ProductArgs p) {
                 if constexpr (ROWS) cs[j + 2] = column_scales(from, ahead);
                 // The new loads one by one between the last columns' instructions: one after the other they
                 // would hold up every wave for as long as the loads take.
-                constexpr int SLOTS = 2 * T::SM * Ready<EXACT>::N, PER = (LOADS + SLOTS - 1) / SLOTS;
+                // (the early ones over the four columns up to the second barrier's, the others over two)
+                const bool early = EARLY && j >= 2 && j < T::SN - 2, late = j >= T::SN - 2;
+                const int before = (early ? j - 2 : j - (T::SN - 2)) * T::SM * Ready<EXACT>::N;
                 const auto load_some = [&](int slot) {
+                    const int lo = early ? 0 : FIRST, hi = early ? FIRST : LOADS;
+                    const int slots = (early ? T::SN - 4 : 2) * T::SM * Ready<EXACT>::N;
 #pragma unroll
-                    for (int part = slot * PER; part < (slot + 1) * PER && part < LOADS; ++part) issue(place, round + S, part);
+                    for (int n = lo; n < hi; ++n)
+                        if ((n - lo) * slots / (hi - lo) == before + slot) issue(place, round + S, order(n));
                 };
                 const auto read_next = [&](int i) {
                     x_raw[i] = operand(lds + next + at_x, i);
                     sa[i] = row_scale(next, i);
                 };
-                const int last = j - (T::SN - 2);                // 0 and 1: the columns behind the barrier
                 if constexpr (EXACT) {
 #pragma unroll
                     for (int q = 0; q < Ready<EXACT>::N; ++q)
@@ -310,9 +331,9 @@ __global__ void __launch_bounds__(T::NT) moe_product(ProductArgs p) {
                         for (int i = 0; i < T::SM; ++i) {
                             f32x4_t& o = d[(j * T::SM + i) % RING];
                             o = y.times(x[i], q, q == 0 ? f32x4_t{} : o);
-                            if (last >= 0) {
+                            if (early || late) {
                                 __builtin_amdgcn_sched_barrier(0);
-                                load_some((last * Ready<EXACT>::N + q) * T::SM + i);
+                                load_some(q * T::SM + i);
                                 __builtin_amdgcn_sched_barrier(0);
                             }
                         }
@@ -329,7 +350,7 @@ __global__ void __launch_bounds__(T::NT) moe_product(ProductArgs p) {
                         const int n = j * T::SM + i;
                         d[n % RING] = y.times(x[i], 0, f32x4_t{});
                         __builtin_amdgcn_sched_barrier(0);
-                        if (last >= 0) load_some(last * T::SM + i);
+                        if (early || late) load_some(i);
                         if (j + 1 == T::SN) read_next(i);
                         if (n >= BEHIND) add_block(n - BEHIND);
                         __builtin_amdgcn_sched_barrier(0);
