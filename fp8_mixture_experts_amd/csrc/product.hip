@@ -114,30 +114,26 @@ struct Tile {
     static constexpr int NW = WM * WN, NT = 64 * NW * WK;  // NW: of a group
     static constexpr int TM = BM / WM, TN = BN / WN;       // a wave's
     static constexpr int SM = TM / 16, SN = TN / 16;
-    static constexpr int A_LOADS = BM / 8 / NW, B_LOADS = BN / 8 / NW;     // of 1 KB
-    static constexpr int A_SF = BM / NW, B_SF = BN / NW;   // scales that a wave loads, a lane each
-    static constexpr int OFF_B = BM * BK, OFF_SFA = OFF_B + BN * BK, OFF_SFB = OFF_SFA + NW * 256;
-    template <bool ROWS>
-    static constexpr int stage() { return OFF_SFB + (ROWS ? NW * 256 : 0); } // of a group
-    // A wave's scales lie in 256 bytes of LDS, the lanes behind A_SF (B_SF) repeating the
-    // last: masking them off would end the block of code that the compiler schedules as one.
-    static constexpr int at_sfa(int row) { return row / A_SF * 256 + row % A_SF * 4; }
-    static constexpr int at_sfb(int row) { return row / B_SF * 256 + row % B_SF * 4; }
-    template <bool ROWS>
-    static constexpr int loads() { return A_LOADS + B_LOADS + 1 + (ROWS ? 1 : 0); }
+    static constexpr int A_LOADS = BM / 8 / NW, B_LOADS = BN / 8 / NW;     // of 1 KB, of a wave and step
+    static constexpr int LOADS = A_LOADS + B_LOADS;
+    static constexpr int OFF_B = BM * BK, STAGE = OFF_B + BN * BK;         // of a group
+    static constexpr int ROUND = STAGE * WK;
+    // behind the rounds the scales of eight steps, twice: [row][step] of a, [8 rows][step][row] of b
+    static constexpr int OFF_SFA = S * ROUND, SFA = BM * 32, OFF_SFB = OFF_SFA + 2 * SFA, SFB = BN * 32;
     // two rounds of the widest tile fill LDS; each wave's first columns of b are the even blocks of loads
     static constexpr bool EARLY = SN >= 8 && S == 2 && TN / 2 == 8 * NW;
     // results leave through LDS, PW columns of a wave at a time
     static constexpr int PW = TN < 64 ? TN : 64, PITCH = PW + 4;
     template <bool ROWS>
     static constexpr int lds() {
-        const int a = S * WK * stage<ROWS>(), b = WK * NW * TM * PITCH * 4;
+        const int a = OFF_SFB + (ROWS ? 2 * SFB : 0), b = WK * NW * TM * PITCH * 4;
         return a > b ? a : b;
     }
-    static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && A_SF <= 64 && B_SF <= 64, "loads");
+    static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0, "loads");
     static_assert((8 * NW) % 16 == 0, "turn() is the same for a wave's rows");
-    static_assert(TM % A_SF == 0 && TN % B_SF == 0 && A_SF % 16 == 0 && B_SF % 16 == 0, "scales of a wave's rows");
     static_assert(TN == 128 || 128 % TN == 0, "one block of scales to a wave");
+    static_assert(SN >= 2, "two columns are read ahead");
+    static_assert(8 % WK == 0 && WK < 8, "scales of eight steps last for whole rounds, and two or more");
     static_assert(lds<true>() <= 160 * 1024, "LDS");
 };
 
@@ -161,7 +157,7 @@ __device__ __forceinline__ int in_order(int id, int total) {
 template <typename T, bool EXACT, bool ROWS>
 __global__ void __launch_bounds__(T::NT) moe_product(ProductArgs p) {
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-    constexpr int STAGE = T::template stage<ROWS>(), LOADS = T::template loads<ROWS>(), S = T::S, ROUND = STAGE * T::WK;
+    constexpr int S = T::S, LOADS = T::LOADS, ROUND = T::ROUND;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int group = wave / T::NW, w = wave % T::NW;
     const int wm = w / T::WN, wn = w % T::WN;
@@ -192,25 +188,37 @@ __global__ void __launch_bounds__(T::NT) moe_product(ProductArgs p) {
     const int voff_a = r8 * (int)p.a_stride + 16 * ((lane & 7) ^ turn(r8));
     const int voff_b = r8 * (int)p.b_stride + 16 * ((lane & 7) ^ turn(r8));
     const int jump_a = 8 * T::NW * (int)p.a_stride, jump_b = 8 * T::NW * (int)p.b_stride;
-    const int voff_sfa = (w * T::A_SF + min(lane, T::A_SF - 1)) * (int)p.a_sf_stride * 4;
-    const int voff_sfb = (w * T::B_SF + min(lane, T::B_SF - 1)) * (int)p.b_sf_stride * 4;
 
     // Load `part` (of LOADS) of the group's step of a round; past the last step the same
     // instructions, on buffers of no bytes: LDS gets zeros.
     const auto issue = [&](int place, int round, int part) {
-        uint8_t* stage = lds + place + group * STAGE;
+        uint8_t* stage = lds + place + group * T::STAGE;
         const int step = round * T::WK + group;
         const uint32_t real = step < steps ? ~0u : 0u;
         if (part < T::A_LOADS) {
             load16_lds(buffer(a0, bytes_a & real), stage + (T::NW * part + w) * 1024, voff_a + part * jump_a, step * BK);
-        } else if (part < T::A_LOADS + T::B_LOADS) {
+        } else {
             const int j = part - T::A_LOADS;
             load16_lds(buffer(b0, bytes_b & real), stage + T::OFF_B + (T::NW * j + w) * 1024, voff_b + j * jump_b, step * BK);
-        } else if (part == T::A_LOADS + T::B_LOADS) {
-            load4_lds(buffer(a_sf0, bytes_sfa & real), stage + T::OFF_SFA + w * 256, voff_sfa, step * 4);
-        } else if constexpr (ROWS) {
-            load4_lds(buffer(b_sf0, bytes_sfb & real), stage + T::OFF_SFB + w * 256, voff_sfb, step * 4);
         }
+    };
+    // The scales of steps [8 chunk, 8 chunk + 8), eight rows to an instruction: step by step each would
+    // be a line of its own, half as many again as the codes' (which cost the widest tile 6%, 128 x 128 12%).
+    // 0 behind the last step.
+    const auto load_scales = [&](int chunk) {
+        // lanes are [row][step] of a's eight rows and steps, [step][row] of b's, whose scales are read by rows
+        const auto rows_of = [&](const float* base, uint32_t bytes, int stride, int rows, uint8_t* to, int row, int step) {
+            const bool real = chunk * 8 + step < steps;
+#pragma unroll
+            for (int b = 0; b < (rows / 8 + T::NT / 64 - 1) / (T::NT / 64); ++b) {
+                const int block = b * (T::NT / 64) + wave;
+                if (rows / 8 % (T::NT / 64) && block >= rows / 8) break;
+                load4_lds(buffer(base, bytes), to + block * 256, real ? ((8 * block + row) * stride + step) * 4 : 0x7fffff00, chunk * 32);
+            }
+        };
+        rows_of(a_sf0, bytes_sfa, (int)p.a_sf_stride, T::BM, lds + T::OFF_SFA + (chunk & 1) * T::SFA, lane >> 3, lane & 7);
+        if constexpr (ROWS)
+            rows_of(b_sf0, bytes_sfb, (int)p.b_sf_stride, T::BN, lds + T::OFF_SFB + (chunk & 1) * T::SFB, lane & 7, lane >> 3);
     };
 
     // b's block of scales: one for the wave (tiles start and end with blocks, or within one)
@@ -225,35 +233,31 @@ __global__ void __launch_bounds__(T::NT) moe_product(ProductArgs p) {
 #pragma unroll
         for (int i = 0; i < T::SM; ++i) acc[j][i] = f32x4_t{};
 
-    // where the wave's rows of a stage are: a's, b's and the scales of both
-    const int at_x = group * STAGE + wm * T::TM * BK, at_y = group * STAGE + T::OFF_B + wn * T::TN * BK;
-    const int at_sa = group * STAGE + T::OFF_SFA + wm * T::at_sfa(T::TM) + (lane & 15) * 4;
-    const int at_sb = group * STAGE + T::OFF_SFB + wn * T::at_sfb(T::TN) + (lane >> 4) * 16;
+    // where the wave's rows of a stage are, and its scales
+    const int at_x = group * T::STAGE + wm * T::TM * BK, at_y = group * T::STAGE + T::OFF_B + wn * T::TN * BK;
+    const int at_sa = T::OFF_SFA + (wm * T::TM + (lane & 15)) * 32, at_sb = T::OFF_SFB + (wn * T::TN + (lane >> 5) * 8) * 32 + (lane >> 4 & 1) * 16;
     // (loaded past the end too: a branch around it would end the block of code)
     const auto block_scale = [&](int step) {
         if constexpr (ROWS) return 1.0f;
         const float s = b_sf[min(step, steps - 1)];
         return step < steps ? s : 0.0f;
     };
-    const auto row_scale = [&](int place, int i) {
-        return __int_as_float(*reinterpret_cast<const int*>(lds + place + at_sa + T::at_sfa(16 * i)));
+    const auto row_scale = [&](int step, int i) {
+        return __int_as_float(*reinterpret_cast<const int*>(lds + (step >> 3 & 1) * T::SFA + (step & 7) * 4 + at_sa + 16 * i * 32));
     };
-    const auto column_scales = [&](int place, int j) {
-        return *reinterpret_cast<const i32x4_t*>(lds + place + at_sb + T::at_sfb(16 * j));
+    const auto column_scales = [&](int step, int j) {
+        return *reinterpret_cast<const i32x4_t*>(lds + (step >> 3 & 1) * T::SFB + (step & 7) * 32 + at_sb + 16 * j * 32);
     };
     // With wide tiles, whose two rounds fill LDS, what of a round's place is read first takes new loads half a
-    // round earlier: a's rows and scales, and the rows of b's first columns (loads 0, 2, .. of b).
+    // round earlier: a's rows, and the rows of b's first columns (loads 0, 2, .. of b).
     constexpr bool EARLY = T::EARLY;
-    constexpr int FIRST = EARLY ? T::A_LOADS + T::B_LOADS / 2 + 1 : 0;
+    constexpr int FIRST = EARLY ? T::A_LOADS + T::B_LOADS / 2 : 0;
     const auto order = [&](int n) {                      // of the loads
-        if (!EARLY) return n;
-        if (n < T::A_LOADS) return n;
-        if (n < FIRST - 1) return T::A_LOADS + 2 * (n - T::A_LOADS);
-        if (n == FIRST - 1) return T::A_LOADS + T::B_LOADS;
-        if (n < T::A_LOADS + T::B_LOADS + 1) return T::A_LOADS + 2 * (n - FIRST) + 1;
-        return n;
+        if (!EARLY || n < T::A_LOADS) return n;
+        return n < FIRST ? T::A_LOADS + 2 * (n - T::A_LOADS) : T::A_LOADS + 2 * (n - FIRST) + 1;
     };
-    // this wave's loads of the next round are there and its reads of this one done, then every wave's
+    // This wave's loads of the next round are there and its reads of this one done, then every wave's.  (Scales
+    // loaded since are older than the loads that are left in flight: they are waited for too.)
     const auto meet = [&]() {
         asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((S - 2) * LOADS + FIRST) : "memory");
     };
@@ -261,6 +265,7 @@ __global__ void __launch_bounds__(T::NT) moe_product(ProductArgs p) {
     const auto meet_early = [&]() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); };
 
     if (steps > 0) {
+        load_scales(0);
 #pragma unroll
         for (int i = 0; i < S; ++i)
 #pragma unroll
@@ -269,23 +274,24 @@ __global__ void __launch_bounds__(T::NT) moe_product(ProductArgs p) {
         int place = 0, step = group;
         float sa[T::SM], sb = block_scale(step);
         i32x8_t x_raw[T::SM], y_raw[2] = {operand(lds + at_y, 0), operand(lds + at_y, 1)};
-        i32x4_t cs_next[2] = {};
-        if constexpr (ROWS) cs_next[0] = column_scales(0, 0), cs_next[1] = column_scales(0, 1);
+        i32x4_t cs_next = {};
+        if constexpr (ROWS) cs_next = column_scales(step, 0);
 #pragma unroll
         for (int i = 0; i < T::SM; ++i) {
             x_raw[i] = operand(lds + at_x, i);
-            sa[i] = row_scale(0, i);
+            sa[i] = row_scale(step, i);
         }
-        static_assert(T::SN >= 2, "two columns are read ahead");
         for (int round = 0; round < rounds; ++round, step += T::WK) {
             const int next = place + ROUND == S * ROUND ? 0 : place + ROUND;
+            // the next eight steps' scales, in the place of the last eight's
+            if (round * T::WK % 8 == 0) load_scales(round * T::WK / 8 + 1);
             // while the matrix unit has the next blocks, those before them are added: EXACT by whole
             // columns of blocks, whose chains of four go on side by side, else three blocks later
             constexpr int BEHIND = EXACT ? T::SM : 3, RING = EXACT ? 2 * T::SM : 4, BLOCKS = T::SN * T::SM;
             f32x4_t d[RING];
             float s[T::SM];
-            i32x4_t cs[T::SN + 2];
-            cs[0] = cs_next[0], cs[1] = cs_next[1];
+            i32x4_t cs[T::SN];
+            cs[0] = cs_next;
             const auto add_block = [&](int n) {
                 const int j = n / T::SM, i = n % T::SM;
 #pragma unroll
@@ -301,13 +307,21 @@ __global__ void __launch_bounds__(T::NT) moe_product(ProductArgs p) {
 #pragma unroll
             for (int j = 0; j < T::SN; ++j) {
                 const Ready<EXACT> y(y_raw[0]);
+                if constexpr (ROWS && T::SN == 2) {
+                    if (j == 0) cs[1] = column_scales(step, 1);
+                }
                 // the round's last reads were those of two columns ahead
                 if (EARLY && j == 2) meet_early();
                 if (j == T::SN - 2) meet();
                 const int from = j + 2 < T::SN ? place : next, ahead = (j + 2) % T::SN;
                 y_raw[0] = y_raw[1];
                 y_raw[1] = operand(lds + from + at_y, ahead);
-                if constexpr (ROWS) cs[j + 2] = column_scales(from, ahead);
+                // b's scales a column ahead, the last column's before the barrier
+                if constexpr (ROWS) {
+                    if (j + 2 < T::SN) cs[j + 1] = column_scales(step, j + 1);
+                    if (j + 3 == T::SN) cs[j + 2] = column_scales(step, j + 2);
+                    if (j + 1 == T::SN) cs_next = column_scales(step + T::WK, 0);
+                }
                 // The new loads one by one between the last columns' instructions: one after the other they
                 // would hold up every wave for as long as the loads take.
                 // (the early ones over the four columns up to the second barrier's, the others over two)
@@ -322,7 +336,7 @@ __global__ void __launch_bounds__(T::NT) moe_product(ProductArgs p) {
                 };
                 const auto read_next = [&](int i) {
                     x_raw[i] = operand(lds + next + at_x, i);
-                    sa[i] = row_scale(next, i);
+                    sa[i] = row_scale(step + T::WK, i);
                 };
                 if constexpr (EXACT) {
 #pragma unroll
@@ -359,7 +373,6 @@ __global__ void __launch_bounds__(T::NT) moe_product(ProductArgs p) {
             }
 #pragma unroll
             for (int n = BLOCKS > BEHIND ? BLOCKS - BEHIND : 0; n < BLOCKS; ++n) add_block(n);
-            cs_next[0] = cs[T::SN], cs_next[1] = cs[T::SN + 1];
             place = next;
         }
     }
