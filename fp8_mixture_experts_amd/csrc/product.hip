@@ -542,6 +542,8 @@ __global__ void __launch_bounds__(256) moe_product_join(ProductArgs p) {
 namespace {
 
 using Wide = Tile<256, 256, 4, 2, 1, 2>;
+using WideExact = Tile<128, 256, 2, 4, 1, 2>; // in its place with F32 results: the conversions' registers
+                                              // leave no room for 256 x 256 (4096 x 4096 x 2048: 67 us, Mid 74)
 using Mid = Tile<128, 128, 2, 2, 1, 2>;
 using Pair = Tile<64, 64, 2, 2, 1, 3>;       // two workgroups to a compute unit
 using Deep = Tile<64, 64, 2, 2, 2, 3>;       // one, of two groups of waves
@@ -549,29 +551,30 @@ using Low = Tile<32, 32, 2, 1, 4, 3>;
 
 int64_t tiles_of(int m, int n, int bm, int bn) { return (int64_t)((m + bm - 1) / bm) * ((n + bn - 1) / bn); }
 
-// What a kind takes, in us, with f tiles on the busiest of 256 compute units and s steps:
-//   call + f * tile + f * s * step + s * fill,
-// and what splitting it adds. Fitted (non-negative least squares of relative errors) to 64 shapes of m in
-// [1, 8192], k in [128, 8192], n in [64, 16384]: the least of them is on average within 2% of
-// the fastest of all measured, 14% at worst. Beside these, 32 x 64, 128 x 64, 256 x 128 and
-// 128 x 256 were measured; without them the choice is 1% worse.
+// What a kind takes, in us, beside the 2 of any call, with f tiles on the busiest of 256 compute units
+// and s steps: f * (tile + s * step) + s * fill, and what splitting it adds. Fitted (non-negative least
+// squares of relative errors) to 108 shapes of m in [1, 8192], k in [128, 8192], n in [64, 8192]: the
+// least of them is on average within 2% of the fastest of all measured, 20% at worst. Beside these,
+// 32 x 64, 128 x 64 and 256 x 128 were measured; without them the choice is no worse.
 struct Cost {
-    float call, tile, step, fill;
+    float tile, step, fill;
 };
-constexpr Cost COST_FP8[] = {{2.9f, 0.84f, 0.086f, 0.0f},   // few rows (16 columns to a workgroup)
-                             {2.0f, 2.4f, 0.103f, 0.0f},    // Low
-                             {1.3f, 2.9f, 0.219f, 0.0f},    // Deep
-                             {3.4f, 0.37f, 0.209f, 0.058f}, // Pair
-                             {3.2f, 1.1f, 0.541f, 0.062f},  // Mid
-                             {0.0f, 5.7f, 1.45f, 0.0f}};    // Wide
-constexpr Cost COST_EXACT[] = {{2.9f, 0.84f, 0.086f, 0.0f},
-                               {1.9f, 2.7f, 0.136f, 0.0f},
-                               {1.3f, 3.4f, 0.381f, 0.0f},
-                               {2.6f, 1.3f, 0.347f, 0.123f},
-                               {0.8f, 4.4f, 0.98f, 0.201f}};
-constexpr float JOIN = 4.4f, JOIN_ELEMENT = 1.37e-6f;       // a second launch, and its sums
+constexpr Cost COST_FP8[] = {{0.81f, 0.092f, 0.0f},     // few rows (16 columns to a workgroup)
+                             {1.85f, 0.108f, 0.0f},     // Low
+                             {1.77f, 0.216f, 0.0f},     // Deep
+                             {1.16f, 0.146f, 0.133f},   // Pair
+                             {1.97f, 0.463f, 0.092f},   // Mid
+                             {4.24f, 1.218f, 0.0f}};    // Wide
+constexpr Cost COST_EXACT[] = {{0.81f, 0.092f, 0.0f},
+                               {2.50f, 0.142f, 0.0f},
+                               {2.87f, 0.365f, 0.0f},
+                               {1.69f, 0.306f, 0.253f},
+                               {3.60f, 0.835f, 0.332f},
+                               {4.68f, 1.699f, 0.0f}};  // WideExact
+constexpr float JOIN = 4.2f, JOIN_ELEMENT = 1.32e-6f;       // a second launch, and its sums
 enum Kind { FEW, LOW, DEEP, PAIR, MID, WIDE };
 constexpr int ROWS_OF[] = {16, 32, 64, 64, 128, 256}, COLUMNS_OF[] = {16, 32, 64, 64, 128, 256};
+constexpr int WIDE_EXACT_ROWS = 128;
 
 template <typename T, bool EXACT, bool ROWS>
 void go(const ProductArgs& p, hipStream_t stream) {
@@ -590,8 +593,7 @@ void go(int kind, const ProductArgs& p, hipStream_t stream) {
         case DEEP: go<Deep, EXACT, ROWS>(p, stream); break;
         case PAIR: go<Pair, EXACT, ROWS>(p, stream); break;
         case MID: go<Mid, EXACT, ROWS>(p, stream); break;
-        default:
-            if constexpr (!EXACT) go<Wide, EXACT, ROWS>(p, stream);
+        default: go<std::conditional_t<EXACT, WideExact, Wide>, EXACT, ROWS>(p, stream);
     }
 }
 
@@ -603,12 +605,12 @@ ProductPlan product_plan(int m, int n, int k, int out_type) {
     const int steps = k / BK;
     ProductPlan best = {m <= 16 ? FEW : LOW, 1};
     float least = INFINITY;
-    for (int kind = m <= 16 ? FEW : LOW; kind <= (f32 ? MID : WIDE); ++kind) {
-        const int64_t tiles = tiles_of(m, n, ROWS_OF[kind], COLUMNS_OF[kind]);
+    for (int kind = m <= 16 ? FEW : LOW; kind <= WIDE; ++kind) {
+        const int64_t tiles = tiles_of(m, n, f32 && kind == WIDE ? WIDE_EXACT_ROWS : ROWS_OF[kind], COLUMNS_OF[kind]);
         // parts of the steps only where a compute unit would have no tile without them
         for (int splits = 1; splits == 1 || (kind != FEW && splits <= steps && tiles * splits <= 512 && splits <= 64); splits *= 2) {
             const float f = (float)((tiles * splits + 255) / 256), s = (float)((steps + splits - 1) / splits);
-            float us = cost[kind].call + f * (cost[kind].tile + s * cost[kind].step) + s * cost[kind].fill;
+            float us = f * (cost[kind].tile + s * cost[kind].step) + s * cost[kind].fill;
             if (splits > 1) us += JOIN + JOIN_ELEMENT * splits * (float)m * n;
             if (us < least) {
                 least = us;
