@@ -633,7 +633,7 @@ typedef struct mega_moe_product_args {
     void* workspace;          /* may be NULL where the bytes needed are 0        */
     int64_t workspace_bytes;
     int64_t a_stride, b_stride;          /* >= k, of 16, up to 2^22              */
-    int64_t a_sf_stride, b_sf_stride;    /* >= k/128, up to 2^22                 */
+    int64_t a_sf_stride, b_sf_stride;    /* >= k/128, up to 2^20                 */
     int64_t add_stride, out_stride;      /* >= n, of 8                           */
 } mega_moe_product_args;
 int mega_moe_product(const mega_moe_product_args* a, void* stream);
