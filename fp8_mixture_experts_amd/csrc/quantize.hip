@@ -171,21 +171,39 @@ __global__ void __launch_bounds__(256) moe_quantize_rows(QuantArgs a) {
     }
 }
 
+// The largest of eight columns over the wave's four groups of 16 lanes: the columns
+// part as the groups meet, so that a lane is left with two of its eight, from columns_of() on.
+__device__ __forceinline__ uint2 over_groups(const uint32_t (&m)[8]) {
+    uint32_t four[4], two[2];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const auto p = __builtin_amdgcn_permlane16_swap(m[e], m[e + 4], false, false);
+        four[e] = larger(p[0], p[1]);
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const auto p = __builtin_amdgcn_permlane32_swap(four[e], four[e + 2], false, false);
+        two[e] = larger(p[0], p[1]);
+    }
+    return uint2{two[0], two[1]};
+}
+__device__ __forceinline__ int columns_of() { return (threadIdx.x & 16) / 4 + (threadIdx.x & 32) / 16; }
+
 // Codes by columns, by blocks, and by rows beside them: a workgroup has a tile
 // of 128 rows x 128 columns, a thread eight columns of R rows that follow
 // each other.  A column's largest value is that of the thread's rows, of the
-// wave's four groups of rows and, through LDS, of the eight waves; its scale is worked
+// wave's four groups of rows and, through LDS, of the waves; its scale is worked
 // out by one thread, a row's by one of the row's lanes (three divisions each, of
-// which a thread would have 36).  The codes by columns turn in LDS: a thread has four
+// which a thread would have 36).  The codes by columns turn in LDS: a thread has R
 // neighbours of each, and a row of 128 leaves as whole lines.
 template <int KIND, bool F32, bool BLOCK, int R>
 __global__ void __launch_bounds__(2048 / R) moe_quantize_tile(QuantArgs a) {
     constexpr int OUTS = KIND == GRAD ? 2 : 1, WAVES = 32 / R;
     constexpr bool AHEAD = R == 2 && !F32;               // the next tile's loads in flight behind this one's codes
-    __shared__ uint32_t top[WAVES][128];
-    __shared__ __attribute__((aligned(16))) float col_up[128], col_hi[128], col_lo[128];
-    __shared__ int col_tiny[2];
-    __shared__ __attribute__((aligned(16))) uint8_t turned[128 * 128];   // [column][row], chunks of 16 swizzled
+    __shared__ __attribute__((aligned(16))) uint32_t top[OUTS][WAVES][128];
+    __shared__ __attribute__((aligned(16))) float col_up[OUTS * 128], col_hi[OUTS * 128], col_lo[OUTS * 128];
+    __shared__ int col_tiny[OUTS * 2];
+    __shared__ __attribute__((aligned(16))) uint8_t turned[OUTS][128 * 128];   // [column][row], chunks of 16 swizzled
     const int lane = threadIdx.x & 15, group = threadIdx.x >> 4, wave = threadIdx.x >> 6;
     const int blocks = a.C / 128, row_blocks = (a.T + 127) / 128;
     const int64_t tiles = (int64_t)blocks * row_blocks;
@@ -196,6 +214,7 @@ __global__ void __launch_bounds__(2048 / R) moe_quantize_tile(QuantArgs a) {
 #pragma unroll
         for (int r = 0; r < R; ++r) raw[r].load(a, t + r, col, t + r < a.T);
     };
+    const auto max_bits = [](uint32_t x, uint32_t y) { return larger(x, y); };
     Rows ahead;
     if constexpr (AHEAD) {
         if (blockIdx.x < tiles) fetch(ahead, blockIdx.x);
@@ -204,6 +223,7 @@ __global__ void __launch_bounds__(2048 / R) moe_quantize_tile(QuantArgs a) {
         const int rb = (int)(tile / blocks), b = (int)(tile - (int64_t)rb * blocks);
         const int col = b * 128 + lane * 8;
         const int64_t t0 = (int64_t)rb * 128 + group * R;
+        const auto qt_row = [&](int c) { return (int64_t)(c / 128) * a.C + b * 128 + (c & 127); };
         Rows here;
         if constexpr (!AHEAD) fetch(here, tile);
         float made[OUTS][R][8];
@@ -223,69 +243,66 @@ __global__ void __launch_bounds__(2048 / R) moe_quantize_tile(QuantArgs a) {
         if constexpr (AHEAD) {
             if (tile + gridDim.x < tiles) fetch(ahead, tile + gridDim.x);
         }
+        uint32_t most[OUTS][R];                          // of the thread's part of a row
+        Scale of_block;
 #pragma unroll
         for (int which = 0; which < OUTS; ++which) {
             const float (&v)[R][8] = made[which];
-            const int64_t row0 = (int64_t)which * a.C + b * 128;         // of qt
-            const auto max_bits = [](uint32_t x, uint32_t y) { return larger(x, y); };
-            float m[R], mc[8];                           // by rows, and by columns
 #pragma unroll
             for (int r = 0; r < R; ++r) {
-                m[r] = larger(v[r][0], v[r][1]);
+                float m = larger(v[r][0], v[r][1]);
 #pragma unroll
-                for (int e = 2; e < 8; e += 2) m[r] = larger(larger(v[r][e], v[r][e + 1]), m[r]);
+                for (int e = 2; e < 8; e += 2) m = larger(larger(v[r][e], v[r][e + 1]), m);
+                most[which][r] = __float_as_uint(m);
             }
-            Scale of_block;
             if constexpr (BLOCK) {
-                float most = m[0];
+                uint32_t all = most[which][0];
 #pragma unroll
-                for (int r = 1; r < R; ++r) most = larger(most, m[r]);
-                uint32_t all = over_lanes<64>(__float_as_uint(most), max_bits);
-                if ((threadIdx.x & 63) == 0) top[wave][0] = all;
-                __syncthreads();
-#pragma unroll
-                for (int w = 0; w < WAVES; ++w) all = larger(all, top[w][0]);
-                of_block = Scale(all);
-                if (threadIdx.x == 0) {
-                    if (a.q) a.q_sf[(int64_t)rb * blocks + b] = of_block.sf;
-                    if (a.qt) a.qt_sf[(int64_t)b * row_blocks + rb] = of_block.sf;
-                }
+                for (int r = 1; r < R; ++r) all = larger(all, most[which][r]);
+                all = over_lanes<64>(all, max_bits);
+                if ((threadIdx.x & 63) == 0) top[which][wave][0] = all;
             } else {
                 uint32_t bits[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    mc[e] = larger(v[0][e], v[1][e]);
+                    float m = larger(v[0][e], v[1][e]);
 #pragma unroll
-                    for (int r = 2; r < R; r += 2) mc[e] = larger(larger(v[r][e], v[r + 1][e]), mc[e]);
-                    bits[e] = __float_as_uint(mc[e]);
-                    auto p = __builtin_amdgcn_permlane16_swap(bits[e], bits[e], false, false);
-                    bits[e] = larger(p[0], p[1]);
-                    p = __builtin_amdgcn_permlane32_swap(bits[e], bits[e], false, false);
-                    bits[e] = larger(p[0], p[1]);
+                    for (int r = 2; r < R; r += 2) m = larger(larger(v[r][e], v[r + 1][e]), m);
+                    bits[e] = __float_as_uint(m);
                 }
-                if ((threadIdx.x & 63) < 16) {
-#pragma unroll
-                    for (int e = 0; e < 8; e += 4)
-                        *reinterpret_cast<u32x4_t*>(&top[wave][lane * 8 + e]) = u32x4_t{bits[e], bits[e + 1], bits[e + 2], bits[e + 3]};
-                }
-                __syncthreads();
-                if (threadIdx.x < 128) {
-                    uint32_t x = top[0][threadIdx.x];
-#pragma unroll
-                    for (int w = 1; w < WAVES; ++w) x = larger(x, top[w][threadIdx.x]);
-                    const Scale s(x);
-                    a.qt_sf[(row0 + threadIdx.x) * row_blocks + rb] = s.sf;
-                    col_up[threadIdx.x] = s.up, col_hi[threadIdx.x] = s.hi, col_lo[threadIdx.x] = s.lo;
-                    const bool tiny = __any(s.up != 1.0f);
-                    if ((threadIdx.x & 63) == 0) col_tiny[wave] = tiny;
-                }
+                *reinterpret_cast<uint2*>(&top[which][wave][lane * 8 + columns_of()]) = over_groups(bits);
             }
-            if (a.q) {
+        }
+        __syncthreads();
+        if constexpr (BLOCK) {
+            uint32_t all = top[0][0][0];
+#pragma unroll
+            for (int w = 1; w < WAVES; ++w) all = larger(all, top[0][w][0]);
+            of_block = Scale(all);
+            if (threadIdx.x == 0) {
+                if (a.q) a.q_sf[(int64_t)rb * blocks + b] = of_block.sf;
+                if (a.qt) a.qt_sf[(int64_t)b * row_blocks + rb] = of_block.sf;
+            }
+        } else if (threadIdx.x < OUTS * 128) {
+            const int which = OUTS == 1 ? 0 : threadIdx.x >> 7, c = threadIdx.x & 127;
+            uint32_t x = top[which][0][c];
+#pragma unroll
+            for (int w = 1; w < WAVES; ++w) x = larger(x, top[which][w][c]);
+            const Scale s(x);
+            a.qt_sf[qt_row(threadIdx.x) * row_blocks + rb] = s.sf;
+            col_up[threadIdx.x] = s.up, col_hi[threadIdx.x] = s.hi, col_lo[threadIdx.x] = s.lo;
+            const bool tiny = __any(s.up != 1.0f);
+            if ((threadIdx.x & 63) == 0) col_tiny[wave] = tiny;
+        }
+        if (a.q) {
+#pragma unroll
+            for (int which = 0; which < OUTS; ++which) {
+                const float (&v)[R][8] = made[which];
                 Scale mine = of_block;
                 if constexpr (!BLOCK) {
                     uint32_t bits[R];
 #pragma unroll
-                    for (int r = 0; r < R; ++r) bits[r] = over_lanes<16>(__float_as_uint(m[r]), max_bits);
+                    for (int r = 0; r < R; ++r) bits[r] = over_lanes<16>(most[which][r], max_bits);
                     uint32_t own = lane & 1 ? bits[1] : bits[0];
                     if constexpr (R == 4) own = lane & 2 ? (lane & 1 ? bits[3] : bits[2]) : own;
                     mine = Scale(own);
@@ -303,35 +320,40 @@ __global__ void __launch_bounds__(2048 / R) moe_quantize_tile(QuantArgs a) {
                 if (__any(mine.up != 1.0f)) row_codes(std::true_type());
                 else row_codes(std::false_type());
             }
-            if (a.qt) {
-                if (!BLOCK) __syncthreads();
+        }
+        if (a.qt) {
+            if (!BLOCK) __syncthreads();
+#pragma unroll
+            for (int which = 0; which < OUTS; ++which) {
+                const float (&v)[R][8] = made[which];
                 const auto column_codes = [&](auto tiny) {
                     constexpr bool TINY = decltype(tiny)::value;
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         Scale s = of_block;
                         if constexpr (!BLOCK) {
-                            s.hi = col_hi[lane * 8 + e], s.lo = col_lo[lane * 8 + e];
-                            if constexpr (TINY) s.up = col_up[lane * 8 + e];
+                            const int c = which * 128 + lane * 8 + e;
+                            s.hi = col_hi[c], s.lo = col_lo[c];
+                            if constexpr (TINY) s.up = col_up[c];
                         }
                         // the 16 bytes of a row lie at chunk ^ (column / 8 % 8)
-                        uint8_t* to = turned + (lane * 8 + e) * 128 + ((group * R) ^ ((lane & 7) * 16));
+                        uint8_t* to = turned[which] + (lane * 8 + e) * 128 + ((group * R) ^ ((lane & 7) * 16));
                         if constexpr (R == 4) *reinterpret_cast<uint32_t*>(to) = s.codes<TINY>(v[0][e], v[1][e], v[2][e], v[R - 1][e]);
                         else *reinterpret_cast<uint16_t*>(to) = (uint16_t)__builtin_amdgcn_cvt_pk_fp8_f32(s.quotient<TINY>(v[0][e]), s.quotient<TINY>(v[1][e]), 0, false);
                     }
                 };
-                if (BLOCK ? of_block.up != 1.0f : (col_tiny[0] | col_tiny[1]) != 0) column_codes(std::true_type());
+                if (BLOCK ? of_block.up != 1.0f : (col_tiny[2 * which] | col_tiny[2 * which + 1]) != 0) column_codes(std::true_type());
                 else column_codes(std::false_type());
-                __syncthreads();
-#pragma unroll
-                for (int i = 0; i < R / 2; ++i) {
-                    const int c = (threadIdx.x >> 3) + 256 / R * i, w = (threadIdx.x & 7) * 16;
-                    const u32x4_t d = *reinterpret_cast<const u32x4_t*>(turned + c * 128 + (w ^ (((c >> 3) & 7) * 16)));
-                    *reinterpret_cast<u32x4_t*>(a.qt + (row0 + c) * ((int64_t)row_blocks * 128) + (int64_t)rb * 128 + w) = d;
-                }
             }
-            if (BLOCK) __syncthreads();                  // top is written again (else two barriers lie between)
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < OUTS * R / 2; ++i) {
+                const int c = (threadIdx.x >> 3) + 256 / R * i, w = (threadIdx.x & 7) * 16;
+                const u32x4_t d = *reinterpret_cast<const u32x4_t*>(turned[0] + c * 128 + (w ^ (((c >> 3) & 7) * 16)));
+                *reinterpret_cast<u32x4_t*>(a.qt + qt_row(c) * ((int64_t)row_blocks * 128) + (int64_t)rb * 128 + w) = d;
+            }
         }
+        if (BLOCK) __syncthreads();                      // top is written again (else two barriers lie between)
     }
 }
 
