@@ -366,15 +366,22 @@ template <int KIND, bool F32>
 void launch(const QuantArgs& a, bool block, hipStream_t stream) {
     if (a.qt || (block && a.q)) {
         const int64_t tiles = (int64_t)(a.C / 128) * ((a.T + 127) / 128);
-        // The gradients' values, of two outputs, leave a compute unit one workgroup: of 16 waves, which
-        // goes on to further tiles with their loads in flight (float32's do not fit beside the values).
-        constexpr int R = KIND == GRAD ? 2 : 4;
-        const int64_t most = R == 2 && !F32 ? 256 : MAX_GRID;
-        const auto go = [&](auto kernel) {
-            hipLaunchKernelGGL(kernel, dim3((unsigned)(tiles < most ? tiles : most)), dim3(2048 / R), 0, stream, a);
+        const auto go = [&](auto kernel, int rows, int64_t most) {
+            hipLaunchKernelGGL(kernel, dim3((unsigned)(tiles < most ? tiles : most)), dim3(2048 / rows), 0, stream, a);
         };
-        if (KIND != GRAD && block) go(moe_quantize_tile<KIND, F32, KIND != GRAD, R>);
-        else go(moe_quantize_tile<KIND, F32, false, R>);
+        if constexpr (KIND == GRAD) {
+            // The values of two outputs leave a compute unit two workgroups of 8 waves with four rows to a
+            // thread, or one of 16 with two, which goes on to further tiles with their loads in flight
+            // (float32's do not fit beside the values). Codes alone are better made by the former (4096 x 2048:
+            // 20.5 us, 22.2 with two rows), with the gradients stored too (33.8, 30.2) and of float32 (38, 35.7)
+            // the latter is.
+            if (F32 || a.out[0] || a.out[1]) go(moe_quantize_tile<KIND, F32, false, 2>, 2, F32 ? MAX_GRID : 256);
+            else go(moe_quantize_tile<KIND, false, false, 4>, 4, MAX_GRID);
+        } else if (block) {
+            go(moe_quantize_tile<KIND, F32, true, 4>, 4, MAX_GRID);
+        } else {
+            go(moe_quantize_tile<KIND, F32, false, 4>, 4, MAX_GRID);
+        }
     } else {
         const int64_t n = ((int64_t)a.T * (a.C / 128) + 15) / 16;
         hipLaunchKernelGGL((moe_quantize_rows<KIND, F32>), dim3((unsigned)(n < MAX_GRID ? n : MAX_GRID)), dim3(256), 0, stream, a);
