@@ -134,6 +134,7 @@ struct Tile {
     static_assert(TN == 128 || 128 % TN == 0, "one block of scales to a wave");
     static_assert(SN >= 2, "two columns are read ahead");
     static_assert(8 % WK == 0 && WK < 8, "scales of eight steps last for whole rounds, and two or more");
+    static_assert(8 / WK >= S - 1, "the next scales are older than the loads that meet() leaves in flight");
     static_assert(lds<true>() <= 160 * 1024, "LDS");
 };
 
@@ -544,37 +545,48 @@ namespace {
 using Wide = Tile<256, 256, 4, 2, 1, 2>;
 using WideExact = Tile<128, 256, 2, 4, 1, 2>; // in its place with F32 results: the conversions' registers
                                               // leave no room for 256 x 256 (4096 x 4096 x 2048: 67 us, Mid 74)
-using Mid = Tile<128, 128, 2, 2, 1, 2>;
-using Pair = Tile<64, 64, 2, 2, 1, 3>;       // two workgroups to a compute unit
-using Deep = Tile<64, 64, 2, 2, 2, 3>;       // one, of two groups of waves
+using Mid = Tile<128, 128, 2, 2, 1, 2>;       // two workgroups to a compute unit
+using Long = Tile<128, 128, 2, 2, 1, 4>;      // one, with three rounds in flight: only up to 256 tiles, which have a
+                                              // compute unit each anyway (1024 x 7168 x 4096: 37 us, Mid 42; from HBM
+                                              // 41 and 55; but 2048 x 7168 x 4096: 73 us, Mid 61)
+using Pair = Tile<64, 64, 2, 2, 1, 3>;        // two or three workgroups
+using Deep = Tile<64, 64, 2, 2, 2, 3>;        // one, of two groups of waves
+using Strip = Tile<32, 64, 1, 2, 4, 3>;       // (128 x 7168 x 4096 from HBM: 16.6 us, Deep's halves 18.2)
 using Low = Tile<32, 32, 2, 1, 4, 3>;
 
 int64_t tiles_of(int m, int n, int bm, int bn) { return (int64_t)((m + bm - 1) / bm) * ((n + bn - 1) / bn); }
 
 // What a kind takes, in us, beside the 2 of any call, with f tiles on the busiest of 256 compute units
-// and s steps: f * (tile + s * step) + s * fill, and what splitting it adds. Fitted (non-negative least
-// squares of relative errors) to 108 shapes of m in [1, 8192], k in [128, 8192], n in [64, 8192]: the
-// least of them is on average within 2% of the fastest of all measured, 20% at worst. Beside these,
-// 32 x 64, 128 x 64 and 256 x 128 were measured; without them the choice is no worse.
-struct Cost {
-    float tile, step, fill;
+// and s steps: f * tile + s * step for each tile, or s * alone for the last of an odd f where
+// two share a compute unit; and what splitting it adds. Fitted (non-negative least
+// squares of relative errors) to 131 shapes of m in [1, 8192], k in [128, 8192], n in [64, 18432], with
+// operands that come from HBM (from the last-level cache the small tiles' steps take a fifth less): the
+// least of them is on average within 2% of the fastest of all measured, 19% (F32: 22%) at worst. Beside these,
+// 128 x 64 (with and without two groups) and 256 x 128 were measured; without them the choice is no worse.
+// With F32 results Strip and Long are never the fastest.
+struct Kind {
+    int rows, columns;
+    float tile, step, alone;
 };
-constexpr Cost COST_FP8[] = {{0.81f, 0.092f, 0.0f},     // few rows (16 columns to a workgroup)
-                             {1.85f, 0.108f, 0.0f},     // Low
-                             {1.77f, 0.216f, 0.0f},     // Deep
-                             {1.16f, 0.146f, 0.133f},   // Pair
-                             {1.97f, 0.463f, 0.092f},   // Mid
-                             {4.24f, 1.218f, 0.0f}};    // Wide
-constexpr Cost COST_EXACT[] = {{0.81f, 0.092f, 0.0f},
-                               {2.50f, 0.142f, 0.0f},
-                               {2.87f, 0.365f, 0.0f},
-                               {1.69f, 0.306f, 0.253f},
-                               {3.60f, 0.835f, 0.332f},
-                               {4.68f, 1.699f, 0.0f}};  // WideExact
-constexpr float JOIN = 4.2f, JOIN_ELEMENT = 1.32e-6f;       // a second launch, and its sums
-enum Kind { FEW, LOW, DEEP, PAIR, MID, WIDE };
-constexpr int ROWS_OF[] = {16, 32, 64, 64, 128, 256}, COLUMNS_OF[] = {16, 32, 64, 64, 128, 256};
-constexpr int WIDE_EXACT_ROWS = 128;
+enum { FEW, LOW, STRIP, DEEP, PAIR, MID, LONG, WIDE, KINDS };
+constexpr float NEVER = INFINITY;
+constexpr Kind FP8[KINDS] = {{16, 16, 1.21f, 0.091f, 0.091f},     // few rows (16 columns to a workgroup)
+                             {32, 32, 2.22f, 0.125f, 0.125f},
+                             {32, 64, 2.59f, 0.178f, 0.178f},
+                             {64, 64, 2.12f, 0.262f, 0.262f},
+                             {64, 64, 1.27f, 0.214f, 0.355f},
+                             {128, 128, 1.93f, 0.551f, 0.749f},
+                             {128, 128, 2.78f, 0.535f, 0.535f},
+                             {256, 256, 4.37f, 1.283f, 1.283f}};
+constexpr Kind EXACT_F32[KINDS] = {{16, 16, 1.21f, 0.091f, 0.091f},
+                                   {32, 32, 2.59f, 0.145f, 0.145f},
+                                   {32, 64, NEVER, 0.0f, 0.0f},
+                                   {64, 64, 3.14f, 0.370f, 0.370f},
+                                   {64, 64, 1.70f, 0.342f, 0.613f},
+                                   {128, 128, 3.74f, 0.891f, 1.200f},
+                                   {128, 128, NEVER, 0.0f, 0.0f},
+                                   {128, 256, 4.99f, 1.728f, 1.728f}};
+constexpr float JOIN = 3.9f, JOIN_ELEMENT = 1.4e-6f;        // a second launch, and its sums
 
 template <typename T, bool EXACT, bool ROWS>
 void go(const ProductArgs& p, hipStream_t stream) {
@@ -593,6 +605,12 @@ void go(int kind, const ProductArgs& p, hipStream_t stream) {
         case DEEP: go<Deep, EXACT, ROWS>(p, stream); break;
         case PAIR: go<Pair, EXACT, ROWS>(p, stream); break;
         case MID: go<Mid, EXACT, ROWS>(p, stream); break;
+        case STRIP:
+            if constexpr (!EXACT) go<Strip, EXACT, ROWS>(p, stream);
+            break;
+        case LONG:
+            if constexpr (!EXACT) go<Long, EXACT, ROWS>(p, stream);
+            break;
         default: go<std::conditional_t<EXACT, WideExact, Wide>, EXACT, ROWS>(p, stream);
     }
 }
@@ -600,17 +618,18 @@ void go(int kind, const ProductArgs& p, hipStream_t stream) {
 }  // namespace
 
 ProductPlan product_plan(int m, int n, int k, int out_type) {
-    const bool f32 = out_type == MEGA_MOE_F32;
-    const Cost* cost = f32 ? COST_EXACT : COST_FP8;
-    const int steps = k / BK;
-    ProductPlan best = {m <= 16 ? FEW : LOW, 1};
+    const Kind* kinds = out_type == MEGA_MOE_F32 ? EXACT_F32 : FP8;
+    const int steps = k / BK, first = m <= 16 ? FEW : LOW;
+    ProductPlan best = {first, 1};
     float least = INFINITY;
-    for (int kind = m <= 16 ? FEW : LOW; kind <= WIDE; ++kind) {
-        const int64_t tiles = tiles_of(m, n, f32 && kind == WIDE ? WIDE_EXACT_ROWS : ROWS_OF[kind], COLUMNS_OF[kind]);
+    for (int kind = first; kind < KINDS; ++kind) {
+        const Kind& o = kinds[kind];
+        const int64_t tiles = tiles_of(m, n, o.rows, o.columns);
         // parts of the steps only where a compute unit would have no tile without them
         for (int splits = 1; splits == 1 || (kind != FEW && splits <= steps && tiles * splits <= 512 && splits <= 64); splits *= 2) {
-            const float f = (float)((tiles * splits + 255) / 256), s = (float)((steps + splits - 1) / splits);
-            float us = f * (cost[kind].tile + s * cost[kind].step) + s * cost[kind].fill;
+            if (kind == LONG && tiles * splits > 256) break;
+            const int64_t f = (tiles * splits + 255) / 256;
+            float us = f * o.tile + (float)((steps + splits - 1) / splits) * ((f - f % 2) * o.step + f % 2 * o.alone);
             if (splits > 1) us += JOIN + JOIN_ELEMENT * splits * (float)m * n;
             if (us < least) {
                 least = us;

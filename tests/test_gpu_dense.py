@@ -35,6 +35,24 @@ def test_product(m, k, n, out_type, scale):
     D.check_product(out, a, a_sf, b, b_sf, scale, add)
 
 
+# sizes that go through each of the kinds of tiles, whole and split, with rows and columns left over
+KINDS = [(33, 1664, 8440), (33, 10240, 1112), (133, 640, 11064), (1027, 10240, 72), (1025, 10240, 8), (1, 1152, 8200), (1, 16384, 520),
+         (129, 10240, 5576), (65, 2944, 8424), (67, 7168, 2744), (259, 128, 10952), (65, 128, 8840), (1025, 128, 7208), (33, 896, 4136)]
+
+
+@pytest.mark.parametrize("m,k,n", KINDS)
+@pytest.mark.parametrize("out_type", [BF16, F32], ids=["bf16", "f32"])
+def test_product_by_every_tile(m, k, n, out_type):
+    g = D.generator(m + n)
+    a, a_sf = D.operand(g, m, k)
+    for scale in ("block", "row"):
+        b, b_sf = D.operand(g, n, k, scale)
+        out = torch.full((m + 1, n), 7.0, dtype=out_type, device="cuda")
+        D.product(a, a_sf, b, b_sf, out[:m], scale)
+        D.check_product(out[:m], a, a_sf, b, b_sf, scale)
+        assert bool((out[m] == 7).all())
+
+
 @pytest.mark.parametrize("m,k,n", [(5, 256, 72), (70, 1024, 136), (300, 512, 264), (4100, 128, 4104)])
 @pytest.mark.parametrize("out_type", [BF16, F32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("scale", ["block", "row"])
