@@ -36,7 +36,10 @@ EXPORTS = ["mega_moe_create", "mega_moe_forward", "mega_moe_forward_mxfp4", "meg
            "mega_moe_router_logits", "mega_moe_router_logits_backward",
            "mega_moe_router_logits_workspace_bytes", "mega_moe_router_topk",
            "mega_moe_balance_loss", "mega_moe_balance_loss_workspace_bytes",
-           "mega_moe_router_backward"]
+           "mega_moe_router_backward",
+           "mega_moe_product", "mega_moe_product_workspace_bytes", "mega_moe_quantize",
+           "mega_moe_swiglu_backward", "mega_moe_rotary", "mega_moe_rotary_backward",
+           "mega_moe_rotary_workspace_bytes", "mega_moe_rotary_frequencies"]
 
 MEGA_MOE_BF16 = 0
 MEGA_MOE_F32 = 1

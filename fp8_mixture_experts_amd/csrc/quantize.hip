@@ -141,7 +141,9 @@ __device__ __forceinline__ void store_out(const QuantArgs& a, int which, int64_t
 
 }  // namespace
 
-// Codes by rows and values alone: 16 lanes hold 128 columns of a row.
+// Codes by rows and values alone: 16 lanes hold 128 columns of a row, whose largest value they find in four
+// lane moves.  One pass over the data: the launch bounds small batches (128 x 2048 of SwiGLU 6.9 us with the
+// call, 2.8 the kernel; 577 x 2048 gradients 6.7), memory large ones.
 template <int KIND, bool F32>
 __global__ void __launch_bounds__(256) moe_quantize_rows(QuantArgs a) {
     constexpr int OUTS = KIND == GRAD ? 2 : 1;
@@ -196,6 +198,10 @@ __device__ __forceinline__ int columns_of() { return (threadIdx.x & 16) / 4 + (t
 // out by one thread, a row's by one of the row's lanes (three divisions each, of
 // which a thread would have 36).  The codes by columns turn in LDS: a thread has R
 // neighbours of each, and a row of 128 leaves as whole lines.
+//
+// One pass: 8192 x 7168 BF16 to codes by rows and by columns 53 us (235 MB, 4.4 TB/s with the call; a copy's rate
+// would be 47), SwiGLU gradients 4096 x 2048 to both 20.5 us (84 MB; 16.7): vector instructions are
+// busy for about half of the time, beside the memory, and a compute unit's tiles start and end together.
 template <int KIND, bool F32, bool BLOCK, int R>
 __global__ void __launch_bounds__(2048 / R) moe_quantize_tile(QuantArgs a) {
     constexpr int OUTS = KIND == GRAD ? 2 : 1, WAVES = 32 / R;

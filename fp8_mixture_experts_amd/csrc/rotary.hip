@@ -124,6 +124,8 @@ int lanes_of(int D) { return D <= 64 ? 8 : D <= 128 ? 16 : D <= 256 ? 32 : 64; }
 // round of 256 / LANES: q's, then k's.  Eight workgroups to a compute unit keep the
 // memory busy: with the next round's loads in flight in each, whose registers
 // leave room for seven, 49 us against 38 (8192 tokens of 32 + 8 heads of 128).
+// That is 168 MB, 4.5 TB/s with the call (a copy's rate would be 33 us; 32768 tokens go at 5.2);
+// one token takes the launch and its angles (6.6 us with the call, 3.3 the kernel).
 template <bool F32, int LANES>
 __global__ void __launch_bounds__(THREADS) moe_rotary(mega_moe_rotary_args a, int tokens) {
     extern __shared__ float2 turns[];
@@ -163,7 +165,9 @@ __global__ void __launch_bounds__(THREADS) moe_rotary(mega_moe_rotary_args a, in
 // takes every gridDim.y-th round).  Its sums over tokens and heads lie in LDS, a place
 // for each thread, and in registers during a run; at the end the groups' meet
 // in order and the workgroup's go to the workspace, [grid][sums][D].  The next round's loads
-// are in flight over the two sums of a head.
+// are in flight over the two sums of a head; two rounds ahead, or the first loaded over the angles, was no faster.
+// Memory bounds it, and the second launch: 4096 tokens of 32 + 8 heads of 128 32.3 us with the sums' (126 MB; a
+// copy's rate would be 24.7, the second launch is 4), 16384 tokens 108 us (4.7 TB/s).
 template <bool F32, int LANES>
 __global__ void __launch_bounds__(BACK_THREADS) moe_rotary_backward(mega_moe_rotary_backward_args a, float* ws, int tokens) {
     extern __shared__ float2 turns[];
@@ -247,8 +251,8 @@ __global__ void __launch_bounds__(BACK_THREADS) moe_rotary_backward(mega_moe_rot
     }
 }
 
-// Adds the workgroups' sums: a workgroup has 16 of the sums' columns, its 64
-// groups of 16 lanes every 64th row each.
+// Adds the workgroups' sums (atomics would add them in an order that changes): a workgroup has 16 of the
+// sums' columns, its 64 groups of 16 lanes every 64th row each. A launch and two latencies: 4 us.
 __global__ void __launch_bounds__(1024)
 moe_rotary_reduce(const float* ws, float* out0, float* out1, int D, int sums, int rows) {
     __shared__ float part[64][17];
