@@ -70,16 +70,16 @@ struct Heads {
     }
 };
 
-// Of `tokens` tokens from t0 on, every by-th.
+// Of `tokens` tokens from t0 on, every by-th; `sign` is the angles'.
 template <int NT, typename Args>
-__device__ __forceinline__ void fill_turns(const Args& a, float2* cs, int t0, int by, int tokens) {
+__device__ __forceinline__ void fill_turns(const Args& a, float2* cs, int t0, int by, int tokens, float sign = 1.0f) {
     const int half = a.rotary_dim / 2;
     const float scale = a.scale == 0.0f ? 1.0f : a.scale;
     for (int i = threadIdx.x; i < tokens * half; i += NT) {
         const int t = i / half;
         const int token = t0 + t * by;
         const int p = a.positions ? a.positions[token] : a.first_position + token;
-        cs[i] = turn(p, a.inv_freq[i - t * half], scale);
+        cs[i] = turn(p, a.inv_freq[i - t * half] * sign, scale);
     }
 }
 
@@ -127,12 +127,12 @@ int lanes_of(int D) { return D <= 64 ? 8 : D <= 128 ? 16 : D <= 256 ? 32 : 64; }
 // That is 168 MB, 4.5 TB/s with the call (a copy's rate would be 33 us; 32768 tokens go at 5.2);
 // one token takes the launch and its angles (6.6 us with the call, 3.3 the kernel).
 template <bool F32, int LANES>
-__global__ void __launch_bounds__(THREADS) moe_rotary(mega_moe_rotary_args a, int tokens) {
+__global__ void __launch_bounds__(THREADS) moe_rotary(mega_moe_rotary_args a, int tokens, float sign) {
     extern __shared__ float2 turns[];
     constexpr int G = THREADS / LANES;
     const int t0 = blockIdx.x * tokens, n = min(tokens, a.num_tokens - t0), by = gridDim.y * G;
     const Heads<LANES, mega_moe_rotary_args> h(a, turns);
-    fill_turns<THREADS>(a, turns, t0, 1, n);
+    fill_turns<THREADS>(a, turns, t0, 1, n, sign);
     __syncthreads();
     const float inv_d = 1.0f / (float)a.head_dim;
     const auto run = [&](int heads, const Rows& in, const Rows& out, const void* weight) {
@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(THREADS) moe_rotary(mega_moe_rotary_args a, in
     run(a.k_heads, Rows{a.k, a.k_stride, a.k_head_stride}, Rows{a.k_out, a.k_out_stride, a.k_out_head_stride}, a.k_weight);
 }
 
-// Gradients: a workgroup goes from one run of tokens to another (of their heads it
+// Gradients where there is a weight: a workgroup goes from one run of tokens to another (of their heads it
 // takes every gridDim.y-th round).  Its sums over tokens and heads lie in LDS, a place
 // for each thread, and in registers during a run; at the end the groups' meet
 // in order and the workgroup's go to the workspace, [grid][sums][D].  The next round's loads
@@ -313,7 +313,9 @@ dim3 back_grid(const mega_moe_rotary_backward_args& a) {
 
 }  // namespace
 
-void launch_rotary(const mega_moe_rotary_args& a, hipStream_t stream) {
+namespace {
+
+void launch_turned(const mega_moe_rotary_args& a, float sign, hipStream_t stream) {
     const int tokens = tokens_of(a.num_tokens, a.rotary_dim);
     const int blocks = (a.num_tokens + tokens - 1) / tokens;
     // few tokens: their heads over several workgroups
@@ -324,12 +326,16 @@ void launch_rotary(const mega_moe_rotary_args& a, hipStream_t stream) {
     const auto go = [&](auto f32) {
         by_lanes<decltype(f32)::value>(a, [&](auto lanes) {
             hipLaunchKernelGGL((moe_rotary<decltype(f32)::value, decltype(lanes)::value>), dim3((unsigned)blocks, (unsigned)split),
-                               dim3(THREADS), lds, stream, a, tokens);
+                               dim3(THREADS), lds, stream, a, tokens, sign);
         });
     };
     if (a.type == MEGA_MOE_F32) go(std::true_type());
     else go(std::false_type());
 }
+
+}  // namespace
+
+void launch_rotary(const mega_moe_rotary_args& a, hipStream_t stream) { launch_turned(a, 1.0f, stream); }
 
 int rotary_backward_blocks(const mega_moe_rotary_backward_args& a) {
     const dim3 g = back_grid(a);
@@ -337,6 +343,16 @@ int rotary_backward_blocks(const mega_moe_rotary_backward_args& a) {
 }
 
 void launch_rotary_backward(const mega_moe_rotary_backward_args& a, hipStream_t stream) {
+    if (!a.q_weight && !a.k_weight) {
+        // gradients of the rotation alone: the rotation by the opposite angles (8192 tokens of 32 + 8 heads of
+        // 128 in 36.8 us, in the kernel for weights 41.7)
+        const mega_moe_rotary_args f = {a.num_tokens, a.q_heads, a.k_heads, a.head_dim, a.rotary_dim, a.rotary_start, a.layout, a.type,
+                                        a.weight_type, a.first_position, a.eps, a.scale, a.dq_out, a.dk_out, nullptr, nullptr,
+                                        a.positions, a.inv_freq, a.dq, a.dk, a.dq_out_stride, a.dk_out_stride, a.dq_stride,
+                                        a.dk_stride, a.dq_out_head_stride, a.dk_out_head_stride, a.dq_head_stride, a.dk_head_stride};
+        launch_turned(f, -1.0f, stream);
+        return;
+    }
     const int tokens = back_tokens(a), blocks = rotary_backward_blocks(a);
     const unsigned lds = (unsigned)(tokens * a.rotary_dim * 4);
     float* ws = static_cast<float*>(a.workspace);
