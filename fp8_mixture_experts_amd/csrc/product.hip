@@ -122,17 +122,16 @@ struct Tile {
     static constexpr int OFF_SFA = S * ROUND, SFA = BM * 32, OFF_SFB = OFF_SFA + 2 * SFA, SFB = BN * 32;
     // two rounds of the widest tile fill LDS; each wave's first columns of b are the even blocks of loads
     static constexpr bool EARLY = SN >= 8 && S == 2 && TN / 2 == 8 * NW;
-    // results leave through LDS, PW columns of a wave at a time
-    static constexpr int PW = TN < 64 ? TN : 64, PITCH = PW + 4;
+    static constexpr int PITCH = TN + 4;                 // of the groups' sums, which meet in LDS
     template <bool ROWS>
     static constexpr int lds() {
-        const int a = OFF_SFB + (ROWS ? 2 * SFB : 0), b = WK * NW * TM * PITCH * 4;
+        const int a = OFF_SFB + (ROWS ? 2 * SFB : 0), b = WK == 1 ? 0 : WK * NW * TM * PITCH * 4;
         return a > b ? a : b;
     }
     static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0, "loads");
     static_assert((8 * NW) % 16 == 0, "turn() is the same for a wave's rows");
     static_assert(TN == 128 || 128 % TN == 0, "one block of scales to a wave");
-    static_assert(SN >= 2, "two columns are read ahead");
+    static_assert(SN >= 2 && SN % 2 == 0, "two columns are read ahead, and leave together");
     static_assert(8 % WK == 0 && WK < 8, "scales of eight steps last for whole rounds, and two or more");
     static_assert(8 / WK >= S - 1, "the next scales are older than the loads that meet() leaves in flight");
     static_assert(lds<true>() <= 160 * 1024, "LDS");
@@ -386,53 +385,70 @@ __global__ void __launch_bounds__(T::NT) moe_product(ProductArgs p) {
             place = next;
         }
     }
-    // the loads past the end are done, and every wave has read its last stage
+    // Eight results of a row leave the lane that has them.
+    const auto leave = [&](int64_t row, int64_t col, float (&v)[8]) {
+        if (row >= p.m || col >= p.n) return;
+        if (p.splits > 1) {
+            store8<true>(p.parts, ((size_t)split * p.m + row) * p.n + col, v);
+            return;
+        }
+        if (p.add) {
+            float o[8];
+            load8<EXACT>(p.add, row * p.add_stride + col, o);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] += o[e];
+        }
+        store8<EXACT>(p.out, row * p.out_stride + col, v);
+    };
+    // the loads past the end are done: LDS is the workgroup's until then
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-    __syncthreads();
-    // a group's wave has TM x PW sums at a time in LDS; the groups' are added in order
+    if constexpr (T::WK == 1) {
+        // A lane has four columns of a block; two blocks side by side give it eight of one, whose 16 rows' stores
+        // are 64 bytes or more each. (Through LDS, in whole lines, 8192 x 7168 x 4096 takes 1% less, but 8192 x 2048
+        // x 7168 with an addend 172 us, not 162, and 4096 x 512 x 4096 with F32 results 34.5, not 32.4.)
+        const int g = lane >> 4;
+        const int64_t row0 = m0 + wm * T::TM + (lane & 15), col0 = n0 + wn * T::TN + (g & 1) * 16 + (g >> 1) * 8;
+#pragma unroll
+        for (int i = 0; i < T::SM; ++i)
+#pragma unroll
+            for (int j = 0; j < T::SN; j += 2) {
+                float v[8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const auto x = __builtin_amdgcn_permlane16_swap(__float_as_uint(acc[j][i][e]), __float_as_uint(acc[j + 1][i][e]), false, false);
+                    v[e] = __uint_as_float(x[0]);
+                    v[4 + e] = __uint_as_float(x[1]);
+                }
+                leave(row0 + 16 * i, col0 + 16 * j, v);
+            }
+        return;
+    }
+    __syncthreads();                                     // every wave has read its last stage
+    // a group's wave has TM x TN sums in LDS; the groups' are added in order
     float* tile = reinterpret_cast<float*>(lds);
     constexpr int OF_WAVE = T::TM * T::PITCH;
 #pragma unroll
-    for (int piece = 0; piece < T::TN / T::PW; ++piece) {
+    for (int j = 0; j < T::SN; ++j)
 #pragma unroll
-        for (int j = 0; j < T::PW / 16; ++j)
-#pragma unroll
-            for (int i = 0; i < T::SM; ++i)
-                *reinterpret_cast<f32x4_t*>(tile + wave * OF_WAVE + (16 * i + (lane & 15)) * T::PITCH + 16 * j + 4 * (lane >> 4)) =
-                    acc[piece * (T::PW / 16) + j][i];
-        if constexpr (T::WK == 1) __builtin_amdgcn_wave_barrier();   // the wave's own LDS operations stay in order
-        else __syncthreads();
-        constexpr int ACROSS = T::PW / 8;                // lanes of a row
-        constexpr int ITEMS = T::TM * ACROSS, AT_ONCE = 64 * T::WK;
+        for (int i = 0; i < T::SM; ++i)
+            *reinterpret_cast<f32x4_t*>(tile + wave * OF_WAVE + (16 * i + (lane & 15)) * T::PITCH + 16 * j + 4 * (lane >> 4)) = acc[j][i];
+    __syncthreads();
+    constexpr int ACROSS = T::TN / 8;                    // lanes of a row
+    constexpr int ITEMS = T::TM * ACROSS, AT_ONCE = 64 * T::WK;
 #pragma unroll 2
-        for (int i = 0; i < (ITEMS + AT_ONCE - 1) / AT_ONCE; ++i) {
-            const int r = ((i * T::WK + group) * 64 + lane) / ACROSS, c = (lane % ACROSS) * 8;
-            if (ITEMS % AT_ONCE && r >= T::TM) continue;
-            const int64_t row = m0 + wm * T::TM + r, col = n0 + wn * T::TN + piece * T::PW + c;
-            if (row >= p.m || col >= p.n) continue;
-            float v[8];
-            load8<true>(tile + w * OF_WAVE, (size_t)r * T::PITCH + c, v);
+    for (int i = 0; i < (ITEMS + AT_ONCE - 1) / AT_ONCE; ++i) {
+        const int r = ((i * T::WK + group) * 64 + lane) / ACROSS, c = (lane % ACROSS) * 8;
+        if (ITEMS % AT_ONCE && r >= T::TM) continue;
+        float v[8];
+        load8<true>(tile + w * OF_WAVE, (size_t)r * T::PITCH + c, v);
 #pragma unroll
-            for (int g = 1; g < T::WK; ++g) {
-                float o[8];
-                load8<true>(tile + (g * T::NW + w) * OF_WAVE, (size_t)r * T::PITCH + c, o);
+        for (int g = 1; g < T::WK; ++g) {
+            float o[8];
+            load8<true>(tile + (g * T::NW + w) * OF_WAVE, (size_t)r * T::PITCH + c, o);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] += o[e];
-            }
-            if (p.splits > 1) {
-                store8<true>(p.parts, ((size_t)split * p.m + row) * p.n + col, v);
-                continue;
-            }
-            if (p.add) {
-                float o[8];
-                load8<EXACT>(p.add, row * p.add_stride + col, o);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] += o[e];
-            }
-            store8<EXACT>(p.out, row * p.out_stride + col, v);
+            for (int e = 0; e < 8; ++e) v[e] += o[e];
         }
-        if constexpr (T::WK == 1) __builtin_amdgcn_wave_barrier();
-        else __syncthreads();
+        leave(m0 + wm * T::TM + r, n0 + wn * T::TN + c, v);
     }
 }
 
