@@ -43,6 +43,7 @@ struct Tensors {
         int64_t bytes;      // from its first to its last element
         int64_t row, pitch; // bytes of a row and from row to row; pitch 0: dense
         bool out;
+        int64_t part = 0, part_pitch = 0;   // of parts that make up every row at one distance, rows too; 0: whole rows
     };
     One list[24];
     int n = 0;
@@ -53,14 +54,30 @@ struct Tensors {
         list[n++] = One{name, p, p ? bytes : 0, cols * size, stride == cols || rows <= 1 ? 0 : stride * size, out};
     }
 
+    // rows of `parts` parts of `cols` elements each, `part_stride` elements apart
+    void add_parts(const char* name, const void* p, int64_t rows, int64_t parts, int64_t cols, int64_t part_stride, int64_t stride, int64_t size, bool out) {
+        add(name, p, rows, (parts - 1) * part_stride + cols, stride, size, out);
+        if (parts > 1 && (rows <= 1 || stride % part_stride == 0)) {
+            list[n - 1].part = cols * size;
+            list[n - 1].part_pitch = part_stride * size;
+        }
+    }
+
+    // Whether pieces of `row` bytes, `pitch` apart, from p on meet those of `other` bytes from q on.
+    static bool between(const void* p, int64_t row, const void* q, int64_t other, int64_t pitch) {
+        const int64_t d = (int64_t)(((uintptr_t)q - (uintptr_t)p) % (uintptr_t)pitch);
+        const int64_t gap = (uintptr_t)q >= (uintptr_t)p ? d : (pitch - (int64_t)(((uintptr_t)p - (uintptr_t)q) % (uintptr_t)pitch)) % pitch;
+        return gap < row || gap + other > pitch;
+    }
+
     // An output and another tensor share an element?  Two views with the same
-    // pitch may lie between each other's rows (columns of one wider array).
+    // pitch may lie between each other's rows (columns of one wider array), or
+    // between each other's parts (heads of q, k and v in turn).
     static bool share(const One& a, const One& b) {
         if (!meet(a.p, a.bytes, b.p, b.bytes)) return false;
+        if (a.part_pitch && a.part_pitch == b.part_pitch && !between(a.p, a.part, b.p, b.part, a.part_pitch)) return false;
         if (a.pitch == 0 || a.pitch != b.pitch) return true;
-        const int64_t d = (int64_t)(((uintptr_t)b.p - (uintptr_t)a.p) % (uintptr_t)a.pitch);
-        const int64_t gap = (uintptr_t)b.p >= (uintptr_t)a.p ? d : (a.pitch - (int64_t)(((uintptr_t)a.p - (uintptr_t)b.p) % (uintptr_t)a.pitch)) % a.pitch;
-        return gap < a.row || gap + b.row > a.pitch;
+        return between(a.p, a.row, b.p, b.row, a.pitch);
     }
 
     // `may`: outputs that may be exactly the input `same`

@@ -80,7 +80,7 @@ bool head_strides(int64_t& token, int64_t& head, int heads, int D) {
 }
 
 void add_heads(Tensors& ts, const char* name, const void* p, int64_t T, int heads, int D, int64_t token, int64_t head, int64_t size, bool out) {
-    if (heads > 0) ts.add(name, p, T, (heads - 1) * head + D, token, size, out);
+    if (heads > 0) ts.add_parts(name, p, T, heads, D, head, token, size, out);
 }
 
 int64_t rotary_bytes(const mega_moe_rotary_backward_args& a) {

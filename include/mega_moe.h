@@ -732,7 +732,8 @@ typedef struct mega_moe_rotary_args {
     const float* inv_freq;    /* [R/2] (mega_moe_rotary_frequencies)             */
     void* q_out;              /* [T, q_heads, D]; may be q itself (same strides) */
     void* k_out;              /* [T, k_heads, D]; may be k itself                */
-    int64_t q_stride, k_stride, q_out_stride, k_out_stride;  /* of a token, of 8; 0: dense */
+    int64_t q_stride, k_stride, q_out_stride, k_out_stride;
+                              /* of a token, whose heads it holds; of 8; 0: dense */
     int64_t q_head_stride, k_head_stride, q_out_head_stride, k_out_head_stride;
                               /* of a head: >= D, of 8, up to 2^20; 0: D         */
 } mega_moe_rotary_args;

@@ -143,6 +143,24 @@ def test_good_calls_pass_the_checks_and_stop_at_the_device():
         assert ei.value.code in (B.MEGA_MOE_ERR_HIP, B.MEGA_MOE_ERR_UNSUPPORTED), B.mega_moe_last_error()
 
 
+# heads of q, k and v in turn: [tokens, heads, 3, 64]
+IN_TURN = dict(q_heads=4, k_heads=4, q=M, k=M + 128)
+IN_TURN_STRIDES = dict(q_stride=768, k_stride=768, q_head_stride=192, k_head_stride=192)
+
+
+@pytest.mark.parametrize("kw,good", [
+    (dict(q_out=M, k_out=M + 128), True), (dict(q_out=7 * M, k_out=7 * M + 128), True), (dict(q_out=M + 256, k_out=7 * M), True),
+    (dict(q_out=M + 64, k_out=7 * M), False), (dict(q_out=7 * M, k_out=7 * M + 112), False), (dict(q_out=M + 128, k_out=M), False),
+    (dict(q_out=7 * M, k_out=7 * M + 128, q_out_stride=776), False), (dict(q_out=M, k_out=M + 128, k_out_head_stride=128), False)])
+def test_heads_in_turn_pass_the_checks_where_they_do_not_meet(kw, good):
+    if good and torch.cuda.is_available():
+        pytest.skip("a GPU is present: stand-in pointers must not reach it")
+    args = _rotary(**IN_TURN, **IN_TURN_STRIDES, **{**dict(q_out_stride=768, k_out_stride=768, q_out_head_stride=192, k_out_head_stride=192), **kw})
+    with pytest.raises(B.MegaMoEError) as ei:
+        B.mega_moe_rotary(args, None)
+    assert (ei.value.code == B.MEGA_MOE_ERR_INVALID_ARG) == (not good), B.mega_moe_last_error()
+
+
 def test_workspace_bytes_need_no_gpu_and_refuse_bad_sizes():
     assert B.mega_moe_product_workspace_bytes(_product(a=None, workspace=None)) >= 0
     assert B.mega_moe_product_workspace_bytes(_product(k=0)) == 0

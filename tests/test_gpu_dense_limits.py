@@ -135,6 +135,39 @@ def test_head_gradients_beyond_32_bit_offsets():
     U.near(dw, want[2], want[3], 96 + 2 * T, "dw")
 
 
+# ---- heads of q, k and v in turn ----------------------------------------------------------------
+
+@pytest.mark.parametrize("T", [1, 37, 600])
+def test_heads_in_turn_are_turned_in_place(T):
+    g = D.generator(T)
+    heads, dim = 5, 64
+    buf = D.randn(g, T, heads, 3, dim, dtype=BF16)
+    first, d = buf.clone(), D.randn(g, T, heads, 3, dim, dtype=BF16)
+    grads = d.clone()
+    weight = 1 + D.randn(g, dim, scale=0.1)
+    freq = torch.tensor([10000.0 ** (-i / 32) for i in range(32)], device="cuda")
+    dw = _new(2, dim)
+    f = dict(num_tokens=T, q_heads=heads, k_heads=heads, head_dim=dim, rotary_dim=dim, weight_type=B.MEGA_MOE_F32, eps=1e-6, inv_freq=freq,
+             q_weight=weight, k_weight=weight)
+    names = lambda *n: {k: v for name in n for k, v in ((name + "_stride", 3 * heads * dim), (name + "_head_stride", 3 * dim))}   # noqa: E731
+    q, k = buf[:, :, 0], buf[:, :, 1]
+    B.mega_moe_rotary(B.make_args(B.mega_moe_rotary_args, q=q, k=k, q_out=q, k_out=k, **f, **names("q", "k", "q_out", "k_out")),
+                      U.current_stream())
+    dq, dk, x = grads[:, :, 0], grads[:, :, 1], first
+    args = B.make_args(B.mega_moe_rotary_backward_args, q=x[:, :, 0], k=x[:, :, 1], dq_out=dq, dk_out=dk, dq=dq, dk=dk, dq_weight=dw[0],
+                       dk_weight=dw[1], **f, **names("q", "k", "dq_out", "dk_out", "dq", "dk"))
+    B.set_args(args, **U.workspace(B.mega_moe_rotary_workspace_bytes(args)))
+    B.mega_moe_rotary_backward(args, U.current_stream())
+    for i in range(2):
+        x = U.f64(first[:, :, i])
+        want, mag = dense.rotary(x, U.f64(weight), range(T), U.f64(freq), eps=1e-6)
+        U.near(buf[:, :, i], want, mag, 40, f"heads {i}")
+        want = dense.rotary_backward(x, U.f64(weight), U.f64(d[:, :, i]), range(T), U.f64(freq), eps=1e-6)
+        U.near(grads[:, :, i], want[0], want[1], 96, f"gradients {i}")
+        U.near(dw[i], want[2], want[3], 96 + heads * T, f"weight {i}")
+    assert torch.equal(buf[:, :, 2], first[:, :, 2]) and torch.equal(grads[:, :, 2], d[:, :, 2])
+
+
 # ---- memory behind the last row -----------------------------------------------------------------
 
 @pytest.mark.parametrize("m", [1, 13, 61, 129, 300])
