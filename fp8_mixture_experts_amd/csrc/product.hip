@@ -452,15 +452,17 @@ __global__ void __launch_bounds__(T::NT) moe_product(ProductArgs p) {
     }
 }
 
-// Up to 16 rows of a: a workgroup has 16 rows of b over all of k, its eight waves every
-// eighth step each, from memory into registers, and their sums
-// meet in LDS.  b is read once and by no other workgroup, so it streams past the
-// caches; a comes from the caches.  Memory bounds it: 1 x 7168 x 4096 7.9 us with the call (29 MB), 1 x 7168 x
-// 18432 from HBM 33 us (4.0 TB/s; the 32-row tiles 34). Eight steps in flight to a wave; 16 rows read
-// as much of a as of b, and large n goes to the tiles then (18432: 48 us against 34).
-template <bool EXACT, bool ROWS>
-__global__ void __launch_bounds__(512) moe_product_few(ProductArgs p) {
-    constexpr int W = 8, U = 4, PITCH = 20;
+// Up to 16 rows of a: a workgroup has 16 rows of b over all of k, its W waves every W-th step each, from memory
+// into registers, and their sums meet in LDS.  b is read once and by no other workgroup; a comes from
+// the caches.  Memory bounds it.  Up to 256 workgroups (and with F32 results, whose operands fill the registers) 16
+// waves of two steps at a time, and two ahead: 1 x 7168 x 4096 6.9 us, from HBM 7.6 (29 MB; eight waves of four steps
+// 7.2 and 7.8). More of them two to a compute unit, of eight waves of three steps: 1 x 7168 x 18432 from HBM
+// 25.9 us (5.1 TB/s; 16 waves 29.5). Loads of b past the caches took 10% longer, whole lines of
+// eight rows to a load 5%. 16 rows read as much of a as of b, and large n goes to the tiles then (18432:
+// 42 us against 34).
+template <bool EXACT, bool ROWS, bool PAIRED>
+__global__ void __launch_bounds__(PAIRED ? 512 : 1024, 4) moe_product_few(ProductArgs p) {
+    constexpr int W = PAIRED ? 8 : 16, U = PAIRED ? 3 : 2, PITCH = 20;
     __shared__ __attribute__((aligned(16))) float sums[W][16][PITCH];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, g = lane >> 4;
@@ -481,14 +483,16 @@ __global__ void __launch_bounds__(512) moe_product_few(ProductArgs p) {
     const auto fetch = [&](Step& s, int step) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            s.b[h] = __builtin_amdgcn_raw_buffer_load_b128(rb, voff_b + 64 * h, step * BK, 2);
+            s.b[h] = __builtin_amdgcn_raw_buffer_load_b128(rb, voff_b + 64 * h, step * BK, 0);
             s.a[h] = __builtin_amdgcn_raw_buffer_load_b128(ra, voff_a + 64 * h, step * BK, 0);
         }
         s.sa = __builtin_amdgcn_raw_buffer_load_b32(rsa, voff_sa, step * 4, 0);
-        s.sb = __builtin_amdgcn_raw_buffer_load_b32(rsb, voff_sb, step * 4, 0);
+        if constexpr (ROWS) s.sb = __builtin_amdgcn_raw_buffer_load_b32(rsb, voff_sb, step * 4, 0);
     };
+    typedef const __attribute__((address_space(4))) float* constants_t;
+    const constants_t b_sf = (constants_t)(ROWS ? nullptr : p.b_sf + n0 / 128 * p.b_sf_stride);
     f32x4_t acc = f32x4_t{};
-    const auto add_step = [&](const Step& s) {
+    const auto add_step = [&](const Step& s, int step) {
         const Ready<EXACT> y(__builtin_bit_cast(i32x8_t, __builtin_shufflevector(s.b[0], s.b[1], 0, 1, 2, 3, 4, 5, 6, 7)));
         const Ready<EXACT> x(__builtin_bit_cast(i32x8_t, __builtin_shufflevector(s.a[0], s.a[1], 0, 1, 2, 3, 4, 5, 6, 7)));
         f32x4_t d = f32x4_t{};
@@ -497,7 +501,7 @@ __global__ void __launch_bounds__(512) moe_product_few(ProductArgs p) {
         const float sa = __uint_as_float(s.sa);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const float sb = ROWS ? __shfl(__uint_as_float(s.sb), 4 * g + e) : __uint_as_float(s.sb);
+            const float sb = ROWS ? __shfl(__uint_as_float(s.sb), 4 * g + e) : b_sf[step];
             acc[e] = fmaf(d[e], sa * sb, acc[e]);
         }
     };
@@ -512,7 +516,7 @@ __global__ void __launch_bounds__(512) moe_product_few(ProductArgs p) {
             if (step + W * (U + u) < p.steps) fetch(next[u], step + W * (U + u));
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (step + W * u < p.steps) add_step(now[u]);
+            if (step + W * u < p.steps) add_step(now[u], step + W * u);
 #pragma unroll
         for (int u = 0; u < U; ++u) now[u] = next[u];
     }
@@ -586,35 +590,36 @@ int64_t tiles_of(int m, int n, int bm, int bn) { return (int64_t)((m + bm - 1) /
 
 // What a kind takes, in us, beside the 2 of any call, with f tiles on the busiest of 256 compute units
 // and s steps: f * tile + s * step for each tile, or s * alone for the last of an odd f where
-// two share a compute unit; and what splitting it adds. Fitted (non-negative least
-// squares of relative errors) to 131 shapes of m in [1, 8192], k in [128, 8192], n in [64, 18432], with
+// two share a compute unit (few rows: tile + f * s * (step + alone * m / 16), of b's rows and of a's); and what
+// splitting it adds. Fitted (non-negative least
+// squares of relative errors) to 146 shapes of m in [1, 8192], k in [128, 8192], n in [64, 18432], with
 // operands that come from HBM (from the last-level cache the small tiles' steps take a fifth less): the
-// least of them is on average within 2% of the fastest of all measured, 19% (F32: 22%) at worst. Beside these,
-// 128 x 64 (with and without two groups) and 256 x 128 were measured; without them the choice is no worse.
-// With F32 results Strip and Long are never the fastest.
+// least of them is on average within 1% of the fastest of all measured, 15% at worst (F32: 2% and 19%). Beside these,
+// 128 x 64 (with and without two groups), 192 x 128, 256 x 128 and (BF16) 128 x 256 were measured; without them the choice
+// is no worse. With F32 results Strip and Long are never the fastest.
 struct Kind {
     int rows, columns;
     float tile, step, alone;
 };
 enum { FEW, LOW, STRIP, DEEP, PAIR, MID, LONG, WIDE, KINDS };
 constexpr float NEVER = INFINITY;
-constexpr Kind FP8[KINDS] = {{16, 16, 1.21f, 0.091f, 0.091f},     // few rows (16 columns to a workgroup)
-                             {32, 32, 2.22f, 0.125f, 0.125f},
-                             {32, 64, 2.59f, 0.178f, 0.178f},
-                             {64, 64, 2.12f, 0.262f, 0.262f},
-                             {64, 64, 1.27f, 0.214f, 0.355f},
-                             {128, 128, 1.93f, 0.551f, 0.749f},
-                             {128, 128, 2.78f, 0.535f, 0.535f},
-                             {256, 256, 4.37f, 1.283f, 1.283f}};
-constexpr Kind EXACT_F32[KINDS] = {{16, 16, 1.21f, 0.091f, 0.091f},
-                                   {32, 32, 2.59f, 0.145f, 0.145f},
+constexpr Kind FP8[KINDS] = {{16, 16, 1.37f, 0.069f, 0.063f},
+                             {32, 32, 2.23f, 0.128f, 0.128f},
+                             {32, 64, 2.63f, 0.182f, 0.182f},
+                             {64, 64, 2.11f, 0.264f, 0.264f},
+                             {64, 64, 1.22f, 0.215f, 0.379f},
+                             {128, 128, 1.60f, 0.557f, 0.758f},
+                             {128, 128, 2.39f, 0.528f, 0.528f},
+                             {256, 256, 3.26f, 1.273f, 1.273f}};
+constexpr Kind EXACT_F32[KINDS] = {{16, 16, 1.34f, 0.107f, 0.064f},
+                                   {32, 32, 2.58f, 0.147f, 0.147f},
                                    {32, 64, NEVER, 0.0f, 0.0f},
-                                   {64, 64, 3.14f, 0.370f, 0.370f},
-                                   {64, 64, 1.70f, 0.342f, 0.613f},
-                                   {128, 128, 3.74f, 0.891f, 1.200f},
+                                   {64, 64, 3.10f, 0.370f, 0.370f},
+                                   {64, 64, 1.72f, 0.346f, 0.603f},
+                                   {128, 128, 3.47f, 0.898f, 1.196f},
                                    {128, 128, NEVER, 0.0f, 0.0f},
-                                   {128, 256, 4.99f, 1.728f, 1.728f}};
-constexpr float JOIN = 3.9f, JOIN_ELEMENT = 1.4e-6f;        // a second launch, and its sums
+                                   {128, 256, 4.69f, 1.682f, 1.682f}};
+constexpr float JOIN = 3.9f, JOIN_ELEMENT = 1.5e-6f;        // a second launch, and its sums
 
 template <typename T, bool EXACT, bool ROWS>
 void go(const ProductArgs& p, hipStream_t stream) {
@@ -626,9 +631,12 @@ void go(const ProductArgs& p, hipStream_t stream) {
 template <bool EXACT, bool ROWS>
 void go(int kind, const ProductArgs& p, hipStream_t stream) {
     switch (kind) {
-        case FEW:
-            hipLaunchKernelGGL((moe_product_few<EXACT, ROWS>), dim3((unsigned)((p.n + 15) / 16)), dim3(512), 0, stream, p);
+        case FEW: {
+            const unsigned blocks = (unsigned)((p.n + 15) / 16);
+            if (EXACT || blocks <= 256) hipLaunchKernelGGL((moe_product_few<EXACT, ROWS, false>), dim3(blocks), dim3(1024), 0, stream, p);
+            else if constexpr (!EXACT) hipLaunchKernelGGL((moe_product_few<EXACT, ROWS, true>), dim3(blocks), dim3(512), 0, stream, p);
             break;
+        }
         case LOW: go<Low, EXACT, ROWS>(p, stream); break;
         case DEEP: go<Deep, EXACT, ROWS>(p, stream); break;
         case PAIR: go<Pair, EXACT, ROWS>(p, stream); break;
@@ -656,8 +664,8 @@ ProductPlan product_plan(int m, int n, int k, int out_type) {
         // parts of the steps only where a compute unit would have no tile without them
         for (int splits = 1; splits == 1 || (kind != FEW && splits <= steps && tiles * splits <= 512 && splits <= 64); splits *= 2) {
             if (kind == LONG && tiles * splits > 256) break;
-            const int64_t f = (tiles * splits + 255) / 256;
-            float us = f * o.tile + (float)((steps + splits - 1) / splits) * ((f - f % 2) * o.step + f % 2 * o.alone);
+            const int64_t f = (tiles * splits + 255) / 256, s = (steps + splits - 1) / splits;
+            float us = kind == FEW ? o.tile + f * s * (o.step + o.alone * m / 16.0f) : f * o.tile + s * ((f - f % 2) * o.step + f % 2 * o.alone);
             if (splits > 1) us += JOIN + JOIN_ELEMENT * splits * (float)m * n;
             if (us < least) {
                 least = us;
