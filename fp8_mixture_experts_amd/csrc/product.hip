@@ -578,9 +578,10 @@ using Wide = Tile<256, 256, 4, 2, 1, 2>;
 using WideExact = Tile<128, 256, 2, 4, 1, 2>; // in its place with F32 results: the conversions' registers
                                               // leave no room for 256 x 256 (4096 x 4096 x 2048: 67 us, Mid 74)
 using Mid = Tile<128, 128, 2, 2, 1, 2>;       // two workgroups to a compute unit
-using Long = Tile<128, 128, 2, 2, 1, 4>;      // one, with three rounds in flight: only up to 256 tiles, which have a
-                                              // compute unit each anyway (1024 x 7168 x 4096: 37 us, Mid 42; from HBM
-                                              // 41 and 55; but 2048 x 7168 x 4096: 73 us, Mid 61)
+using Long = Tile<128, 128, 4, 2, 1, 4>;      // one, of eight waves with three rounds in flight: only up to 256 tiles,
+                                              // which have a compute unit each anyway (1024 x 7168 x 4096: 34 us, Mid
+                                              // 40; from HBM 39 and 55; but 2048 x 7168 x 4096: 73 us, Mid 61)
+using Half = Tile<64, 128, 2, 2, 2, 3>;       // one, of two groups of waves (512 x 7168 x 4096: 21.5 us, Pair 25.5)
 using Pair = Tile<64, 64, 2, 2, 1, 3>;        // two or three workgroups
 using Deep = Tile<64, 64, 2, 2, 2, 3>;        // one, of two groups of waves
 using Strip = Tile<32, 64, 1, 2, 4, 3>;       // (128 x 7168 x 4096 from HBM: 16.6 us, Deep's halves 18.2)
@@ -592,34 +593,37 @@ int64_t tiles_of(int m, int n, int bm, int bn) { return (int64_t)((m + bm - 1) /
 // and s steps: f * tile + s * step for each tile, or s * alone for the last of an odd f where
 // two share a compute unit (few rows: tile + f * s * (step + alone * m / 16), of b's rows and of a's); and what
 // splitting it adds. Fitted (non-negative least
-// squares of relative errors) to 146 shapes of m in [1, 8192], k in [128, 8192], n in [64, 18432], with
+// squares of relative errors) to 153 shapes of m in [1, 8192], k in [128, 8192], n in [64, 18432], with
 // operands that come from HBM (from the last-level cache the small tiles' steps take a fifth less): the
-// least of them is on average within 1% of the fastest of all measured, 15% at worst (F32: 2% and 19%). Beside these,
+// least of them is on average within 1% of the fastest of all measured, 13% at worst (F32: 2% and 19%). Beside these,
 // 128 x 64 (with and without two groups), 192 x 128, 256 x 128 and (BF16) 128 x 256 were measured; without them the choice
-// is no worse. With F32 results Strip and Long are never the fastest.
+// is no worse but at single shapes (576 x 2048 x 7168: 192 x 128 18 us, Mid 20). With F32 results Strip,
+// Half and Long are hardly ever the fastest.
 struct Kind {
     int rows, columns;
     float tile, step, alone;
 };
-enum { FEW, LOW, STRIP, DEEP, PAIR, MID, LONG, WIDE, KINDS };
+enum { FEW, LOW, STRIP, DEEP, PAIR, HALF, MID, LONG, WIDE, KINDS };
 constexpr float NEVER = INFINITY;
-constexpr Kind FP8[KINDS] = {{16, 16, 1.37f, 0.069f, 0.063f},
-                             {32, 32, 2.23f, 0.128f, 0.128f},
-                             {32, 64, 2.63f, 0.182f, 0.182f},
-                             {64, 64, 2.11f, 0.264f, 0.264f},
-                             {64, 64, 1.22f, 0.215f, 0.379f},
-                             {128, 128, 1.60f, 0.557f, 0.758f},
-                             {128, 128, 2.39f, 0.528f, 0.528f},
-                             {256, 256, 3.26f, 1.273f, 1.273f}};
-constexpr Kind EXACT_F32[KINDS] = {{16, 16, 1.34f, 0.107f, 0.064f},
-                                   {32, 32, 2.58f, 0.147f, 0.147f},
+constexpr Kind FP8[KINDS] = {{16, 16, 1.45f, 0.067f, 0.062f},
+                             {32, 32, 2.25f, 0.128f, 0.128f},
+                             {32, 64, 2.62f, 0.182f, 0.182f},
+                             {64, 64, 2.13f, 0.265f, 0.265f},
+                             {64, 64, 1.23f, 0.213f, 0.382f},
+                             {64, 128, 2.44f, 0.383f, 0.383f},
+                             {128, 128, 1.58f, 0.558f, 0.768f},
+                             {128, 128, 2.21f, 0.519f, 0.519f},
+                             {256, 256, 3.29f, 1.275f, 1.275f}};
+constexpr Kind EXACT_F32[KINDS] = {{16, 16, 0.96f, 0.112f, 0.067f},
+                                   {32, 32, 2.61f, 0.146f, 0.146f},
                                    {32, 64, NEVER, 0.0f, 0.0f},
-                                   {64, 64, 3.10f, 0.370f, 0.370f},
-                                   {64, 64, 1.72f, 0.346f, 0.603f},
-                                   {128, 128, 3.47f, 0.898f, 1.196f},
+                                   {64, 64, 3.10f, 0.371f, 0.371f},
+                                   {64, 64, 1.70f, 0.345f, 0.603f},
+                                   {64, 128, NEVER, 0.0f, 0.0f},
+                                   {128, 128, 3.48f, 0.886f, 1.194f},
                                    {128, 128, NEVER, 0.0f, 0.0f},
-                                   {128, 256, 4.69f, 1.682f, 1.682f}};
-constexpr float JOIN = 3.9f, JOIN_ELEMENT = 1.5e-6f;        // a second launch, and its sums
+                                   {128, 256, 4.69f, 1.677f, 1.677f}};
+constexpr float JOIN = 3.9f, JOIN_ELEMENT = 1.6e-6f;        // a second launch, and its sums
 
 template <typename T, bool EXACT, bool ROWS>
 void go(const ProductArgs& p, hipStream_t stream) {
@@ -643,6 +647,9 @@ void go(int kind, const ProductArgs& p, hipStream_t stream) {
         case MID: go<Mid, EXACT, ROWS>(p, stream); break;
         case STRIP:
             if constexpr (!EXACT) go<Strip, EXACT, ROWS>(p, stream);
+            break;
+        case HALF:
+            if constexpr (!EXACT) go<Half, EXACT, ROWS>(p, stream);
             break;
         case LONG:
             if constexpr (!EXACT) go<Long, EXACT, ROWS>(p, stream);
