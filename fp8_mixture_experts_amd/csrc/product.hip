@@ -581,6 +581,7 @@ using Mid = Tile<128, 128, 2, 2, 1, 2>;       // two workgroups to a compute uni
 using Long = Tile<128, 128, 4, 2, 1, 4>;      // one, of eight waves with three rounds in flight: only up to 256 tiles,
                                               // which have a compute unit each anyway (1024 x 7168 x 4096: 34 us, Mid
                                               // 40; from HBM 39 and 55; but 2048 x 7168 x 4096: 73 us, Mid 61)
+using Tall = Tile<192, 128, 4, 2, 1, 3>;      // one (576 x 2048 x 7168: 16.2 us, Mid 17.7; 417 x 3328 x 10288 24.7 and 31.1)
 using Half = Tile<64, 128, 2, 2, 2, 3>;       // one, of two groups of waves (512 x 7168 x 4096: 21.5 us, Pair 25.5)
 using Pair = Tile<64, 64, 2, 2, 1, 3>;        // two or three workgroups
 using Deep = Tile<64, 64, 2, 2, 2, 3>;        // one, of two groups of waves
@@ -595,15 +596,14 @@ int64_t tiles_of(int m, int n, int bm, int bn) { return (int64_t)((m + bm - 1) /
 // splitting it adds. Fitted (non-negative least
 // squares of relative errors) to 153 shapes of m in [1, 8192], k in [128, 8192], n in [64, 18432], with
 // operands that come from HBM (from the last-level cache the small tiles' steps take a fifth less): the
-// least of them is on average within 1% of the fastest of all measured, 13% at worst (F32: 2% and 19%). Beside these,
-// 128 x 64 (with and without two groups), 192 x 128, 256 x 128 and (BF16) 128 x 256 were measured; without them the choice
-// is no worse but at single shapes (576 x 2048 x 7168: 192 x 128 18 us, Mid 20). With F32 results Strip,
-// Half and Long are hardly ever the fastest.
+// least of them is on average within 1% of the fastest of all measured, 12% at worst (F32: 2% and 19%). Beside these,
+// 128 x 64 (with and without two groups), 256 x 128 and (BF16) 128 x 256 were measured; without them the choice
+// is no worse. With F32 results Strip, Half, Tall and Long are hardly ever the fastest.
 struct Kind {
     int rows, columns;
     float tile, step, alone;
 };
-enum { FEW, LOW, STRIP, DEEP, PAIR, HALF, MID, LONG, WIDE, KINDS };
+enum { FEW, LOW, STRIP, DEEP, PAIR, HALF, MID, TALL, LONG, WIDE, KINDS };
 constexpr float NEVER = INFINITY;
 constexpr Kind FP8[KINDS] = {{16, 16, 1.45f, 0.067f, 0.062f},
                              {32, 32, 2.25f, 0.128f, 0.128f},
@@ -612,6 +612,7 @@ constexpr Kind FP8[KINDS] = {{16, 16, 1.45f, 0.067f, 0.062f},
                              {64, 64, 1.23f, 0.213f, 0.382f},
                              {64, 128, 2.44f, 0.383f, 0.383f},
                              {128, 128, 1.58f, 0.558f, 0.768f},
+                             {192, 128, 2.53f, 0.678f, 0.678f},
                              {128, 128, 2.21f, 0.519f, 0.519f},
                              {256, 256, 3.29f, 1.275f, 1.275f}};
 constexpr Kind EXACT_F32[KINDS] = {{16, 16, 0.96f, 0.112f, 0.067f},
@@ -621,6 +622,7 @@ constexpr Kind EXACT_F32[KINDS] = {{16, 16, 0.96f, 0.112f, 0.067f},
                                    {64, 64, 1.70f, 0.345f, 0.603f},
                                    {64, 128, NEVER, 0.0f, 0.0f},
                                    {128, 128, 3.48f, 0.886f, 1.194f},
+                                   {192, 128, NEVER, 0.0f, 0.0f},
                                    {128, 128, NEVER, 0.0f, 0.0f},
                                    {128, 256, 4.69f, 1.677f, 1.677f}};
 constexpr float JOIN = 3.9f, JOIN_ELEMENT = 1.6e-6f;        // a second launch, and its sums
@@ -650,6 +652,9 @@ void go(int kind, const ProductArgs& p, hipStream_t stream) {
             break;
         case HALF:
             if constexpr (!EXACT) go<Half, EXACT, ROWS>(p, stream);
+            break;
+        case TALL:
+            if constexpr (!EXACT) go<Tall, EXACT, ROWS>(p, stream);
             break;
         case LONG:
             if constexpr (!EXACT) go<Long, EXACT, ROWS>(p, stream);

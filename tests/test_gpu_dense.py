@@ -38,7 +38,7 @@ def test_product(m, k, n, out_type, scale):
 # sizes that go through each of the kinds of tiles, whole and split, with rows and columns left over
 KINDS = [(33, 1664, 8440), (33, 10240, 1112), (133, 640, 11064), (1027, 10240, 72), (1025, 10240, 8), (1, 1152, 8200), (1, 16384, 520),
          (129, 10240, 5576), (65, 2944, 8424), (67, 7168, 2744), (259, 128, 10952), (65, 128, 8840), (1025, 128, 7208), (33, 896, 4136),
-         (1, 1664, 12408), (65, 16384, 1416), (1, 10240, 136), (13, 384, 6504), (3, 16384, 1032)]
+         (1, 1664, 12408), (65, 16384, 1416), (1, 10240, 136), (13, 384, 6504), (3, 16384, 1032), (523, 16384, 8)]
 
 
 @pytest.mark.parametrize("m,k,n", KINDS)
