@@ -57,10 +57,14 @@ def product(*args, stream=None, **kw):
     B.mega_moe_product(product_args(*args, **kw), U.current_stream() if stream is None else stream)
 
 
-def check_product(out, a, a_sf, b, b_sf, scale, add=None, label=""):
+def reference(a, a_sf, b, b_sf, scale, add=None):
+    return dense.product(U.codes(a), U.f64(a_sf), U.codes(b), U.f64(b_sf), scale == "row", None if add is None else U.f64(add))
+
+
+def check_product(out, a, a_sf, b, b_sf, scale, add=None, label="", ref=None):
     """Every element within its type's half step and float32's roundings (a sum of k products of two
     scales; with a BF16 output what the instruction leaves out)."""
-    want, mag, cut = dense.product(U.codes(a), U.f64(a_sf), U.codes(b), U.f64(b_sf), scale == "row", None if add is None else U.f64(add))
+    want, mag, cut = reference(a, a_sf, b, b_sf, scale, add) if ref is None else ref
     k = a.shape[1]
     # products are exact; k additions, the scales' product, their application, `add`
     roundings = k + k // 128 + 4
