@@ -385,16 +385,22 @@ __global__ void __launch_bounds__(T::NT) moe_product(ProductArgs p) {
             place = next;
         }
     }
+    const bool adds = p.add && p.splits == 1;
+    const auto load_add = [&](int64_t row, int64_t col, u32x4_t (&o)[EXACT ? 2 : 1]) {
+        const bool real = adds && row < p.m && col < p.n;
+#pragma unroll
+        for (int h = 0; h < (EXACT ? 2 : 1); ++h) o[h] = real ? raw8<EXACT>(p.add, row * p.add_stride + col)[h] : u32x4_t{0u, 0u, 0u, 0u};
+    };
     // Eight results of a row leave the lane that has them.
-    const auto leave = [&](int64_t row, int64_t col, float (&v)[8]) {
+    const auto leave = [&](int64_t row, int64_t col, float (&v)[8], const u32x4_t (&add)[EXACT ? 2 : 1]) {
         if (row >= p.m || col >= p.n) return;
         if (p.splits > 1) {
             store8<true>(p.parts, ((size_t)split * p.m + row) * p.n + col, v);
             return;
         }
-        if (p.add) {
+        if (adds) {
             float o[8];
-            load8<EXACT>(p.add, row * p.add_stride + col, o);
+            values8<EXACT>(add, o);
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] += o[e];
         }
@@ -408,8 +414,16 @@ __global__ void __launch_bounds__(T::NT) moe_product(ProductArgs p) {
         // x 7168 with an addend 172 us, not 162, and 4096 x 512 x 4096 with F32 results 34.5, not 32.4.)
         const int g = lane >> 4;
         const int64_t row0 = m0 + wm * T::TM + (lane & 15), col0 = n0 + wn * T::TN + (g & 1) * 16 + (g >> 1) * 8;
+        // (the addend a row of blocks ahead of the stores: it may be the output itself, whose stores its loads wait for)
+        u32x4_t add[2][T::SN / 2][EXACT ? 2 : 1];
+        const auto load_row = [&](int i) {
 #pragma unroll
-        for (int i = 0; i < T::SM; ++i)
+            for (int j = 0; j < T::SN; j += 2) load_add(row0 + 16 * i, col0 + 16 * j, add[i & 1][j / 2]);
+        };
+        if (adds) load_row(0);
+#pragma unroll
+        for (int i = 0; i < T::SM; ++i) {
+            if (adds && i + 1 < T::SM) load_row(i + 1);
 #pragma unroll
             for (int j = 0; j < T::SN; j += 2) {
                 float v[8];
@@ -419,8 +433,9 @@ __global__ void __launch_bounds__(T::NT) moe_product(ProductArgs p) {
                     v[e] = __uint_as_float(x[0]);
                     v[4 + e] = __uint_as_float(x[1]);
                 }
-                leave(row0 + 16 * i, col0 + 16 * j, v);
+                leave(row0 + 16 * i, col0 + 16 * j, v, add[i & 1][j / 2]);
             }
+        }
         return;
     }
     __syncthreads();                                     // every wave has read its last stage
@@ -448,7 +463,9 @@ __global__ void __launch_bounds__(T::NT) moe_product(ProductArgs p) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] += o[e];
         }
-        leave(m0 + wm * T::TM + r, n0 + wn * T::TN + c, v);
+        u32x4_t add[EXACT ? 2 : 1];
+        load_add(m0 + wm * T::TM + r, n0 + wn * T::TN + c, add);
+        leave(m0 + wm * T::TM + r, n0 + wn * T::TN + c, v, add);
     }
 }
 
