@@ -54,7 +54,8 @@ def _blocks(lines):
 def _k_loop(lines):
     blocks = [b for b in _blocks(lines) if any("v_mfma" in line for line in b)]
     assert len(blocks) == 1, len(blocks)
-    return blocks[0]
+    # up to the branch that goes on with the loop: behind it is its exit
+    return blocks[0][:max(i for i, line in enumerate(blocks[0]) if "s_cbranch" in line) + 1]
 
 
 @pytest.fixture(scope="module")
