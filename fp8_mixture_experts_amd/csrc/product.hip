@@ -118,14 +118,15 @@ struct Tile {
     static constexpr int LOADS = A_LOADS + B_LOADS;
     static constexpr int OFF_B = BM * BK, STAGE = OFF_B + BN * BK;         // of a group
     static constexpr int ROUND = STAGE * WK;
-    // behind the rounds the scales of eight steps, twice: [row][step] of a, [8 rows][step][row] of b
+    // behind the rounds the scales of eight steps, twice: [row][step] of a, [8 rows][step][row] of b, or
+    // [128 rows][step] (and zeros behind them, as far as a load goes)
     static constexpr int OFF_SFA = S * ROUND, SFA = BM * 32, OFF_SFB = OFF_SFA + 2 * SFA, SFB = BN * 32;
     // two rounds of the widest tile fill LDS; each wave's first columns of b are the even blocks of loads
     static constexpr bool EARLY = SN >= 8 && S == 2 && TN / 2 == 8 * NW;
     static constexpr int PITCH = TN + 4;                 // of the groups' sums, which meet in LDS
     template <bool ROWS>
     static constexpr int lds() {
-        const int a = OFF_SFB + (ROWS ? 2 * SFB : 0), b = WK == 1 ? 0 : WK * NW * TM * PITCH * 4;
+        const int a = OFF_SFB + 2 * (ROWS ? SFB : 256), b = WK == 1 ? 0 : WK * NW * TM * PITCH * 4;
         return a > b ? a : b;
     }
     static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0, "loads");
@@ -186,11 +187,12 @@ __global__ void __launch_bounds__(T::NT) moe_product(ProductArgs p) {
     const uint8_t* const a0 = p.a + m0 * p.a_stride + (int64_t)step0 * BK;
     const uint8_t* const b0 = p.b + n0 * p.b_stride + (int64_t)step0 * BK;
     const float* const a_sf0 = p.a_sf + m0 * p.a_sf_stride + step0;
-    const float* const b_sf0 = ROWS ? p.b_sf + n0 * p.b_sf_stride + step0 : nullptr;
+    const float* const b_sf0 = p.b_sf + (ROWS ? n0 : n0 / 128) * p.b_sf_stride + step0;
+    const int rows_sfb = ROWS ? rows_b : (rows_b + 127) / 128;
     const uint32_t bytes_a = (uint32_t)((rows_a - 1) * p.a_stride + (int64_t)steps * BK);
     const uint32_t bytes_b = (uint32_t)((rows_b - 1) * p.b_stride + (int64_t)steps * BK);
     const uint32_t bytes_sfa = (uint32_t)((rows_a - 1) * p.a_sf_stride + steps) * 4;
-    const uint32_t bytes_sfb = (uint32_t)((rows_b - 1) * p.b_sf_stride + steps) * 4;
+    const uint32_t bytes_sfb = (uint32_t)((rows_sfb - 1) * p.b_sf_stride + steps) * 4;
     // a wave's rows of a step: 8 (NW j + w) + lane / 8, and the chunk that belongs to lane % 8;
     // rows behind the last lie beyond the buffer by this offset alone
     const int r8 = 8 * w + (lane >> 3);
@@ -228,13 +230,9 @@ __global__ void __launch_bounds__(T::NT) moe_product(ProductArgs p) {
         rows_of(a_sf0, bytes_sfa, (int)p.a_sf_stride, T::BM, lds + T::OFF_SFA + (chunk & 1) * T::SFA, lane >> 3, lane & 7);
         if constexpr (ROWS)
             rows_of(b_sf0, bytes_sfb, (int)p.b_sf_stride, T::BN, lds + T::OFF_SFB + (chunk & 1) * T::SFB, lane & 7, lane >> 3);
+        else if (wave == 0)
+            rows_of(b_sf0, bytes_sfb, (int)p.b_sf_stride, 8, lds + T::OFF_SFB + (chunk & 1) * 256, lane >> 3, lane & 7);
     };
-
-    // b's block of scales: one for the wave (tiles start and end with blocks, or within one)
-    const int64_t last_block = (p.n - 1) / 128;
-    // read through the scalar cache: a vector load's wait would be one for the stages in flight too
-    typedef const __attribute__((address_space(4))) float* constants_t;
-    const constants_t b_sf = (constants_t)(ROWS ? nullptr : p.b_sf + min((n0 + wn * T::TN) / 128, last_block) * p.b_sf_stride + step0);
 
     f32x4_t acc[T::SN][T::SM];
 #pragma unroll
@@ -245,11 +243,10 @@ __global__ void __launch_bounds__(T::NT) moe_product(ProductArgs p) {
     // where the wave's rows of a stage are, and its scales
     const int at_x = group * T::STAGE + wm * T::TM * BK, at_y = group * T::STAGE + T::OFF_B + wn * T::TN * BK;
     const int at_sa = T::OFF_SFA + (wm * T::TM + (lane & 15)) * 32, at_sb = T::OFF_SFB + (wn * T::TN + (lane >> 5) * 8) * 32 + (lane >> 4 & 1) * 16;
-    // (loaded past the end too: a branch around it would end the block of code)
+    // b's block of scales is one for the wave (tiles start and end with blocks, or within one)
     const auto block_scale = [&](int step) {
         if constexpr (ROWS) return 1.0f;
-        const float s = b_sf[min(step, steps - 1)];
-        return step < steps ? s : 0.0f;
+        else return __int_as_float(*reinterpret_cast<const int*>(lds + T::OFF_SFB + (step >> 3 & 1) * 256 + (step & 7) * 4 + wn * T::TN / 128 * 32));
     };
     const auto row_scale = [&](int step, int i) {
         return __int_as_float(*reinterpret_cast<const int*>(lds + (step >> 3 & 1) * T::SFA + (step & 7) * 4 + at_sa + 16 * i * 32));
@@ -309,7 +306,6 @@ __global__ void __launch_bounds__(T::NT) moe_product(ProductArgs p) {
             };
 #pragma unroll
             for (int i = 0; i < T::SM; ++i) s[i] = sa[i] * sb;
-            sb = block_scale(step + T::WK);
             Ready<EXACT> x[T::SM];
 #pragma unroll
             for (int i = 0; i < T::SM; ++i) x[i] = Ready<EXACT>(x_raw[i]);
@@ -343,10 +339,13 @@ __global__ void __launch_bounds__(T::NT) moe_product(ProductArgs p) {
                     for (int n = lo; n < hi; ++n)
                         if ((n - lo) * slots / (hi - lo) == before + slot) issue(place, round + S, order(n));
                 };
-                const auto read_next = [&](int i) {
-                    x_raw[i] = operand(lds + next + at_x, i);
-                    sa[i] = row_scale(step + T::WK, i);
-                };
+                // (the scales a column before the operands: what the next round waits for first)
+                if (j == T::SN - 2) {
+#pragma unroll
+                    for (int i = 0; i < T::SM; ++i) sa[i] = row_scale(step + T::WK, i);
+                    sb = block_scale(step + T::WK);
+                }
+                const auto read_next = [&](int i) { x_raw[i] = operand(lds + next + at_x, i); };
                 if constexpr (EXACT) {
 #pragma unroll
                     for (int q = 0; q < Ready<EXACT>::N; ++q)
