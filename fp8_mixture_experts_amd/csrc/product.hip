@@ -159,7 +159,7 @@ __device__ __forceinline__ int in_order(int id, int total) {
 //
 // What bounds it: with few rows what a compute unit takes in, some 50 to 70 KB/us of operands (deeper
 // rounds, more waves, or fewer bytes of b and more of a, change nothing), so that small tiles, all compute units
-// and no second launch are best: 128 x 7168 x 4096 12.2 us, 128 x 2048 x 7168 7.7. With many rows the matrix
+// and no second launch are best: 128 x 7168 x 4096 11.7 us, 128 x 2048 x 7168 7.6. With many rows the matrix
 // unit and the scaling's vector instructions, which share the issue (their busy shares add up to
 // 91%), and the card's power: 8192 x 7168 x 4096 200 us (2.4 PFLOP/s; a library product of the same codes without
 // scales 175 to 193). F32 results: four F16 instructions (twice the FP8's time in all) behind 16
