@@ -311,7 +311,7 @@ int mega_moe_rotary_frequencies(const mega_moe_rotary_frequencies_args* a) {
             return a->rotary_dim * std::log(a->original_length / (turns * 6.283185307179586)) / (2.0 * std::log(a->base));
         };
         lo = std::fmax(std::floor(index(a->fast_turns)), 0.0);
-        hi = std::fmin(std::ceil(index(a->slow_turns)), half - 1.0);
+        hi = std::fmin(std::ceil(index(a->slow_turns)), a->rotary_dim - 1.0);    // the last frequency may lie between both
         if (!(hi - lo > 0.001)) hi = lo + 0.001;
     }
     for (int i = 0; i < half; ++i) {

@@ -781,8 +781,9 @@ int64_t mega_moe_rotary_workspace_bytes(const mega_moe_rotary_backward_args* a);
  * copies them to the device), and the scale that goes with them.  BY_PARTS:
  * a frequency that makes more than fast_turns turns over original_length
  * positions stays, one that makes fewer than slow_turns is divided by factor,
- * and between them (by index, over the whole indices around both bounds) the
- * two are mixed linearly; scale = 0.1 ln(factor) + 1 (else 1).
+ * and between them (by index, over the whole indices around both bounds, kept
+ * within [0, R - 1]) the two are mixed linearly; scale = 0.1 ln(factor) + 1
+ * (else 1).
  */
 typedef struct mega_moe_rotary_frequencies_args {
     int32_t rotary_dim;       /* R, a positive multiple of 16                    */
