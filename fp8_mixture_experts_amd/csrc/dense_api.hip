@@ -312,7 +312,7 @@ int mega_moe_rotary_frequencies(const mega_moe_rotary_frequencies_args* a) {
         };
         lo = std::fmax(std::floor(index(a->fast_turns)), 0.0);
         hi = std::fmin(std::ceil(index(a->slow_turns)), a->rotary_dim - 1.0);    // the last frequency may lie between both
-        if (!(hi - lo > 0.001)) hi = lo + 0.001;
+        lo = std::fmin(lo, hi - 1.0);                   // all of them are slow, or all fast
     }
     for (int i = 0; i < half; ++i) {
         double f = std::pow(a->base, -2.0 * i / a->rotary_dim);

@@ -150,6 +150,6 @@ def frequencies(rotary_dim, base, factor=None, original=None, fast=None, slow=No
         return math.log(turns[0] / n) / math.log(base) * rotary_dim / 2.0
 
     lo, hi = max(math.floor(index(fast)), 0), min(math.ceil(index(slow)), rotary_dim - 1)
-    hi = hi if hi > lo else lo + 0.001
+    lo = min(lo, hi - 1)        # all of them are slow, or all fast
     share = [min(max((i - lo) / (hi - lo), 0.0), 1.0) for i in range(rotary_dim // 2)]
     return [v * (1.0 - s) + v / factor * s for v, s in zip(f, share)], 0.1 * math.log(factor) + 1.0

@@ -42,3 +42,19 @@ def test_ramp_goes_from_one_bound_to_the_other(dim, base, length, fast, slow, lo
     np.testing.assert_allclose(inv, want, rtol=2.0 ** -24 + 1e-12, atol=0)
     assert abs(scale - (0.1 * math.log(factor) + 1.0)) <= 2.0 ** -24 * scale
     np.testing.assert_allclose(dense.frequencies(dim, base, factor, length, fast, slow)[0], want, rtol=1e-12, atol=0)
+
+
+@pytest.mark.parametrize("dim,base,length,fast,slow", [(64, 1e4, 4.0, 32.0, 1.0), (16, 1e4, 2 * math.pi * 0.999, 2.0, 1.0),
+                                                       (32, 500.0, 100.0, 64.0, 16.0), (16, 1e4, 1e-3, 32.0, 1.0)])
+def test_frequencies_that_are_all_slow_are_all_divided(dim, base, length, fast, slow):
+    plain = [base ** (-2.0 * i / dim) for i in range(dim // 2)]
+    assert length * plain[0] / (2 * math.pi) < slow
+    want = [f / 8.0 for f in plain]
+    np.testing.assert_allclose(_by_parts(dim, base, length, fast, slow, 8.0)[0], want, rtol=2.0 ** -24 + 1e-12, atol=0)
+    np.testing.assert_allclose(dense.frequencies(dim, base, 8.0, length, fast, slow)[0], want, rtol=1e-12, atol=0)
+
+
+def test_frequencies_that_are_all_fast_all_stay():
+    # 10^12 positions: the last of 32 makes 10^7 turns
+    inv, _ = _by_parts(64, 1e4, 1e12, 32.0, 1.0, 8.0)
+    np.testing.assert_allclose(inv, [1e4 ** (-i / 32.0) for i in range(32)], rtol=2.0 ** -24 + 1e-12, atol=0)
