@@ -70,12 +70,13 @@ int check_rotary(const Args& a) {
 }
 
 // The strides of one tensor of heads, resolved; false if they cannot be used.
-// Dense rows of one head after another where they are 0.
+// Dense rows of one head after another where they are 0.  Those of no heads are of no matter.
 bool head_strides(int64_t& token, int64_t& head, int heads, int D) {
+    if (heads == 0) return true;
     if (head == 0) head = D;
     if (head < D || head % 8 || head > MAX_HEAD_STRIDE) return false;
-    const int64_t row = heads > 0 ? (heads - 1) * head + D : D;
-    if (token == 0) token = head * (heads > 0 ? heads : 1);
+    const int64_t row = (heads - 1) * head + D;
+    if (token == 0) token = head * heads;
     return token >= row && token % 8 == 0 && token <= ((int64_t)1 << 38);
 }
 
@@ -219,9 +220,9 @@ int mega_moe_rotary(const mega_moe_rotary_args* args, void* stream) {
         !head_strides(a.k_out_stride, a.k_out_head_stride, a.k_heads, D))
         return bad("a stride is shorter than its row or head, too long, or not a multiple of 8");
     const int64_t T = a.num_tokens, size = type_bytes(a.type), ws = type_bytes(a.weight_type);
-    if (a.q_out == a.q && (a.q_out_stride != a.q_stride || a.q_out_head_stride != a.q_head_stride))
+    if (a.q_heads > 0 && a.q_out == a.q && (a.q_out_stride != a.q_stride || a.q_out_head_stride != a.q_head_stride))
         return bad("q_out may be q only with the same strides");
-    if (a.k_out == a.k && (a.k_out_stride != a.k_stride || a.k_out_head_stride != a.k_head_stride))
+    if (a.k_heads > 0 && a.k_out == a.k && (a.k_out_stride != a.k_stride || a.k_out_head_stride != a.k_head_stride))
         return bad("k_out may be k only with the same strides");
     Tensors ts;
     add_heads(ts, "q", a.q, T, a.q_heads, D, a.q_stride, a.q_head_stride, size, false);
@@ -262,9 +263,9 @@ int mega_moe_rotary_backward(const mega_moe_rotary_backward_args* args, void* st
         !head_strides(a.dk_out_stride, a.dk_out_head_stride, a.k_heads, D) ||
         !head_strides(a.dq_stride, a.dq_head_stride, a.q_heads, D) || !head_strides(a.dk_stride, a.dk_head_stride, a.k_heads, D))
         return bad("a stride is shorter than its row or head, too long, or not a multiple of 8");
-    if (a.dq && a.dq == a.dq_out && (a.dq_stride != a.dq_out_stride || a.dq_head_stride != a.dq_out_head_stride))
+    if (a.q_heads > 0 && a.dq && a.dq == a.dq_out && (a.dq_stride != a.dq_out_stride || a.dq_head_stride != a.dq_out_head_stride))
         return bad("dq may be dq_out only with the same strides");
-    if (a.dk && a.dk == a.dk_out && (a.dk_stride != a.dk_out_stride || a.dk_head_stride != a.dk_out_head_stride))
+    if (a.k_heads > 0 && a.dk && a.dk == a.dk_out && (a.dk_stride != a.dk_out_stride || a.dk_head_stride != a.dk_out_head_stride))
         return bad("dk may be dk_out only with the same strides");
     const int64_t need = rotary_bytes(a);
     if ((rc = check_workspace(a.workspace, a.workspace_bytes, need))) return rc;
