@@ -61,7 +61,7 @@ int check_rotary(const Args& a) {
         return bad("rotary_start must be a multiple of 8, with the rotated columns inside the head");
     if (a.layout != MEGA_MOE_ROTARY_HALF && a.layout != MEGA_MOE_ROTARY_INTERLEAVED) return bad("unknown layout");
     if (!type_ok(a.type) || !type_ok(a.weight_type)) return bad("a type is neither MEGA_MOE_BF16 nor MEGA_MOE_F32");
-    if (a.first_position < 0 || (int64_t)a.first_position + a.num_tokens > (int64_t)INT32_MAX)
+    if (a.first_position < 0 || (int64_t)a.first_position + a.num_tokens > (int64_t)INT32_MAX + 1)
         return bad("first_position must be >= 0, and the last position a 32-bit number");
     if (!(a.eps >= 0.0f) || std::isinf(a.eps)) return bad("eps must be finite and >= 0");
     if (!std::isfinite(a.scale)) return bad("scale must be finite");

@@ -48,3 +48,14 @@ def test_strides_of_heads_in_place_still_have_to_agree(name):
     call, make = CALLS[name]
     f = dict(q_out=M, q_out_stride=512) if name == "rotary" else dict(dq=7 * M, dq_stride=512)
     assert _code(call, make(**f)) == B.MEGA_MOE_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("name", list(CALLS))
+@pytest.mark.parametrize("tokens,first,good", [(1, 2 ** 31 - 1, True), (2, 2 ** 31 - 2, True), (5, 2 ** 31 - 5, True),
+                                               (2, 2 ** 31 - 1, False), (5, 2 ** 31 - 4, False)])
+def test_last_position_is_the_largest_32_bit_number(name, tokens, first, good):
+    if good:
+        _no_gpu()
+    call, make = CALLS[name]
+    code = _code(call, make(num_tokens=tokens, first_position=first, positions=None))
+    assert (code == B.MEGA_MOE_ERR_INVALID_ARG) == (not good), B.mega_moe_last_error()
