@@ -29,6 +29,9 @@ struct QuantArgs {
     float clamp;                // infinite: none
 };
 
+// As the layer clamps: fminf and fmaxf would turn a NaN into a bound.
+__device__ __forceinline__ float clamped(float v, float c) { return v > c ? c : v < -c ? -c : v; }
+
 // A block's scale, and what its values are multiplied by, from the largest magnitude
 // as float32 bits (a NaN is the largest).
 struct Scale {
@@ -39,8 +42,8 @@ struct Scale {
         sf = amax / 448.0f;
         // tiny blocks are scaled up first, so that the reciprocal is finite
         up = sf < 0x1p-100f ? 0x1p100f : 1.0f;
-        const float d = (amax * up) / 448.0f;
-        hi = amax == 0.0f ? 0.0f : 1.0f / d;
+        const float d = sf * up;             // exact, also of a subnormal scale
+        hi = d == 0.0f ? 0.0f : 1.0f / d;
         // a scale of 0 or infinity: codes of 0
         lo = hi == 0.0f ? 0.0f : fmaf(-d, hi, 1.0f) * hi;
     }
@@ -57,10 +60,12 @@ struct Scale {
     }
     // v / sf: one rounding of a sum that is off by 2^-46, so that it is the quotient's own
     // but within that of the middle between two floats; no tie between codes lies there.
+    // (A subnormal scale may be rounded down by up to a third: the largest code then.)
     template <bool TINY>
     __device__ __forceinline__ float quotient(float v) const {
         if constexpr (TINY) v *= up;
-        return fmaf(v, hi, v * lo);
+        const float q = fmaf(v, hi, v * lo);
+        return TINY ? clamped(q, 448.0f) : q;
     }
     template <bool TINY>
     __device__ __forceinline__ uint32_t codes(float a, float b, float c, float e) const {
@@ -85,9 +90,6 @@ __device__ __forceinline__ float sigmoid(float g) {
     const float e = fmaf(hh, off * TWO_LN2, hh), t = 1.0f + e, r = __builtin_amdgcn_rcpf(t);
     return (g < 0.0f ? e : 1.0f) * fmaf(fmaf(-t, r, 1.0f), r, r);
 }
-
-// The layer's clamp: fminf and fmaxf would turn a NaN into a bound.
-__device__ __forceinline__ float clamped(float v, float c) { return v > c ? c : v < -c ? -c : v; }
 
 // Eight columns of one row as they lie in memory, and what is made of them.
 template <int KIND, bool F32>
@@ -166,8 +168,13 @@ __global__ void __launch_bounds__(256) moe_quantize_rows(QuantArgs a) {
             for (int e = 0; e < 8; ++e) m = larger(m, v[e]);
             const Scale s(over_lanes<16>(__float_as_uint(m), [](uint32_t x, uint32_t y) { return larger(x, y); }));
             const int64_t row = t * OUTS + which;        // [T, OUTS * C] codes
-            *reinterpret_cast<uint2*>(a.q + row * a.C + col) =
-                uint2{s.codes<true>(v[0], v[1], v[2], v[3]), s.codes<true>(v[4], v[5], v[6], v[7])};
+            const auto row_codes = [&](auto tiny) {
+                constexpr bool TINY = decltype(tiny)::value;
+                *reinterpret_cast<uint2*>(a.q + row * a.C + col) =
+                    uint2{s.codes<TINY>(v[0], v[1], v[2], v[3]), s.codes<TINY>(v[4], v[5], v[6], v[7])};
+            };
+            if (__any(s.up != 1.0f)) row_codes(std::true_type());
+            else row_codes(std::false_type());
             if (lane == 0) a.q_sf[row * blocks + b] = s.sf;
         }
     }

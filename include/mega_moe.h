@@ -647,9 +647,11 @@ int64_t mega_moe_product_workspace_bytes(const mega_moe_product_args* a);
 
 /*
  * The operands of the products: h = x, or silu(x) * up in float32, as E4M3
- * codes with scales, as the norm makes them (sf = max |h| of the block / 448,
- * code = e4m3(h / sf), the quotient rounded as float32 divides; a block whose
- * maximum is 0 has scale and codes 0, one with a NaN has both NaN).  q are h's rows; qt those of its transpose, with the tokens
+ * codes with scales: sf = max |h| of the block / 448, code = e4m3(h / sf), the
+ * quotient rounded as float32 divides and at most 448 (a subnormal sf, which is
+ * rounded to fewer bits, can leave more; the norm divides by such a scale
+ * before it is rounded).  A block whose sf is 0 has codes 0, one with a NaN has
+ * scale and codes NaN.  q are h's rows; qt those of its transpose, with the tokens
  * behind num_tokens, up to a multiple of 128, as codes 0 (they take no part in
  * scales).  With SCALE_ROW every row of q, and of qt, has a scale for 128 of
  * its codes; with SCALE_BLOCK (weights, "tokens" being their rows) q and qt
