@@ -40,8 +40,9 @@ struct Scale {
     __device__ __forceinline__ explicit Scale(uint32_t m) {
         const float amax = __uint_as_float(m);
         sf = amax / 448.0f;
-        // tiny blocks are scaled up first, so that the reciprocal is finite
-        up = sf < 0x1p-100f ? 0x1p100f : 1.0f;
+        // tiny blocks are scaled up first, so that the reciprocal is finite, and large ones down, so
+        // that what is left of it is no subnormal number (from scales of 2^102 on it would lose bits)
+        up = sf < 0x1p-100f ? 0x1p100f : sf > 0x1p64f ? 0x1p-64f : 1.0f;
         const float d = sf * up;             // exact, also of a subnormal scale
         hi = d == 0.0f ? 0.0f : 1.0f / d;
         // a scale of 0 or infinity: codes of 0
@@ -61,16 +62,16 @@ struct Scale {
     // v / sf: one rounding of a sum that is off by 2^-46, so that it is the quotient's own
     // but within that of the middle between two floats; no tie between codes lies there.
     // (A subnormal scale may be rounded down by up to a third: the largest code then.)
-    template <bool TINY>
+    template <bool SCALED>
     __device__ __forceinline__ float quotient(float v) const {
-        if constexpr (TINY) v *= up;
+        if constexpr (SCALED) v *= up;
         const float q = fmaf(v, hi, v * lo);
-        return TINY ? clamped(q, 448.0f) : q;
+        return SCALED ? clamped(q, 448.0f) : q;
     }
-    template <bool TINY>
+    template <bool SCALED>
     __device__ __forceinline__ uint32_t codes(float a, float b, float c, float e) const {
-        const int p = __builtin_amdgcn_cvt_pk_fp8_f32(quotient<TINY>(a), quotient<TINY>(b), 0, false);
-        return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(quotient<TINY>(c), quotient<TINY>(e), p, true);
+        const int p = __builtin_amdgcn_cvt_pk_fp8_f32(quotient<SCALED>(a), quotient<SCALED>(b), 0, false);
+        return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(quotient<SCALED>(c), quotient<SCALED>(e), p, true);
     }
 };
 
@@ -168,10 +169,10 @@ __global__ void __launch_bounds__(256) moe_quantize_rows(QuantArgs a) {
             for (int e = 0; e < 8; ++e) m = larger(m, v[e]);
             const Scale s(over_lanes<16>(__float_as_uint(m), [](uint32_t x, uint32_t y) { return larger(x, y); }));
             const int64_t row = t * OUTS + which;        // [T, OUTS * C] codes
-            const auto row_codes = [&](auto tiny) {
-                constexpr bool TINY = decltype(tiny)::value;
+            const auto row_codes = [&](auto scaled) {
+                constexpr bool SCALED = decltype(scaled)::value;
                 *reinterpret_cast<uint2*>(a.q + row * a.C + col) =
-                    uint2{s.codes<TINY>(v[0], v[1], v[2], v[3]), s.codes<TINY>(v[4], v[5], v[6], v[7])};
+                    uint2{s.codes<SCALED>(v[0], v[1], v[2], v[3]), s.codes<SCALED>(v[4], v[5], v[6], v[7])};
             };
             if (__any(s.up != 1.0f)) row_codes(std::true_type());
             else row_codes(std::false_type());
@@ -209,13 +210,16 @@ __device__ __forceinline__ int columns_of() { return (threadIdx.x & 16) / 4 + (t
 // One pass: 8192 x 7168 BF16 to codes by rows and by columns 53 us (235 MB, 4.4 TB/s with the call; a copy's rate
 // would be 47), SwiGLU gradients 4096 x 2048 to both 20.5 us (84 MB; 16.7): vector instructions are
 // busy for about half of the time, beside the memory, and a compute unit's tiles start and end together.
+//
+// Four waves to a vector unit (two workgroups of 8 to a compute unit, or one of 16): the gradients' codes fill
+// the registers that this leaves, and with two more take 26.7 us, not 20.5.
 template <int KIND, bool F32, bool BLOCK, int R>
-__global__ void __launch_bounds__(2048 / R) moe_quantize_tile(QuantArgs a) {
+__global__ void __launch_bounds__(2048 / R, 4) moe_quantize_tile(QuantArgs a) {
     constexpr int OUTS = KIND == GRAD ? 2 : 1, WAVES = 32 / R;
     constexpr bool AHEAD = R == 2 && !F32;               // the next tile's loads in flight behind this one's codes
     __shared__ __attribute__((aligned(16))) uint32_t top[OUTS][WAVES][128];
     __shared__ __attribute__((aligned(16))) float col_up[OUTS * 128], col_hi[OUTS * 128], col_lo[OUTS * 128];
-    __shared__ int col_tiny[OUTS * 2];
+    __shared__ int col_scaled[OUTS * 2];
     __shared__ __attribute__((aligned(16))) uint8_t turned[OUTS][128 * 128];   // [column][row], chunks of 16 swizzled
     const int lane = threadIdx.x & 15, group = threadIdx.x >> 4, wave = threadIdx.x >> 6;
     const int blocks = a.C / 128, row_blocks = (a.T + 127) / 128;
@@ -304,8 +308,8 @@ __global__ void __launch_bounds__(2048 / R) moe_quantize_tile(QuantArgs a) {
             const Scale s(x);
             a.qt_sf[qt_row(threadIdx.x) * row_blocks + rb] = s.sf;
             col_up[threadIdx.x] = s.up, col_hi[threadIdx.x] = s.hi, col_lo[threadIdx.x] = s.lo;
-            const bool tiny = __any(s.up != 1.0f);
-            if ((threadIdx.x & 63) == 0) col_tiny[wave] = tiny;
+            const bool scaled = __any(s.up != 1.0f);
+            if ((threadIdx.x & 63) == 0) col_scaled[wave] = scaled;
         }
         if (a.q) {
 #pragma unroll
@@ -321,12 +325,12 @@ __global__ void __launch_bounds__(2048 / R) moe_quantize_tile(QuantArgs a) {
                     mine = Scale(own);
                     if (lane < R && t0 + lane < a.T) a.q_sf[((t0 + lane) * OUTS + which) * blocks + b] = mine.sf;
                 }
-                const auto row_codes = [&](auto tiny) {
-                    constexpr bool TINY = decltype(tiny)::value;
+                const auto row_codes = [&](auto scaled) {
+                    constexpr bool SCALED = decltype(scaled)::value;
 #pragma unroll
                     for (int r = 0; r < R; ++r) {
                         const Scale s = r == 0 ? mine.of_quad<0>() : r == 1 ? mine.of_quad<1>() : r == 2 ? mine.of_quad<2>() : mine.of_quad<3>();
-                        const uint2 d = {s.codes<TINY>(v[r][0], v[r][1], v[r][2], v[r][3]), s.codes<TINY>(v[r][4], v[r][5], v[r][6], v[r][7])};
+                        const uint2 d = {s.codes<SCALED>(v[r][0], v[r][1], v[r][2], v[r][3]), s.codes<SCALED>(v[r][4], v[r][5], v[r][6], v[r][7])};
                         if (t0 + r < a.T) *reinterpret_cast<uint2*>(a.q + ((t0 + r) * OUTS + which) * a.C + col) = d;
                     }
                 };
@@ -339,23 +343,23 @@ __global__ void __launch_bounds__(2048 / R) moe_quantize_tile(QuantArgs a) {
 #pragma unroll
             for (int which = 0; which < OUTS; ++which) {
                 const float (&v)[R][8] = made[which];
-                const auto column_codes = [&](auto tiny) {
-                    constexpr bool TINY = decltype(tiny)::value;
+                const auto column_codes = [&](auto scaled) {
+                    constexpr bool SCALED = decltype(scaled)::value;
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         Scale s = of_block;
                         if constexpr (!BLOCK) {
                             const int c = which * 128 + lane * 8 + e;
                             s.hi = col_hi[c], s.lo = col_lo[c];
-                            if constexpr (TINY) s.up = col_up[c];
+                            if constexpr (SCALED) s.up = col_up[c];
                         }
                         // the 16 bytes of a row lie at chunk ^ (column / 8 % 8)
                         uint8_t* to = turned[which] + (lane * 8 + e) * 128 + ((group * R) ^ ((lane & 7) * 16));
-                        if constexpr (R == 4) *reinterpret_cast<uint32_t*>(to) = s.codes<TINY>(v[0][e], v[1][e], v[2][e], v[R - 1][e]);
-                        else *reinterpret_cast<uint16_t*>(to) = (uint16_t)__builtin_amdgcn_cvt_pk_fp8_f32(s.quotient<TINY>(v[0][e]), s.quotient<TINY>(v[1][e]), 0, false);
+                        if constexpr (R == 4) *reinterpret_cast<uint32_t*>(to) = s.codes<SCALED>(v[0][e], v[1][e], v[2][e], v[R - 1][e]);
+                        else *reinterpret_cast<uint16_t*>(to) = (uint16_t)__builtin_amdgcn_cvt_pk_fp8_f32(s.quotient<SCALED>(v[0][e]), s.quotient<SCALED>(v[1][e]), 0, false);
                     }
                 };
-                if (BLOCK ? of_block.up != 1.0f : (col_tiny[2 * which] | col_tiny[2 * which + 1]) != 0) column_codes(std::true_type());
+                if (BLOCK ? of_block.up != 1.0f : (col_scaled[2 * which] | col_scaled[2 * which + 1]) != 0) column_codes(std::true_type());
                 else column_codes(std::false_type());
             }
             __syncthreads();

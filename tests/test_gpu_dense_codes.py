@@ -1,11 +1,11 @@
 """E4M3 codes of mega_moe_quantize where scales are far from 1: those next to
-the smallest float32 numbers, rounded or lost."""
+the smallest float32 numbers, rounded or lost, and those next to the largest."""
 
 import pytest
 import torch
 
 from fp8_mixture_experts_amd import binding as B
-from tests.test_gpu_dense_limits import _new, _quantize
+from tests.test_gpu_dense_limits import _new, _next_to_ties, _quantize
 
 pytestmark = pytest.mark.gpu
 
@@ -68,6 +68,30 @@ def test_codes_of_subnormal_scales_are_those_of_the_quotient(way):
     # float64's quotient of a float32 number, rounded to a subnormal float32: a float32 division's own
     assert torch.equal(sf, (_most(x, way).double() / 448.0).float())
     assert bool((sf == 0).any()) and bool((sf == 2.0 ** -149).any()) and bool((sf > 2.0 ** -126).any())
+    _same(got, _want(x, sf))
+
+
+@pytest.mark.parametrize("way", WAYS)
+def test_codes_of_the_largest_scales_are_those_of_the_quotient(way):
+    g = torch.Generator()
+    g.manual_seed(6)
+    x = _next_to_ties(_scales(16384, 100, 118, way, g).float(), 7)
+    got, sf = _codes(x, way)
+    assert torch.equal(sf, _most(x, way) / 448.0) and bool(sf.isfinite().all())
+    _same(got, _want(x, sf))
+
+
+@pytest.mark.parametrize("way", WAYS)
+def test_codes_where_scales_of_all_sizes_meet(way):
+    # tiny, ordinary and large blocks side by side, in one wave's rows and columns
+    g = torch.Generator()
+    g.manual_seed(8)
+    exponents = torch.tensor([-130.0, -127.0, -101.0, -99.0, -3.0, 0.0, 60.0, 63.0, 64.0, 65.0, 110.0, 118.0])
+    n = 32 if way == "blocks" else 4096
+    scales = (torch.rand(n, generator=g) + 0.5) * torch.exp2(exponents[torch.randint(0, len(exponents), (n,), generator=g)])
+    x = _next_to_ties(scales.repeat_interleave(4096 // n), 9)
+    got, sf = _codes(x, way)
+    assert torch.equal(sf, (_most(x, way).double() / 448.0).float())
     _same(got, _want(x, sf))
 
 
