@@ -563,7 +563,8 @@ __global__ void __launch_bounds__(PAIRED ? 512 : 1024, 4) moe_product_few(Produc
     }
 }
 
-// Adds the parts of the sums, in order, and `add`: a launch (3.9 us of a call) and 8 bytes of each part's elements.
+// Adds the parts of the sums, in order, and `add`: a launch (2.8 us of a call), 0.23 us for each part that a thread adds and
+// 8 bytes of each of its elements.
 template <bool F32>
 __global__ void __launch_bounds__(256) moe_product_join(ProductArgs p) {
     const int across = p.n / 8;
@@ -604,48 +605,9 @@ using Deep = Tile<64, 64, 2, 2, 2, 3>;        // one, of two groups of waves
 using Strip = Tile<32, 64, 1, 2, 4, 3>;       // (128 x 7168 x 4096 from HBM: 16.6 us, Deep's halves 18.2)
 using Low = Tile<32, 32, 2, 1, 4, 3>;
 
-int64_t tiles_of(int m, int n, int bm, int bn) { return (int64_t)((m + bm - 1) / bm) * ((n + bn - 1) / bn); }
-
-// What a kind takes, in us, beside the 2 of any call, with f tiles on the busiest of 256 compute units
-// and s steps: f * tile + s * step for each tile, or s * alone for the last of an odd f where
-// two share a compute unit (few rows: tile + f * s * (step + alone * m / 16), of b's rows and of a's); and what
-// splitting it adds. Fitted (non-negative least
-// squares of relative errors) to 153 shapes of m in [1, 8192], k in [128, 8192], n in [64, 18432], with
-// operands that come from HBM (from the last-level cache the small tiles' steps take a fifth less): the
-// least of them is on average within 1% of the fastest of all measured, 12% at worst (F32: 2% and 19%). Beside these,
-// 128 x 64 (with and without two groups), 256 x 128 and (BF16) 128 x 256 were measured; without them the choice
-// is no worse. With F32 results Strip, Half, Tall and Long are hardly ever the fastest.
-struct Kind {
-    int rows, columns;
-    float tile, step, alone;
-};
-enum { FEW, LOW, STRIP, DEEP, PAIR, HALF, MID, TALL, LONG, WIDE, KINDS };
-constexpr float NEVER = INFINITY;
-constexpr Kind FP8[KINDS] = {{16, 16, 1.45f, 0.067f, 0.062f},
-                             {32, 32, 2.25f, 0.128f, 0.128f},
-                             {32, 64, 2.62f, 0.182f, 0.182f},
-                             {64, 64, 2.13f, 0.265f, 0.265f},
-                             {64, 64, 1.23f, 0.213f, 0.382f},
-                             {64, 128, 2.44f, 0.383f, 0.383f},
-                             {128, 128, 1.58f, 0.558f, 0.768f},
-                             {192, 128, 2.53f, 0.678f, 0.678f},
-                             {128, 128, 2.21f, 0.519f, 0.519f},
-                             {256, 256, 3.29f, 1.275f, 1.275f}};
-constexpr Kind EXACT_F32[KINDS] = {{16, 16, 0.96f, 0.112f, 0.067f},
-                                   {32, 32, 2.61f, 0.146f, 0.146f},
-                                   {32, 64, NEVER, 0.0f, 0.0f},
-                                   {64, 64, 3.10f, 0.371f, 0.371f},
-                                   {64, 64, 1.70f, 0.345f, 0.603f},
-                                   {64, 128, NEVER, 0.0f, 0.0f},
-                                   {128, 128, 3.48f, 0.886f, 1.194f},
-                                   {192, 128, NEVER, 0.0f, 0.0f},
-                                   {128, 128, NEVER, 0.0f, 0.0f},
-                                   {128, 256, 4.69f, 1.677f, 1.677f}};
-constexpr float JOIN = 3.9f, JOIN_ELEMENT = 1.6e-6f;        // a second launch, and its sums
-
 template <typename T, bool EXACT, bool ROWS>
 void go(const ProductArgs& p, hipStream_t stream) {
-    const int64_t blocks = tiles_of(p.m, p.n, T::BM, T::BN) * p.splits;
+    const int64_t blocks = product_tiles(p.m, p.n, T::BM, T::BN) * p.splits;
     hipLaunchKernelGGL((moe_product<T, EXACT, ROWS>), dim3((unsigned)blocks), dim3(T::NT),
                        (unsigned)T::template lds<ROWS>(), stream, p);
 }
@@ -680,29 +642,6 @@ void go(int kind, const ProductArgs& p, hipStream_t stream) {
 }
 
 }  // namespace
-
-ProductPlan product_plan(int m, int n, int k, int out_type) {
-    const Kind* kinds = out_type == MEGA_MOE_F32 ? EXACT_F32 : FP8;
-    const int steps = k / BK, first = m <= 16 ? FEW : LOW;
-    ProductPlan best = {first, 1};
-    float least = INFINITY;
-    for (int kind = first; kind < KINDS; ++kind) {
-        const Kind& o = kinds[kind];
-        const int64_t tiles = tiles_of(m, n, o.rows, o.columns);
-        // parts of the steps only where a compute unit would have no tile without them
-        for (int splits = 1; splits == 1 || (kind != FEW && splits <= steps && tiles * splits <= 512 && splits <= 64); splits *= 2) {
-            if (kind == LONG && tiles * splits > 256) break;
-            const int64_t f = (tiles * splits + 255) / 256, s = (steps + splits - 1) / splits;
-            float us = kind == FEW ? o.tile + f * s * (o.step + o.alone * m / 16.0f) : f * o.tile + s * ((f - f % 2) * o.step + f % 2 * o.alone);
-            if (splits > 1) us += JOIN + JOIN_ELEMENT * splits * (float)m * n;
-            if (us < least) {
-                least = us;
-                best = {kind, splits};
-            }
-        }
-    }
-    return best;
-}
 
 int64_t product_workspace(const ProductPlan& plan, int m, int n) { return plan.splits > 1 ? (int64_t)plan.splits * m * n * 4 : 0; }
 
