@@ -10,6 +10,8 @@ import pytest
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 KINDS = ["FEW", "LOW", "STRIP", "DEEP", "PAIR", "HALF", "MID", "TALL", "LONG", "WIDE"]
+TILE = {"FEW": (16, 16), "LOW": (32, 32), "STRIP": (32, 64), "DEEP": (64, 64), "PAIR": (64, 64), "HALF": (64, 128), "MID": (128, 128),
+        "TALL": (192, 128), "LONG": (128, 128)}
 BF16, F32 = 0, 1
 SOURCE = """
 #include <cstdio>
@@ -91,3 +93,26 @@ def test_choice_can_be_launched(plan):
                     assert parts == 1 or (parts <= k // 128 and kind != "FEW")
                     assert kind != "FEW" or m <= 16
                     assert out_type == BF16 or kind not in ("STRIP", "HALF", "TALL", "LONG")
+
+
+def test_sizes_of_the_long_loops_reach_every_kind(plan):
+    import torch
+
+    from tests.test_gpu_dense_tiles import CASES
+    for dtype, sizes in CASES.items():
+        out_type = F32 if dtype == torch.float32 else BF16
+        for size, want in sizes.items():
+            m, k, n = size
+            assert plan(m, k, n, out_type) == want, size
+            # (a wave of the few rows' kernel has every 8th or 16th step, and takes three or two at a time)
+            steps = k // 128 // want[1]
+            assert steps >= 17 and (steps % 8 or size == (1, 7168, 18432)), size
+            rows, columns = TILE.get(want[0], (128, 256))
+            assert m % rows and (want[0] == "FEW" or n % columns), size
+        kinds = {kind for kind, _ in sizes.values()}
+        assert kinds == set(KINDS) - (set() if out_type == BF16 else {"STRIP", "HALF", "TALL", "LONG"})
+        in_parts = {kind for kind, parts in sizes.values() if parts > 1}
+        assert in_parts == ({"LOW", "STRIP", "DEEP", "HALF", "TALL", "LONG", "WIDE"} if out_type == BF16 else {"LOW", "DEEP", "MID", "WIDE"})
+    few = [size for size, (kind, _) in CASES[torch.bfloat16].items() if kind == "FEW"]
+    # two workgroups to a compute unit: twice and more around their loop of 24 steps
+    assert sum(n > 4096 and k // 128 > 24 for m, k, n in few) >= 3 and any(n > 4096 and k // 128 > 48 for m, k, n in few)
