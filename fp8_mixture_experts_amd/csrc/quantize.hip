@@ -388,11 +388,16 @@ void launch(const QuantArgs& a, bool block, hipStream_t stream) {
         };
         if constexpr (KIND == GRAD) {
             // The values of two outputs leave a compute unit two workgroups of 8 waves with four rows to a
-            // thread, or one of 16 with two, which goes on to further tiles with their loads in flight
-            // (float32's do not fit beside the values). Codes alone are better made by the former (4096 x 2048:
-            // 20.5 us, 22.2 with two rows), with the gradients stored too (33.8, 30.2) and of float32 (38, 35.7)
-            // the latter is.
-            if (F32 || a.out[0] || a.out[1]) go(moe_quantize_tile<KIND, F32, false, 2>, 2, F32 ? MAX_GRID : 256);
+            // thread, or one of 16 with two, which goes on to further tiles, with their loads in flight
+            // (float32's do not fit beside the values; with four rows float32 has scratch).  Codes of BF16 alone are
+            // better made by the former, with the gradients stored too and of float32 by the latter.  Both ways, us
+            // (four rows, two):
+            //                      1000 x 4096   4096 x 2048   8192 x 2048   2304 x 7168   8192 x 4096
+            //   codes              13.9  13.1    20.0  21.8    44.0  45.2    42.4  45.0    79.5   81.5
+            //   codes, gradients   14.8  14.2    34.9  28.5    59.6  57.2    57.2  56.3    107.1  108.4
+            //   float32, codes     19.4  15.0    41.1  36.2    75.5  66.2    73.8  66.8
+            // and within 4% of each other below 256 tiles (float32 two rows: 15%).
+            if (F32 || a.out[0] || a.out[1]) go(moe_quantize_tile<KIND, F32, false, 2>, 2, 256);
             else go(moe_quantize_tile<KIND, false, false, 4>, 4, MAX_GRID);
         } else if (block) {
             go(moe_quantize_tile<KIND, F32, true, 4>, 4, MAX_GRID);
