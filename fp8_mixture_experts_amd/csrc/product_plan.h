@@ -22,8 +22,8 @@ inline int64_t product_tiles(int m, int n, int bm, int bn) { return (int64_t)((m
 // that come from HBM: m in [1, 8192], k in [128, 8192] and n in [64, 18432] spread over their logarithms; m up to 128 and n
 // up to 904 with k of 3840, 5632 and 8192; m and n up to 1024 with k up to 131072.  The least of the estimates is on
 // average within 0.3% of the fastest of all kinds in 1, 2, 4 .. 64 parts, 10% at worst; on 74 shapes of the first sort
-// that the fit has not seen 0.4% and 20%.  F32: 0.4% and 21%, on 36 not seen 2.2% and 29%, the worst of them results of many
-// columns from k = 128, whose stores the estimates leave out.
+// that the fit has not seen 0.4% and 20%.  F32, fitted to the kinds within 30% of a shape's fastest (the stores of many
+// results from a short k would bend the others): 0.3% and 5%, on 36 not seen 0.9% and 9%.
 // Beside these, 128 x 64 (with and without two groups), 256 x 128 and (BF16) 128 x 256 were measured; without them the
 // choice is no worse.  With F32 results Strip, Half, Tall and Long are hardly ever the fastest.
 struct ProductKind {
@@ -44,21 +44,21 @@ inline ProductPlan product_plan(int m, int n, int k, int out_type) {
                                                {192, 128, 3.24f, 0.630f, 0.630f},
                                                {128, 128, 2.76f, 0.455f, 0.455f},
                                                {256, 256, 4.43f, 1.145f, 1.145f}};
-    static constexpr ProductKind EXACT_F32[KINDS] = {{16, 16, 0.0f, 0.108f, 0.059f},
-                                                     {32, 32, 2.69f, 0.141f, 0.141f},
+    static constexpr ProductKind EXACT_F32[KINDS] = {{16, 16, 0.0f, 0.113f, 0.052f},
+                                                     {32, 32, 2.69f, 0.138f, 0.138f},
                                                      {32, 64, NEVER, 0.0f, 0.0f},
-                                                     {64, 64, 3.34f, 0.362f, 0.362f},
-                                                     {64, 64, 2.05f, 0.347f, 0.584f},
+                                                     {64, 64, 3.26f, 0.388f, 0.388f},
+                                                     {64, 64, 2.02f, 0.342f, 0.660f},
                                                      {64, 128, NEVER, 0.0f, 0.0f},
-                                                     {128, 128, 3.79f, 0.998f, 1.157f},
+                                                     {128, 128, 3.77f, 0.985f, 1.340f},
                                                      {192, 128, NEVER, 0.0f, 0.0f},
                                                      {128, 128, NEVER, 0.0f, 0.0f},
-                                                     {128, 256, 4.92f, 1.661f, 1.661f}};
+                                                     {128, 256, 7.59f, 1.851f, 1.851f}};
     const bool f32 = out_type == MEGA_MOE_F32;
     // what parts add: a second launch, whose threads add the parts one after another, and the sums' bytes
     // (in both kernels, where BF16 results leave the first one at half of a sum's)
     constexpr float JOIN = 2.8f, JOIN_PART = 0.23f;
-    const float join_element = f32 ? 1.35e-6f : 2e-6f;
+    const float join_element = f32 ? 0.9e-6f : 2e-6f;
     const ProductKind* kinds = f32 ? EXACT_F32 : FP8;
     const int steps = k / 128, first = m <= 16 ? FEW : LOW;
     ProductPlan best = {first, 1};

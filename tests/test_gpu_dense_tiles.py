@@ -24,9 +24,9 @@ CASES = {
         (136, 2176, 17248): ("TALL", 1), (143, 8704, 5496): ("TALL", 4), (65, 2304, 16800): ("LONG", 1), (68, 8832, 5640): ("LONG", 4),
         (388, 2304, 16464): ("WIDE", 1), (513, 2176, 13624): ("WIDE", 1), (203, 4864, 16800): ("WIDE", 2)},
     F32: {
-        (5, 4736, 19144): ("FEW", 1), (1, 2176, 18440): ("FEW", 1), (3, 9344, 264): ("FEW", 1),
-        (17, 2304, 72): ("LOW", 1), (1, 10752, 1048): ("LOW", 4), (5, 3200, 12456): ("DEEP", 1), (33, 4352, 4560): ("DEEP", 2),
-        (65, 2304, 8224): ("PAIR", 1), (65, 2304, 16800): ("MID", 1), (2163, 13824, 312): ("MID", 4),
+        (4, 4480, 19160): ("FEW", 1), (1, 2176, 18440): ("FEW", 1), (15, 8064, 3832): ("FEW", 1),
+        (17, 2304, 72): ("LOW", 1), (1, 10752, 1048): ("LOW", 4), (10, 2304, 13152): ("DEEP", 1), (33, 4352, 4560): ("DEEP", 2),
+        (65, 2304, 8224): ("PAIR", 1), (65, 2304, 16800): ("MID", 1), (276, 4992, 10760): ("MID", 2),
         (193, 2304, 17624): ("WIDE", 1), (66, 8832, 8352): ("WIDE", 4), (65, 4736, 17184): ("WIDE", 2)},
 }
 
