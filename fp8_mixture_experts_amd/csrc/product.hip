@@ -157,13 +157,14 @@ __device__ __forceinline__ int in_order(int id, int total) {
 // registers by then: behind it the round's place in LDS is free for new loads,
 // and the next round's operands are read while the matrix unit has those columns.
 //
-// What bounds it: with few rows what a compute unit takes in, some 50 to 70 KB/us of operands (deeper
+// What bounds it: with few rows what a compute unit takes in, some 40 to 65 KB/us of operands (deeper
 // rounds, more waves, or fewer bytes of b and more of a, change nothing), so that small tiles, all compute units
-// and no second launch are best: 128 x 7168 x 4096 11.7 us, 128 x 2048 x 7168 7.6. With many rows the matrix
-// unit and the scaling's vector instructions, which share the issue (their busy shares add up to
-// 91%), and the card's power: 8192 x 7168 x 4096 200 us (2.4 PFLOP/s; a library product of the same codes without
-// scales 175 to 193). F32 results: four F16 instructions (twice the FP8's time in all) behind 16
-// conversions for each operand; 4096 x 4096 x 2048 with scales of rows 67 us (1.0 PFLOP/s).
+// and no second launch are best: 128 x 7168 x 4096 11.9 us, 128 x 2048 x 7168 7.4. With many rows the matrix
+// unit (busy for 60% of the cycles) and the scaling's vector instructions (39%; both for 27%), which share the issue,
+// and the card's power: 8192 x 7168 x 4096 197 to 211 us by the card (2.3 to 2.45 PFLOP/s; a library product of the same
+// codes with one scale, on a card where this one takes 200 to 206, 157 at first and 202 once it is warm). F32 results:
+// four F16 instructions (twice the FP8's time in all) behind 16 conversions for each operand; 4096 x 4096 x 2048 with
+// scales of rows 68 to 74 us (1.0 PFLOP/s).
 template <typename T, bool EXACT, bool ROWS>
 __global__ void __launch_bounds__(T::NT) moe_product(ProductArgs p) {
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
@@ -471,11 +472,11 @@ __global__ void __launch_bounds__(T::NT) moe_product(ProductArgs p) {
 // Up to 16 rows of a: a workgroup has 16 rows of b over all of k, its W waves every W-th step each, from memory
 // into registers, and their sums meet in LDS.  b is read once and by no other workgroup; a comes from
 // the caches.  Memory bounds it.  Up to 256 workgroups (and with F32 results, whose operands fill the registers) 16
-// waves of two steps at a time, and two ahead: 1 x 7168 x 4096 6.9 us, from HBM 7.6 (29 MB; eight waves of four steps
+// waves of two steps at a time, and two ahead: 1 x 7168 x 4096 6.8 us, from HBM 7.6 (29 MB; eight waves of four steps
 // 7.2 and 7.8). More of them two to a compute unit, of eight waves of three steps: 1 x 7168 x 18432 from HBM
-// 25.9 us (5.1 TB/s; 16 waves 29.5). Loads of b past the caches took 10% longer, whole lines of
+// 25.8 us (5.1 TB/s; 16 waves 29.5). Loads of b past the caches took 10% longer, whole lines of
 // eight rows to a load 5%. 16 rows read as much of a as of b, and large n goes to the tiles then (18432:
-// 42 us against 34).
+// 42 us against 31).
 template <bool EXACT, bool ROWS, bool PAIRED>
 __global__ void __launch_bounds__(PAIRED ? 512 : 1024, 4) moe_product_few(ProductArgs p) {
     constexpr int W = PAIRED ? 8 : 16, U = PAIRED ? 3 : 2, PITCH = 20;
@@ -593,16 +594,16 @@ namespace {
 
 using Wide = Tile<256, 256, 4, 2, 1, 2>;
 using WideExact = Tile<128, 256, 2, 4, 1, 2>; // in its place with F32 results: the conversions' registers
-                                              // leave no room for 256 x 256 (4096 x 4096 x 2048: 67 us, Mid 74)
+                                              // leave no room for 256 x 256 (4096 x 4096 x 2048: 68 us, Mid 72)
 using Mid = Tile<128, 128, 2, 2, 1, 2>;       // two workgroups to a compute unit
 using Long = Tile<128, 128, 4, 2, 1, 4>;      // one, of eight waves with three rounds in flight: only up to 256 tiles,
-                                              // which have a compute unit each anyway (1024 x 7168 x 4096: 34 us, Mid
-                                              // 40; from HBM 39 and 55; but 2048 x 7168 x 4096: 73 us, Mid 61)
-using Tall = Tile<192, 128, 4, 2, 1, 3>;      // one (576 x 2048 x 7168: 16.2 us, Mid 17.7; 417 x 3328 x 10288 24.7 and 31.1)
-using Half = Tile<64, 128, 2, 2, 2, 3>;       // one, of two groups of waves (512 x 7168 x 4096: 21.5 us, Pair 25.5)
+                                              // which have a compute unit each anyway (1024 x 7168 x 4096: 37 us, Mid
+                                              // 42; from HBM 40 and 57; but 2048 x 7168 x 4096: 71 us, Mid 65)
+using Tall = Tile<192, 128, 4, 2, 1, 3>;      // one (576 x 2048 x 7168: 16.6 us, Mid 18.4; 417 x 3328 x 10288 23.4 and 26.5)
+using Half = Tile<64, 128, 2, 2, 2, 3>;       // one, of two groups of waves (512 x 7168 x 4096: 23.9 us, Pair 25.6)
 using Pair = Tile<64, 64, 2, 2, 1, 3>;        // two or three workgroups
 using Deep = Tile<64, 64, 2, 2, 2, 3>;        // one, of two groups of waves
-using Strip = Tile<32, 64, 1, 2, 4, 3>;       // (128 x 7168 x 4096 from HBM: 16.6 us, Deep's halves 18.2)
+using Strip = Tile<32, 64, 1, 2, 4, 3>;       // (128 x 7168 x 4096 from HBM: 16.4 us, Deep's halves 18.1)
 using Low = Tile<32, 32, 2, 1, 4, 3>;
 
 template <typename T, bool EXACT, bool ROWS>

@@ -145,8 +145,8 @@ __device__ __forceinline__ void store_out(const QuantArgs& a, int which, int64_t
 }  // namespace
 
 // Codes by rows and values alone: 16 lanes hold 128 columns of a row, whose largest value they find in four
-// lane moves.  One pass over the data: the launch bounds small batches (128 x 2048 of SwiGLU 6.9 us with the
-// call, 2.8 the kernel; 577 x 2048 gradients 6.7), memory large ones.
+// lane moves.  One pass over the data: the launch bounds small batches (128 x 2048 of SwiGLU 7.1 us with the
+// call, 3.0 the kernel; 577 x 2048 gradients 6.7), memory large ones.
 template <int KIND, bool F32>
 __global__ void __launch_bounds__(256) moe_quantize_rows(QuantArgs a) {
     constexpr int OUTS = KIND == GRAD ? 2 : 1;
@@ -207,9 +207,9 @@ __device__ __forceinline__ int columns_of() { return (threadIdx.x & 16) / 4 + (t
 // which a thread would have 36).  The codes by columns turn in LDS: a thread has R
 // neighbours of each, and a row of 128 leaves as whole lines.
 //
-// One pass: 8192 x 7168 BF16 to codes by rows and by columns 53 us (235 MB, 4.4 TB/s with the call; a copy's rate
-// would be 47), SwiGLU gradients 4096 x 2048 to both 20.5 us (84 MB; 16.7): vector instructions are
-// busy for about half of the time, beside the memory, and a compute unit's tiles start and end together.
+// One pass: 8192 x 7168 BF16 to codes by rows and by columns 54 us (239 MB, 4.4 TB/s with the call; a copy's rate
+// would be 47), SwiGLU gradients 4096 x 2048 to both 20.3 us (85 MB; 16.7): vector instructions have 40% and
+// 44% of the cycles, beside the memory, and a compute unit's tiles start and end together.
 //
 // Four waves to a vector unit (two workgroups of 8 to a compute unit, or one of 16): the gradients' codes fill
 // the registers that this leaves, and with two more take 26.7 us, not 20.5.
